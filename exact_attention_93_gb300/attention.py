@@ -15,15 +15,20 @@ extension of that argument list) restricts attention to the kept blocks of
 for it raises.  flash_attn_fp8_func is the forward on e4m3 inputs
 (FlashAttention-3's FP8 forward, which the "Flash Attention" wiki page and
 the v1 -> v3 table of "FlashAttention 深入" list), with per-(batch, head)
-descale factors; it has no backward.
+descale factors; it has no backward.  flash_attn_paged_func is the forward of
+new tokens (one each while generating, chunks or whole prompts) over a paged
+key/value cache (kvcache.py), with grouped heads and packed sequences of
+different lengths.
 """
 from __future__ import annotations
 
 import torch
 
 from . import fattn
+from .kvcache import check_devices
 
-__all__ = ["flash_attn_func", "flash_attn_qkvpacked_func", "flash_attn_fp8_func"]
+__all__ = ["flash_attn_func", "flash_attn_qkvpacked_func", "flash_attn_fp8_func",
+           "flash_attn_paged_func"]
 
 
 def _check_block_mask(block_mask, N, H):
@@ -187,4 +192,46 @@ def flash_attn_fp8_func(q, k, v, softmax_scale=None, causal=False, window_size=(
     opts = fattn.options(window, slopes, bmask)
     fattn.fa_fwd_fp8(q, k, v, o, lse, _layout(q, k, v, o), opts, B, H, N, D, scale,
                      bool(causal), *desc)
+    return (o, lse) if return_lse else o
+
+
+def flash_attn_paged_func(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
+                          softmax_scale=None, causal=True, window_size=(-1, -1),
+                          alibi_slopes=None, k_exp=None, v_exp=None, return_lse=False):
+    """Attention of packed new tokens over a paged cache that already holds
+    their keys and values (kvcache.kv_cache_append).
+
+    q: (total, nheads, headdim) bf16 or fp16, headdim 64 or 128; rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32, (batch + 1,)) are the newest
+    tokens of sequence b, whose cached length, those tokens included, is
+    seqlens[b] (int32, (batch,)).  Row i of sequence b sits at position
+    seqlens[b] - rows(b) + i.  k_pages, v_pages: (pages, page_size, nheads_k,
+    headdim) of q's type, or e4m3 with k_exp and v_exp; nheads is a multiple of
+    nheads_k, and nheads / nheads_k query heads share a key head.  block_table:
+    int32 (batch, max_pages).
+
+    causal, window_size and alibi_slopes ((nheads,) or (batch, nheads)) as for
+    flash_attn_func, in positions of the sequence.  Returns (total, nheads,
+    headdim) (and the fp32 (nheads, total) log-sum-exp when return_lse).  A row
+    that sees no key gets zeros and -inf; rows behind the last sequence are not
+    written.  Forward only."""
+    if torch.is_grad_enabled() and q.requires_grad:
+        raise ValueError("attention over a cache has no backward: call under torch.no_grad()")
+    cache = fattn.kv_pages(k_pages, v_pages, k_exp, v_exp)
+    if q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be a packed (total, nheads, headdim) tensor of the cache's "
+                         "headdim, which must be contiguous")
+    total, H, D = q.shape
+    if H % cache.heads:
+        raise ValueError("nheads must be a multiple of the cache's heads")
+    batch = fattn.ragged(block_table, cu_seqlens, seqlens, total)
+    window, slopes = _check_options(0.0, window_size, alibi_slopes, batch.batch, H)
+    opts = None
+    with check_devices(q, k_pages, v_pages, block_table, cu_seqlens, seqlens, slopes):
+        if slopes is not None or window != (-1, -1):
+            opts = fattn.options(window, slopes)
+        o = torch.empty((total, H, D), dtype=q.dtype, device=q.device)
+        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
+        fattn.fa_fwd_paged(q, o, lse, cache, batch, opts,
+                           D ** -0.5 if softmax_scale is None else float(softmax_scale), causal)
     return (o, lse) if return_lse else o

@@ -8,6 +8,7 @@
 #include "fattn.h"
 #include "fa_internal.h"
 #include "host_tmap.hpp"
+#include "sm103_primitives.cuh"
 
 namespace fa {
 namespace {
@@ -501,7 +502,7 @@ fa_status fa_device_error(void* stream, int* code) {
     if (cudaMemcpy(p, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
       return FA_ERR_CUDA;
   }
-  *code = v == 0 ? FA_OK : FA_ERR_TIMEOUT;
+  *code = v == kDevErrNone ? FA_OK : v == kDevErrBadIndex ? FA_ERR_INVALID_ARG : FA_ERR_TIMEOUT;
   return FA_OK;
 }
 

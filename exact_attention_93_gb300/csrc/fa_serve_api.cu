@@ -1,0 +1,316 @@
+// fa_serve_api.cu -- the C ABI of include/fattn_cache.h: argument checks, TMA
+// descriptor set-up, workspace layout and kernel launches.  No arithmetic of
+// the operators lives here.
+#include <cmath>
+#include <cstdint>
+
+#include "fa_internal.h"
+#include "fa_serve.h"
+#include "fattn_cache.h"
+#include "host_tmap.hpp"
+
+namespace fa {
+namespace {
+
+constexpr long long kMaxBytes = 1ll << 40;  // every operand lies below this from its base
+constexpr int kMaxRows = 1 << 29;           // packed rows, keys of a sequence, window bounds
+constexpr float kLog2e = 1.4426950408889634f;
+
+bool aligned(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int elem_bytes(int elem) { return elem == FA_ELEM_FP32 ? 4 : elem == FA_ELEM_E4M3 ? 1 : 2; }
+
+bool is16(int elem) { return elem == FA_ELEM_BF16 || elem == FA_ELEM_FP16; }
+
+// Strides of one operand: non-negative, `unit`-byte multiples, and the last
+// element below kMaxBytes.
+bool strides_ok(const long long* st, const long long* extent, int n, int D, int es, int unit) {
+  double last = D;
+  for (int i = 0; i < n; ++i) {
+    if (st[i] < 0 || (st[i] * es) % unit != 0 || st[i] > kMaxBytes) return false;
+    last += static_cast<double>(extent[i] - 1) * st[i];
+  }
+  return last * es < static_cast<double>(kMaxBytes);
+}
+
+fa_status check_batch(const fa_ragged* b, bool lens_needed) {
+  if (!b || b->batch < 1 || b->total < 0 || b->total > kMaxRows || b->max_pages < 1)
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(b->block_table, 4) || !aligned(b->cu_seqlens, 4) || b->table_stride < b->max_pages)
+    return FA_ERR_INVALID_ARG;
+  if (lens_needed && !aligned(b->seqlens, 4)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa_status check_pages(const fa_kv_pages* c, const fa_ragged* b, fa_elem dtype) {
+  if (!c) return FA_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return FA_ERR_UNSUPPORTED;
+  if (!is16(dtype) || (!is16(c->type) && c->type != FA_ELEM_E4M3)) return FA_ERR_UNSUPPORTED;
+  if (is16(c->type) && c->type != static_cast<int>(dtype)) return FA_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return FA_ERR_UNSUPPORTED;
+  if (c->pages < 1 || c->heads < 1 || c->heads > 65535) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(b->max_pages) * c->page_size > kMaxRows) return FA_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID_ARG;
+  if (c->type == FA_ELEM_E4M3 && (!aligned(c->k_exp, 16) || !aligned(c->v_exp, 16)))
+    return FA_ERR_INVALID_ARG;
+  const long long extent[3] = {c->pages, c->page_size, c->heads};
+  const long long ks[3] = {c->k_page, c->k_token, c->k_head};
+  const long long vs[3] = {c->v_page, c->v_token, c->v_head};
+  const int es = elem_bytes(c->type);
+  if (!strides_ok(ks, extent, 3, c->head_dim, es, 16) ||
+      !strides_ok(vs, extent, 3, c->head_dim, es, 16))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+// A packed [total][heads][D] operand of 16-bit elements.
+bool packed_ok(const void* p, long long token, long long head, int total, int heads, int D) {
+  const long long extent[2] = {total, heads}, st[2] = {token, head};
+  return aligned(p, 16) && strides_ok(st, extent, 2, D, 2, 16);
+}
+
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+Ragged ragged_of(const fa_ragged* b, const int* lens) {
+  return Ragged{b->block_table, b->table_stride, b->max_pages, b->cu_seqlens, lens, b->batch,
+                b->total};
+}
+
+fa_status cache_rows(const fa_kv_pages* cache, const fa_ragged* batch, const int* lens,
+                     const void* k, long long k_token, long long k_head, const void* v,
+                     long long v_token, long long v_head, fa_elem dtype, void* stream,
+                     cudaError_t (*launch)(const CacheLaunch&, cudaStream_t)) {
+  fa_status st;
+  if ((st = check_pages(cache, batch, dtype)) != FA_OK) return st;
+  if (batch->total == 0) return FA_OK;
+  if (!packed_ok(k, k_token, k_head, batch->total, cache->heads, cache->head_dim) ||
+      !packed_ok(v, v_token, v_head, batch->total, cache->heads, cache->head_dim))
+    return FA_ERR_INVALID_ARG;
+  CacheLaunch a{};
+  a.c = Pages{{cache->k, cache->v},
+              {cache->k_exp, cache->v_exp},
+              {cache->k_page, cache->v_page},
+              {cache->k_token, cache->v_token},
+              {cache->k_head, cache->v_head},
+              cache->pages,
+              cache->page_size,
+              log2_of(cache->page_size),
+              cache->heads,
+              cache->head_dim,
+              cache->type};
+  a.r = ragged_of(batch, lens);
+  a.rows[0] = const_cast<void*>(k);
+  a.rows[1] = const_cast<void*>(v);
+  a.row_token[0] = k_token;
+  a.row_token[1] = v_token;
+  a.row_head[0] = k_head;
+  a.row_head[1] = v_head;
+  a.elem = dtype;
+  a.err = device_error_word();
+  if (!a.err) return FA_ERR_CUDA;
+  return launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Query rows per sequence and key head that the batch has on average decide
+// the kernel's row blocks.
+struct PagedPlan {
+  int block_rows;
+  size_t o_bytes, total_bytes;
+};
+
+bool paged_plan(int batch, int total, int heads, int heads_k, int D, PagedPlan* plan) {
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) sms = 160;  // no device: sizes for the checks alone
+  plan->block_rows =
+      paged_few_rows(static_cast<long long>(total) * (heads / heads_k), batch);
+  const size_t rows = 2ull * sms * plan->block_rows;
+  plan->o_bytes = round256(rows * D * sizeof(float));
+  plan->total_bytes = plan->o_bytes + round256(rows * sizeof(float2));
+  return true;
+}
+
+bool paged_sizes_ok(int batch, int total, int heads, int heads_k, int D) {
+  return batch >= 1 && total >= 0 && total <= kMaxRows && heads_k >= 1 && heads >= heads_k &&
+         heads % heads_k == 0 && heads / heads_k <= 128 && (D == 64 || D == 128) &&
+         static_cast<long long>(total) * heads < (1ll << 31);
+}
+
+// One cache tensor for the kernels' boxes of min(page_size, 128) rows.
+bool page_map(CUtensorMap* m, const void* base, const fa_kv_pages* c, long long page,
+              long long token, long long head) {
+  const bool fp8 = c->type == FA_ELEM_E4M3;
+  const uint32_t rows = static_cast<uint32_t>(c->page_size < kTile ? c->page_size : kTile);
+  return make_tmap_4d(
+      m, base,
+      fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+          : c->type == FA_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+      static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(c->page_size),
+      static_cast<uint64_t>(c->heads), static_cast<uint64_t>(c->pages),
+      static_cast<uint64_t>(token), static_cast<uint64_t>(head), static_cast<uint64_t>(page),
+      fp8 ? static_cast<uint32_t>(c->head_dim) : 64u, rows,
+      fp8 && c->head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+      fp8 ? 1 : 2);
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_rotary(const fa_rotary_operand* q, const fa_rotary_operand* k, int B, int N, int D,
+                    int rotary_dim, const double* inv_freq, const void* positions,
+                    int position_bits, long long position_batch_stride, float magnitude,
+                    int interleaved, int inverse, fa_elem dtype, void* stream) {
+  if (!q || B < 0 || N < 0 || B > kMaxRows || N > kMaxRows) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (!is16(dtype) && dtype != FA_ELEM_FP32) return FA_ERR_UNSUPPORTED;
+  if (rotary_dim < 16 || rotary_dim > D || rotary_dim % 16) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N > (1ll << 40)) return FA_ERR_INVALID_ARG;
+  if (!aligned(inv_freq, 8) || !std::isfinite(magnitude)) return FA_ERR_INVALID_ARG;
+  if (positions ? (position_bits != 32 && position_bits != 64) ||
+                      !aligned(positions, position_bits / 8) || position_batch_stride < 0
+                : position_bits != 0)
+    return FA_ERR_INVALID_ARG;
+  RotaryLaunch a{};
+  const fa_rotary_operand* ops[2] = {q, k};
+  for (int i = 0; i < 2; ++i) {
+    const fa_rotary_operand* t = ops[i];
+    if (!t) continue;
+    if (t->heads < 1 || t->heads > 65535) return FA_ERR_INVALID_ARG;
+    if (B == 0 || N == 0) continue;
+    const long long extent[3] = {B, t->heads, N};
+    const long long xs[3] = {t->xs.batch, t->xs.head, t->xs.seq};
+    const long long ys[3] = {t->ys.batch, t->ys.head, t->ys.seq};
+    const int es = elem_bytes(dtype);
+    if (!aligned(t->x, 16) || !aligned(t->y, 16) || !strides_ok(xs, extent, 3, D, es, 16) ||
+        !strides_ok(ys, extent, 3, D, es, 16))
+      return FA_ERR_INVALID_ARG;
+    if (t->x == t->y && (xs[0] != ys[0] || xs[1] != ys[1] || xs[2] != ys[2]))
+      return FA_ERR_INVALID_ARG;
+    for (int d = 0; d < 3; ++d)  // an output element of its own for every index
+      if (extent[d] > 1 && ys[d] < D) return FA_ERR_INVALID_ARG;
+    a.x[i] = t->x;
+    a.y[i] = t->y;
+    a.xs[i] = RowStrides{t->xs.batch, t->xs.head, t->xs.seq};
+    a.ys[i] = RowStrides{t->ys.batch, t->ys.head, t->ys.seq};
+    a.heads[i] = t->heads;
+  }
+  if (B == 0 || N == 0) return FA_OK;
+  a.B = B;
+  a.N = N;
+  a.D = D;
+  a.rotary = rotary_dim;
+  a.inv_freq = inv_freq;
+  a.positions = positions;
+  a.position_bits = position_bits;
+  a.position_bstride = position_batch_stride;
+  a.magnitude = magnitude;
+  a.interleaved = interleaved != 0;
+  a.inverse = inverse != 0;
+  a.elem = dtype;
+  return launch_rotary(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_append(const fa_kv_pages* cache, const fa_ragged* batch, const void* k,
+                          long long k_token, long long k_head, const void* v, long long v_token,
+                          long long v_head, fa_elem dtype, void* stream) {
+  const fa_status st = check_batch(batch, true);
+  if (st != FA_OK) return st;
+  return cache_rows(cache, batch, batch->seqlens, k, k_token, k_head, v, v_token, v_head, dtype,
+                    stream, launch_cache_append);
+}
+
+fa_status fa_cache_read(const fa_kv_pages* cache, const fa_ragged* batch, const int* starts,
+                        void* k, long long k_token, long long k_head, void* v, long long v_token,
+                        long long v_head, fa_elem dtype, void* stream) {
+  const fa_status st = check_batch(batch, false);
+  if (st != FA_OK) return st;
+  if (starts && !aligned(starts, 4)) return FA_ERR_INVALID_ARG;
+  return cache_rows(cache, batch, starts, k, k_token, k_head, v, v_token, v_head, dtype, stream,
+                    launch_cache_read);
+}
+
+size_t fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k, int D) {
+  PagedPlan plan;
+  if (!paged_sizes_ok(batch, total, heads, heads_k, D) ||
+      !paged_plan(batch, total, heads, heads_k, D, &plan))
+    return 0;
+  return plan.total_bytes;
+}
+
+fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void* o,
+                       long long o_token, long long o_head, float* lse, const fa_kv_pages* cache,
+                       const fa_ragged* batch, int heads, const fa_options* options, float scale,
+                       int causal, fa_elem dtype, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  fa_status st;
+  if ((st = check_batch(batch, true)) != FA_OK) return st;
+  if ((st = check_pages(cache, batch, dtype)) != FA_OK) return st;
+  if (!paged_sizes_ok(batch->batch, batch->total, heads, cache->heads, cache->head_dim) ||
+      !std::isfinite(scale))
+    return FA_ERR_INVALID_ARG;
+  PagedLaunch a{};
+  a.win_left = a.win_right = -1;
+  if (options) {
+    if (options->block_mask) return FA_ERR_UNSUPPORTED;
+    if (options->window_left < -1 || options->window_right < -1) return FA_ERR_INVALID_ARG;
+    if (options->alibi_slopes && !aligned(options->alibi_slopes, 4)) return FA_ERR_INVALID_ARG;
+    a.win_left = options->window_left < kMaxRows ? options->window_left : -1;
+    a.win_right = options->window_right < kMaxRows ? options->window_right : -1;
+    a.alibi = options->alibi_slopes;
+    a.alibi_bstride = options->alibi_per_batch ? heads : 0;
+  }
+  if (causal) a.win_right = 0;
+  if (batch->total == 0) return FA_OK;
+  const int D = cache->head_dim;
+  if (!packed_ok(q, q_token, q_head, batch->total, heads, D) ||
+      !packed_ok(o, o_token, o_head, batch->total, heads, D) || !aligned(lse, 4))
+    return FA_ERR_INVALID_ARG;
+  PagedPlan plan;
+  if (!paged_plan(batch->batch, batch->total, heads, cache->heads, D, &plan))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || workspace_bytes < plan.total_bytes) return FA_ERR_INVALID_ARG;
+  if (!page_map(&a.map_k, cache->k, cache, cache->k_page, cache->k_token, cache->k_head) ||
+      !page_map(&a.map_v, cache->v, cache, cache->v_page, cache->v_token, cache->v_head))
+    return FA_ERR_CUDA;
+  a.q = q;
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.o = o;
+  a.o_token = o_token;
+  a.o_head = o_head;
+  a.lse = lse;
+  a.k_exp = cache->k_exp;
+  a.v_exp = cache->v_exp;
+  a.r = ragged_of(batch, batch->seqlens);
+  a.heads = heads;
+  a.heads_k = cache->heads;
+  a.group = heads / cache->heads;
+  a.D = D;
+  a.pages = cache->pages;
+  a.page_size = cache->page_size;
+  a.page_log2 = log2_of(cache->page_size);
+  a.cache_elem = cache->type;
+  a.elem = dtype;
+  a.scale_log2 = scale * kLog2e;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.o_bytes);
+  if (sm_count(&a.sms) != cudaSuccess) return FA_ERR_CUDA;
+  a.err = device_error_word();
+  if (!a.err) return FA_ERR_CUDA;
+  return launch_paged_few(a, plan.block_rows, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+}  // extern "C"

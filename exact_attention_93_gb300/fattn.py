@@ -1,4 +1,4 @@
-"""ctypes binding to libfattn.so (include/fattn.h).
+"""ctypes binding to libfattn.so (include/fattn.h, include/fattn_cache.h).
 
 Argument marshalling only: every step of the computation runs in the
 library's CUDA kernels.  The functions take torch CUDA tensors (PyTorch
@@ -16,9 +16,11 @@ import threading
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfattn.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "fattn.h")
+CACHE_HEADER = os.path.join(os.path.dirname(HERE), "include", "fattn_cache.h")
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
 FA_BF16, FA_FP16 = 0, 1
+FA_ELEM_BF16, FA_ELEM_FP16, FA_ELEM_FP32, FA_ELEM_E4M3 = range(4)
 
 _lock = threading.Lock()
 _lib = None
@@ -42,6 +44,30 @@ class FaOptions(ctypes.Structure):
                 ("block_mask", ctypes.c_void_p), ("block_mask_per_head", ctypes.c_int)]
 
 
+class FaRotaryOperand(ctypes.Structure):
+    """fa_rotary_operand: one tensor fa_rotary turns, and where to."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("xs", FaStrides), ("ys", FaStrides)]
+
+
+class FaKvPages(ctypes.Structure):
+    """fa_kv_pages: a paged key/value cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("k_page", ctypes.c_longlong), ("k_token", ctypes.c_longlong),
+                ("k_head", ctypes.c_longlong), ("v_page", ctypes.c_longlong),
+                ("v_token", ctypes.c_longlong), ("v_head", ctypes.c_longlong),
+                ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("type", ctypes.c_int)]
+
+
+class FaRagged(ctypes.Structure):
+    """fa_ragged: a batch of sequences packed along their tokens."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
+                ("max_pages", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("batch", ctypes.c_int), ("total", ctypes.c_int)]
+
+
 class FattnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -56,9 +82,9 @@ def _status_name(s: int) -> str:
         return str(s)
 
 
-def declared_symbols() -> list[str]:
-    """Every function include/fattn.h declares."""
-    text = open(HEADER).read()
+def declared_symbols(header: str = HEADER) -> list[str]:
+    """Every function a header (include/fattn.h) declares."""
+    text = open(header).read()
     return sorted(set(re.findall(r"^[a-z_ ]+\**\s*\**(fa_\w+)\(", text, re.M)))
 
 
@@ -78,6 +104,7 @@ def load(path: str | None = None):
             raise FileNotFoundError(f"libfattn.so not found at {p}; run build()")
         lib = ctypes.CDLL(p)
         vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        ll = ctypes.c_longlong
         sig = {
             "fa_abi_version": (i, []),
             "fa_status_string": (ctypes.c_char_p, [i]),
@@ -103,6 +130,11 @@ def load(path: str | None = None):
             "fa_fwd_fp8_workspace_size": (sz, [i, i, i, i]),
             "fa_fwd_fp8": (i, [vp, vp, vp, vp, vp, i, i, i, i, ctypes.POINTER(FaLayout),
                                ctypes.POINTER(FaOptions), vp, vp, vp, f, i, vp, sz, vp]),
+            "fa_rotary": (i, [vp, vp, i, i, i, i, vp, vp, i, ll, f, i, i, i, vp]),
+            "fa_cache_append": (i, [vp, vp, vp, ll, ll, vp, ll, ll, i, vp]),
+            "fa_cache_read": (i, [vp, vp, vp, vp, ll, ll, vp, ll, ll, i, vp]),
+            "fa_fwd_paged_workspace_size": (sz, [i, i, i, i, i]),
+            "fa_fwd_paged": (i, [vp, ll, ll, vp, ll, ll, vp, vp, vp, i, vp, f, i, i, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -437,3 +469,140 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, deterministic=False,
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd(q, k, v, o, lse, do, dq, dk, dv, scale, causal, deterministic, stream=stream)
     return dq, dk, dv
+
+
+# --------------------------------------------------------------------------
+# include/fattn_cache.h: rotary positions, the paged cache, attention over it
+# --------------------------------------------------------------------------
+
+_ELEMS = None
+
+
+def elem_code(dtype) -> int:
+    """fa_elem of a torch dtype."""
+    global _ELEMS
+    if _ELEMS is None:
+        torch = _torch()
+        _ELEMS = {torch.bfloat16: FA_ELEM_BF16, torch.float16: FA_ELEM_FP16,
+                  torch.float32: FA_ELEM_FP32, torch.float8_e4m3fn: FA_ELEM_E4M3}
+    code = _ELEMS.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def rotary_operand(x, y) -> FaRotaryOperand:
+    """fa_rotary_operand of (batch, seq, heads, D) tensors x -> y (or packed
+    (seq, heads, D) ones)."""
+    def strides(t):
+        st = t.stride()
+        if st[-1] != 1:
+            raise ValueError("the head dimension D must be contiguous")
+        return FaStrides(st[0], st[2], st[1]) if len(st) == 4 else FaStrides(0, st[1], st[0])
+    return FaRotaryOperand(x.data_ptr(), y.data_ptr(), x.shape[-2], strides(x), strides(y))
+
+
+def kv_pages(k_pages, v_pages, k_exp=None, v_exp=None) -> FaKvPages:
+    """fa_kv_pages of (pages, page_size, heads, D) tensors, and for e4m3 ones
+    their (pages, heads, page_size) exponent bytes."""
+    torch = _torch()
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages and v_pages must be (pages, page_size, heads, D) tensors of "
+                         "one shape and type")
+    pages, page_size, heads, dim = k_pages.shape
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the head dimension D must be contiguous")
+    code = elem_code(k_pages.dtype)
+    if code == FA_ELEM_E4M3:
+        for e in (k_exp, v_exp):
+            if (e is None or e.dtype != torch.uint8 or tuple(e.shape) != (pages, heads, page_size)
+                    or not e.is_contiguous() or e.device != k_pages.device):
+                raise ValueError("an e4m3 cache needs k_exp and v_exp: contiguous uint8 "
+                                 "(pages, heads, page_size) tensors on its device")
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
+    else:
+        if k_exp is not None or v_exp is not None:
+            raise ValueError("k_exp and v_exp belong to an e4m3 cache")
+        ke = ve = None
+    return FaKvPages(k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, ks[0], ks[1], ks[2], vs[0],
+                     vs[1], vs[2], pages, page_size, heads, dim, code)
+
+
+def ragged(block_table, cu_seqlens, seqlens, total: int) -> FaRagged:
+    """fa_ragged of a (batch, max_pages) table, (batch + 1) boundaries and
+    (batch) lengths (or None), int32 tensors."""
+    torch = _torch()
+    i32 = torch.int32
+    if (block_table.dim() != 2 or block_table.dtype != i32
+            or (block_table.stride(1) != 1 and block_table.shape[1] > 1)):
+        raise ValueError("block_table must be an int32 (batch, max_pages) tensor with "
+                         "contiguous rows")
+    batch, max_pages = block_table.shape
+    if cu_seqlens.dtype != i32 or not cu_seqlens.is_contiguous() or cu_seqlens.shape != (batch + 1,):
+        raise ValueError("cu_seqlens must be a contiguous int32 (batch + 1) tensor")
+    if seqlens is not None and (seqlens.dtype != i32 or not seqlens.is_contiguous()
+                                or seqlens.shape != (batch,)):
+        raise ValueError("sequence lengths and starts must be contiguous int32 (batch) tensors")
+    stride = block_table.stride(0) if batch > 1 else max(max_pages, block_table.stride(0))
+    return FaRagged(block_table.data_ptr(), stride, max_pages, cu_seqlens.data_ptr(),
+                    None if seqlens is None else seqlens.data_ptr(), batch, total)
+
+
+def stream_of(stream=None) -> int:
+    return (stream or _torch().cuda.current_stream()).cuda_stream
+
+
+def fa_rotary(q: FaRotaryOperand, k, B: int, N: int, D: int, rotary_dim: int, inv_freq: int,
+              positions, position_bits: int, position_batch_stride: int, magnitude: float,
+              interleaved: bool, inverse: bool, elem: int, stream=None):
+    """fa_rotary: operands from rotary_operand (k may be None), device
+    pointers for inv_freq and positions."""
+    st = load().fa_rotary(ctypes.addressof(q), None if k is None else ctypes.addressof(k), B, N,
+                          D, rotary_dim, inv_freq, positions, position_bits,
+                          position_batch_stride, magnitude, int(interleaved), int(inverse), elem,
+                          stream_of(stream))
+    _check(st, "fa_rotary")
+
+
+def fa_cache_append(cache: FaKvPages, batch: FaRagged, k, v, stream=None):
+    """fa_cache_append of packed (total, heads, D) tensors k, v."""
+    ks, vs = k.stride(), v.stride()
+    st = load().fa_cache_append(ctypes.addressof(cache), ctypes.addressof(batch), k.data_ptr(),
+                                ks[0], ks[1], v.data_ptr(), vs[0], vs[1], elem_code(k.dtype),
+                                stream_of(stream))
+    _check(st, "fa_cache_append")
+
+
+def fa_cache_read(cache: FaKvPages, batch: FaRagged, starts, k, v, stream=None):
+    """fa_cache_read into packed (total, heads, D) tensors k, v; starts: an
+    int32 (batch) tensor or None."""
+    ks, vs = k.stride(), v.stride()
+    st = load().fa_cache_read(ctypes.addressof(cache), ctypes.addressof(batch),
+                              None if starts is None else starts.data_ptr(), k.data_ptr(), ks[0],
+                              ks[1], v.data_ptr(), vs[0], vs[1], elem_code(k.dtype),
+                              stream_of(stream))
+    _check(st, "fa_cache_read")
+
+
+def fa_fwd_paged_workspace_size(batch: int, total: int, heads: int, heads_k: int, D: int) -> int:
+    return int(load().fa_fwd_paged_workspace_size(batch, total, heads, heads_k, D))
+
+
+def fa_fwd_paged(q, o, lse, cache: FaKvPages, batch: FaRagged, opts, scale: float, causal: bool,
+                 workspace=None, stream=None):
+    """fa_fwd_paged of packed (total, heads, D) tensors q, o and an fp32
+    (heads, total) lse; opts: FaOptions or None."""
+    total, heads, dim = q.shape
+    if workspace is None:
+        n = fa_fwd_paged_workspace_size(batch.batch, total, heads, cache.heads, dim)
+        if n == 0:
+            raise ValueError("invalid sizes for attention over a paged cache")
+        workspace = _torch().empty(n, dtype=_torch().uint8, device=q.device)
+    qs, os_ = q.stride(), o.stride()
+    st = load().fa_fwd_paged(q.data_ptr(), qs[0], qs[1], o.data_ptr(), os_[0], os_[1],
+                             lse.data_ptr(), ctypes.addressof(cache), ctypes.addressof(batch),
+                             heads, None if opts is None else ctypes.addressof(opts), scale,
+                             int(causal), elem_code(q.dtype), workspace.data_ptr(),
+                             workspace.numel(), stream_of(stream))
+    _check(st, "fa_fwd_paged")

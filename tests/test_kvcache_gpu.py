@@ -1,0 +1,189 @@
+"""Writing the paged cache and reading it back, on the GPU."""
+import math
+
+import pytest
+import torch
+
+import paged_ref as R
+from exact_attention_93_gb300 import attention, fattn, kvcache, rotary
+
+pytestmark = pytest.mark.gpu
+BF, HF, E4 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+def bytes_of(t):
+    return t.contiguous().view(torch.uint8)
+
+
+def setup(rows, ctx, heads, D, page, cache_dtype, dtype, seed=0, tail=0):
+    """An empty cache over scattered pages, and packed rows."""
+    b = R.Batch(rows, ctx, heads, D, page, BF, False, seed=seed, tail=tail)
+    cache = kvcache.alloc_kv_cache(b.pool.shape[1], page, heads, D, cache_dtype)
+    g = torch.Generator().manual_seed(seed + 1)
+    k, v = (torch.randn(b.total, heads, D, generator=g) *
+            torch.exp2(3 * torch.randn(b.total, heads, 1, generator=g)) for _ in range(2))
+    return b, cache, k.to(dtype), v.to(dtype)
+
+
+CASES = [
+    ([1], [0], 1, 64, 16),
+    ([1] * 70, list(range(70)), 8, 128, 32),
+    ([5, 0, 33, 1], [0, 10, 15, 64], 3, 64, 64),
+    ([300, 17], [0, 1000], 2, 128, 256),
+    ([129, 1, 2], [5, 127, 126], 17, 128, 128),
+]
+
+
+@pytest.mark.parametrize("rows,ctx,heads,D,page", CASES)
+@pytest.mark.parametrize("cache_dtype,dtype", [(E4, BF), (E4, HF), (BF, BF), (HF, HF)])
+def test_append_and_read(rows, ctx, heads, D, page, cache_dtype, dtype):
+    b, cache, k, v = setup(rows, ctx, heads, D, page, cache_dtype, dtype, seed=len(rows), tail=3)
+    kp, vp, ke, ve = cache
+    table, cu, lens = b.table.cuda(), b.cu.cuda(), b.len_t.cuda()
+    kvcache.kv_cache_append(k.cuda(), v.cuda(), kp, vp, table, cu, lens, k_exp=ke, v_exp=ve)
+    starts = lens - (cu[1:] - cu[:-1])
+    out = tuple(torch.full((b.total, heads, D), 9.0, dtype=dtype, device="cuda") for _ in range(2))
+    got = kvcache.kv_cache_read(kp, vp, table, cu, b.total, starts=starts, k_exp=ke, v_exp=ve,
+                                dtype=dtype, out=out)
+    torch.cuda.synchronize()
+    assert fattn.fa_device_error() == fattn.FA_OK
+    n = sum(rows)
+    where = torch.zeros(kp.shape[:2], dtype=torch.bool)
+    for w, (x, y, exp) in enumerate(zip((k, v), got, (ke, ve))):
+        if cache_dtype == E4:
+            ref, e = R.quantise(x[:n])
+            # dequantised values fit bf16 exactly and fp16 to its rounding
+            assert torch.equal(y[:n].cpu(), ref.to(dtype))
+            at = 0
+            for s, r in enumerate(rows):
+                for i in range(r):
+                    pos = b.lens[s] - r + i
+                    pg = int(b.table[s, pos // page])
+                    assert torch.equal(exp[pg, :, pos % page].cpu(), e[at])
+                    where[pg, pos % page] = True
+                    at += 1
+        else:
+            assert torch.equal(y[:n].cpu(), x[:n])
+            at = 0
+            for s, r in enumerate(rows):
+                for i in range(r):
+                    pos = b.lens[s] - r + i
+                    where[int(b.table[s, pos // page]), pos % page] = True
+        assert (y[n:] == 9).all()  # rows behind the last sequence
+    # slots that no row went to are as they were
+    for t in (kp, vp):
+        assert not bytes_of(t).cpu().view(*kp.shape[:2], -1)[~where].any()
+
+
+def special(dtype):
+    x = torch.zeros(12, 1, 64)
+    x[0] = 0.0
+    x[1, 0, 3] = 448.0
+    x[2, 0, 3] = 448.0 + 2  # rounds into the next binade's scale
+    x[3, 0, :] = torch.linspace(-1, 1, 64)
+    x[4, 0, 0], x[4, 0, 1] = math.inf, 1.0
+    x[5, 0, 0], x[5, 0, 1] = math.nan, 3.0
+    x[6, 0, :] = math.nan
+    x[7, 0, 0] = -math.inf
+    x[8, 0, 9] = torch.finfo(dtype).max
+    x[9, 0, 9] = torch.finfo(dtype).tiny
+    x[10, 0, 9] = torch.finfo(dtype).smallest_normal * 2 ** -6
+    x[11, 0, :] = torch.tensor([1.0625, 1.1875, 17 / 16 * 256, 19 / 16 * 256] * 16)  # ties
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_special_rows(dtype):
+    x = special(dtype)
+    n = x.shape[0]
+    kp, vp, ke, ve = kvcache.alloc_kv_cache(1, 16, 1, 64, E4)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    kvcache.kv_cache_append(x.cuda(), x.cuda(), kp, vp, table, cu, lens, k_exp=ke, v_exp=ve)
+    y, _ = kvcache.kv_cache_read(kp, vp, table, cu, n, k_exp=ke, v_exp=ve, dtype=BF)
+    ref, e = R.quantise(x)
+    assert torch.equal(ke[0, 0, :n].cpu(), e[:, 0])
+    ref, got = ref.to(BF), y.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    ok = ~torch.isnan(ref)
+    assert torch.equal(got[ok], ref[ok])
+
+
+def test_strided_rows_and_pages():
+    b, _, k, v = setup([20, 3], [4, 40], 2, 64, 16, BF, BF)
+    qkv = torch.zeros(b.total, 3, 4, 64, dtype=BF, device="cuda")
+    qkv[:, 1, :2], qkv[:, 2, 2:] = k.cuda(), v.cuda()
+    kv = torch.zeros(b.pool.shape[1], 2, 2, 16, 64, dtype=BF, device="cuda")  # heads before tokens
+    kp, vp = kv[:, 0].transpose(1, 2), kv[:, 1].transpose(1, 2)
+    args = b.table.cuda(), b.cu.cuda(), b.len_t.cuda()
+    kvcache.kv_cache_append(qkv[:, 1, :2], qkv[:, 2, 2:], kp, vp, *args)
+    gk, gv = kvcache.kv_cache_read(kp, vp, args[0], args[1], b.total,
+                                   starts=torch.tensor([4, 40], dtype=torch.int32, device="cuda"))
+    assert torch.equal(gk.cpu(), k) and torch.equal(gv.cpu(), v)
+
+
+def test_bad_pages_are_contained():
+    b, (kp, vp, ke, ve), k, v = setup([3, 20, 2], [0, 30, 5], 2, 64, 16, E4, BF)
+    table = b.table.clone()
+    table[1, 2], table[2, 0] = kp.shape[0], -1
+    args = table.cuda(), b.cu.cuda(), b.len_t.cuda()
+    kvcache.kv_cache_append(k.cuda(), v.cuda(), kp, vp, *args, k_exp=ke, v_exp=ve)
+    assert fattn.fa_device_error() == fattn.FA_ERR_INVALID_ARG
+    starts = torch.tensor([0, 30, 5], dtype=torch.int32, device="cuda")
+    gk, _ = kvcache.kv_cache_read(kp, vp, args[0], args[1], b.total, starts=starts, k_exp=ke,
+                                  v_exp=ve)
+    assert fattn.fa_device_error() == fattn.FA_ERR_INVALID_ARG
+    ref, _ = R.quantise(k)
+    good = [0, 1, 2, 3, 4] + list(range(21, 23))  # rows of whole pages
+    assert torch.equal(gk[good].cpu(), ref[good].to(BF))
+    assert not gk[5:21].any() and not gk[23:].any()
+    # lengths beyond the table, and shorter than the rows
+    lens = torch.tensor([2, 1 << 30, -4], dtype=torch.int32, device="cuda")
+    kvcache.kv_cache_append(k.cuda(), v.cuda(), kp, vp, b.table.cuda(), args[1], lens, k_exp=ke,
+                            v_exp=ve)
+    assert fattn.fa_device_error() == fattn.FA_ERR_INVALID_ARG
+
+
+def test_a_decoder_layer_from_prompt_to_tokens():
+    """Rotary, cache and attention as they are used: a ragged prompt, then
+    single tokens, against the dense 64-bit attention of the whole sequence."""
+    g = torch.Generator().manual_seed(0)
+    H, Hk, D, page, steps = 8, 2, 64, 16, 3
+    prompts = [37, 5, 64]
+    freq, mag = rotary.rotary_frequencies(D)
+    full = [p + steps for p in prompts]
+    x = [[torch.randn(n, h, D, generator=g).to(BF) for h in (H, Hk, Hk)] for n in full]
+    kp, vp, _, _ = kvcache.alloc_kv_cache(40, page, Hk, D)
+    table = torch.randperm(40, generator=g)[:3 * 6].view(3, 6).to(torch.int32).cuda()
+    done = [0, 0, 0]
+    outs = [[] for _ in prompts]
+    turned = [[] for _ in prompts]
+    for step in range(steps + 1):
+        new = prompts if step == 0 else [1, 1, 1]
+        cut = [[t[d:d + n] for t in seq] for seq, d, n in zip(x, done, new)]
+        q, k, v = (torch.cat([c[i] for c in cut]).cuda() for i in range(3))
+        pos = torch.cat([torch.arange(d, d + n) for d, n in zip(done, new)]).cuda()
+        done = [d + n for d, n in zip(done, new)]
+        cu = torch.tensor([0] + new).cumsum(0).to(torch.int32).cuda()
+        lens = torch.tensor(done, dtype=torch.int32).cuda()
+        q, k = rotary.rotary_func(q, k, freq, positions=pos, inplace=True)
+        kvcache.kv_cache_append(k, v, kp, vp, table, cu, lens)
+        o = attention.flash_attn_paged_func(q, kp, vp, table, cu, lens)
+        at = 0
+        for s, n in enumerate(new):
+            outs[s].append(o[at:at + n].cpu())
+            turned[s].append((q[at:at + n].cpu(), k[at:at + n].cpu()))
+            at += n
+    torch.cuda.synchronize()
+    assert fattn.fa_device_error() == fattn.FA_OK
+    for s, n in enumerate(full):
+        q, k = (torch.cat([t[i] for t in turned[s]]) for i in range(2))
+        dense = R.Batch([n], [0], Hk, D, page, BF, False)
+        dense.k, dense.v = [k.double()], [x[s][2].double()]
+        ref, lse, A, S = R.attention(dense, q, D ** -0.5)
+        tol, _ = R.attention_bounds(ref, lse, A, S, BF, R.EPS[BF], D)
+        assert ((torch.cat(outs[s]).double() - ref).abs() <= tol).all()
+        # and the rows went in turned by their positions
+        want = R.rotary(x[s][0][None], torch.arange(n)[None], freq.cpu())[0]
+        assert ((q.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -18).all()
