@@ -2,16 +2,22 @@
 // block of queries sees, how the work is split over the CTAs, and the joining
 // of blocks that several CTAs worked on.
 //
-// Units.  A unit is one block of query rows (kRows of the rows token * group +
+// Units.  A unit is one block of query rows (rows token * group +
 // head-in-group of one sequence) against one key head.  It walks tiles of 128
-// keys.  All units of a sequence are given the same weight, the number of key
-// tiles that any of its queries sees (at least 1, so that rows without keys
-// are written too).  Units are laid end to end, sequence by sequence, and each
-// CTA takes an equal stretch of the whole, cutting units where the stretch
-// ends: a long context over few rows is spread over every SM, ragged batches
-// stay balanced, and a CTA leaves at most two cut pieces whatever the batch.
-// Cut pieces go to the workspace in fp32 (unnormalised O, maximum, sum) and
-// paged_join_kernel adds them up in a fixed order.
+// keys.  Units are laid end to end by their weights, sequence by sequence,
+// head by head, and each CTA takes an equal stretch of the whole, cutting
+// units where the stretch ends: a long context over few rows is spread over
+// every SM, ragged batches stay balanced, and a CTA leaves at most two cut
+// pieces whatever the batch.  Cut pieces go to the workspace in fp32
+// (unnormalised O, maximum, sum) and paged_join_kernel adds them up in a fixed
+// order.
+//
+// Weights.  The few-row kernel gives all units of a sequence the number of key
+// tiles that any of its queries sees, at least 1 (a sequence usually is one
+// block).  The many-row kernel counts each block's own tiles, plus one for
+// what a unit costs beside its tiles: under a causal mask the blocks of a
+// prompt see from one tile to all of them.  The sums over blocks that this
+// needs are sums of floor((a + i b) / 128), taken in closed form.
 #pragma once
 
 #include "fa_ragged.cuh"
@@ -25,35 +31,86 @@ __device__ __forceinline__ void visible_span(const PagedLaunch& p, const Seq& s,
                                              int& lo, int& hi) {
   lo = p.win_left < 0 ? 0 : max(0, s.pos0 + t0 - p.win_left);
   const long long last = static_cast<long long>(s.pos0) + t1 - 1 + p.win_right;
-  hi = p.win_right < 0 ? s.len : static_cast<int>(max(0LL, min(static_cast<long long>(s.len), last + 1)));
+  hi = p.win_right < 0 ? s.len
+                       : static_cast<int>(max(0LL, min(static_cast<long long>(s.len), last + 1)));
   if (lo >= hi) lo = hi = 0;
 }
 
+// sum over i < n of floor((a i + b) / m), a and b not negative, by Euclid's
+// algorithm on (a, m).
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  long long sum = 0;
+  while (n > 0) {
+    if (a >= m) {
+      sum += static_cast<long long>(n) * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += static_cast<long long>(n) * (b / m);
+      b %= m;
+    }
+    const unsigned long long y = static_cast<unsigned long long>(a) * n + b;
+    if (y < m) break;
+    n = static_cast<uint32_t>(y / m);
+    b = static_cast<uint32_t>(y % m);
+    const uint32_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// sum over i < n of max(0, floor((a + i b) / 128)).
+__device__ __forceinline__ long long tile_sum(int n, int a, int b) {
+  const int skip = a < 0 ? min(n, (-a + b - 1) / b) : 0;
+  return floor_sum(static_cast<uint32_t>(n - skip), kTile, static_cast<uint32_t>(b),
+                   static_cast<uint32_t>(a + skip * b));
+}
+
 // A sequence as the work split sees it.
-template <int kRows>
+template <bool kMany>
 struct SeqWork {
   Seq s;
-  int blocks;      // query blocks per key head
-  int first_tile;  // key tiles first_tile .. first_tile + weight - 1
-  int weight;
+  int blocks;  // query blocks per key head
+  int flat;    // few rows: the weight of every unit
+  int first;   // few rows: the first key tile
+  long long per_head;
   __device__ __forceinline__ void load(const PagedLaunch& p, int b, uint32_t* err = nullptr) {
     s = load_seq(p.r, p.page_log2, b, err);
-    blocks = (s.rows * p.group + kRows - 1) / kRows;
-    int lo, hi;
-    visible_span(p, s, 0, s.rows, lo, hi);
-    first_tile = lo / kTile;
-    weight = max(1, (hi + kTile - 1) / kTile - first_tile);
+    blocks = (s.rows * p.group + p.block_rows - 1) / p.block_rows;
+    if constexpr (kMany) {
+      per_head = before(p, blocks);
+    } else {
+      int lo, hi;
+      visible_span(p, s, 0, s.rows, lo, hi);
+      first = lo / kTile;
+      flat = max(1, (hi + kTile - 1) / kTile - first);
+      per_head = static_cast<long long>(flat) * blocks;
+    }
   }
-  __device__ __forceinline__ long long work(const PagedLaunch& p) const {
-    return static_cast<long long>(weight) * blocks * p.heads_k;
+  // Weight of the blocks before block i of a head.
+  __device__ __forceinline__ long long before(const PagedLaunch& p, int i) const {
+    if constexpr (!kMany) return static_cast<long long>(flat) * i;
+    const int bt = p.block_rows / p.group;  // tokens of a block
+    long long sum = i;
+    int open = 0;  // leading blocks whose keys end before the sequence's
+    if (p.win_right >= 0) {
+      const int end = s.len - s.pos0 - p.win_right;
+      open = min(i, max(0, (end + bt - 1) / bt - 1));
+      sum += tile_sum(open, s.pos0 + bt + p.win_right + kTile - 1, bt);
+    }
+    sum += static_cast<long long>(i - open) * ((s.len + kTile - 1) / kTile);
+    if (p.win_left >= 0) sum -= tile_sum(i, s.pos0 - p.win_left, bt);
+    return sum;
   }
 };
 
-// A place in the laid-out work: sequence b, unit u of it, tile `off` of that.
+// A CTA's place in the laid-out work.
 struct Place {
-  int b, unit, off;
+  int b, hk, block;
+  long long off;    // into the unit
+  long long pos;    // into the whole
   long long left;   // of this CTA's stretch
-  long long begin;  // of this CTA's stretch
   long long total;
 };
 
@@ -67,32 +124,27 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-// The whole work, by one warp.
-template <int kRows>
-__device__ __forceinline__ long long warp_total_work(const PagedLaunch& p) {
-  long long sum = 0;
-  for (int b = threadIdx.x & 31; b < p.r.batch; b += 32) {
-    SeqWork<kRows> w;
-    w.load(p, b, blockIdx.x == 0 ? p.err : nullptr);
-    sum += w.work(p);
-  }
-  return warp_sum(sum);
-}
-
-// The sequence, unit and tile at position `at` (< the whole work), by one
-// warp; unit_start gets the position of the unit's first tile.
-template <int kRows>
-__device__ __forceinline__ void warp_locate(const PagedLaunch& p, long long at, Place& out,
-                                            long long& unit_start) {
+// Where CTA c of n begins, by one warp.
+template <bool kMany>
+__device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) {
   const int lane = threadIdx.x & 31;
-  long long before = 0;
+  Place at{};
+  for (int b = lane; b < p.r.batch; b += 32) {
+    SeqWork<kMany> w;
+    w.load(p, b, c == 0 ? p.err : nullptr);
+    at.total += w.per_head * p.heads_k;
+  }
+  at.total = warp_sum(at.total);
+  at.pos = stretch(at.total, n, c);
+  at.left = stretch(at.total, n, c + 1) - at.pos;
+  if (at.left == 0) return at;
+  long long ahead = 0;
   for (int b0 = 0; b0 < p.r.batch; b0 += 32) {
-    SeqWork<kRows> w;
-    w.weight = 1;
+    SeqWork<kMany> w;
     long long mine = 0;
     if (b0 + lane < p.r.batch) {
       w.load(p, b0 + lane);
-      mine = w.work(p);
+      mine = w.per_head * p.heads_k;
     }
     long long upto = mine;
 #pragma unroll
@@ -100,78 +152,113 @@ __device__ __forceinline__ void warp_locate(const PagedLaunch& p, long long at, 
       const long long o = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += o;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > at);
+    const uint32_t past = __ballot_sync(0xffffffffu, ahead + upto > at.pos);
     if (past) {
       const int src = __ffs(past) - 1;
-      const long long start = before + __shfl_sync(0xffffffffu, upto - mine, src);
-      const int weight = __shfl_sync(0xffffffffu, w.weight, src);
-      const long long in = at - start;
-      out.b = b0 + src;
-      out.unit = static_cast<int>(in / weight);
-      out.off = static_cast<int>(in - static_cast<long long>(out.unit) * weight);
-      unit_start = at - out.off;
-      return;
+      at.b = b0 + src;
+      const long long in = at.pos - ahead - __shfl_sync(0xffffffffu, upto - mine, src);
+      w.load(p, at.b);
+      at.hk = static_cast<int>(in / w.per_head);
+      const long long rem = in - at.hk * w.per_head;
+      // the last block whose predecessors weigh at most rem: 32 tries at once
+      int lo = 0, hi = w.blocks;  // it is in [lo, hi)
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int i = lo + lane * step;
+        const uint32_t ok = __ballot_sync(0xffffffffu, i < hi && w.before(p, i) <= rem);
+        lo += (__popc(ok) - 1) * step;
+        hi = min(hi, lo + step);
+      }
+      at.block = lo;
+      at.off = rem - w.before(p, lo);
+      return at;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    ahead += __shfl_sync(0xffffffffu, upto, 31);
   }
-  out.b = p.r.batch;
-  out.unit = out.off = 0;
-  unit_start = at;
+  at.left = 0;  // not reached
+  return at;
 }
 
 // A CTA's next piece of work.
 struct Piece {
   int b, hk, block;
-  int t0, t1;            // the block's tokens
-  int rows;              // valid rows of the block
-  int lo, hi;            // keys some row of the block sees
-  int tile0, tile1;      // key tiles to walk (none: tile0 >= tile1)
-  bool whole;            // the piece covers its unit
-  int slot;              // of the CTA's two partial results, when it does not
+  int t0, t1;        // the block's tokens
+  int rows;          // valid rows of the block
+  int lo, hi;        // keys some row of the block sees
+  int tile0, tile1;  // key tiles to walk (none: tile0 >= tile1)
+  bool whole;        // the piece covers its unit
+  int slot;          // of the CTA's two partial results, when it does not
+  int last;          // when the unit begins here and goes on: the CTA that ends it
+};
+
+// What paged_join_kernel does for a CTA: add up the unit that it began and
+// did not finish.
+struct JoinTask {
+  int rows;  // 0: nothing to do; -1: the CTA had no work at all
+  int start, first_row, hk, last;
 };
 
 // Walks a CTA's stretch.  Every role of the CTA runs its own copy.
-template <int kRows>
+template <bool kMany>
 struct WorkWalk {
   Place at;
-  SeqWork<kRows> w;
+  SeqWork<kMany> w;
   bool loaded;
   __device__ __forceinline__ explicit WorkWalk(const Place& start) : at(start), loaded(false) {}
-  __device__ __forceinline__ bool next(const PagedLaunch& p, Piece& x, Seq& seq) {
+  __device__ __forceinline__ bool next(const PagedLaunch& p, Piece& x) {
     if (at.left <= 0) return false;
     if (!loaded) {
       w.load(p, at.b);
       loaded = true;
     }
-    while (at.unit >= w.blocks * p.heads_k) {  // (a sequence without rows has no units)
-      at.unit = 0;
+    if (at.block >= w.blocks) {
+      at.block = 0;
+      ++at.hk;
+    }
+    while (at.hk >= p.heads_k || w.blocks == 0) {
+      at.hk = 0;
       if (++at.b >= p.r.batch) return false;
       w.load(p, at.b);
     }
-    const int take = static_cast<int>(min(at.left, static_cast<long long>(w.weight - at.off)));
     x.b = at.b;
-    x.hk = at.unit / w.blocks;
-    x.block = at.unit - x.hk * w.blocks;
-    x.rows = min(kRows, w.s.rows * p.group - x.block * kRows);
-    x.t0 = x.block * kRows / p.group;
-    x.t1 = (x.block * kRows + x.rows - 1) / p.group + 1;
+    x.hk = at.hk;
+    x.block = at.block;
+    const int row0 = x.block * p.block_rows;
+    x.rows = min(p.block_rows, w.s.rows * p.group - row0);
+    x.t0 = row0 / p.group;
+    x.t1 = (row0 + x.rows - 1) / p.group + 1;
     visible_span(p, w.s, x.t0, x.t1, x.lo, x.hi);
-    x.whole = take == w.weight;
-    x.slot = at.off > 0 ? 0 : 1;
-    x.tile0 = max(w.first_tile + at.off, x.lo / kTile);
-    x.tile1 = min(w.first_tile + at.off + take, (x.hi + kTile - 1) / kTile);
-    seq = w.s;
+    const int lo_tile = x.lo / kTile, hi_tile = (x.hi + kTile - 1) / kTile;
+    const int weight = kMany ? 1 + hi_tile - lo_tile : w.flat;
+    const int off = static_cast<int>(at.off);
+    const int take = static_cast<int>(min(at.left, static_cast<long long>(weight - off)));
+    x.whole = take == weight;
+    x.slot = off > 0 ? 0 : 1;
+    const int base = kMany ? lo_tile - 1 : w.first;
+    x.tile0 = max(base + off, lo_tile);
+    x.tile1 = min(base + off + take, hi_tile);
+    x.last = -1;
+    if (off == 0 && take < weight)
+      x.last = static_cast<int>(((at.pos + weight) * static_cast<long long>(gridDim.x) - 1) /
+                                at.total);
     at.off += take;
+    at.pos += take;
     at.left -= take;
-    if (at.off == w.weight) {
+    if (off + take == weight) {
       at.off = 0;
-      ++at.unit;
+      ++at.block;
     }
     return true;
   }
 };
 
-// Row r of a piece: its token's index in the sequence and its query head.
+// By one thread of the CTA: the task for its last piece.
+__device__ __forceinline__ JoinTask join_task(const PagedLaunch& p, const Piece& x, const Seq& s) {
+  return JoinTask{x.last >= 0 ? x.rows : 0, s.start, x.block * p.block_rows, x.hk, x.last};
+}
+
+// Row r of a block that starts at row first_row of its sequence: its token
+// and its query head.
 __device__ __forceinline__ void row_of(const PagedLaunch& p, int first_row, int r, int hk,
                                        int& token, int& head) {
   token = (first_row + r) / p.group;
@@ -192,59 +279,28 @@ __device__ __forceinline__ void store16(uint16_t* dst, const float (&o)[kN], flo
   }
 }
 
-// Adds up the units that several CTAs worked on.  Block c looks at the unit
-// its CTA c began and did not finish; the pieces are CTA c's second partial
-// result and the first ones of the CTAs after it.  Warp w takes rows w,
-// w + 8, ...; its lanes the D columns.  Launched to overlap the end of the
-// kernel before it; the split is worked out again before waiting for it.
-template <int kRows, int D, bool kBf16>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedLaunch p,
-                                                         int n) {
-  __shared__ Place sh;
-  __shared__ long long sh_start;
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    Place at{};
-    long long start = 0;
-    at.total = warp_total_work<kRows>(p);
-    at.begin = stretch(at.total, n, c);
-    const long long end = stretch(at.total, n, c + 1);
-    at.left = end - at.begin;
-    if (at.left > 0) warp_locate<kRows>(p, end - 1, at, start);
-    if (lane == 0) {
-      sh = at;
-      sh_start = start;
-    }
-  }
-  __syncthreads();
-  const Place at = sh;
-  const long long start = sh_start, end = at.begin + at.left;
+// Adds up the units that several CTAs worked on.  Block (c, y) takes rows y * 8
+// + warp, ... of the unit that CTA c began and did not finish; its pieces are
+// CTA c's second partial result and the first ones of the CTAs after it.  A
+// warp's lanes are the D columns.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait();
-  if (at.left <= 0 || at.b >= p.r.batch) return;
-  SeqWork<kRows> w;
-  w.load(p, at.b);
-  if (start < at.begin || start + w.weight <= end) return;
-  int last = c;  // CTAs c .. last hold pieces
-  while (stretch(at.total, n, last + 1) < start + w.weight) ++last;
-  const int hk = at.unit / w.blocks, block = at.unit - hk * w.blocks;
-  const int rows = min(kRows, w.s.rows * p.group - block * kRows);
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const JoinTask task = p.tasks[c];
   constexpr int kN = D / 32;
-  for (int r = warp; r < rows; r += 8) {
-    auto piece = [&](int i) {
-      return (2LL * i + (i == c ? 1 : 0)) * kRows + r;
-    };
-    // (a CTA with an empty stretch wrote nothing)
-    auto empty = [&](int i) { return stretch(at.total, n, i) == stretch(at.total, n, i + 1); };
+  for (int r = blockIdx.y * 8 + warp; r < task.rows; r += gridDim.y * 8) {
+    auto piece = [&](int i) { return (2LL * i + (i == c ? 1 : 0)) * p.block_rows + r; };
     float m = -INFINITY;
-    for (int i = c + lane; i <= last; i += 32)
-      if (!empty(i)) m = fmaxf(m, p.part_ml[piece(i)].x);
+    for (int i = c + lane; i <= task.last; i += 32)
+      if (p.tasks[i].rows >= 0) m = fmaxf(m, p.part_ml[piece(i)].x);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
     const float ref = m == -INFINITY ? 0.f : m;
     float o[kN] = {}, l = 0.f;
 #pragma unroll 4
-    for (int i = c; i <= last; ++i) {
-      if (empty(i)) continue;
+    for (int i = c; i <= task.last; ++i) {
+      if (p.tasks[i].rows < 0) continue;
       const float2 ml = p.part_ml[piece(i)];
       const float a = ex2_approx(ml.x - ref);
       l = fmaf(ml.y, a, l);
@@ -261,14 +317,28 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
       for (int e = 0; e < kN; ++e) o[e] = fmaf(x[e], a, o[e]);
     }
     int token, head;
-    row_of(p, block * kRows, r, hk, token, head);
-    const long long row = w.s.start + token;
+    row_of(p, task.first_row, r, task.hk, token, head);
+    const long long row = task.start + token;
     store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head + lane * kN, o,
                    l == 0.f ? 0.f : 1.f / l);
     if (lane == 0)
       p.lse[static_cast<long long>(head) * p.r.total + row] =
           l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kPagedLn2;
   }
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_join(const PagedLaunch& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.sms), static_cast<unsigned>((a.block_rows + 31) / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16>, a);
 }
 
 }  // namespace fa

@@ -123,13 +123,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                                      ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
-    Place at{};
-    long long unit_start;
-    at.total = warp_total_work<kRows>(p);
-    at.begin = stretch(at.total, gridDim.x, blockIdx.x);
-    at.left = stretch(at.total, gridDim.x, blockIdx.x + 1) - at.begin;
-    if (at.left > 0) warp_locate<kRows>(p, at.begin, at, unit_start);
-    if (lane == 0) s.place = at;
+    const Place at = warp_place<false>(p, gridDim.x, blockIdx.x);
+    if (lane == 0) {
+      s.place = at;
+      if (at.left == 0) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
+    }
   }
   if (threadIdx.x == 32) {
     for (int i = 0; i < kSlots; ++i) {
@@ -141,10 +139,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
   __syncthreads();
   volatile int* abort_flag = &s.abort_flag;
-  WorkWalk<kRows> walk(s.place);
-  if (walk.at.b >= p.r.batch) walk.at.left = 0;
+  WorkWalk<false> walk(s.place);
   Piece x;
-  Seq seq;
 
   if (warp == kConsumers) {
     // ---------------------------------------------------------------- producer
@@ -155,7 +151,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       tma_prefetch_desc(&p.map_v);
     }
     uint32_t n = 0;  // slots filled
-    while (walk.next(p, x, seq)) {
+    while (walk.next(p, x)) {
       const int* table = p.r.table + x.b * p.r.table_stride;
       // lane i < per_tile: the i-th box of a tile, if a visible key lies in it
       auto page_of = [&](int tile) {
@@ -214,8 +210,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // --------------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
     uint32_t n = 0;  // slots consumed
-    while (walk.next(p, x, seq)) {
+    while (walk.next(p, x)) {
+      const Seq& seq = walk.w.s;
       const int row0 = x.block * kRows;
+      if (threadIdx.x == 0) p.tasks[blockIdx.x] = join_task(p, x, seq);
       // -- queries as B operands, and what each of this lane's columns sees
       uint32_t qf[kQRegs ? NB : 1][kSteps][2];
       float qscale[NB][2];
@@ -630,26 +628,23 @@ cudaError_t launch_few_t(const PagedLaunch& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, static_cast<unsigned>(a.sms), kFewThreads, smem, s, a);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_join_kernel<8 * NB, D, kBf16>, static_cast<unsigned>(a.sms), 256, 0, s, a,
-                 a.sms);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return launch_join<D, kBf16>(a, s);
 }
 
 template <int D, bool kFp8, bool kBf16>
-cudaError_t launch_few_n(const PagedLaunch& a, int block_rows, cudaStream_t s) {
-  return block_rows == 8    ? launch_few_t<D, kFp8, kBf16, 1>(a, s)
-         : block_rows == 16 ? launch_few_t<D, kFp8, kBf16, 2>(a, s)
+cudaError_t launch_few_n(const PagedLaunch& a, cudaStream_t s) {
+  return a.block_rows == 8    ? launch_few_t<D, kFp8, kBf16, 1>(a, s)
+         : a.block_rows == 16 ? launch_few_t<D, kFp8, kBf16, 2>(a, s)
                             : launch_few_t<D, kFp8, kBf16, 4>(a, s);
 }
 
 template <int D>
-cudaError_t launch_few_d(const PagedLaunch& a, int block_rows, cudaStream_t s) {
+cudaError_t launch_few_d(const PagedLaunch& a, cudaStream_t s) {
   const bool fp8 = a.cache_elem == kElemE4m3, bf16 = a.elem == kElemBf16;
-  return fp8 ? (bf16 ? launch_few_n<D, true, true>(a, block_rows, s)
-                     : launch_few_n<D, true, false>(a, block_rows, s))
-             : (bf16 ? launch_few_n<D, false, true>(a, block_rows, s)
-                     : launch_few_n<D, false, false>(a, block_rows, s));
+  return fp8 ? (bf16 ? launch_few_n<D, true, true>(a, s)
+                     : launch_few_n<D, true, false>(a, s))
+             : (bf16 ? launch_few_n<D, false, true>(a, s)
+                     : launch_few_n<D, false, false>(a, s));
 }
 
 }  // namespace
@@ -658,8 +653,8 @@ int paged_few_rows(long long rows, int batch) {
   return rows <= 8LL * batch ? 8 : rows <= 16LL * batch ? 16 : 32;
 }
 
-cudaError_t launch_paged_few(const PagedLaunch& a, int block_rows, cudaStream_t s) {
-  return a.D == 64 ? launch_few_d<64>(a, block_rows, s) : launch_few_d<128>(a, block_rows, s);
+cudaError_t launch_paged_few(const PagedLaunch& a, cudaStream_t s) {
+  return a.D == 64 ? launch_few_d<64>(a, s) : launch_few_d<128>(a, s);
 }
 
 }  // namespace fa

@@ -1,0 +1,820 @@
+// fa_paged_many.cu -- attention over a paged cache for many query rows per
+// sequence: chunks of prompts over long contexts, whole packed prompts.
+//
+// What bounds it.  A unit's 2 x 128 query rows make 4 * 256 * D operations of
+// each 4 * D byte key and value: the tensor cores are the bound, and beside
+// them the exponentials.  The kernel is the design of the dense forward
+// (fa_fwd.cu: two 128-row tiles in turn, S and O in tensor memory, P written
+// over S) fed from pages:
+//
+//   - The rows of a tile are tokens x the G query heads that share a key head
+//     (row = token * G + head), so K and V are staged once for all of them.  A
+//     tile holds floor(128 / G) tokens; with a G that does not divide 128 its
+//     last rows idle.
+//   - K and V tiles of 128 keys are gathered by TMA page by page: one lane of
+//     the producer warp per page.  Only pages that hold a key some row of the
+//     unit sees are touched.
+//   - CTAs stay resident and walk a stretch of the units laid end to end
+//     (fa_paged.cuh); a unit that a stretch's end cuts leaves its partial O,
+//     maximum and sum in fp32 for the joining kernel.
+//   - O goes straight from tensor memory to the caller's rows: a packed batch's
+//     tiles end anywhere, and a tensor-map store would run into the next
+//     sequence.
+//
+// Values outside the visible span (behind the sequence's end, in pages not
+// loaded) may be anything, and 0 * NaN is NaN: two spare warps make those rows
+// of a tile zeros before the P V product reads it.
+//
+// e4m3 caches: the two spare warps convert each 8-bit tile to fp16 in shared
+// memory (exactly, relative to the largest row exponent so far, which scales
+// the scores, and O, in fp32), and bf16 queries to fp16 under a power-of-two
+// scale per row; both products then run in fp16.
+//
+// Warps (384 threads): 0-3 softmax of tile A, 4-7 of tile B, 8 producer,
+// 9 MMA issue, 10-11 zeroing or conversion.
+#include "fa_paged.cuh"
+#include "fa_serve.h"
+#include "sm103_primitives.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kManyThreads = 384;
+// registers: as in the dense forward, 2 x 208 + 80 per lane of a sub-partition
+constexpr uint32_t kManyLow = 80, kManyHigh = 208;
+// references of key and value exponents, one per key tile: a softmax group is
+// never more than three tiles behind the conversion's stages (a tile pair's
+// ranges end within two tiles of each other)
+constexpr int kRefs = 8;
+
+template <int D, bool kFp8>
+struct ManySmem {
+  static constexpr int kBlocks = D / 64;               // 64-column blocks of a 16-bit tile
+  static constexpr int kBlockBytes = kTile * 128;
+  static constexpr int kTileBytes = kBlocks * kBlockBytes;
+  static constexpr int kTile8 = kTile * D;             // an e4m3 tile
+  static constexpr int kSlots8 = D == 64 ? 4 : 2;      // K and V tiles alternate
+  alignas(1024) uint8_t q[2][kTileBytes];
+  alignas(1024) uint8_t k[2][kTileBytes];
+  alignas(1024) uint8_t v[2][kTileBytes];
+  alignas(1024) uint8_t raw[kFp8 ? kSlots8 : 1][kFp8 ? kTile8 : 16];
+  alignas(16) uint8_t exps[kFp8 ? kSlots8 : 1][kTile];
+  int8_t qshift[2][kFp8 ? 2 * kTile : 1];  // [unit & 1]: rows of q were scaled by 2^this
+  int kref[kRefs], vref[kRefs];
+  uint64_t q_full, q_empty, q_ready;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t raw_full[kSlots8], raw_empty[kSlots8];
+  uint64_t v_fixed[2];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t drain;
+  Place place;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__device__ __forceinline__ bool many_warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                               volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, err, abort_flag);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The key tiles of a piece: of query tile t [lo_t, hi_t], none when lo_t >
+// hi_t, and the K/V stream over their union.
+struct ManyTiles {
+  int lo0, hi0, lo1, hi1;
+  int first, last;  // of the stream; first > last: nothing to multiply
+  bool both;        // tile B has rows
+  __device__ __forceinline__ ManyTiles(const PagedLaunch& p, const Piece& x, const Seq& s) {
+    const int tokens = p.block_rows / p.group / 2;
+    range(p, x, s, x.t0, min(x.t1, x.t0 + tokens), lo0, hi0);
+    both = x.t1 > x.t0 + tokens;
+    if (both) {
+      range(p, x, s, x.t0 + tokens, x.t1, lo1, hi1);
+    } else {
+      lo1 = 1;
+      hi1 = 0;
+    }
+    first = lo0 <= hi0 ? lo0 : lo1;
+    last = max(hi0, hi1);
+    if (lo0 > hi0 && lo1 > hi1) {
+      first = 1;
+      last = 0;
+    }
+  }
+  static __device__ __forceinline__ void range(const PagedLaunch& p, const Piece& x, const Seq& s,
+                                               int t0, int t1, int& lo, int& hi) {
+    int a, b;
+    visible_span(p, s, t0, t1, a, b);
+    lo = max(a / kTile, x.tile0);
+    hi = min((b + kTile - 1) / kTile, x.tile1) - 1;
+    if (lo > hi) {
+      lo = 1;
+      hi = 0;
+    }
+  }
+  __device__ __forceinline__ int count(int t) const {
+    return t ? max(0, hi1 - lo1 + 1) : max(0, hi0 - lo0 + 1);
+  }
+  __device__ __forceinline__ int streamed() const { return max(0, last - first + 1); }
+};
+
+// 2^(n - 127) for an exponent field n, 0 below the normal range.
+__device__ __forceinline__ float many_exp2_field(int n) {
+  return __uint_as_float(static_cast<uint32_t>(min(max(n, 0), 254)) << 23);
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+template <int D, bool kFp8, bool kBf16, bool kAlibi>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    paged_many_kernel(const __grid_constant__ PagedLaunch p) {
+  pdl_wait_and_release();
+  using Smem = ManySmem<D, kFp8>;
+  constexpr bool kMmaBf16 = kBf16 && !kFp8;  // type of the products
+  // P = 2^(x - m + kPOffset [+ up to 3, e4m3]), the reference m lagging the
+  // true maximum by at most kThreshold: bf16 has the range for no offset, and
+  // fp16 P of an e4m3 cache stays below 2^15 and normal down to 2^-18 of m
+  constexpr float kThreshold = 8.0f;
+  constexpr float kPOffset = kFp8 ? 4.0f : 0.0f;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                     ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile_tokens = p.block_rows / p.group / 2, tile_rows = tile_tokens * p.group;
+  if (warp == 0) {
+    const Place at = warp_place<true>(p, gridDim.x, blockIdx.x);
+    if (lane == 0) {
+      s.place = at;
+      if (at.left == 0) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
+    }
+  }
+  if (tid == 32) {
+    mbar_init(&s.q_full, 1);
+    mbar_init(&s.q_empty, 1);
+    mbar_init(&s.q_ready, 64);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.k_full[i], kFp8 ? 64 : 1);
+      mbar_init(&s.k_empty[i], 1);
+      mbar_init(&s.v_full[i], kFp8 ? 64 : 1);
+      mbar_init(&s.v_empty[i], 1);
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], 128);
+      mbar_init(&s.o_done[i], 1);
+      mbar_init(&s.v_fixed[i], 64);
+    }
+    for (int i = 0; i < Smem::kSlots8; ++i) {
+      mbar_init(&s.raw_full[i], 1);
+      mbar_init(&s.raw_empty[i], 64);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&s.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = s.tmem_base;
+  volatile int* abort_flag = &s.abort_flag;
+  WorkWalk<true> walk(s.place);
+  Piece x{};
+  // a tile of the piece with rows outside the visible span
+  auto ragged = [&](int j) { return j * kTile < x.lo || (j + 1) * kTile > x.hi; };
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kManyLow>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        tma_prefetch_desc(&p.map_q);
+        tma_prefetch_desc(&p.map_k);
+        tma_prefetch_desc(&p.map_v);
+      }
+      constexpr int kRowBytes = kFp8 ? D : 2 * D;
+      const int box_rows = min(p.page_size, kTile), per_tile = kTile / box_rows;
+      uint32_t units = 0, ring = 0;  // Q loads, key tiles streamed
+      uint32_t loads = 0;            // K and V tiles issued
+      bool stop = false;
+      while (!stop && walk.next(p, x)) {
+        const ManyTiles tl(p, x, walk.w.s);
+        if (tl.first > tl.last) continue;
+        const int* table = p.r.table + x.b * p.r.table_stride;
+        auto page_of = [&](int tile) {
+          const int k0 = tile * kTile + lane * box_rows;
+          const bool wanted =
+              lane < per_tile && tile <= tl.last && k0 < x.hi && k0 + box_rows > x.lo;
+          return wanted ? table[k0 >> p.page_log2] : -2;
+        };
+        int page = page_of(tl.first);
+        // Q once the last S product of the unit before has read it
+        if (units > 0 && !many_warp_wait(&s.q_empty, (units - 1) & 1, p.err, abort_flag)) break;
+        if (lane == 0) {
+          const int n_q = tl.both ? 2 : 1;
+          mbar_arrive_expect_tx(&s.q_full, n_q * tile_rows * 2 * D);
+          for (int t = 0; t < n_q; ++t)
+            for (int kb = 0; kb < Smem::kBlocks; ++kb)
+              tma_load_4d(s.q[t] + kb * Smem::kBlockBytes, &p.map_q, &s.q_full, kb * 64,
+                          x.hk * p.group, walk.w.s.start + x.t0 + t * tile_tokens, 0);
+        }
+        ++units;
+        for (int j = tl.first; j <= tl.last; ++j, ++ring) {
+          const int k0 = j * kTile + lane * box_rows;
+          const bool mine = lane < per_tile && k0 < x.hi && k0 + box_rows > x.lo;
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+          const int next_page = page_of(j + 1);
+          if (mine && (page < 0 || page >= p.pages)) {
+            atomicExch(p.err, kDevErrBadIndex);
+            page = p.pages;  // out of range for the tensor map: reads as zeros
+          }
+          const int row = k0 & (p.page_size - 1);
+#pragma unroll
+          for (int kv = 0; kv < 2 && !stop; ++kv) {
+            uint64_t *full, *empty;
+            uint8_t* dst;
+            uint32_t use;
+            if constexpr (kFp8) {
+              const int slot = loads % Smem::kSlots8;
+              use = loads / Smem::kSlots8;
+              full = &s.raw_full[slot];
+              empty = &s.raw_empty[slot];
+              dst = s.raw[slot];
+            } else {
+              const int st = ring & 1;
+              use = ring >> 1;
+              full = kv ? &s.v_full[st] : &s.k_full[st];
+              empty = kv ? &s.v_empty[st] : &s.k_empty[st];
+              dst = kv ? s.v[st] : s.k[st];
+            }
+            if (use > 0 && !many_warp_wait(empty, (use - 1) & 1, p.err, abort_flag)) {
+              stop = true;
+              break;
+            }
+            if (lane == 0)
+              mbar_arrive_expect_tx(full, boxes * box_rows * (kRowBytes + (kFp8 ? 1 : 0)));
+            __syncwarp();
+            if (mine) {
+              dst += lane * box_rows * (kRowBytes < 128 ? kRowBytes : 128);
+#pragma unroll
+              for (int kb = 0; kb < (kRowBytes + 127) / 128; ++kb)
+                tma_load_4d(dst + kb * Smem::kBlockBytes, kv ? &p.map_v : &p.map_k, full, kb * 64,
+                            row, x.hk, page);
+              if constexpr (kFp8) {
+                const uint8_t* e = (kv ? p.v_exp : p.k_exp) +
+                                   (static_cast<long long>(page < p.pages ? page : 0) * p.heads_k +
+                                    x.hk) * p.page_size + row;
+                bulk_load(s.exps[loads % Smem::kSlots8] + lane * box_rows, e, box_rows, full);
+              }
+            }
+            ++loads;
+          }
+          if (stop) break;
+          page = next_page;
+        }
+      }
+      if (*abort_flag && lane == 0) {
+        // Copies already in flight land before the CTA's shared memory goes away.
+        int zero = 0;
+        if (units > 0) mbar_wait(&s.q_full, (units - 1) & 1, p.err, &zero, 100000000ull);
+        if constexpr (kFp8) {
+          for (uint32_t i = loads > Smem::kSlots8 ? loads - Smem::kSlots8 : 0; i < loads; ++i)
+            mbar_wait(&s.raw_full[i % Smem::kSlots8], (i / Smem::kSlots8) & 1, p.err, &zero,
+                      100000000ull);
+        } else {
+          for (uint32_t i = loads > 4 ? loads - 4 : 0; i < loads; ++i) {
+            const uint32_t n = i >> 1;
+            mbar_wait((i & 1) ? &s.v_full[n & 1] : &s.k_full[n & 1], (n >> 1) & 1, p.err, &zero,
+                      100000000ull);
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- MMA issuer
+      // Every lane computes the same descriptors and waits; one issues.
+      const bool leader = elect_one_sync();
+      auto commit = [&](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+      };
+      constexpr uint32_t ab = kMmaBf16 ? 1u : 0u;
+      constexpr uint32_t idS = idesc_f16(128, 128, ab, 0, 0);
+      constexpr uint32_t idPV = idesc_f16(128, D, ab, 0, 1);
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(s.q[0]), 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(s.k[0]), 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(s.v[0]), Smem::kBlockBytes, 1024);
+      uint32_t units = 0, ring = 0;
+      uint32_t fixed = 0;  // bit st: parity of the next zeroed tile in V stage st
+      int base0 = 0, base1 = 0;  // P V products of tiles A, B in earlier units
+      bool ok = true;
+      while (ok && walk.next(p, x)) {
+        const ManyTiles tl(p, x, walk.w.s);
+        if (tl.first > tl.last) continue;
+        int s_left = tl.count(0) + tl.count(1);
+        auto issue_s = [&](int t, int kst) {
+          const uint64_t dq = desc_add(dq0, t * Smem::kTileBytes);
+          const uint64_t dk = desc_add(dk0, kst * Smem::kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * Smem::kBlockBytes + (kk & 3) * 32;
+            if (leader)
+              tc_mma_ss(tbase + t * 128, desc_add(dq, off), desc_add(dk, off), idS,
+                        kk > 0 ? 1u : 0u);
+          }
+          commit(&s.s_full[t]);
+          if (--s_left == 0) commit(&s.q_empty);  // the next unit's Q may come
+        };
+        auto k_wait = [&](uint32_t g) {
+          return mbar_wait_poll(&s.k_full[g & 1], (g >> 1) & 1, p.err, abort_flag);
+        };
+        ok = mbar_wait_poll(kFp8 && kBf16 ? &s.q_ready : &s.q_full, units & 1, p.err,
+                            abort_flag) &&
+             k_wait(ring);
+        ++units;
+        if (!ok) break;
+        tc_fence_after();
+        if (tl.first >= tl.lo0 && tl.first <= tl.hi0) issue_s(0, ring & 1);
+        if (tl.first >= tl.lo1 && tl.first <= tl.hi1) issue_s(1, ring & 1);
+        commit(&s.k_empty[ring & 1]);
+        for (int j = tl.first; ok && j <= tl.last; ++j) {
+          const uint32_t g = ring + static_cast<uint32_t>(j - tl.first);
+          const int st = g & 1;
+          if (!kFp8 && ragged(j)) {
+            ok = mbar_wait_poll(&s.v_fixed[st], (fixed >> st) & 1, p.err, abort_flag);
+            fixed ^= 1u << st;
+          } else {
+            ok = mbar_wait_poll(&s.v_full[st], (g >> 1) & 1, p.err, abort_flag);
+          }
+          if (!ok) break;
+          bool k_next = false;  // K_{j+1} has landed
+          for (int t = 0; ok && t < 2; ++t) {
+            const int lt = t ? tl.lo1 : tl.lo0, ht = t ? tl.hi1 : tl.hi0;
+            const bool active = j >= lt && j <= ht;
+            // S_t(j + 1) is next: after P V of tile j, or as the first product
+            // of a tile whose range starts there
+            const bool s_next = active ? j + 1 <= ht : (j + 1 == lt && lt <= ht);
+            if (active) {
+              ok = mbar_wait_poll(&s.p_full[t], ((t ? base1 : base0) + j - lt) & 1, p.err,
+                                  abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dv = desc_add(dv0, st * Smem::kTileBytes);
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                if (leader)
+                  tc_mma_ts(tbase + 256 + t * D, tbase + t * 128 + kk * 8,
+                            desc_add(dv, kk * 16 * 128), idPV, (j > lt || kk > 0) ? 1u : 0u);
+              commit(&s.o_done[t]);
+            }
+            if (s_next) {
+              if (!k_next) {
+                ok = k_wait(g + 1);
+                if (!ok) break;
+                tc_fence_after();
+                k_next = true;
+              }
+              issue_s(t, (g + 1) & 1);
+            }
+          }
+          commit(&s.v_empty[st]);
+          if (k_next) commit(&s.k_empty[(g + 1) & 1]);
+        }
+        ring += static_cast<uint32_t>(tl.streamed());
+        base0 += tl.count(0);
+        base1 += tl.count(1);
+      }
+      // Every product issued above completes before TMEM is released.
+      commit(&s.drain);
+      int zero = 0;
+      mbar_wait(&s.drain, 0, p.err, &zero, 100000000ull);
+    } else {
+      // --------------------------------------------- zeroing, or conversion
+      const int w64 = tid - 320;  // 0 .. 63
+      uint32_t ring = 0, units = 0, n8 = 0;
+      bool ok = true;
+      while (ok && walk.next(p, x)) {
+        const ManyTiles tl(p, x, walk.w.s);
+        if (tl.first > tl.last) continue;
+        if constexpr (!kFp8) {
+          for (int j = tl.first; ok && j <= tl.last; ++j, ++ring) {
+            if (!ragged(j)) continue;
+            const int st = ring & 1;
+            ok = many_warp_wait(&s.v_full[st], (ring >> 1) & 1, p.err, abort_flag);
+            if (!ok) break;
+            for (int i = w64; i < kTile * (2 * D / 16); i += 64) {
+              const int r = i & (kTile - 1), c = i >> 7;  // 16-byte chunk c of row r
+              const int key = j * kTile + r;
+              if (key < x.lo || key >= x.hi)
+                *reinterpret_cast<uint4*>(s.v[st] + (c >> 3) * Smem::kBlockBytes + r * 128 +
+                                          (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&s.v_fixed[st]);
+          }
+        } else {
+          if constexpr (kBf16) {
+            // Q to fp16, each row under the power of two that takes its largest
+            // magnitude into [2^14, 2^15)
+            ok = many_warp_wait(&s.q_full, units & 1, p.err, abort_flag);
+            if (!ok) break;
+            for (int i = w64; i < 2 * kTile; i += 64) {
+              uint8_t* row = s.q[i >> 7] + (i & 127) * 128;
+              float top = 0.f;
+#pragma unroll 4
+              for (int c = 0; c < 2 * D / 16; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4*>(
+                    row + (c >> 3) * Smem::kBlockBytes + (((c & 7) ^ (i & 7)) << 4));
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 f = unpack2<true>(u[e]);
+                  top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+              }
+              const int e = static_cast<int>(__float_as_uint(top) >> 23);
+              const int shift = min(max(141 - e, -112), 126);
+              const float down = many_exp2_field(127 + shift);
+              s.qshift[units & 1][i] = static_cast<int8_t>(shift);
+#pragma unroll 4
+              for (int c = 0; c < 2 * D / 16; ++c) {
+                uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * Smem::kBlockBytes +
+                                                     (((c & 7) ^ (i & 7)) << 4));
+                const uint4 v = *at;
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                uint32_t h[4];
+#pragma unroll
+                for (int e2 = 0; e2 < 4; ++e2) {
+                  const float2 f = unpack2<true>(u[e2]);
+                  h[e2] = pack2<false>(f.x * down, f.y * down);
+                }
+                *at = make_uint4(h[0], h[1], h[2], h[3]);
+              }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&s.q_ready);
+          }
+          ++units;
+          int ref[2] = {0, 0};  // largest key, value exponent of the piece so far
+          for (int j = tl.first; ok && j <= tl.last; ++j, ++ring) {
+            const int st = ring & 1;
+            const bool cut = ragged(j);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, ++n8) {
+              const int slot = n8 % Smem::kSlots8;
+              ok = many_warp_wait(&s.raw_full[slot], (n8 / Smem::kSlots8) & 1, p.err, abort_flag);
+              if (!ok) break;
+              if (ring >= 2)
+                ok = many_warp_wait(kv ? &s.v_empty[st] : &s.k_empty[st], ((ring >> 1) - 1) & 1,
+                                    p.err, abort_flag);
+              if (!ok) break;
+              int top = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = lane * 4 + i, key = j * kTile + r;
+                if (key >= x.lo && key < x.hi) top = max(top, static_cast<int>(s.exps[slot][r]));
+              }
+#pragma unroll
+              for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+              ref[kv] = max(ref[kv], top);
+              if (w64 == 0) (kv ? s.vref : s.kref)[ring % kRefs] = ref[kv];
+              uint8_t* to = kv ? s.v[st] : s.k[st];
+              constexpr int kChunks = D / 16;  // 16 codes each
+#pragma unroll 4
+              for (int i = w64; i < kTile * kChunks; i += 64) {
+                const int r = i / kChunks, c = i % kChunks, key = j * kTile + r;
+                const int e = s.exps[slot][r];
+                const uint8_t* from =
+                    D == 128 ? s.raw[slot] + r * 128 + ((c ^ (r & 7)) << 4)
+                             : s.raw[slot] + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+                const uint4 v = *reinterpret_cast<const uint4*>(from);
+                // 2^(e - ref + 7): codes stay below 448 * 128
+                const float f = many_exp2_field(127 + e - ref[kv] + 7);
+                const bool none = e == 0 || (cut && (key < x.lo || key >= x.hi));
+                const uint32_t f2 = pack2<false>(f, f);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                uint32_t h[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  h[2 * q] = none ? 0u : mul_f16x2(e4m3x2_to_f16x2(u[q]), f2);
+                  h[2 * q + 1] = none ? 0u : mul_f16x2(e4m3x2_to_f16x2(u[q] >> 16), f2);
+                }
+                uint8_t* row = to + (c >> 2) * Smem::kBlockBytes + r * 128;
+                const int c0 = (c & 3) * 2;
+                const uint4 a = make_uint4(h[0], h[1], h[2], h[3]),
+                            b = make_uint4(h[4], h[5], h[6], h[7]);
+                // the upper block's lanes write their odd chunk first: the
+                // blocks share banks
+                const bool odd = (c >> 2) & 1;
+                *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
+                *reinterpret_cast<uint4*>(row + (((c0 + !odd) ^ (r & 7)) << 4)) = odd ? a : b;
+              }
+              fence_proxy_async_smem();
+              mbar_arrive(kv ? &s.v_full[st] : &s.k_full[st]);
+              mbar_arrive(&s.raw_empty[slot]);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    setmaxnreg_inc<kManyHigh>();
+    // -------------------------------------------------------------- softmax
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tbase + t * 128, tO = tbase + 256 + t * D;
+    const int row_token = r / p.group, row_head = r - row_token * p.group;
+    int base = 0;  // key tiles of this query tile in earlier units
+    uint32_t ring = 0, units = 0;
+    bool ok = true;
+    while (ok && walk.next(p, x)) {
+      const Seq& seq = walk.w.s;
+      if (tid == 0) p.tasks[blockIdx.x] = join_task(p, x, seq);
+      const ManyTiles tl(p, x, seq);
+      const int lt = t ? tl.lo1 : tl.lo0, n_tiles = tl.count(t);
+      const int token = x.t0 + t * tile_tokens + row_token;  // of the sequence
+      const bool mine = r < tile_rows && token < x.t1;       // a row to write
+      // rows that are none see what the tile's last token sees
+      const int first_token = x.t0 + t * tile_tokens;
+      const int last_token = min(x.t1, first_token + tile_tokens) - 1;
+      const int pos = seq.pos0 + min(token, last_token);
+      const int head = x.hk * p.group + row_head;
+      const float nslope2 = kAlibi && mine ? paged_slope2(p, x.b, head) : 0.f;
+      // visible keys: of this row, and those that every row of the tile sees
+      const int first = p.win_left < 0 ? 0 : pos - p.win_left;
+      const int last = p.win_right < 0 ? seq.len - 1 : min(seq.len - 1, pos + p.win_right);
+      const int pos_a = seq.pos0 + first_token, pos_b = seq.pos0 + last_token;
+      const int all_first = p.win_left < 0 ? 0 : pos_b - p.win_left;
+      const int all_last = p.win_right < 0 ? seq.len - 1 : min(seq.len - 1, pos_a + p.win_right);
+      // some row of the tile sees at most 128 keys (the count is concave in the
+      // row, so an end row has the fewest): see lo below
+      const bool few_keys = [&] {
+        auto count = [&](int q) {
+          return min(seq.len - 1, p.win_right < 0 ? seq.len - 1 : q + p.win_right) -
+                 max(0, p.win_left < 0 ? 0 : q - p.win_left) + 1;
+        };
+        return min(count(pos_a), count(pos_b)) <= kTile;
+      }();
+      float sl2 = p.scale_log2;
+      int vbase = 0;  // e4m3: the value exponent that O is relative to
+      float m = -INFINITY;  // reference maximum, log2 units
+      float l = 0.f;        // sum of 2^(t - m)
+      // The sum O is divided by: the largest weight of each tile enters as
+      // rounded to 16 bits, and in cut tiles of rows with few keys every weight,
+      // so that the weights that dominate O sum to one as rounded (as in the
+      // dense forward).  The LSE keeps the exact sum l.
+      float lo = 0.f;
+      for (int jj = 0, j = lt; jj < n_tiles; ++jj, ++j) {
+        ok = many_warp_wait(&s.s_full[t], (base + jj) & 1, p.err, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t g = ring + static_cast<uint32_t>(j - tl.first);
+        float mult = sl2;   // scores -> log2 units
+        int vshift = 0;     // e4m3: this tile's value exponent over vbase
+        bool rebase = false;
+        float down = 1.f;
+        if constexpr (kFp8) {
+          // converted V comes after K and Q by the same threads
+          ok = many_warp_wait(&s.v_full[g & 1], (g >> 1) & 1, p.err, abort_flag);
+          if (!ok) break;
+          if (jj == 0 && kBf16) sl2 *= many_exp2_field(127 - s.qshift[units & 1][t * kTile + r]);
+          // K was scaled by 2^(127 - kref + 7)
+          mult = sl2 * many_exp2_field(s.kref[g % kRefs] - 7);
+          const int vr = s.vref[g % kRefs];
+          if (jj == 0) vbase = vr;
+          if (vr - vbase > 3) {
+            down = many_exp2_field(127 + vbase - vr);
+            vbase = vr;
+            rebase = jj > 0;
+          }
+          vshift = vr - vbase;
+        }
+        const bool pos_scale = mult > 0.f;
+        float sv[kTile];
+        {
+          uint32_t raw[kTile / 32][32];
+#pragma unroll
+          for (int c = 0; c < kTile / 32; ++c) tmem_ld32(tS + lane_off + c * 32, raw[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < kTile / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sv[c * 32 + e] = __uint_as_float(raw[c][e]);
+        }
+        const int k0 = j * kTile;
+        const bool prescale = kAlibi || !pos_scale;
+        if (kAlibi) {
+          const float d0 = static_cast<float>(k0 - pos);
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            sv[c] = fmaf(sv[c], mult, nslope2 * fabsf(d0 + static_cast<float>(c)));
+        } else if (!pos_scale) {
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) sv[c] *= mult;
+        }
+        const bool masked = k0 < all_first || k0 + kTile - 1 > all_last;
+        if (masked) {
+          const int cf = first - k0, cl = last - k0;  // visible columns cf .. cl
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c < cf || c > cl) sv[c] = -INFINITY;
+        }
+        float mxs[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mxs[e] = sv[e];
+#pragma unroll
+        for (int c = 8; c < kTile; c += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            mxs[e] = c + 8 < kTile ? fmax3(mxs[e], sv[c + e], sv[c + 8 + e])
+                                   : fmaxf(mxs[e], sv[c + e]);
+        const float mx = fmax3(fmax3(mxs[0], mxs[1], mxs[2]), fmax3(mxs[3], mxs[4], mxs[5]),
+                               fmaxf(mxs[6], mxs[7]));
+        // (a masked score times a positive scale stays -inf)
+        const float m_tile = prescale ? mx : mx * mult;
+        const float m_new = fmaxf(m, m_tile);
+        const bool need = m_new > m + kThreshold;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2_approx(m - m_new);  // 0 on the first tile (m = -inf)
+          l *= alpha;
+          lo *= alpha;
+          m = m_new;
+        }
+        if (jj > 0 && __any_sync(0xffffffffu, need || rebase)) {
+          ok = many_warp_wait(&s.o_done[t], (base + jj - 1) & 1, p.err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          alpha *= down;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + lane_off + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + lane_off + c * 32, o);
+          }
+        }
+        // e4m3: weights are 2^(kPOffset + vshift) times the others'; unscale
+        // brings their sum back
+        const float offset = kPOffset + static_cast<float>(vshift);
+        const float unscale = kFp8 ? many_exp2_field(127 - static_cast<int>(kPOffset) - vshift)
+                                   : 1.f;
+        const float mneg = (m == -INFINITY) ? 0.f : offset - m;
+        const float em = prescale ? 1.f : mult;
+        const uint64_t mult2 = f32x2(em, em), mneg2 = f32x2(mneg, mneg);
+        const float pmax = ex2_approx(fmaf(mx, em, mneg));
+        const float pmax_corr = unpack2<kMmaBf16>(pack2<kMmaBf16>(pmax, 0.f)).x - pmax;
+        uint64_t sums[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float2 z = split_f32x2(
+                fma_f32x2(f32x2(sv[h * 64 + 2 * c], sv[h * 64 + 2 * c + 1]), mult2, mneg2));
+            const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+            sums[c & 1] = add_f32x2(sums[c & 1], f32x2(p0, p1));
+            pk[c] = pack2<kMmaBf16>(p0, p1);
+          }
+          tmem_st32(tS + lane_off + h * 32, pk);
+        }
+        const float2 s0 = split_f32x2(sums[0]), s1 = split_f32x2(sums[1]);
+        const float tile_sum = (s0.x + s0.y) + (s1.x + s1.y);
+        l = fmaf(tile_sum, unscale, l);
+        if (masked && few_keys) {
+          tmem_st_wait();
+          uint64_t rs = f32x2(0.f, 0.f);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pr[32];
+            tmem_ld32(tS + lane_off + h * 32, pr);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float2 q2 = unpack2<kMmaBf16>(pr[c]);
+              rs = add_f32x2(rs, f32x2(q2.x, q2.y));
+            }
+          }
+          const float2 r2 = split_f32x2(rs);
+          lo = fmaf(r2.x + r2.y, unscale, lo);
+        } else {
+          lo = fmaf(tile_sum + pmax_corr, unscale, lo);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&s.p_full[t]);
+      }
+      if (!ok) break;
+
+      // ------------------------------------------------------------ epilogue
+      const bool have = n_tiles > 0;
+      if (have) {
+        ok = many_warp_wait(&s.o_done[t], (base + n_tiles - 1) & 1, p.err, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (t == 0 || tl.both) {
+        // O in tensor memory is 2^kPOffset (e4m3: and 2^(127 + 7 - vbase)) times
+        // the sum of weights times values
+        const float back = kFp8 ? many_exp2_field(vbase - 7 - static_cast<int>(kPOffset)) : 1.f;
+        const float per = lo == 0.f ? 0.f : back / lo;
+        const long long at = (2LL * blockIdx.x + x.slot) * p.block_rows + t * tile_rows + r;
+        const long long row = seq.start + token;
+        uint16_t* out = static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head;
+        // partial results are divided by their sum as rounded and multiplied by
+        // the exact one, which is what they are joined with
+        const float scale = x.whole ? per : per * l;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (have) {
+            tmem_ld32(tO + lane_off + c * 32, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (!mine) continue;
+          if (x.whole) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                pk[e] = pack2<kBf16>(__uint_as_float(o[8 * q + 2 * e]) * scale,
+                                     __uint_as_float(o[8 * q + 2 * e + 1]) * scale);
+              *reinterpret_cast<uint4*>(out + c * 32 + q * 8) =
+                  make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          } else {
+            float* dst = p.part_o + at * D + c * 32;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(dst + q * 4) =
+                  make_float4(__uint_as_float(o[4 * q]) * scale,
+                              __uint_as_float(o[4 * q + 1]) * scale,
+                              __uint_as_float(o[4 * q + 2]) * scale,
+                              __uint_as_float(o[4 * q + 3]) * scale);
+          }
+        }
+        if (mine) {
+          if (x.whole)
+            p.lse[static_cast<long long>(head) * p.r.total + row] =
+                l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kPagedLn2;
+          else
+            p.part_ml[at] = make_float2(m, l);
+        }
+      }
+      if (tl.first <= tl.last) ++units;
+      ring += static_cast<uint32_t>(tl.streamed());
+      base += n_tiles;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int D, bool kFp8, bool kBf16, bool kAlibi>
+cudaError_t launch_many_t(const PagedLaunch& a, cudaStream_t s) {
+  auto kern = paged_many_kernel<D, kFp8, kBf16, kAlibi>;
+  const int smem = static_cast<int>(sizeof(ManySmem<D, kFp8>)) + 1024;
+  static_assert(sizeof(ManySmem<D, kFp8>) + 1024 <= 232448, "shared memory of one CTA");
+  static AttrCache configured;
+  cudaError_t e = ensure_dynamic_smem(kern, smem, configured);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, static_cast<unsigned>(a.sms), kManyThreads, smem, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_join<D, kBf16>(a, s);
+}
+
+template <int D, bool kFp8>
+cudaError_t launch_many_d(const PagedLaunch& a, cudaStream_t s) {
+  const bool bf16 = a.elem == kElemBf16, alibi = a.alibi != nullptr;
+  return bf16 ? (alibi ? launch_many_t<D, kFp8, true, true>(a, s)
+                       : launch_many_t<D, kFp8, true, false>(a, s))
+              : (alibi ? launch_many_t<D, kFp8, false, true>(a, s)
+                       : launch_many_t<D, kFp8, false, false>(a, s));
+}
+
+}  // namespace
+
+int paged_many_rows(int group) { return 2 * (kTile / group) * group; }
+
+cudaError_t launch_paged_many(const PagedLaunch& a, cudaStream_t s) {
+  const bool fp8 = a.cache_elem == kElemE4m3;
+  if (a.D == 64) return fp8 ? launch_many_d<64, true>(a, s) : launch_many_d<64, false>(a, s);
+  return fp8 ? launch_many_d<128, true>(a, s) : launch_many_d<128, false>(a, s);
+}
+
+}  // namespace fa

@@ -61,6 +61,8 @@ struct CacheLaunch {
 cudaError_t launch_cache_append(const CacheLaunch& a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheLaunch& a, cudaStream_t s);
 
+struct JoinTask;
+
 // Attention over pages.  Scores work in log2 units.
 struct PagedLaunch {
   // keys and values: {D, page_size, heads, pages}, box {128 bytes (64 for
@@ -82,15 +84,19 @@ struct PagedLaunch {
   int win_left, win_right;  // causal: win_right = 0
   const float* alibi;
   int alibi_bstride;
-  float* part_o;   // [2 grid][rows of a block][D]
-  float2* part_ml;  // [2 grid][rows of a block]: maximum, sum
-  int sms;
+  int block_rows;   // query rows of a unit
+  float* part_o;    // [2 sms][block_rows][D]
+  float2* part_ml;  // [2 sms][block_rows]: maximum, sum
+  JoinTask* tasks;  // [sms]
+  int sms;          // CTAs of the grid
   uint32_t* err;
 };
 
 // Query rows (tokens x group) of a block of the few-row kernel, by the mean
-// number of rows a sequence has; see fa_paged_few.cu.
+// number of rows a sequence has, and of the many-row kernel.
 int paged_few_rows(long long rows, int batch);
-cudaError_t launch_paged_few(const PagedLaunch& a, int block_rows, cudaStream_t s);
+int paged_many_rows(int group);
+cudaError_t launch_paged_many(const PagedLaunch& a, cudaStream_t s);
+cudaError_t launch_paged_few(const PagedLaunch& a, cudaStream_t s);
 
 }  // namespace fa

@@ -119,27 +119,31 @@ fa_status cache_rows(const fa_kv_pages* cache, const fa_ragged* batch, const int
 }
 
 // Query rows per sequence and key head that the batch has on average decide
-// the kernel's row blocks.
+// the kernel and its row blocks.
 struct PagedPlan {
+  bool many;
   int block_rows;
-  size_t o_bytes, total_bytes;
+  size_t o_bytes, ml_bytes, total_bytes;
 };
 
 bool paged_plan(int batch, int total, int heads, int heads_k, int D, PagedPlan* plan) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) sms = 160;  // no device: sizes for the checks alone
-  plan->block_rows =
-      paged_few_rows(static_cast<long long>(total) * (heads / heads_k), batch);
+  const int group = heads / heads_k;
+  const long long all = static_cast<long long>(total) * group;
+  plan->many = all > 32LL * batch;
+  plan->block_rows = plan->many ? paged_many_rows(group) : paged_few_rows(all, batch);
   const size_t rows = 2ull * sms * plan->block_rows;
   plan->o_bytes = round256(rows * D * sizeof(float));
-  plan->total_bytes = plan->o_bytes + round256(rows * sizeof(float2));
+  plan->ml_bytes = round256(rows * sizeof(float2));
+  plan->total_bytes = plan->o_bytes + plan->ml_bytes + round256(32ull * sms);
   return true;
 }
 
 bool paged_sizes_ok(int batch, int total, int heads, int heads_k, int D) {
   return batch >= 1 && total >= 0 && total <= kMaxRows && heads_k >= 1 && heads >= heads_k &&
          heads % heads_k == 0 && heads / heads_k <= 128 && (D == 64 || D == 128) &&
-         static_cast<long long>(total) * heads < (1ll << 31);
+         static_cast<long long>(total) * heads < (1ll << 30);
 }
 
 // One cache tensor for the kernels' boxes of min(page_size, 128) rows.
@@ -305,12 +309,25 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
   a.scale_log2 = scale * kLog2e;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.o_bytes);
+  a.tasks = reinterpret_cast<JoinTask*>(static_cast<uint8_t*>(workspace) + plan.o_bytes +
+                                        plan.ml_bytes);
+  a.block_rows = plan.block_rows;
   if (sm_count(&a.sms) != cudaSuccess) return FA_ERR_CUDA;
   a.err = device_error_word();
   if (!a.err) return FA_ERR_CUDA;
-  return launch_paged_few(a, plan.block_rows, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FA_OK
-             : FA_ERR_CUDA;
+  // {D, heads, total}: a box is the heads of one key head for a tile's tokens
+  if (plan.many &&
+      !make_tmap_4d(&a.map_q, q,
+                    dtype == FA_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    static_cast<uint64_t>(D), static_cast<uint64_t>(heads),
+                    static_cast<uint64_t>(batch->total), 1, static_cast<uint64_t>(q_head),
+                    static_cast<uint64_t>(q_token), static_cast<uint64_t>(q_token), 64,
+                    static_cast<uint32_t>(a.group), CU_TENSOR_MAP_SWIZZLE_128B, 2,
+                    static_cast<uint32_t>(kTile / a.group)))
+    return FA_ERR_CUDA;
+  const auto launch = plan.many ? launch_paged_many : launch_paged_few;
+  return launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -30,20 +30,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // A [batch][head][rows][inner] tensor of elem_bytes-byte elements with
 // arbitrary element strides for rows, heads and batches (inner contiguous).
-// Boxes are box_inner x box_rows x 1 x 1; out-of-range rows (and inner
+// Boxes are box_inner x box_rows x box_heads x 1; out-of-range rows (and inner
 // elements) read as zero and are not written.  Returns false when the driver
 // rejects the map (alignment, sizes).
 inline bool make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
                          uint64_t inner, uint64_t rows, uint64_t heads, uint64_t batches,
                          uint64_t row_stride, uint64_t head_stride, uint64_t batch_stride,
                          uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle,
-                         uint64_t elem_bytes = 2) {
+                         uint64_t elem_bytes = 2, uint32_t box_heads = 1) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[4] = {inner, rows, heads, batches};
   cuuint64_t strides[3] = {row_stride * elem_bytes, head_stride * elem_bytes,
                            batch_stride * elem_bytes};
-  cuuint32_t box[4] = {box_inner, box_rows, 1, 1};
+  cuuint32_t box[4] = {box_inner, box_rows, box_heads, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, dtype, 4, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
