@@ -118,6 +118,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   constexpr int kSteps = Smem::kSteps;      // k16 steps over the head, and m16 blocks of V^T
   constexpr bool kMmaBf16 = kBf16 && !kFp8;  // type of the products
   constexpr bool kQRegs = NB < 4;
+  // weights are kept as 2^(s - m + kLift): fp16 ones reach up to 2^15 and stay
+  // normal down to 2^-29 of the largest (e4m3: see pfac)
+  constexpr float kLift = !kFp8 && !kBf16 ? 15.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                      ~uintptr_t(1023));
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             alpha[nb][c] = m_new > m[nb][c] ? ex2_approx(m[nb][c] - m_new) : 1.f;
             moved |= m_new > m[nb][c];
             m[nb][c] = m_new;
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
+            const float ref = m_new == -INFINITY ? 0.f : m_new - kLift;
             acc[nb][c] = ex2_approx(acc[nb][c] - ref);
             acc[nb][c + 2] = ex2_approx(acc[nb][c + 2] - ref);
             l[nb][c] = fmaf(l[nb][c], alpha[nb][c], acc[nb][c] + acc[nb][c + 2]);
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           sum += __shfl_xor_sync(0xffffffffu, sum, 8);
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
           if (g == 0) {
-            s.m[warp][nb * 8 + 2 * t + c] = m[nb][c];
+            s.m[warp][nb * 8 + 2 * t + c] = m[nb][c] - kLift;
             s.l[warp][nb * 8 + 2 * t + c] = sum;
           }
         }

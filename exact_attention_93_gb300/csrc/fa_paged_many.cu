@@ -22,10 +22,10 @@
 //     sequence.
 //
 // Values outside the visible span (behind the sequence's end, in pages not
-// loaded) may be anything, and 0 * NaN is NaN: two spare warps make those rows
-// of a tile zeros before the P V product reads it.
+// loaded) may be anything, and 0 * NaN is NaN: a spare warp makes those rows of
+// a tile zeros before the P V product reads it.
 //
-// e4m3 caches: the two spare warps convert each 8-bit tile to fp16 in shared
+// e4m3 caches: two spare warps convert each 8-bit tile to fp16 in shared
 // memory (exactly, relative to the largest row exponent so far, which scales
 // the scores, and O, in fp32), and bf16 queries to fp16 under a power-of-two
 // scale per row; both products then run in fp16.
@@ -64,7 +64,7 @@ struct ManySmem {
   uint64_t q_full, q_empty, q_ready;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw_full[kSlots8], raw_empty[kSlots8];
-  uint64_t v_fixed[2];
+  uint64_t v_raw[2];  // 16-bit: V tiles with rows to make zeros land here first
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t drain;
   Place place;
@@ -136,10 +136,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   using Smem = ManySmem<D, kFp8>;
   constexpr bool kMmaBf16 = kBf16 && !kFp8;  // type of the products
   // P = 2^(x - m + kPOffset [+ up to 3, e4m3]), the reference m lagging the
-  // true maximum by at most kThreshold: bf16 has the range for no offset, and
-  // fp16 P of an e4m3 cache stays below 2^15 and normal down to 2^-18 of m
+  // true maximum by at most kThreshold.  bf16 has the range for no offset; fp16
+  // P stays below 2^15 (e4m3) or 2^14 and normal down to 2^-18 or 2^-20 of m:
+  // without the offset, keys of weight 2^-15 lost most of their bits.
   constexpr float kThreshold = 8.0f;
-  constexpr float kPOffset = kFp8 ? 4.0f : 0.0f;
+  constexpr int kPOffset = kMmaBf16 ? 0 : kFp8 ? 4 : 6;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                      ~uintptr_t(1023));
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 128);
       mbar_init(&s.o_done[i], 1);
-      mbar_init(&s.v_fixed[i], 64);
+      mbar_init(&s.v_raw[i], 1);
     }
     for (int i = 0; i < Smem::kSlots8; ++i) {
       mbar_init(&s.raw_full[i], 1);
@@ -201,6 +202,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int box_rows = min(p.page_size, kTile), per_tile = kTile / box_rows;
       uint32_t units = 0, ring = 0;  // Q loads, key tiles streamed
       uint32_t loads = 0;            // K and V tiles issued
+      uint32_t cut = 0;              // bit st: parity of V stage st's next ragged tile
+      uint32_t to_raw = 0;           // bit st: V stage st's last load was one
       bool stop = false;
       while (!stop && walk.next(p, x)) {
         const ManyTiles tl(p, x, walk.w.s);
@@ -249,6 +252,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               const int st = ring & 1;
               use = ring >> 1;
               full = kv ? &s.v_full[st] : &s.k_full[st];
+              if (kv) to_raw &= ~(1u << st);
+              if (kv && ragged(j)) {
+                full = &s.v_raw[st];
+                cut ^= 1u << st;
+                to_raw |= 1u << st;
+              }
               empty = kv ? &s.v_empty[st] : &s.k_empty[st];
               dst = kv ? s.v[st] : s.k[st];
             }
@@ -288,9 +297,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                       100000000ull);
         } else {
           for (uint32_t i = loads > 4 ? loads - 4 : 0; i < loads; ++i) {
-            const uint32_t n = i >> 1;
-            mbar_wait((i & 1) ? &s.v_full[n & 1] : &s.k_full[n & 1], (n >> 1) & 1, p.err, &zero,
-                      100000000ull);
+            const uint32_t n = i >> 1, st = n & 1;
+            if ((i & 1) && ((to_raw >> st) & 1))
+              mbar_wait(&s.v_raw[st], ((cut >> st) & 1) ^ 1, p.err, &zero, 100000000ull);
+            else
+              mbar_wait((i & 1) ? &s.v_full[st] : &s.k_full[st], (n >> 1) & 1, p.err, &zero,
+                        100000000ull);
           }
         }
       }
@@ -309,7 +321,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const uint64_t dk0 = smem_desc_sw128(smem_u32(s.k[0]), 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(smem_u32(s.v[0]), Smem::kBlockBytes, 1024);
       uint32_t units = 0, ring = 0;
-      uint32_t fixed = 0;  // bit st: parity of the next zeroed tile in V stage st
       int base0 = 0, base1 = 0;  // P V products of tiles A, B in earlier units
       bool ok = true;
       while (ok && walk.next(p, x)) {
@@ -344,12 +355,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (int j = tl.first; ok && j <= tl.last; ++j) {
           const uint32_t g = ring + static_cast<uint32_t>(j - tl.first);
           const int st = g & 1;
-          if (!kFp8 && ragged(j)) {
-            ok = mbar_wait_poll(&s.v_fixed[st], (fixed >> st) & 1, p.err, abort_flag);
-            fixed ^= 1u << st;
-          } else {
-            ok = mbar_wait_poll(&s.v_full[st], (g >> 1) & 1, p.err, abort_flag);
-          }
+          ok = mbar_wait_poll(&s.v_full[st], (g >> 1) & 1, p.err, abort_flag);
           if (!ok) break;
           bool k_next = false;  // K_{j+1} has landed
           for (int t = 0; ok && t < 2; ++t) {
@@ -392,10 +398,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       commit(&s.drain);
       int zero = 0;
       mbar_wait(&s.drain, 0, p.err, &zero, 100000000ull);
-    } else {
-      // --------------------------------------------- zeroing, or conversion
+    } else if (kFp8 || warp == 10) {
+      // ------------------------- zeroing (one warp), or conversion (two warps)
       const int w64 = tid - 320;  // 0 .. 63
       uint32_t ring = 0, units = 0, n8 = 0;
+      uint32_t fixed = 0;  // bit st: parity of V stage st's next ragged tile
       bool ok = true;
       while (ok && walk.next(p, x)) {
         const ManyTiles tl(p, x, walk.w.s);
@@ -404,9 +411,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           for (int j = tl.first; ok && j <= tl.last; ++j, ++ring) {
             if (!ragged(j)) continue;
             const int st = ring & 1;
-            ok = many_warp_wait(&s.v_full[st], (ring >> 1) & 1, p.err, abort_flag);
+            // (a barrier of their own: these warps skip the other tiles, whose
+            // phases they would lose count of)
+            ok = many_warp_wait(&s.v_raw[st], (fixed >> st) & 1, p.err, abort_flag);
             if (!ok) break;
-            for (int i = w64; i < kTile * (2 * D / 16); i += 64) {
+            fixed ^= 1u << st;
+            for (int i = lane; i < kTile * (2 * D / 16); i += 32) {
               const int r = i & (kTile - 1), c = i >> 7;  // 16-byte chunk c of row r
               const int key = j * kTile + r;
               if (key < x.lo || key >= x.hi)
@@ -414,7 +424,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
-            mbar_arrive(&s.v_fixed[st]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.v_full[st]);
           }
         } else {
           if constexpr (kBf16) {
@@ -660,11 +671,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             tmem_st32(tO + lane_off + c * 32, o);
           }
         }
-        // e4m3: weights are 2^(kPOffset + vshift) times the others'; unscale
+        // the tile's P is 2^(kPOffset + vshift) times the weights; unscale
         // brings their sum back
-        const float offset = kPOffset + static_cast<float>(vshift);
-        const float unscale = kFp8 ? many_exp2_field(127 - static_cast<int>(kPOffset) - vshift)
-                                   : 1.f;
+        const float offset = static_cast<float>(kPOffset + vshift);
+        const float unscale = many_exp2_field(127 - kPOffset - vshift);
         const float mneg = (m == -INFINITY) ? 0.f : offset - m;
         const float em = prescale ? 1.f : mult;
         const uint64_t mult2 = f32x2(em, em), mneg2 = f32x2(mneg, mneg);
@@ -722,7 +732,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (t == 0 || tl.both) {
         // O in tensor memory is 2^kPOffset (e4m3: and 2^(127 + 7 - vbase)) times
         // the sum of weights times values
-        const float back = kFp8 ? many_exp2_field(vbase - 7 - static_cast<int>(kPOffset)) : 1.f;
+        const float back = many_exp2_field((kFp8 ? vbase - 7 : 127) - kPOffset);
         const float per = lo == 0.f ? 0.f : back / lo;
         const long long at = (2LL * blockIdx.x + x.slot) * p.block_rows + t * tile_rows + r;
         const long long row = seq.start + token;

@@ -86,9 +86,10 @@ class Batch:
 
 
 def attention(batch, q, scale, causal=True, window=(-1, -1), slopes=None):
-    """(o, lse, bound on |o| error / eps-free parts) for packed q (total, H, D):
-    o fp64 (rows, H, D), lse (H, rows), A = sum_j P |v|, S = the largest
-    sum_d |scale q_d k_d| + |bias| of a row."""
+    """For packed q (total, H, D) in fp64: o (rows, H, D), lse (H, rows), A =
+    sum_j P |v| + 2^-20 sum_j |v| over the keys a row sees (16-bit weights are
+    rounded relatively down to 2^-20 of the largest at least, and by a share of
+    that below), S = the largest sum_d |scale q_d k_d| + |bias| of a row."""
     H, G = q.shape[1], q.shape[1] // batch.heads_k
     os_, ls, As, Ss, at = [], [], [], [], 0
     for b, n in enumerate(batch.rows):
@@ -115,7 +116,8 @@ def attention(batch, q, scale, causal=True, window=(-1, -1), slopes=None):
         lse = torch.logsumexp(z, -1) if L else torch.full((H, n), -math.inf, dtype=torch.float64)
         p = torch.exp(z - torch.where(lse == -math.inf, 0.0, lse)[..., None])
         os_.append(torch.einsum("hij,jhd->ihd", p, v))
-        As.append(torch.einsum("hij,jhd->ihd", p, v.abs()))
+        weak = p + 2.0 ** -20 * seen * (lse > -math.inf)[..., None]
+        As.append(torch.einsum("hij,jhd->ihd", weak, v.abs()))
         Ss.append(mag.masked_fill(~seen, 0.0).amax(-1) if L else torch.zeros(H, n).double())
         ls.append(lse)
     return torch.cat(os_), torch.cat(ls, 1), torch.cat(As), torch.cat(Ss, 1)

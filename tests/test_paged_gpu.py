@@ -197,3 +197,14 @@ def test_many_short_sequences():
                 seed=1)
     q, o, lse = run(b, 2)
     check(b, 2, q, o, lse)
+
+
+@pytest.mark.parametrize("fp8,D,H,Hk,dtype", [(False, 128, 16, 4, BF), (True, 128, 16, 4, BF),
+                                              (False, 64, 24, 8, HF), (True, 64, 15, 5, HF)])
+def test_several_long_units_per_cta(fp8, D, H, Hk, dtype):
+    b = R.Batch([1900, 1, 700, 0, 1333], [0, 900, 650, 10, 3], Hk, D, 64, dtype, fp8, seed=12)
+    q, o, lse = run(b, H)
+    check(b, H, q, o, lse)
+    b = R.Batch([1900, 700, 1333], [0, 650, 3], Hk, D, 32, dtype, fp8, seed=13)
+    q, o, lse = run(b, H, window=(500, 0))
+    check(b, H, q, o, lse, window=(500, 0))
