@@ -25,7 +25,6 @@ from __future__ import annotations
 import torch
 
 from . import fattn
-from .kvcache import check_devices
 
 __all__ = ["flash_attn_func", "flash_attn_qkvpacked_func", "flash_attn_fp8_func",
            "flash_attn_paged_func"]
@@ -218,20 +217,26 @@ def flash_attn_paged_func(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
     if torch.is_grad_enabled() and q.requires_grad:
         raise ValueError("attention over a cache has no backward: call under torch.no_grad()")
     cache = fattn.kv_pages(k_pages, v_pages, k_exp, v_exp)
-    if q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != cache.head_dim:
+    shape, heads_k = q.shape, k_pages.shape[2]
+    if len(shape) != 3 or q.stride(2) != 1 or shape[2] != k_pages.shape[3]:
         raise ValueError("q must be a packed (total, nheads, headdim) tensor of the cache's "
                          "headdim, which must be contiguous")
-    total, H, D = q.shape
-    if H % cache.heads:
+    total, H, D = shape
+    if H % heads_k:
         raise ValueError("nheads must be a multiple of the cache's heads")
+    if seqlens is None:
+        raise ValueError("seqlens is needed")
     batch = fattn.ragged(block_table, cu_seqlens, seqlens, total)
-    window, slopes = _check_options(0.0, window_size, alibi_slopes, batch.batch, H)
-    opts = None
-    with check_devices(q, k_pages, v_pages, block_table, cu_seqlens, seqlens, slopes):
-        if slopes is not None or window != (-1, -1):
-            opts = fattn.options(window, slopes)
-        o = torch.empty((total, H, D), dtype=q.dtype, device=q.device)
+    n, opts = seqlens.shape[0], None
+    if alibi_slopes is not None or window_size != (-1, -1):
+        window, alibi_slopes = _check_options(0.0, window_size, alibi_slopes, n, H)
+    device = fattn.one_device(q, k_pages, v_pages, block_table, cu_seqlens, seqlens, alibi_slopes)
+    if alibi_slopes is not None or window_size != (-1, -1):
+        opts = fattn.options(window, alibi_slopes)
+    with fattn.on_device(device):
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
         lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
-        fattn.fa_fwd_paged(q, o, lse, cache, batch, opts,
-                           D ** -0.5 if softmax_scale is None else float(softmax_scale), causal)
+        fattn.fa_fwd_paged(q, o, lse, cache, batch, n, heads_k, opts,
+                           D ** -0.5 if softmax_scale is None else float(softmax_scale),
+                           bool(causal), fattn.raw_stream(device))
     return (o, lse) if return_lse else o

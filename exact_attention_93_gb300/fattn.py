@@ -8,9 +8,11 @@ missing or cannot load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,30 +44,6 @@ class FaOptions(ctypes.Structure):
     _fields_ = [("window_left", ctypes.c_int), ("window_right", ctypes.c_int),
                 ("alibi_slopes", ctypes.c_void_p), ("alibi_per_batch", ctypes.c_int),
                 ("block_mask", ctypes.c_void_p), ("block_mask_per_head", ctypes.c_int)]
-
-
-class FaRotaryOperand(ctypes.Structure):
-    """fa_rotary_operand: one tensor fa_rotary turns, and where to."""
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
-                ("xs", FaStrides), ("ys", FaStrides)]
-
-
-class FaKvPages(ctypes.Structure):
-    """fa_kv_pages: a paged key/value cache."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
-                ("k_page", ctypes.c_longlong), ("k_token", ctypes.c_longlong),
-                ("k_head", ctypes.c_longlong), ("v_page", ctypes.c_longlong),
-                ("v_token", ctypes.c_longlong), ("v_head", ctypes.c_longlong),
-                ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
-                ("head_dim", ctypes.c_int), ("type", ctypes.c_int)]
-
-
-class FaRagged(ctypes.Structure):
-    """fa_ragged: a batch of sequences packed along their tokens."""
-    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
-                ("max_pages", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
-                ("seqlens", ctypes.c_void_p), ("batch", ctypes.c_int), ("total", ctypes.c_int)]
 
 
 class FattnError(RuntimeError):
@@ -473,7 +451,16 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, deterministic=False,
 
 # --------------------------------------------------------------------------
 # include/fattn_cache.h: rotary positions, the paged cache, attention over it
+#
+# These calls are made once per layer and token while generating, so their
+# marshalling is kept short: the C structs are packed as bytes (native
+# alignment), pointers are plain integers, and the current stream is asked for
+# as the raw handle.
 # --------------------------------------------------------------------------
+
+_pack_rotary_operand = struct.Struct("@PPi6q").pack  # fa_rotary_operand
+_pack_kv_pages = struct.Struct("@4P6q5i").pack       # fa_kv_pages
+_pack_ragged = struct.Struct("@PqiPPii").pack        # fa_ragged
 
 _ELEMS = None
 
@@ -491,118 +478,152 @@ def elem_code(dtype) -> int:
     return code
 
 
-def rotary_operand(x, y) -> FaRotaryOperand:
+def raw_stream(device: int, stream=None) -> int:
+    """The cudaStream_t of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(device)
+
+
+def on_device(device: int):
+    """A context in which `device` is the current device."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() == device:
+        return _NOTHING
+    return torch.cuda.device(device)
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def one_device(first, *others) -> int:
+    """The CUDA device that all tensors (None is skipped) are on."""
+    device = first.get_device()
+    if device >= 0:
+        for t in others:
+            if t is not None and t.get_device() != device:
+                break
+        else:
+            return device
+    raise ValueError("libfattn takes CUDA tensors of one device only")
+
+
+def rotary_operand(x, y) -> bytes:
     """fa_rotary_operand of (batch, seq, heads, D) tensors x -> y (or packed
     (seq, heads, D) ones)."""
-    def strides(t):
-        st = t.stride()
-        if st[-1] != 1:
-            raise ValueError("the head dimension D must be contiguous")
-        return FaStrides(st[0], st[2], st[1]) if len(st) == 4 else FaStrides(0, st[1], st[0])
-    return FaRotaryOperand(x.data_ptr(), y.data_ptr(), x.shape[-2], strides(x), strides(y))
+    xs, ys = x.stride(), y.stride()
+    if xs[-1] != 1 or ys[-1] != 1:
+        raise ValueError("the head dimension D must be contiguous")
+    if len(xs) == 3:
+        return _pack_rotary_operand(x.data_ptr(), y.data_ptr(), x.shape[1], 0, xs[1], xs[0], 0,
+                                    ys[1], ys[0])
+    return _pack_rotary_operand(x.data_ptr(), y.data_ptr(), x.shape[2], xs[0], xs[2], xs[1],
+                                ys[0], ys[2], ys[1])
 
 
-def kv_pages(k_pages, v_pages, k_exp=None, v_exp=None) -> FaKvPages:
+def kv_pages(k_pages, v_pages, k_exp=None, v_exp=None) -> bytes:
     """fa_kv_pages of (pages, page_size, heads, D) tensors, and for e4m3 ones
     their (pages, heads, page_size) exponent bytes."""
-    torch = _torch()
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype != dtype:
         raise ValueError("k_pages and v_pages must be (pages, page_size, heads, D) tensors of "
                          "one shape and type")
-    pages, page_size, heads, dim = k_pages.shape
+    pages, page_size, heads, dim = shape
     ks, vs = k_pages.stride(), v_pages.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("the head dimension D must be contiguous")
-    code = elem_code(k_pages.dtype)
+    code = elem_code(dtype)
+    ke = ve = 0
     if code == FA_ELEM_E4M3:
         for e in (k_exp, v_exp):
-            if (e is None or e.dtype != torch.uint8 or tuple(e.shape) != (pages, heads, page_size)
+            if (e is None or e.dtype != _torch().uint8 or e.shape != (pages, heads, page_size)
                     or not e.is_contiguous() or e.device != k_pages.device):
                 raise ValueError("an e4m3 cache needs k_exp and v_exp: contiguous uint8 "
                                  "(pages, heads, page_size) tensors on its device")
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
-    else:
-        if k_exp is not None or v_exp is not None:
-            raise ValueError("k_exp and v_exp belong to an e4m3 cache")
-        ke = ve = None
-    return FaKvPages(k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, ks[0], ks[1], ks[2], vs[0],
-                     vs[1], vs[2], pages, page_size, heads, dim, code)
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError("k_exp and v_exp belong to an e4m3 cache")
+    return _pack_kv_pages(k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, ks[0], ks[1], ks[2],
+                          vs[0], vs[1], vs[2], pages, page_size, heads, dim, code)
 
 
-def ragged(block_table, cu_seqlens, seqlens, total: int) -> FaRagged:
+def ragged(block_table, cu_seqlens, seqlens, total: int) -> bytes:
     """fa_ragged of a (batch, max_pages) table, (batch + 1) boundaries and
     (batch) lengths (or None), int32 tensors."""
-    torch = _torch()
-    i32 = torch.int32
-    if (block_table.dim() != 2 or block_table.dtype != i32
-            or (block_table.stride(1) != 1 and block_table.shape[1] > 1)):
+    i32 = _torch().int32
+    shape, st = block_table.shape, block_table.stride()
+    if len(shape) != 2 or block_table.dtype != i32 or (st[1] != 1 and shape[1] > 1):
         raise ValueError("block_table must be an int32 (batch, max_pages) tensor with "
                          "contiguous rows")
-    batch, max_pages = block_table.shape
-    if cu_seqlens.dtype != i32 or not cu_seqlens.is_contiguous() or cu_seqlens.shape != (batch + 1,):
+    batch, max_pages = shape
+    if (cu_seqlens.dtype != i32 or cu_seqlens.shape != (batch + 1,)
+            or not cu_seqlens.is_contiguous()):
         raise ValueError("cu_seqlens must be a contiguous int32 (batch + 1) tensor")
-    if seqlens is not None and (seqlens.dtype != i32 or not seqlens.is_contiguous()
-                                or seqlens.shape != (batch,)):
-        raise ValueError("sequence lengths and starts must be contiguous int32 (batch) tensors")
-    stride = block_table.stride(0) if batch > 1 else max(max_pages, block_table.stride(0))
-    return FaRagged(block_table.data_ptr(), stride, max_pages, cu_seqlens.data_ptr(),
-                    None if seqlens is None else seqlens.data_ptr(), batch, total)
+    lens = 0
+    if seqlens is not None:
+        if seqlens.dtype != i32 or seqlens.shape != (batch,) or not seqlens.is_contiguous():
+            raise ValueError("sequence lengths and starts must be contiguous int32 (batch) "
+                             "tensors")
+        lens = seqlens.data_ptr()
+    return _pack_ragged(block_table.data_ptr(), st[0] if batch > 1 else max(max_pages, st[0]),
+                        max_pages, cu_seqlens.data_ptr(), lens, batch, total)
 
 
-def stream_of(stream=None) -> int:
-    return (stream or _torch().cuda.current_stream()).cuda_stream
-
-
-def fa_rotary(q: FaRotaryOperand, k, B: int, N: int, D: int, rotary_dim: int, inv_freq: int,
-              positions, position_bits: int, position_batch_stride: int, magnitude: float,
-              interleaved: bool, inverse: bool, elem: int, stream=None):
+def fa_rotary(q: bytes, k, B: int, N: int, D: int, rotary_dim: int, inv_freq: int,
+              positions: int, position_bits: int, position_batch_stride: int, magnitude: float,
+              interleaved: bool, inverse: bool, elem: int, stream: int):
     """fa_rotary: operands from rotary_operand (k may be None), device
-    pointers for inv_freq and positions."""
-    st = load().fa_rotary(ctypes.addressof(q), None if k is None else ctypes.addressof(k), B, N,
-                          D, rotary_dim, inv_freq, positions, position_bits,
-                          position_batch_stride, magnitude, int(interleaved), int(inverse), elem,
-                          stream_of(stream))
-    _check(st, "fa_rotary")
+    pointers for inv_freq and positions (0: none), a raw stream."""
+    st = (_lib or load()).fa_rotary(q, k, B, N, D, rotary_dim, inv_freq, positions,
+                                    position_bits, position_batch_stride, magnitude, interleaved,
+                                    inverse, elem, stream)
+    if st:
+        _check(st, "fa_rotary")
 
 
-def fa_cache_append(cache: FaKvPages, batch: FaRagged, k, v, stream=None):
-    """fa_cache_append of packed (total, heads, D) tensors k, v."""
+def fa_cache_append(cache: bytes, batch: bytes, k, v, stream: int):
+    """fa_cache_append of packed (total, heads, D) tensors k, v; cache and
+    batch from kv_pages and ragged."""
     ks, vs = k.stride(), v.stride()
-    st = load().fa_cache_append(ctypes.addressof(cache), ctypes.addressof(batch), k.data_ptr(),
-                                ks[0], ks[1], v.data_ptr(), vs[0], vs[1], elem_code(k.dtype),
-                                stream_of(stream))
-    _check(st, "fa_cache_append")
+    st = (_lib or load()).fa_cache_append(cache, batch, k.data_ptr(), ks[0], ks[1], v.data_ptr(),
+                                          vs[0], vs[1], elem_code(k.dtype), stream)
+    if st:
+        _check(st, "fa_cache_append")
 
 
-def fa_cache_read(cache: FaKvPages, batch: FaRagged, starts, k, v, stream=None):
+def fa_cache_read(cache: bytes, batch: bytes, starts, k, v, stream: int):
     """fa_cache_read into packed (total, heads, D) tensors k, v; starts: an
     int32 (batch) tensor or None."""
     ks, vs = k.stride(), v.stride()
-    st = load().fa_cache_read(ctypes.addressof(cache), ctypes.addressof(batch),
-                              None if starts is None else starts.data_ptr(), k.data_ptr(), ks[0],
-                              ks[1], v.data_ptr(), vs[0], vs[1], elem_code(k.dtype),
-                              stream_of(stream))
-    _check(st, "fa_cache_read")
+    st = (_lib or load()).fa_cache_read(cache, batch,
+                                        None if starts is None else starts.data_ptr(),
+                                        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                                        elem_code(k.dtype), stream)
+    if st:
+        _check(st, "fa_cache_read")
 
 
 def fa_fwd_paged_workspace_size(batch: int, total: int, heads: int, heads_k: int, D: int) -> int:
     return int(load().fa_fwd_paged_workspace_size(batch, total, heads, heads_k, D))
 
 
-def fa_fwd_paged(q, o, lse, cache: FaKvPages, batch: FaRagged, opts, scale: float, causal: bool,
-                 workspace=None, stream=None):
+def fa_fwd_paged(q, o, lse, cache: bytes, batch: bytes, sequences: int, heads_k: int, opts,
+                 scale: float, causal: bool, stream: int, workspace=None):
     """fa_fwd_paged of packed (total, heads, D) tensors q, o and an fp32
-    (heads, total) lse; opts: FaOptions or None."""
+    (heads, total) lse; cache and batch (of `sequences` sequences) from
+    kv_pages and ragged; opts: FaOptions or None."""
+    lib = _lib or load()
     total, heads, dim = q.shape
     if workspace is None:
-        n = fa_fwd_paged_workspace_size(batch.batch, total, heads, cache.heads, dim)
+        n = lib.fa_fwd_paged_workspace_size(sequences, total, heads, heads_k, dim)
         if n == 0:
             raise ValueError("invalid sizes for attention over a paged cache")
-        workspace = _torch().empty(n, dtype=_torch().uint8, device=q.device)
+        torch = _torch()
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     qs, os_ = q.stride(), o.stride()
-    st = load().fa_fwd_paged(q.data_ptr(), qs[0], qs[1], o.data_ptr(), os_[0], os_[1],
-                             lse.data_ptr(), ctypes.addressof(cache), ctypes.addressof(batch),
-                             heads, None if opts is None else ctypes.addressof(opts), scale,
-                             int(causal), elem_code(q.dtype), workspace.data_ptr(),
-                             workspace.numel(), stream_of(stream))
-    _check(st, "fa_fwd_paged")
+    st = lib.fa_fwd_paged(q.data_ptr(), qs[0], qs[1], o.data_ptr(), os_[0], os_[1],
+                          lse.data_ptr(), cache, batch, heads,
+                          None if opts is None else ctypes.addressof(opts), scale, causal,
+                          elem_code(q.dtype), workspace.data_ptr(), workspace.numel(), stream)
+    if st:
+        _check(st, "fa_fwd_paged")

@@ -12,8 +12,6 @@ attention.flash_attn_paged_func attends over what is cached here.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import fattn
@@ -40,21 +38,13 @@ def alloc_kv_cache(pages, page_size, nheads, headdim, dtype=torch.bfloat16, devi
             make(exp, torch.uint8), make(exp, torch.uint8))
 
 
-def check_devices(first, *others):
-    for t in (first, *others):
-        if t is not None and (not t.is_cuda or t.device != first.device):
-            raise ValueError("libfattn takes CUDA tensors of one device only")
-    if first.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(first.device)
-
-
 def _check_rows(k, v, k_pages):
-    heads, dim = k_pages.shape[2], k_pages.shape[3]
-    if (k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (heads, dim) or k.dtype != v.dtype
+    shape, page = k.shape, k_pages.shape
+    if (len(shape) != 3 or shape != v.shape or shape[1:] != page[2:] or k.dtype != v.dtype
             or k.stride(2) != 1 or v.stride(2) != 1):
-        raise ValueError(f"k and v must be packed (total, {heads}, {dim}) tensors of one type "
-                         "with the head dimension contiguous")
+        raise ValueError(f"k and v must be packed (total, {page[2]}, {page[3]}) tensors of one "
+                         "type with the head dimension contiguous")
+    return shape[0]
 
 
 def kv_cache_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, k_exp=None,
@@ -70,12 +60,13 @@ def kv_cache_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, k_
     if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad):
         raise ValueError("the cache keeps no gradients: call under torch.no_grad()")
     cache = fattn.kv_pages(k_pages, v_pages, k_exp, v_exp)
-    _check_rows(k, v, k_pages)
+    total = _check_rows(k, v, k_pages)
     if seqlens is None:
         raise ValueError("seqlens is needed")
-    batch = fattn.ragged(block_table, cu_seqlens, seqlens, k.shape[0])
-    with check_devices(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens):
-        fattn.fa_cache_append(cache, batch, k, v)
+    batch = fattn.ragged(block_table, cu_seqlens, seqlens, total)
+    device = fattn.one_device(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens)
+    with fattn.on_device(device):
+        fattn.fa_cache_append(cache, batch, k, v, fattn.raw_stream(device))
 
 
 def kv_cache_read(k_pages, v_pages, block_table, cu_seqlens, total, starts=None, k_exp=None,
@@ -89,14 +80,17 @@ def kv_cache_read(k_pages, v_pages, block_table, cu_seqlens, total, starts=None,
     cache = fattn.kv_pages(k_pages, v_pages, k_exp, v_exp)
     if dtype is None:
         dtype = torch.bfloat16 if k_pages.dtype == torch.float8_e4m3fn else k_pages.dtype
-    shape = (int(total), k_pages.shape[2], k_pages.shape[3])
+    total = int(total)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=dtype, device=k_pages.device) for _ in range(2))
-    k, v = out
-    _check_rows(k, v, k_pages)
-    if k.shape[0] != shape[0] or k.dtype != dtype:
-        raise ValueError("out must hold `total` rows of dtype")
-    batch = fattn.ragged(block_table, cu_seqlens, starts, shape[0])
-    with check_devices(k_pages, v_pages, k, v, block_table, cu_seqlens, starts):
-        fattn.fa_cache_read(cache, batch, starts, k, v)
+        # one allocation: [0] keys, [1] values
+        k, v = torch.empty((2, total, *k_pages.shape[2:]), dtype=dtype,
+                           device=k_pages.device).unbind()
+    else:
+        k, v = out
+        if _check_rows(k, v, k_pages) != total or k.dtype != dtype:
+            raise ValueError("out must hold `total` rows of dtype")
+    batch = fattn.ragged(block_table, cu_seqlens, starts, total)
+    device = fattn.one_device(k_pages, v_pages, k, v, block_table, cu_seqlens, starts)
+    with fattn.on_device(device):
+        fattn.fa_cache_read(cache, batch, starts, k, v, fattn.raw_stream(device))
     return k, v

@@ -8,7 +8,6 @@ bases and for contexts stretched beyond the trained length.
 """
 from __future__ import annotations
 
-import contextlib
 import math
 
 import torch
@@ -56,43 +55,42 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
 
 
 def _check(q, k, inv_freq, positions):
-    if q.dim() not in (3, 4):
+    """Checks the arguments; the device they are on."""
+    shape = q.shape
+    if len(shape) not in (3, 4):
         raise ValueError("expected (batch, seqlen, nheads, headdim) or packed "
                          "(total, nheads, headdim) tensors")
-    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2]
-                          or k.shape[-1] != q.shape[-1] or k.dtype != q.dtype):
-        raise ValueError("q and k must agree in type and in every dimension but the heads")
+    if k is not None:
+        other = k.shape
+        if (len(other) != len(shape) or other[:-2] != shape[:-2] or other[-1] != shape[-1]
+                or k.dtype != q.dtype):
+            raise ValueError("q and k must agree in type and in every dimension but the heads")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 (rotary_dim / 2) tensor")
-    B, N = (q.shape[0], q.shape[1]) if q.dim() == 4 else (1, q.shape[0])
     if positions is not None:
         if positions.dtype not in (torch.int32, torch.int64):
             raise TypeError("positions must be int32 or int64")
-        if positions.shape != (N,) and (q.dim() != 4 or positions.shape != (B, N)):
+        if positions.shape != shape[-3:-2] and (len(shape) != 4 or positions.shape != shape[:2]):
             raise ValueError("positions must have shape (seqlen,) or (batch, seqlen)")
-    for t in (q, k, inv_freq, positions):
-        if t is not None and (not t.is_cuda or t.device != q.device):
-            raise ValueError("libfattn takes CUDA tensors of one device only")
-    return B, N
+    return fattn.one_device(q, k, inv_freq, positions)
 
 
-def _turn(xs, ys, inv_freq, positions, magnitude, interleaved, inverse):
-    """Turns the tensors xs (one or two) into ys."""
-    x = xs[0]
-    B, N = (x.shape[0], x.shape[1]) if x.dim() == 4 else (1, x.shape[0])
-    bits, stride, at = 0, 0, None
+def _turn(device, x, y, x2, y2, inv_freq, positions, magnitude, interleaved, inverse):
+    """Turns x into y, and x2 (unless it is None) into y2."""
+    shape = x.shape
+    B, N = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    bits, stride, at = 0, 0, 0
     if positions is not None:
         if positions.stride(-1) != 1:
             positions = positions.contiguous()
         bits, at = 32 if positions.dtype == torch.int32 else 64, positions.data_ptr()
         stride = positions.stride(0) if positions.dim() == 2 else 0
-    ops = [fattn.rotary_operand(a, b) for a, b in zip(xs, ys)]
-    here = (contextlib.nullcontext() if x.device.index == torch.cuda.current_device()
-            else torch.cuda.device(x.device))
-    with here:
-        fattn.fa_rotary(ops[0], ops[1] if len(ops) > 1 else None, B, N, x.shape[-1],
-                        2 * inv_freq.numel(), inv_freq.data_ptr(), at, bits, stride, magnitude,
-                        interleaved, inverse, fattn.elem_code(x.dtype))
+    a = fattn.rotary_operand(x, y)
+    b = None if x2 is None else fattn.rotary_operand(x2, y2)
+    with fattn.on_device(device):
+        fattn.fa_rotary(a, b, B, N, shape[-1], 2 * inv_freq.shape[0], inv_freq.data_ptr(), at,
+                        bits, stride, magnitude, interleaved, inverse, fattn.elem_code(x.dtype),
+                        fattn.raw_stream(device))
 
 
 def _grad_operand(g):
@@ -105,27 +103,29 @@ def _grad_operand(g):
 
 class _Rotary(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, inv_freq, positions, magnitude, interleaved):
+    def forward(ctx, q, k, inv_freq, positions, magnitude, interleaved, device):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(inv_freq, positions)
-        ctx.magnitude, ctx.interleaved = magnitude, interleaved
-        xs = [q] if k is None else [q, k]
-        ys = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
-        _turn(xs, ys, inv_freq, positions, magnitude, interleaved, False)
-        return (ys[0], None) if k is None else tuple(ys)
+        ctx.magnitude, ctx.interleaved, ctx.device = magnitude, interleaved, device
+        yq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        yk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+        _turn(device, q, yq, k, yk, inv_freq, positions, magnitude, interleaved, False)
+        return yq, yk
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq, dk):
         inv_freq, positions = ctx.saved_tensors
-        grads = [None if g is None else _grad_operand(g) for g in (dq, dk)]
-        outs = [None if g is None else torch.empty(g.shape, dtype=g.dtype, device=g.device)
-                for g in grads]
-        have = [i for i in range(2) if grads[i] is not None]
-        if have:
-            _turn([grads[i] for i in have], [outs[i] for i in have], inv_freq, positions,
-                  ctx.magnitude, ctx.interleaved, True)
-        return outs[0], outs[1], None, None, None, None
+        grads = [_grad_operand(g) for g in (dq, dk) if g is not None]
+        if not grads:
+            return None, None, None, None, None, None, None
+        outs = [torch.empty_like(g, memory_format=torch.contiguous_format) for g in grads]
+        two = len(grads) > 1
+        _turn(ctx.device, grads[0], outs[0], grads[1] if two else None, outs[1] if two else None,
+              inv_freq, positions, ctx.magnitude, ctx.interleaved, True)
+        gq = outs[0] if dq is not None else None
+        gk = None if dk is None else outs[-1]
+        return gq, gk, None, None, None, None, None
 
 
 def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0, inplace=False):
@@ -143,18 +143,17 @@ def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0
     Returns new tensors (q, k), or q alone when k is None.  Differentiable in q
     and k.  inplace=True writes over q and k instead and returns them; it is
     for inference and refuses tensors that need a gradient."""
-    _check(q, k, inv_freq, positions)
+    device = _check(q, k, inv_freq, positions)
     magnitude, interleaved = float(magnitude), bool(interleaved)
-    grad = torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad))
-    if grad and not inplace:
-        q, k = _Rotary.apply(q, k, inv_freq, positions, magnitude, interleaved)
-        return q if k is None else (q, k)
-    xs = [q] if k is None else [q, k]
-    if inplace:
-        if grad:
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        if inplace:
             raise ValueError("inplace=True would overwrite tensors that need a gradient")
-        ys = xs
+        yq, yk = _Rotary.apply(q, k, inv_freq, positions, magnitude, interleaved, device)
+        return yq if k is None else (yq, yk)
+    if inplace:
+        yq, yk = q, k
     else:
-        ys = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
-    _turn(xs, ys, inv_freq, positions, magnitude, interleaved, False)
-    return ys[0] if k is None else tuple(ys)
+        yq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        yk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+    _turn(device, q, yq, k, yk, inv_freq, positions, magnitude, interleaved, False)
+    return yq if k is None else (yq, yk)

@@ -103,7 +103,8 @@ def test_rows_without_keys_and_rows_behind_the_last_sequence(rows, fp8):
     o = torch.full((b.total, H, 128), 7.0, dtype=BF, device="cuda")
     lse = torch.full((H, b.total), 7.0, device="cuda")
     fattn.fa_fwd_paged(q.cuda(), o, lse, fattn.kv_pages(k, v, **kw),
-                       fattn.ragged(table, cu, lens, b.total), None, 128 ** -0.5, True)
+                       fattn.ragged(table, cu, lens, b.total), len(rows), 2, None, 128 ** -0.5,
+                       True, fattn.raw_stream(0))
     torch.cuda.synchronize()
     assert fattn_error() == fattn.FA_OK
     check(b, H, q, o.cpu(), lse.cpu())

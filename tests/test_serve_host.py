@@ -14,6 +14,24 @@ FAKE = 1 << 20  # aligned and never dereferenced: every call below fails its che
 INV, UNS = fattn.FA_ERR_INVALID_ARG, fattn.FA_ERR_UNSUPPORTED
 
 
+class KvPages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp")] + [
+        (n, ctypes.c_longlong) for n in ("k_page", "k_token", "k_head", "v_page", "v_token",
+                                         "v_head")] + [
+        (n, ctypes.c_int) for n in ("pages", "page_size", "heads", "head_dim", "type")]
+
+
+class Ragged(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
+                ("max_pages", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("batch", ctypes.c_int), ("total", ctypes.c_int)]
+
+
+class RotaryOperand(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("xs", fattn.FaStrides), ("ys", fattn.FaStrides)]
+
+
 @pytest.fixture(scope="module")
 def lib():
     build.build()
@@ -43,14 +61,14 @@ def pages(**kw):
              v_page=16 * 2 * D, v_token=2 * D, v_head=D, pages=4, page_size=16, heads=2,
              head_dim=64, type=fattn.FA_ELEM_BF16)
     d.update(kw)
-    return fattn.FaKvPages(**d)
+    return KvPages(**d)
 
 
 def ragged(**kw):
     d = dict(block_table=FAKE, table_stride=8, max_pages=8, cu_seqlens=FAKE, seqlens=FAKE, batch=2,
              total=5)
     d.update(kw)
-    return fattn.FaRagged(**d)
+    return Ragged(**d)
 
 
 BAD_CACHE = [
@@ -116,6 +134,22 @@ def test_paged_arguments(lib, kw, status):
     assert paged(lib, **kw) == status
 
 
+def test_packed_structs_match_the_c_layout():
+    kp, vp, ke, ve = kvcache.alloc_kv_cache(3, 16, 2, 64, torch.float8_e4m3fn, device="cpu")
+    c = KvPages.from_buffer_copy(fattn.kv_pages(kp, vp, ke, ve).ljust(ctypes.sizeof(KvPages)))
+    assert (c.k, c.v, c.k_exp, c.v_exp) == tuple(x.data_ptr() for x in (kp, vp, ke, ve))
+    assert (c.k_page, c.k_token, c.k_head) == (2048, 128, 64) == (c.v_page, c.v_token, c.v_head)
+    assert (c.pages, c.page_size, c.heads, c.head_dim, c.type) == (3, 16, 2, 64, 3)
+    table, cu, lens = torch.zeros(2, 5, dtype=torch.int32), i32(0, 1, 4), i32(1, 3)
+    b = Ragged.from_buffer_copy(fattn.ragged(table, cu, lens, 4).ljust(ctypes.sizeof(Ragged)))
+    assert (b.block_table, b.cu_seqlens, b.seqlens) == tuple(x.data_ptr() for x in (table, cu, lens))
+    assert (b.table_stride, b.max_pages, b.batch, b.total) == (5, 5, 2, 4)
+    x, y = t(1, 4, 2, 64), t(1, 4, 2, 64)
+    o = RotaryOperand.from_buffer_copy(fattn.rotary_operand(x, y))
+    assert (o.x, o.y, o.heads) == (x.data_ptr(), y.data_ptr(), 2)
+    assert (o.xs.batch, o.xs.head, o.xs.seq) == (512, 64, 128) == (o.ys.batch, o.ys.head, o.ys.seq)
+
+
 def test_workspace_size(lib):
     size = lib.fa_fwd_paged_workspace_size
     assert size(1, 1, 8, 2, 64) > 0 and size(1, 1, 8, 2, 64) % 256 == 0
@@ -125,7 +159,7 @@ def test_workspace_size(lib):
 
 def rot(lib, B=1, N=4, D=64, r=64, freq=FAKE, pos=None, bits=0, stride=0, mag=1.0, dtype=0, x=FAKE,
         y=2 * FAKE, heads=2, xs=(512, 64, 128), ys=(512, 64, 128)):
-    op = fattn.FaRotaryOperand(x, y, heads, fattn.FaStrides(*xs), fattn.FaStrides(*ys))
+    op = RotaryOperand(x, y, heads, fattn.FaStrides(*xs), fattn.FaStrides(*ys))
     return lib.fa_rotary(ctypes.addressof(op), None, B, N, D, r, freq, pos, bits, stride, mag, 0, 0,
                          dtype, None)
 
