@@ -14,8 +14,8 @@
 //
 // Weights.  The few-row kernel gives all units of a sequence the number of key
 // tiles that any of its queries sees, at least 1 (a sequence usually is one
-// block).  The many-row kernel counts each block's own tiles, plus one for
-// what a unit costs beside its tiles: under a causal mask the blocks of a
+// block).  The many-row kernel counts each block's own tiles, plus kUnitCost
+// for what a unit costs beside its tiles: under a causal mask the blocks of a
 // prompt see from one tile to all of them.  The sums over blocks that this
 // needs are sums of floor((a + i b) / 128), taken in closed form.
 #pragma once
@@ -25,6 +25,9 @@
 namespace fa {
 
 constexpr float kPagedLn2 = 0.6931471805599453f;
+// Loading Q, filling the pipeline and writing O take the many-row kernel about
+// as long as three key tiles.
+constexpr int kUnitCost = 3;
 
 // Keys [lo, hi) that some query of tokens [t0, t1) of the sequence sees.
 __device__ __forceinline__ void visible_span(const PagedLaunch& p, const Seq& s, int t0, int t1,
@@ -74,25 +77,21 @@ struct SeqWork {
   int blocks;  // query blocks per key head
   int flat;    // few rows: the weight of every unit
   int first;   // few rows: the first key tile
-  long long per_head;
   __device__ __forceinline__ void load(const PagedLaunch& p, int b, uint32_t* err = nullptr) {
     s = load_seq(p.r, p.page_log2, b, err);
     blocks = (s.rows * p.group + p.block_rows - 1) / p.block_rows;
-    if constexpr (kMany) {
-      per_head = before(p, blocks);
-    } else {
+    if constexpr (!kMany) {
       int lo, hi;
       visible_span(p, s, 0, s.rows, lo, hi);
       first = lo / kTile;
       flat = max(1, (hi + kTile - 1) / kTile - first);
-      per_head = static_cast<long long>(flat) * blocks;
     }
   }
   // Weight of the blocks before block i of a head.
   __device__ __forceinline__ long long before(const PagedLaunch& p, int i) const {
     if constexpr (!kMany) return static_cast<long long>(flat) * i;
     const int bt = p.block_rows / p.group;  // tokens of a block
-    long long sum = i;
+    long long sum = static_cast<long long>(kUnitCost) * i;
     int open = 0;  // leading blocks whose keys end before the sequence's
     if (p.win_right >= 0) {
       const int end = s.len - s.pos0 - p.win_right;
@@ -129,10 +128,14 @@ template <bool kMany>
 __device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) {
   const int lane = threadIdx.x & 31;
   Place at{};
+  // lane i keeps the work of one head of sequences i, and the first 32 stay
+  SeqWork<kMany> w;
+  long long head0 = 0;
   for (int b = lane; b < p.r.batch; b += 32) {
-    SeqWork<kMany> w;
     w.load(p, b, c == 0 ? p.err : nullptr);
-    at.total += w.per_head * p.heads_k;
+    const long long head = w.blocks ? w.before(p, w.blocks) : 0;
+    if (b == lane) head0 = head;
+    at.total += head * p.heads_k;
   }
   at.total = warp_sum(at.total);
   at.pos = stretch(at.total, n, c);
@@ -140,12 +143,15 @@ __device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) 
   if (at.left == 0) return at;
   long long ahead = 0;
   for (int b0 = 0; b0 < p.r.batch; b0 += 32) {
-    SeqWork<kMany> w;
-    long long mine = 0;
-    if (b0 + lane < p.r.batch) {
-      w.load(p, b0 + lane);
-      mine = w.per_head * p.heads_k;
+    long long head = head0;
+    if (b0 > 0) {
+      head = 0;
+      if (b0 + lane < p.r.batch) {
+        w.load(p, b0 + lane);
+        if (w.blocks) head = w.before(p, w.blocks);
+      }
     }
+    const long long mine = head * p.heads_k;
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -157,9 +163,10 @@ __device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) 
       const int src = __ffs(past) - 1;
       at.b = b0 + src;
       const long long in = at.pos - ahead - __shfl_sync(0xffffffffu, upto - mine, src);
+      head = __shfl_sync(0xffffffffu, head, src);
       w.load(p, at.b);
-      at.hk = static_cast<int>(in / w.per_head);
-      const long long rem = in - at.hk * w.per_head;
+      at.hk = static_cast<int>(in / head);
+      const long long rem = in - at.hk * head;
       // the last block whose predecessors weigh at most rem: 32 tries at once
       int lo = 0, hi = w.blocks;  // it is in [lo, hi)
       while (hi - lo > 1) {
@@ -170,7 +177,7 @@ __device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) 
         hi = min(hi, lo + step);
       }
       at.block = lo;
-      at.off = rem - w.before(p, lo);
+      at.off = lo ? rem - w.before(p, lo) : rem;
       return at;
     }
     ahead += __shfl_sync(0xffffffffu, upto, 31);
@@ -229,12 +236,12 @@ struct WorkWalk {
     x.t1 = (row0 + x.rows - 1) / p.group + 1;
     visible_span(p, w.s, x.t0, x.t1, x.lo, x.hi);
     const int lo_tile = x.lo / kTile, hi_tile = (x.hi + kTile - 1) / kTile;
-    const int weight = kMany ? 1 + hi_tile - lo_tile : w.flat;
+    const int weight = kMany ? kUnitCost + hi_tile - lo_tile : w.flat;
     const int off = static_cast<int>(at.off);
     const int take = static_cast<int>(min(at.left, static_cast<long long>(weight - off)));
     x.whole = take == weight;
     x.slot = off > 0 ? 0 : 1;
-    const int base = kMany ? lo_tile - 1 : w.first;
+    const int base = kMany ? lo_tile - kUnitCost : w.first;
     x.tile0 = max(base + off, lo_tile);
     x.tile1 = min(base + off + take, hi_tile);
     x.last = -1;
@@ -279,59 +286,87 @@ __device__ __forceinline__ void store16(uint16_t* dst, const float (&o)[kN], flo
   }
 }
 
-// Adds up the units that several CTAs worked on.  Block (c, y) takes rows y * 8
-// + warp, ... of the unit that CTA c began and did not finish; its pieces are
-// CTA c's second partial result and the first ones of the CTAs after it.  A
-// warp's lanes are the D columns.
+// Adds up the units that several CTAs worked on.  Block (c, y) takes a share of
+// the rows of the unit that CTA c began and did not finish; its pieces are CTA
+// c's second partial result and the first ones of the CTAs after it.  A warp's
+// lanes are the D columns; it adds kJoinRows rows side by side, as the loads'
+// latency is all this costs.
+constexpr int kJoinRows = 4, kJoinThreads = 64;
+
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedLaunch p) {
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_join_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const JoinTask task = p.tasks[c];
-  constexpr int kN = D / 32;
-  for (int r = blockIdx.y * 8 + warp; r < task.rows; r += gridDim.y * 8) {
-    auto piece = [&](int i) { return (2LL * i + (i == c ? 1 : 0)) * p.block_rows + r; };
-    float m = -INFINITY;
-    for (int i = c + lane; i <= task.last; i += 32)
-      if (p.tasks[i].rows >= 0) m = fmaxf(m, p.part_ml[piece(i)].x);
+  constexpr int kN = D / 32, kWarps = kJoinThreads / 32;
+  const int step = gridDim.y * kWarps * kJoinRows;
+  for (int r0 = (blockIdx.y * kWarps + warp) * kJoinRows; r0 < task.rows; r0 += step) {
+    float m[kJoinRows], l[kJoinRows] = {}, o[kJoinRows][kN] = {};
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float o[kN] = {}, l = 0.f;
-#pragma unroll 4
-    for (int i = c; i <= task.last; ++i) {
-      if (p.tasks[i].rows < 0) continue;
-      const float2 ml = p.part_ml[piece(i)];
-      const float a = ex2_approx(ml.x - ref);
-      l = fmaf(ml.y, a, l);
-      const float* src = p.part_o + piece(i) * D + lane * kN;
-      float x[kN];
-      if constexpr (kN == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        x[0] = v.x; x[1] = v.y;
+    for (int q = 0; q < kJoinRows; ++q) m[q] = -INFINITY;
+    // up to 32 CTAs at a time: lane i knows whether CTA first + i had work
+    for (int first = c; first <= task.last; first += 32) {
+      uint32_t live = __ballot_sync(
+          0xffffffffu, first + lane <= task.last && p.tasks[min(first + lane, task.last)].rows >= 0);
+      while (live) {
+        const int i = first + __ffs(live) - 1;
+        live &= live - 1;
+        const long long at = (2LL * i + (i == c ? 1 : 0)) * p.block_rows + r0;
+        float2 ml[kJoinRows];
+        float x[kJoinRows][kN];
+#pragma unroll
+        for (int q = 0; q < kJoinRows; ++q) {
+          if (r0 + q >= task.rows) {
+            ml[q] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) x[q][e] = 0.f;
+            continue;
+          }
+          ml[q] = p.part_ml[at + q];
+          const float* src = p.part_o + (at + q) * D + lane * kN;
+          if constexpr (kN == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            x[q][0] = v.x; x[q][1] = v.y; x[q][2] = v.z; x[q][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            x[q][0] = v.x; x[q][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kJoinRows; ++q) {
+          const float m_new = fmaxf(m[q], ml[q].x);
+          const float ref = m_new == -INFINITY ? 0.f : m_new;
+          const float a = ex2_approx(m[q] - ref), b = ex2_approx(ml[q].x - ref);
+          m[q] = m_new;
+          l[q] = l[q] * a + ml[q].y * b;
+#pragma unroll
+          for (int e = 0; e < kN; ++e) o[q][e] = o[q][e] * a + x[q][e] * b;
+        }
       }
-#pragma unroll
-      for (int e = 0; e < kN; ++e) o[e] = fmaf(x[e], a, o[e]);
     }
-    int token, head;
-    row_of(p, task.first_row, r, task.hk, token, head);
-    const long long row = task.start + token;
-    store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head + lane * kN, o,
-                   l == 0.f ? 0.f : 1.f / l);
-    if (lane == 0)
-      p.lse[static_cast<long long>(head) * p.r.total + row] =
-          l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kPagedLn2;
+#pragma unroll
+    for (int q = 0; q < kJoinRows; ++q) {
+      if (r0 + q >= task.rows) continue;
+      int token, head;
+      row_of(p, task.first_row, r0 + q, task.hk, token, head);
+      const long long row = task.start + token;
+      store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head + lane * kN,
+                     o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
+      if (lane == 0)
+        p.lse[static_cast<long long>(head) * p.r.total + row] =
+            l[q] == 0.f ? -INFINITY : (m[q] + lg2_approx(l[q])) * kPagedLn2;
+    }
   }
 }
 
 template <int D, bool kBf16>
 cudaError_t launch_join(const PagedLaunch& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.sms), static_cast<unsigned>((a.block_rows + 31) / 32));
-  cfg.blockDim = dim3(256);
+  const int rows = kJoinThreads / 32 * kJoinRows;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.sms),
+                     static_cast<unsigned>((a.block_rows + rows - 1) / rows));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -17,21 +17,25 @@
 //   - CTAs stay resident and walk a stretch of the units laid end to end
 //     (fa_paged.cuh); a unit that a stretch's end cuts leaves its partial O,
 //     maximum and sum in fp32 for the joining kernel.
-//   - O goes straight from tensor memory to the caller's rows: a packed batch's
-//     tiles end anywhere, and a tensor-map store would run into the next
-//     sequence.
+//   - One warp works out the units ahead of the others and hands them over
+//     through a ring in shared memory: the arithmetic is long and rarely run,
+//     and in every role's path it cost some 4 us a unit, mostly fetching its
+//     instructions.
+//   - O goes from tensor memory to the caller's rows by plain stores: a packed
+//     batch's tiles end anywhere, and a tensor-map store would run into the
+//     next sequence.
 //
 // Values outside the visible span (behind the sequence's end, in pages not
 // loaded) may be anything, and 0 * NaN is NaN: a spare warp makes those rows of
 // a tile zeros before the P V product reads it.
 //
-// e4m3 caches: two spare warps convert each 8-bit tile to fp16 in shared
+// e4m3 caches: five warps convert each 8-bit tile to fp16 in shared
 // memory (exactly, relative to the largest row exponent so far, which scales
 // the scores, and O, in fp32), and bf16 queries to fp16 under a power-of-two
 // scale per row; both products then run in fp16.
 //
-// Warps (384 threads): 0-3 softmax of tile A, 4-7 of tile B, 8 producer,
-// 9 MMA issue, 10-11 zeroing or conversion.
+// Warps: 0-3 softmax of tile A, 4-7 of tile B, 8 producer, 9 MMA issue, 10 the
+// units, 11 zeroing (12 warps), or 11-15 conversion (e4m3 caches, 16 warps).
 #include "fa_paged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"
@@ -39,9 +43,16 @@
 namespace fa {
 namespace {
 
-constexpr int kManyThreads = 384;
-// registers: as in the dense forward, 2 x 208 + 80 per lane of a sub-partition
-constexpr uint32_t kManyLow = 80, kManyHigh = 208;
+// Threads, and registers per thread after the softmax warps have taken the
+// others': 12 warps launch with 168 (2 x 208 + 80 <= 3 x 168 on each
+// sub-partition), 16 with 128 (2 x 200 + 2 x 56 = 4 x 128).
+template <bool kFp8>
+struct ManyWarps {
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr uint32_t kLow = kFp8 ? 56 : 80, kHigh = kFp8 ? 200 : 208;
+  static constexpr int kConverters = (kThreads - 352);  // threads of warps 11 ..
+};
+constexpr int kUnitRing = 4;
 // references of key and value exponents, one per key tile: a softmax group is
 // never more than three tiles behind the conversion's stages (a tile pair's
 // ranges end within two tiles of each other)
@@ -61,15 +72,18 @@ struct ManySmem {
   alignas(16) uint8_t exps[kFp8 ? kSlots8 : 1][kTile];
   int8_t qshift[2][kFp8 ? 2 * kTile : 1];  // [unit & 1]: rows of q were scaled by 2^this
   int kref[kRefs], vref[kRefs];
+  int4 unit[kUnitRing][4];  // ManyUnit
+  uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
   uint64_t q_full, q_empty, q_ready;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw_full[kSlots8], raw_empty[kSlots8];
   uint64_t v_raw[2];  // 16-bit: V tiles with rows to make zeros land here first
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t drain;
-  Place place;
   uint32_t tmem_base;
   int abort_flag;
+  // 16-bit caches: O on its way out, 32 rows x 128 bytes per softmax warp
+  alignas(16) uint8_t stage[kFp8 ? 1 : 8][kFp8 ? 16 : 4096];
 };
 
 __device__ __forceinline__ bool many_warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
@@ -78,45 +92,63 @@ __device__ __forceinline__ bool many_warp_wait(uint64_t* bar, uint32_t parity, u
   return __all_sync(0xffffffffu, ok);
 }
 
-// The key tiles of a piece: of query tile t [lo_t, hi_t], none when lo_t >
-// hi_t, and the K/V stream over their union.
-struct ManyTiles {
+// A piece of work as the roles need it.  Key tiles: of query tile t [lo_t,
+// hi_t], none when lo_t > hi_t, and the K/V stream first .. last over their
+// union (first > last: nothing to multiply).
+struct ManyUnit {
   int lo0, hi0, lo1, hi1;
-  int first, last;  // of the stream; first > last: nothing to multiply
-  bool both;        // tile B has rows
-  __device__ __forceinline__ ManyTiles(const PagedLaunch& p, const Piece& x, const Seq& s) {
-    const int tokens = p.block_rows / p.group / 2;
-    range(p, x, s, x.t0, min(x.t1, x.t0 + tokens), lo0, hi0);
-    both = x.t1 > x.t0 + tokens;
-    if (both) {
-      range(p, x, s, x.t0 + tokens, x.t1, lo1, hi1);
-    } else {
-      lo1 = 1;
-      hi1 = 0;
-    }
-    first = lo0 <= hi0 ? lo0 : lo1;
-    last = max(hi0, hi1);
-    if (lo0 > hi0 && lo1 > hi1) {
-      first = 1;
-      last = 0;
-    }
-  }
-  static __device__ __forceinline__ void range(const PagedLaunch& p, const Piece& x, const Seq& s,
-                                               int t0, int t1, int& lo, int& hi) {
-    int a, b;
-    visible_span(p, s, t0, t1, a, b);
-    lo = max(a / kTile, x.tile0);
-    hi = min((b + kTile - 1) / kTile, x.tile1) - 1;
-    if (lo > hi) {
-      lo = 1;
-      hi = 0;
-    }
-  }
+  int first, last;
+  int key_lo, key_hi;  // keys that some row sees
+  int start;           // packed row of the block's first token
+  int tokens;          // of the block
+  int pos;             // position of its first token
+  int len;             // keys of the sequence
+  int b, hk;
+  int slot;            // of the partial result; -1: the piece covers its unit
+  int valid;           // 0: no more work
+
+  __device__ __forceinline__ bool two(int tile_tokens) const { return tokens > tile_tokens; }
   __device__ __forceinline__ int count(int t) const {
     return t ? max(0, hi1 - lo1 + 1) : max(0, hi0 - lo0 + 1);
   }
   __device__ __forceinline__ int streamed() const { return max(0, last - first + 1); }
+  // key tile j has rows that no query sees
+  __device__ __forceinline__ bool ragged(int j) const {
+    return j * kTile < key_lo || (j + 1) * kTile > key_hi;
+  }
 };
+static_assert(sizeof(ManyUnit) == 64, "four 16-byte words");
+
+__device__ __forceinline__ void many_range(const PagedLaunch& p, const Piece& x, const Seq& s,
+                                           int t0, int t1, int& lo, int& hi) {
+  int a, b;
+  visible_span(p, s, t0, t1, a, b);
+  lo = max(a / kTile, x.tile0);
+  hi = min((b + kTile - 1) / kTile, x.tile1) - 1;
+  if (t0 >= t1 || lo > hi) {
+    lo = 1;
+    hi = 0;
+  }
+}
+
+// The next entry of the ring, for a whole warp.  False on a timeout; valid is
+// 0 in the last entry.
+template <class Smem>
+__device__ __forceinline__ bool take_unit(Smem& s, uint32_t n, ManyUnit& u, uint32_t* err,
+                                          volatile int* abort_flag) {
+  const int slot = n % kUnitRing;
+  const bool ok = __all_sync(
+      0xffffffffu, mbar_wait(&s.unit_full[slot], (n / kUnitRing) & 1, err, abort_flag));
+  if (!ok) return false;
+  int4 w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = s.unit[slot][i];
+  u = ManyUnit{w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w,
+               w[2].x, w[2].y, w[2].z, w[2].w, w[3].x, w[3].y, w[3].z, w[3].w};
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&s.unit_empty[slot]);
+  return u.valid != 0;
+}
 
 // 2^(n - 127) for an exponent field n, 0 below the normal range.
 __device__ __forceinline__ float many_exp2_field(int n) {
@@ -130,7 +162,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 
 template <int D, bool kFp8, bool kBf16, bool kAlibi>
-__global__ void __launch_bounds__(kManyThreads, 1)
+__global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
     paged_many_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
   using Smem = ManySmem<D, kFp8>;
@@ -146,21 +178,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                                      ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile_tokens = p.block_rows / p.group / 2, tile_rows = tile_tokens * p.group;
-  if (warp == 0) {
-    const Place at = warp_place<true>(p, gridDim.x, blockIdx.x);
-    if (lane == 0) {
-      s.place = at;
-      if (at.left == 0) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
-    }
-  }
-  if (tid == 32) {
+  constexpr int kConverters = ManyWarps<kFp8>::kConverters;
+  if (tid == 0) {
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 1);
-    mbar_init(&s.q_ready, 64);
+    mbar_init(&s.q_ready, kConverters);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.k_full[i], kFp8 ? 64 : 1);
+      mbar_init(&s.k_full[i], kFp8 ? kConverters : 1);
       mbar_init(&s.k_empty[i], 1);
-      mbar_init(&s.v_full[i], kFp8 ? 64 : 1);
+      mbar_init(&s.v_full[i], kFp8 ? kConverters : 1);
       mbar_init(&s.v_empty[i], 1);
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 128);
@@ -169,7 +195,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
     for (int i = 0; i < Smem::kSlots8; ++i) {
       mbar_init(&s.raw_full[i], 1);
-      mbar_init(&s.raw_empty[i], 64);
+      mbar_init(&s.raw_empty[i], kConverters);
+    }
+    for (int i = 0; i < kUnitRing; ++i) {
+      mbar_init(&s.unit_full[i], 1);
+      mbar_init(&s.unit_empty[i], 10 + kConverters / 32);  // warps that read it
     }
     mbar_init(&s.drain, 1);
     s.abort_flag = 0;
@@ -184,13 +214,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   tc_fence_after();
   const uint32_t tbase = s.tmem_base;
   volatile int* abort_flag = &s.abort_flag;
-  WorkWalk<true> walk(s.place);
-  Piece x{};
-  // a tile of the piece with rows outside the visible span
-  auto ragged = [&](int j) { return j * kTile < x.lo || (j + 1) * kTile > x.hi; };
+  ManyUnit u;
+  uint32_t taken = 0;  // entries of the unit ring
 
   if (warp >= 8) {
-    setmaxnreg_dec<kManyLow>();
+    setmaxnreg_dec<ManyWarps<kFp8>::kLow>();
     if (warp == 8) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
@@ -205,31 +233,30 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       uint32_t cut = 0;              // bit st: parity of V stage st's next ragged tile
       uint32_t to_raw = 0;           // bit st: V stage st's last load was one
       bool stop = false;
-      while (!stop && walk.next(p, x)) {
-        const ManyTiles tl(p, x, walk.w.s);
-        if (tl.first > tl.last) continue;
-        const int* table = p.r.table + x.b * p.r.table_stride;
+      while (!stop && take_unit(s, taken++, u, p.err, abort_flag)) {
+        if (u.first > u.last) continue;
+        const int* table = p.r.table + u.b * p.r.table_stride;
         auto page_of = [&](int tile) {
           const int k0 = tile * kTile + lane * box_rows;
           const bool wanted =
-              lane < per_tile && tile <= tl.last && k0 < x.hi && k0 + box_rows > x.lo;
+              lane < per_tile && tile <= u.last && k0 < u.key_hi && k0 + box_rows > u.key_lo;
           return wanted ? table[k0 >> p.page_log2] : -2;
         };
-        int page = page_of(tl.first);
+        int page = page_of(u.first);
         // Q once the last S product of the unit before has read it
         if (units > 0 && !many_warp_wait(&s.q_empty, (units - 1) & 1, p.err, abort_flag)) break;
         if (lane == 0) {
-          const int n_q = tl.both ? 2 : 1;
+          const int n_q = u.two(tile_tokens) ? 2 : 1;
           mbar_arrive_expect_tx(&s.q_full, n_q * tile_rows * 2 * D);
           for (int t = 0; t < n_q; ++t)
             for (int kb = 0; kb < Smem::kBlocks; ++kb)
               tma_load_4d(s.q[t] + kb * Smem::kBlockBytes, &p.map_q, &s.q_full, kb * 64,
-                          x.hk * p.group, walk.w.s.start + x.t0 + t * tile_tokens, 0);
+                          u.hk * p.group, u.start + t * tile_tokens, 0);
         }
         ++units;
-        for (int j = tl.first; j <= tl.last; ++j, ++ring) {
+        for (int j = u.first; j <= u.last; ++j, ++ring) {
           const int k0 = j * kTile + lane * box_rows;
-          const bool mine = lane < per_tile && k0 < x.hi && k0 + box_rows > x.lo;
+          const bool mine = lane < per_tile && k0 < u.key_hi && k0 + box_rows > u.key_lo;
           const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
           const int next_page = page_of(j + 1);
           if (mine && (page < 0 || page >= p.pages)) {
@@ -253,7 +280,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               use = ring >> 1;
               full = kv ? &s.v_full[st] : &s.k_full[st];
               if (kv) to_raw &= ~(1u << st);
-              if (kv && ragged(j)) {
+              if (kv && u.ragged(j)) {
                 full = &s.v_raw[st];
                 cut ^= 1u << st;
                 to_raw |= 1u << st;
@@ -273,11 +300,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
               for (int kb = 0; kb < (kRowBytes + 127) / 128; ++kb)
                 tma_load_4d(dst + kb * Smem::kBlockBytes, kv ? &p.map_v : &p.map_k, full, kb * 64,
-                            row, x.hk, page);
+                            row, u.hk, page);
               if constexpr (kFp8) {
                 const uint8_t* e = (kv ? p.v_exp : p.k_exp) +
                                    (static_cast<long long>(page < p.pages ? page : 0) * p.heads_k +
-                                    x.hk) * p.page_size + row;
+                                    u.hk) * p.page_size + row;
                 bulk_load(s.exps[loads % Smem::kSlots8] + lane * box_rows, e, box_rows, full);
               }
             }
@@ -323,10 +350,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       uint32_t units = 0, ring = 0;
       int base0 = 0, base1 = 0;  // P V products of tiles A, B in earlier units
       bool ok = true;
-      while (ok && walk.next(p, x)) {
-        const ManyTiles tl(p, x, walk.w.s);
-        if (tl.first > tl.last) continue;
-        int s_left = tl.count(0) + tl.count(1);
+      while (ok && take_unit(s, taken++, u, p.err, abort_flag)) {
+        if (u.first > u.last) continue;
+        int s_left = u.count(0) + u.count(1);
         auto issue_s = [&](int t, int kst) {
           const uint64_t dq = desc_add(dq0, t * Smem::kTileBytes);
           const uint64_t dk = desc_add(dk0, kst * Smem::kTileBytes);
@@ -349,17 +375,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         ++units;
         if (!ok) break;
         tc_fence_after();
-        if (tl.first >= tl.lo0 && tl.first <= tl.hi0) issue_s(0, ring & 1);
-        if (tl.first >= tl.lo1 && tl.first <= tl.hi1) issue_s(1, ring & 1);
+        if (u.first >= u.lo0 && u.first <= u.hi0) issue_s(0, ring & 1);
+        if (u.first >= u.lo1 && u.first <= u.hi1) issue_s(1, ring & 1);
         commit(&s.k_empty[ring & 1]);
-        for (int j = tl.first; ok && j <= tl.last; ++j) {
-          const uint32_t g = ring + static_cast<uint32_t>(j - tl.first);
+        for (int j = u.first; ok && j <= u.last; ++j) {
+          const uint32_t g = ring + static_cast<uint32_t>(j - u.first);
           const int st = g & 1;
           ok = mbar_wait_poll(&s.v_full[st], (g >> 1) & 1, p.err, abort_flag);
           if (!ok) break;
           bool k_next = false;  // K_{j+1} has landed
           for (int t = 0; ok && t < 2; ++t) {
-            const int lt = t ? tl.lo1 : tl.lo0, ht = t ? tl.hi1 : tl.hi0;
+            const int lt = t ? u.lo1 : u.lo0, ht = t ? u.hi1 : u.hi0;
             const bool active = j >= lt && j <= ht;
             // S_t(j + 1) is next: after P V of tile j, or as the first product
             // of a tile whose range starts there
@@ -390,36 +416,80 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           commit(&s.v_empty[st]);
           if (k_next) commit(&s.k_empty[(g + 1) & 1]);
         }
-        ring += static_cast<uint32_t>(tl.streamed());
-        base0 += tl.count(0);
-        base1 += tl.count(1);
+        ring += static_cast<uint32_t>(u.streamed());
+        base0 += u.count(0);
+        base1 += u.count(1);
       }
       // Every product issued above completes before TMEM is released.
       commit(&s.drain);
       int zero = 0;
       mbar_wait(&s.drain, 0, p.err, &zero, 100000000ull);
-    } else if (kFp8 || warp == 10) {
-      // ------------------------- zeroing (one warp), or conversion (two warps)
-      const int w64 = tid - 320;  // 0 .. 63
+    } else if (warp == 10) {
+      // -------------------------------------------------------------- units
+      const Place at = warp_place<true>(p, gridDim.x, blockIdx.x);
+      if (lane == 0 && at.left == 0) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
+      WorkWalk<true> walk(at);
+      Piece x;
+      for (uint32_t n = 0;; ++n) {
+        const bool more = walk.next(p, x);
+        ManyUnit v{};
+        if (more) {
+          const Seq& q = walk.w.s;
+          many_range(p, x, q, x.t0, min(x.t1, x.t0 + tile_tokens), v.lo0, v.hi0);
+          many_range(p, x, q, x.t0 + tile_tokens, x.t1, v.lo1, v.hi1);
+          v.first = v.lo0 <= v.hi0 ? v.lo0 : v.lo1;
+          v.last = max(v.hi0, v.hi1);
+          if (v.lo0 > v.hi0 && v.lo1 > v.hi1) {
+            v.first = 1;
+            v.last = 0;
+          }
+          v.key_lo = x.lo;
+          v.key_hi = x.hi;
+          v.start = q.start + x.t0;
+          v.tokens = x.t1 - x.t0;
+          v.pos = q.pos0 + x.t0;
+          v.len = q.len;
+          v.b = x.b;
+          v.hk = x.hk;
+          v.slot = x.whole ? -1 : x.slot;
+          v.valid = 1;
+          if (lane == 0) p.tasks[blockIdx.x] = join_task(p, x, q);
+        }
+        const int slot = n % kUnitRing;
+        if (n >= kUnitRing && !many_warp_wait(&s.unit_empty[slot], (n / kUnitRing - 1) & 1, p.err,
+                                              abort_flag))
+          break;
+        if (lane == 0) {
+          s.unit[slot][0] = make_int4(v.lo0, v.hi0, v.lo1, v.hi1);
+          s.unit[slot][1] = make_int4(v.first, v.last, v.key_lo, v.key_hi);
+          s.unit[slot][2] = make_int4(v.start, v.tokens, v.pos, v.len);
+          s.unit[slot][3] = make_int4(v.b, v.hk, v.slot, v.valid);
+          mbar_arrive(&s.unit_full[slot]);
+        }
+        __syncwarp();
+        if (!more) break;
+      }
+    } else {
+      // ---------------------- zeroing (warp 11), or conversion (warps 11-15)
+      [[maybe_unused]] const int cv = tid - 352;  // 0 .. kConverters - 1
       uint32_t ring = 0, units = 0, n8 = 0;
       uint32_t fixed = 0;  // bit st: parity of V stage st's next ragged tile
       bool ok = true;
-      while (ok && walk.next(p, x)) {
-        const ManyTiles tl(p, x, walk.w.s);
-        if (tl.first > tl.last) continue;
+      while (ok && take_unit(s, taken++, u, p.err, abort_flag)) {
+        if (u.first > u.last) continue;
         if constexpr (!kFp8) {
-          for (int j = tl.first; ok && j <= tl.last; ++j, ++ring) {
-            if (!ragged(j)) continue;
+          for (int j = u.first; ok && j <= u.last; ++j, ++ring) {
+            if (!u.ragged(j)) continue;
             const int st = ring & 1;
-            // (a barrier of their own: these warps skip the other tiles, whose
-            // phases they would lose count of)
+            // (a barrier of its own: this warp skips the other tiles, whose phases
+            // it would lose count of)
             ok = many_warp_wait(&s.v_raw[st], (fixed >> st) & 1, p.err, abort_flag);
             if (!ok) break;
             fixed ^= 1u << st;
             for (int i = lane; i < kTile * (2 * D / 16); i += 32) {
               const int r = i & (kTile - 1), c = i >> 7;  // 16-byte chunk c of row r
               const int key = j * kTile + r;
-              if (key < x.lo || key >= x.hi)
+              if (key < u.key_lo || key >= u.key_hi)
                 *reinterpret_cast<uint4*>(s.v[st] + (c >> 3) * Smem::kBlockBytes + r * 128 +
                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
@@ -433,7 +503,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             // magnitude into [2^14, 2^15)
             ok = many_warp_wait(&s.q_full, units & 1, p.err, abort_flag);
             if (!ok) break;
-            for (int i = w64; i < 2 * kTile; i += 64) {
+            for (int i = cv; i < 2 * kTile; i += kConverters) {
               uint8_t* row = s.q[i >> 7] + (i & 127) * 128;
               float top = 0.f;
 #pragma unroll 4
@@ -471,9 +541,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
           ++units;
           int ref[2] = {0, 0};  // largest key, value exponent of the piece so far
-          for (int j = tl.first; ok && j <= tl.last; ++j, ++ring) {
+          for (int j = u.first; ok && j <= u.last; ++j, ++ring) {
             const int st = ring & 1;
-            const bool cut = ragged(j);
+            const bool cut = u.ragged(j);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, ++n8) {
               const int slot = n8 % Smem::kSlots8;
@@ -487,16 +557,16 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int r = lane * 4 + i, key = j * kTile + r;
-                if (key >= x.lo && key < x.hi) top = max(top, static_cast<int>(s.exps[slot][r]));
+                if (key >= u.key_lo && key < u.key_hi) top = max(top, static_cast<int>(s.exps[slot][r]));
               }
 #pragma unroll
               for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
               ref[kv] = max(ref[kv], top);
-              if (w64 == 0) (kv ? s.vref : s.kref)[ring % kRefs] = ref[kv];
+              if (cv == 0) (kv ? s.vref : s.kref)[ring % kRefs] = ref[kv];
               uint8_t* to = kv ? s.v[st] : s.k[st];
               constexpr int kChunks = D / 16;  // 16 codes each
 #pragma unroll 4
-              for (int i = w64; i < kTile * kChunks; i += 64) {
+              for (int i = cv; i < kTile * kChunks; i += kConverters) {
                 const int r = i / kChunks, c = i % kChunks, key = j * kTile + r;
                 const int e = s.exps[slot][r];
                 const uint8_t* from =
@@ -505,7 +575,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                 const uint4 v = *reinterpret_cast<const uint4*>(from);
                 // 2^(e - ref + 7): codes stay below 448 * 128
                 const float f = many_exp2_field(127 + e - ref[kv] + 7);
-                const bool none = e == 0 || (cut && (key < x.lo || key >= x.hi));
+                const bool none = e == 0 || (cut && (key < u.key_lo || key >= u.key_hi));
                 const uint32_t f2 = pack2<false>(f, f);
                 const uint32_t u[4] = {v.x, v.y, v.z, v.w};
                 uint32_t h[8];
@@ -533,7 +603,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
     }
   } else {
-    setmaxnreg_inc<kManyHigh>();
+    setmaxnreg_inc<ManyWarps<kFp8>::kHigh>();
     // -------------------------------------------------------------- softmax
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -542,30 +612,27 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     int base = 0;  // key tiles of this query tile in earlier units
     uint32_t ring = 0, units = 0;
     bool ok = true;
-    while (ok && walk.next(p, x)) {
-      const Seq& seq = walk.w.s;
-      if (tid == 0) p.tasks[blockIdx.x] = join_task(p, x, seq);
-      const ManyTiles tl(p, x, seq);
-      const int lt = t ? tl.lo1 : tl.lo0, n_tiles = tl.count(t);
-      const int token = x.t0 + t * tile_tokens + row_token;  // of the sequence
-      const bool mine = r < tile_rows && token < x.t1;       // a row to write
+    while (ok && take_unit(s, taken++, u, p.err, abort_flag)) {
+      const int lt = t ? u.lo1 : u.lo0, n_tiles = u.count(t);
+      const int token = t * tile_tokens + row_token;    // of the block
+      const bool mine = r < tile_rows && token < u.tokens;  // a row to write
       // rows that are none see what the tile's last token sees
-      const int first_token = x.t0 + t * tile_tokens;
-      const int last_token = min(x.t1, first_token + tile_tokens) - 1;
-      const int pos = seq.pos0 + min(token, last_token);
-      const int head = x.hk * p.group + row_head;
-      const float nslope2 = kAlibi && mine ? paged_slope2(p, x.b, head) : 0.f;
+      const int first_token = t * tile_tokens;
+      const int last_token = min(u.tokens, first_token + tile_tokens) - 1;
+      const int pos = u.pos + min(token, last_token);
+      const int head = u.hk * p.group + row_head;
+      const float nslope2 = kAlibi && mine ? paged_slope2(p, u.b, head) : 0.f;
       // visible keys: of this row, and those that every row of the tile sees
       const int first = p.win_left < 0 ? 0 : pos - p.win_left;
-      const int last = p.win_right < 0 ? seq.len - 1 : min(seq.len - 1, pos + p.win_right);
-      const int pos_a = seq.pos0 + first_token, pos_b = seq.pos0 + last_token;
+      const int last = p.win_right < 0 ? u.len - 1 : min(u.len - 1, pos + p.win_right);
+      const int pos_a = u.pos + first_token, pos_b = u.pos + last_token;
       const int all_first = p.win_left < 0 ? 0 : pos_b - p.win_left;
-      const int all_last = p.win_right < 0 ? seq.len - 1 : min(seq.len - 1, pos_a + p.win_right);
+      const int all_last = p.win_right < 0 ? u.len - 1 : min(u.len - 1, pos_a + p.win_right);
       // some row of the tile sees at most 128 keys (the count is concave in the
       // row, so an end row has the fewest): see lo below
       const bool few_keys = [&] {
         auto count = [&](int q) {
-          return min(seq.len - 1, p.win_right < 0 ? seq.len - 1 : q + p.win_right) -
+          return min(u.len - 1, p.win_right < 0 ? u.len - 1 : q + p.win_right) -
                  max(0, p.win_left < 0 ? 0 : q - p.win_left) + 1;
         };
         return min(count(pos_a), count(pos_b)) <= kTile;
@@ -583,7 +650,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         ok = many_warp_wait(&s.s_full[t], (base + jj) & 1, p.err, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t g = ring + static_cast<uint32_t>(j - tl.first);
+        const uint32_t g = ring + static_cast<uint32_t>(j - u.first);
         float mult = sl2;   // scores -> log2 units
         int vshift = 0;     // e4m3: this tile's value exponent over vbase
         bool rebase = false;
@@ -729,60 +796,97 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      if (t == 0 || tl.both) {
+      if (t == 0 || u.two(tile_tokens)) {
         // O in tensor memory is 2^kPOffset (e4m3: and 2^(127 + 7 - vbase)) times
         // the sum of weights times values
         const float back = many_exp2_field((kFp8 ? vbase - 7 : 127) - kPOffset);
         const float per = lo == 0.f ? 0.f : back / lo;
-        const long long at = (2LL * blockIdx.x + x.slot) * p.block_rows + t * tile_rows + r;
-        const long long row = seq.start + token;
-        uint16_t* out = static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head;
+        const bool whole = u.slot < 0;
         // partial results are divided by their sum as rounded and multiplied by
         // the exact one, which is what they are joined with
-        const float scale = x.whole ? per : per * l;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (have) {
-            tmem_ld32(tO + lane_off + c * 32, o);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
-          }
-          if (!mine) continue;
-          if (x.whole) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                pk[e] = pack2<kBf16>(__uint_as_float(o[8 * q + 2 * e]) * scale,
-                                     __uint_as_float(o[8 * q + 2 * e + 1]) * scale);
-              *reinterpret_cast<uint4*>(out + c * 32 + q * 8) =
-                  make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
-          } else {
-            float* dst = p.part_o + at * D + c * 32;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4*>(dst + q * 4) =
-                  make_float4(__uint_as_float(o[4 * q]) * scale,
-                              __uint_as_float(o[4 * q + 1]) * scale,
-                              __uint_as_float(o[4 * q + 2]) * scale,
-                              __uint_as_float(o[4 * q + 3]) * scale);
-          }
-        }
+        const float scale = whole ? per : per * l;
+        const long long at =
+            (2LL * blockIdx.x + max(u.slot, 0)) * p.block_rows + t * tile_rows + r;
+        const long long row = u.start + token;
         if (mine) {
-          if (x.whole)
+          if (whole)
             p.lse[static_cast<long long>(head) * p.r.total + row] =
                 l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kPagedLn2;
           else
             p.part_ml[at] = make_float2(m, l);
         }
+        // this row's 128-byte pieces in the output: D / 64 of 16-bit elements,
+        // D / 32 of fp32
+        uint8_t* out = whole ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) +
+                                                          row * p.o_token + head * p.o_head)
+                             : reinterpret_cast<uint8_t*>(p.part_o + at * D);
+        if (!mine) out = nullptr;
+        const int cols = whole ? 64 : 32;  // columns of a piece
+#pragma unroll 1
+        for (int c = 0; c < D; c += cols) {
+          uint4 w[8];
+          auto take = [&](int col, auto&& put) {
+            uint32_t o[32];
+            if (have) {
+              tmem_ld32(tO + lane_off + col, o);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+            put(o);
+          };
+          if (whole) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              take(c + h * 32, [&](const uint32_t(&o)[32]) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t pk[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    pk[e] = pack2<kBf16>(__uint_as_float(o[8 * q + 2 * e]) * scale,
+                                         __uint_as_float(o[8 * q + 2 * e + 1]) * scale);
+                  w[h * 4 + q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+              });
+          } else {
+            take(c, [&](const uint32_t(&o)[32]) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                w[q] = make_uint4(__float_as_uint(__uint_as_float(o[4 * q]) * scale),
+                                  __float_as_uint(__uint_as_float(o[4 * q + 1]) * scale),
+                                  __float_as_uint(__uint_as_float(o[4 * q + 2]) * scale),
+                                  __float_as_uint(__uint_as_float(o[4 * q + 3]) * scale));
+            });
+          }
+          if constexpr (kFp8) {
+            if (mine)
+#pragma unroll
+              for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(out + q * 16) = w[q];
+          } else {
+            // through shared memory, so that eight lanes write a row's 128 bytes
+            uint8_t* mine_at = s.stage[warp] + lane * 128;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4*>(mine_at + ((q ^ (lane & 7)) << 4)) = w[q];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = i * 4 + (lane >> 3), q = lane & 7;
+              uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(
+                  0xffffffffu, reinterpret_cast<unsigned long long>(out), rr));
+              const uint4 v =
+                  *reinterpret_cast<const uint4*>(s.stage[warp] + rr * 128 + ((q ^ (rr & 7)) << 4));
+              if (dst) *reinterpret_cast<uint4*>(dst + q * 16) = v;
+            }
+            __syncwarp();
+          }
+          if (mine) out += 128;
+        }
       }
-      if (tl.first <= tl.last) ++units;
-      ring += static_cast<uint32_t>(tl.streamed());
+      if (u.first <= u.last) ++units;
+      ring += static_cast<uint32_t>(u.streamed());
       base += n_tiles;
     }
   }
@@ -803,7 +907,7 @@ cudaError_t launch_many_t(const PagedLaunch& a, cudaStream_t s) {
   static AttrCache configured;
   cudaError_t e = ensure_dynamic_smem(kern, smem, configured);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, static_cast<unsigned>(a.sms), kManyThreads, smem, s, a);
+  e = launch_pdl(kern, static_cast<unsigned>(a.sms), ManyWarps<kFp8>::kThreads, smem, s, a);
   if (e != cudaSuccess) return e;
   return launch_join<D, kBf16>(a, s);
 }
