@@ -63,23 +63,31 @@ struct ManySmem {
   static constexpr int kBlocks = D / 64;               // 64-column blocks of a 16-bit tile
   static constexpr int kBlockBytes = kTile * 128;
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
-  static constexpr int kTile8 = kTile * D;             // an e4m3 tile
-  static constexpr int kSlots8 = D == 64 ? 4 : 2;      // K and V tiles alternate
+  // K and V tiles alternate through one ring: tile g's K is number 2 g, its V
+  // 2 g + 1
+  static constexpr int kStages = kFp8 ? (D == 128 ? 5 : 6) : (D == 128 ? 4 : 8);
+  // e4m3, D = 128: a raw tile lands in the upper half of its stage, where each
+  // of its rows lies under the upper half of its own converted row
+  static constexpr bool kInPlace = D == 128;
+  static constexpr int kRawBytes = kTile * D;
   alignas(1024) uint8_t q[2][kTileBytes];
-  alignas(1024) uint8_t k[2][kTileBytes];
-  alignas(1024) uint8_t v[2][kTileBytes];
-  alignas(1024) uint8_t raw[kFp8 ? kSlots8 : 1][kFp8 ? kTile8 : 16];
-  alignas(16) uint8_t exps[kFp8 ? kSlots8 : 1][kTile];
+  alignas(1024) uint8_t kv[kStages][kTileBytes];
+  alignas(1024) uint8_t raw_tiles[kFp8 && !kInPlace ? kStages : 1][kFp8 && !kInPlace ? kRawBytes : 16];
+  alignas(16) uint8_t exps[kFp8 ? kStages : 1][kTile];
   int8_t qshift[2][kFp8 ? 2 * kTile : 1];  // [unit & 1]: rows of q were scaled by 2^this
   int kref[kRefs], vref[kRefs];
   int4 unit[kUnitRing][4];  // ManyUnit
   uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
   uint64_t q_full, q_empty, q_ready;
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t raw_full[kSlots8], raw_empty[kSlots8];
-  uint64_t v_raw[2];  // 16-bit: V tiles with rows to make zeros land here first
+  uint64_t full[kStages], empty[kStages];
+  // tiles that need work before the tensor cores may read them land here first:
+  // e4m3 ones, and V tiles with rows to make zeros
+  uint64_t raw_full[kStages];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t drain;
+  __device__ __forceinline__ uint8_t* raw(int st) {
+    return kInPlace ? kv[st] + kRawBytes : raw_tiles[kInPlace ? 0 : st];
+  }
   uint32_t tmem_base;
   int abort_flag;
   // 16-bit caches: O on its way out, 32 rows x 128 bytes per softmax warp
@@ -178,24 +186,20 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                                      ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile_tokens = p.block_rows / p.group / 2, tile_rows = tile_tokens * p.group;
-  constexpr int kConverters = ManyWarps<kFp8>::kConverters;
+  constexpr int kConverters = ManyWarps<kFp8>::kConverters, kStages = Smem::kStages;
   if (tid == 0) {
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 1);
     mbar_init(&s.q_ready, kConverters);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.k_full[i], kFp8 ? kConverters : 1);
-      mbar_init(&s.k_empty[i], 1);
-      mbar_init(&s.v_full[i], kFp8 ? kConverters : 1);
-      mbar_init(&s.v_empty[i], 1);
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 128);
       mbar_init(&s.o_done[i], 1);
-      mbar_init(&s.v_raw[i], 1);
     }
-    for (int i = 0; i < Smem::kSlots8; ++i) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], kFp8 ? kConverters : 1);
+      mbar_init(&s.empty[i], 1);
       mbar_init(&s.raw_full[i], 1);
-      mbar_init(&s.raw_empty[i], kConverters);
     }
     for (int i = 0; i < kUnitRing; ++i) {
       mbar_init(&s.unit_full[i], 1);
@@ -228,10 +232,10 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
       }
       constexpr int kRowBytes = kFp8 ? D : 2 * D;
       const int box_rows = min(p.page_size, kTile), per_tile = kTile / box_rows;
-      uint32_t units = 0, ring = 0;  // Q loads, key tiles streamed
-      uint32_t loads = 0;            // K and V tiles issued
-      uint32_t cut = 0;              // bit st: parity of V stage st's next ragged tile
-      uint32_t to_raw = 0;           // bit st: V stage st's last load was one
+      uint32_t units = 0;   // Q loads
+      uint32_t n = 0;       // K and V tiles loaded
+      uint32_t cut = 0;     // 16-bit, bit st: parity of the next tile in raw_full[st]
+      uint32_t to_raw = 0;  // bit st: stage st's last load was one
       bool stop = false;
       while (!stop && take_unit(s, taken++, u, p.err, abort_flag)) {
         if (u.first > u.last) continue;
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                           u.hk * p.group, u.start + t * tile_tokens, 0);
         }
         ++units;
-        for (int j = u.first; j <= u.last; ++j, ++ring) {
+        for (int j = u.first; j <= u.last; ++j) {
           const int k0 = j * kTile + lane * box_rows;
           const bool mine = lane < per_tile && k0 < u.key_hi && k0 + box_rows > u.key_lo;
           const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
@@ -266,29 +270,18 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           const int row = k0 & (p.page_size - 1);
 #pragma unroll
           for (int kv = 0; kv < 2 && !stop; ++kv) {
-            uint64_t *full, *empty;
-            uint8_t* dst;
-            uint32_t use;
-            if constexpr (kFp8) {
-              const int slot = loads % Smem::kSlots8;
-              use = loads / Smem::kSlots8;
-              full = &s.raw_full[slot];
-              empty = &s.raw_empty[slot];
-              dst = s.raw[slot];
-            } else {
-              const int st = ring & 1;
-              use = ring >> 1;
-              full = kv ? &s.v_full[st] : &s.k_full[st];
-              if (kv) to_raw &= ~(1u << st);
+            const int st = n % kStages;
+            uint64_t* full = kFp8 ? &s.raw_full[st] : &s.full[st];
+            if constexpr (!kFp8) {
+              to_raw &= ~(1u << st);
               if (kv && u.ragged(j)) {
-                full = &s.v_raw[st];
+                full = &s.raw_full[st];
                 cut ^= 1u << st;
                 to_raw |= 1u << st;
               }
-              empty = kv ? &s.v_empty[st] : &s.k_empty[st];
-              dst = kv ? s.v[st] : s.k[st];
             }
-            if (use > 0 && !many_warp_wait(empty, (use - 1) & 1, p.err, abort_flag)) {
+            if (n >= kStages &&
+                !many_warp_wait(&s.empty[st], (n / kStages - 1) & 1, p.err, abort_flag)) {
               stop = true;
               break;
             }
@@ -296,7 +289,8 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
               mbar_arrive_expect_tx(full, boxes * box_rows * (kRowBytes + (kFp8 ? 1 : 0)));
             __syncwarp();
             if (mine) {
-              dst += lane * box_rows * (kRowBytes < 128 ? kRowBytes : 128);
+              uint8_t* dst = (kFp8 ? s.raw(st) : s.kv[st]) +
+                             lane * box_rows * (kRowBytes < 128 ? kRowBytes : 128);
 #pragma unroll
               for (int kb = 0; kb < (kRowBytes + 127) / 128; ++kb)
                 tma_load_4d(dst + kb * Smem::kBlockBytes, kv ? &p.map_v : &p.map_k, full, kb * 64,
@@ -305,10 +299,10 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                 const uint8_t* e = (kv ? p.v_exp : p.k_exp) +
                                    (static_cast<long long>(page < p.pages ? page : 0) * p.heads_k +
                                     u.hk) * p.page_size + row;
-                bulk_load(s.exps[loads % Smem::kSlots8] + lane * box_rows, e, box_rows, full);
+                bulk_load(s.exps[st] + lane * box_rows, e, box_rows, full);
               }
             }
-            ++loads;
+            ++n;
           }
           if (stop) break;
           page = next_page;
@@ -318,19 +312,12 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
         // Copies already in flight land before the CTA's shared memory goes away.
         int zero = 0;
         if (units > 0) mbar_wait(&s.q_full, (units - 1) & 1, p.err, &zero, 100000000ull);
-        if constexpr (kFp8) {
-          for (uint32_t i = loads > Smem::kSlots8 ? loads - Smem::kSlots8 : 0; i < loads; ++i)
-            mbar_wait(&s.raw_full[i % Smem::kSlots8], (i / Smem::kSlots8) & 1, p.err, &zero,
-                      100000000ull);
-        } else {
-          for (uint32_t i = loads > 4 ? loads - 4 : 0; i < loads; ++i) {
-            const uint32_t n = i >> 1, st = n & 1;
-            if ((i & 1) && ((to_raw >> st) & 1))
-              mbar_wait(&s.v_raw[st], ((cut >> st) & 1) ^ 1, p.err, &zero, 100000000ull);
-            else
-              mbar_wait((i & 1) ? &s.v_full[st] : &s.k_full[st], (n >> 1) & 1, p.err, &zero,
-                        100000000ull);
-          }
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) {
+          const int st = i % kStages;
+          const bool cut_tile = !kFp8 && ((to_raw >> st) & 1);
+          mbar_wait(kFp8 || cut_tile ? &s.raw_full[st] : &s.full[st],
+                    cut_tile ? ((cut >> st) & 1) ^ 1 : (i / kStages) & 1, p.err, &zero,
+                    100000000ull);
         }
       }
       __syncwarp();
@@ -345,17 +332,17 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
       constexpr uint32_t idS = idesc_f16(128, 128, ab, 0, 0);
       constexpr uint32_t idPV = idesc_f16(128, D, ab, 0, 1);
       const uint64_t dq0 = smem_desc_sw128(smem_u32(s.q[0]), 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(smem_u32(s.k[0]), 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(smem_u32(s.v[0]), Smem::kBlockBytes, 1024);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(s.kv[0]), 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(s.kv[0]), Smem::kBlockBytes, 1024);
       uint32_t units = 0, ring = 0;
       int base0 = 0, base1 = 0;  // P V products of tiles A, B in earlier units
       bool ok = true;
       while (ok && take_unit(s, taken++, u, p.err, abort_flag)) {
         if (u.first > u.last) continue;
         int s_left = u.count(0) + u.count(1);
-        auto issue_s = [&](int t, int kst) {
+        auto issue_s = [&](int t, uint32_t g) {  // K of streamed tile g
           const uint64_t dq = desc_add(dq0, t * Smem::kTileBytes);
-          const uint64_t dk = desc_add(dk0, kst * Smem::kTileBytes);
+          const uint64_t dk = desc_add(dk0, (2 * g) % kStages * Smem::kTileBytes);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * Smem::kBlockBytes + (kk & 3) * 32;
@@ -367,7 +354,8 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           if (--s_left == 0) commit(&s.q_empty);  // the next unit's Q may come
         };
         auto k_wait = [&](uint32_t g) {
-          return mbar_wait_poll(&s.k_full[g & 1], (g >> 1) & 1, p.err, abort_flag);
+          return mbar_wait_poll(&s.full[(2 * g) % kStages], (2 * g) / kStages & 1, p.err,
+                                abort_flag);
         };
         ok = mbar_wait_poll(kFp8 && kBf16 ? &s.q_ready : &s.q_full, units & 1, p.err,
                             abort_flag) &&
@@ -375,13 +363,13 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
         ++units;
         if (!ok) break;
         tc_fence_after();
-        if (u.first >= u.lo0 && u.first <= u.hi0) issue_s(0, ring & 1);
-        if (u.first >= u.lo1 && u.first <= u.hi1) issue_s(1, ring & 1);
-        commit(&s.k_empty[ring & 1]);
+        if (u.first >= u.lo0 && u.first <= u.hi0) issue_s(0, ring);
+        if (u.first >= u.lo1 && u.first <= u.hi1) issue_s(1, ring);
+        commit(&s.empty[(2 * ring) % kStages]);
         for (int j = u.first; ok && j <= u.last; ++j) {
           const uint32_t g = ring + static_cast<uint32_t>(j - u.first);
-          const int st = g & 1;
-          ok = mbar_wait_poll(&s.v_full[st], (g >> 1) & 1, p.err, abort_flag);
+          const int st = (2 * g + 1) % kStages;
+          ok = mbar_wait_poll(&s.full[st], (2 * g + 1) / kStages & 1, p.err, abort_flag);
           if (!ok) break;
           bool k_next = false;  // K_{j+1} has landed
           for (int t = 0; ok && t < 2; ++t) {
@@ -410,11 +398,11 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                 tc_fence_after();
                 k_next = true;
               }
-              issue_s(t, (g + 1) & 1);
+              issue_s(t, g + 1);
             }
           }
-          commit(&s.v_empty[st]);
-          if (k_next) commit(&s.k_empty[(g + 1) & 1]);
+          commit(&s.empty[st]);
+          if (k_next) commit(&s.empty[(2 * g + 2) % kStages]);
         }
         ring += static_cast<uint32_t>(u.streamed());
         base0 += u.count(0);
@@ -472,30 +460,31 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
     } else {
       // ---------------------- zeroing (warp 11), or conversion (warps 11-15)
       [[maybe_unused]] const int cv = tid - 352;  // 0 .. kConverters - 1
-      uint32_t ring = 0, units = 0, n8 = 0;
-      uint32_t fixed = 0;  // bit st: parity of V stage st's next ragged tile
+      [[maybe_unused]] uint32_t units = 0;
+      uint32_t ring = 0;
+      [[maybe_unused]] uint32_t fixed = 0;  // bit st: parity of the next tile in raw_full[st]
       bool ok = true;
       while (ok && take_unit(s, taken++, u, p.err, abort_flag)) {
         if (u.first > u.last) continue;
         if constexpr (!kFp8) {
           for (int j = u.first; ok && j <= u.last; ++j, ++ring) {
             if (!u.ragged(j)) continue;
-            const int st = ring & 1;
+            const int st = (2 * ring + 1) % kStages;
             // (a barrier of its own: this warp skips the other tiles, whose phases
             // it would lose count of)
-            ok = many_warp_wait(&s.v_raw[st], (fixed >> st) & 1, p.err, abort_flag);
+            ok = many_warp_wait(&s.raw_full[st], (fixed >> st) & 1, p.err, abort_flag);
             if (!ok) break;
             fixed ^= 1u << st;
             for (int i = lane; i < kTile * (2 * D / 16); i += 32) {
               const int r = i & (kTile - 1), c = i >> 7;  // 16-byte chunk c of row r
               const int key = j * kTile + r;
               if (key < u.key_lo || key >= u.key_hi)
-                *reinterpret_cast<uint4*>(s.v[st] + (c >> 3) * Smem::kBlockBytes + r * 128 +
+                *reinterpret_cast<uint4*>(s.kv[st] + (c >> 3) * Smem::kBlockBytes + r * 128 +
                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.v_full[st]);
+            if (lane == 0) mbar_arrive(&s.full[st]);
           }
         } else {
           if constexpr (kBf16) {
@@ -542,61 +531,80 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           ++units;
           int ref[2] = {0, 0};  // largest key, value exponent of the piece so far
           for (int j = u.first; ok && j <= u.last; ++j, ++ring) {
-            const int st = ring & 1;
             const bool cut = u.ragged(j);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++n8) {
-              const int slot = n8 % Smem::kSlots8;
-              ok = many_warp_wait(&s.raw_full[slot], (n8 / Smem::kSlots8) & 1, p.err, abort_flag);
-              if (!ok) break;
-              if (ring >= 2)
-                ok = many_warp_wait(kv ? &s.v_empty[st] : &s.k_empty[st], ((ring >> 1) - 1) & 1,
-                                    p.err, abort_flag);
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+              const uint32_t n = 2 * ring + kv;
+              const int st = n % kStages;
+              ok = many_warp_wait(&s.raw_full[st], (n / kStages) & 1, p.err, abort_flag);
               if (!ok) break;
               int top = 0;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int r = lane * 4 + i, key = j * kTile + r;
-                if (key >= u.key_lo && key < u.key_hi) top = max(top, static_cast<int>(s.exps[slot][r]));
+                if (key >= u.key_lo && key < u.key_hi)
+                  top = max(top, static_cast<int>(s.exps[st][r]));
               }
+              top = __reduce_max_sync(0xffffffffu, top);
+              const int base_e = max(kv ? ref[1] : ref[0], top);
+              (kv ? ref[1] : ref[0]) = base_e;
+              if (cv == 0) (kv ? s.vref : s.kref)[ring % kRefs] = base_e;
+              // D / 16 lanes share a row: 16 codes each.  A warp reads kBatch
+              // groups of rows before it writes any: in place, a row's raw
+              // bytes lie under its converted ones.
+              constexpr int kChunks = D / 16, kRowsPerWarp = 32 / kChunks;
+              constexpr int kWarps = kConverters / 32, kBatch = 4;
+              const int c = lane % kChunks;
+              const int rw = (warp - 11) * kRowsPerWarp + lane / kChunks;
+              const uint8_t* raw = s.raw(st);
+#pragma unroll 1
+              for (int r0 = rw; r0 - rw + (warp - 11) * kRowsPerWarp < kTile;
+                   r0 += kBatch * kWarps * kRowsPerWarp) {
+                uint4 v[kBatch];
+                int e[kBatch];
 #pragma unroll
-              for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-              ref[kv] = max(ref[kv], top);
-              if (cv == 0) (kv ? s.vref : s.kref)[ring % kRefs] = ref[kv];
-              uint8_t* to = kv ? s.v[st] : s.k[st];
-              constexpr int kChunks = D / 16;  // 16 codes each
-#pragma unroll 4
-              for (int i = cv; i < kTile * kChunks; i += kConverters) {
-                const int r = i / kChunks, c = i % kChunks, key = j * kTile + r;
-                const int e = s.exps[slot][r];
-                const uint8_t* from =
-                    D == 128 ? s.raw[slot] + r * 128 + ((c ^ (r & 7)) << 4)
-                             : s.raw[slot] + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-                const uint4 v = *reinterpret_cast<const uint4*>(from);
-                // 2^(e - ref + 7): codes stay below 448 * 128
-                const float f = many_exp2_field(127 + e - ref[kv] + 7);
-                const bool none = e == 0 || (cut && (key < u.key_lo || key >= u.key_hi));
-                const uint32_t f2 = pack2<false>(f, f);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                uint32_t h[8];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  h[2 * q] = none ? 0u : mul_f16x2(e4m3x2_to_f16x2(u[q]), f2);
-                  h[2 * q + 1] = none ? 0u : mul_f16x2(e4m3x2_to_f16x2(u[q] >> 16), f2);
+                for (int i = 0; i < kBatch; ++i) {
+                  const int r = r0 + i * kWarps * kRowsPerWarp;
+                  e[i] = 0;
+                  v[i] = make_uint4(0u, 0u, 0u, 0u);
+                  if (r < kTile) {
+                    v[i] = *reinterpret_cast<const uint4*>(
+                        D == 128 ? raw + r * 128 + ((c ^ (r & 7)) << 4)
+                                 : raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                    e[i] = s.exps[st][r];
+                  }
                 }
-                uint8_t* row = to + (c >> 2) * Smem::kBlockBytes + r * 128;
-                const int c0 = (c & 3) * 2;
-                const uint4 a = make_uint4(h[0], h[1], h[2], h[3]),
-                            b = make_uint4(h[4], h[5], h[6], h[7]);
-                // the upper block's lanes write their odd chunk first: the
-                // blocks share banks
-                const bool odd = (c >> 2) & 1;
-                *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
-                *reinterpret_cast<uint4*>(row + (((c0 + !odd) ^ (r & 7)) << 4)) = odd ? a : b;
+                if constexpr (Smem::kInPlace) __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                  const int r = r0 + i * kWarps * kRowsPerWarp, key = j * kTile + r;
+                  if (r >= kTile) continue;
+                  // 2^(e - ref + 7): codes stay below 448 * 128
+                  const float f = many_exp2_field(127 + e[i] - base_e + 7);
+                  const uint32_t f2 = pack2<false>(f, f);
+                  const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                  uint32_t h[8];
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    h[2 * q] = mul_f16x2(e4m3x2_to_f16x2(w[q]), f2);
+                    h[2 * q + 1] = mul_f16x2(e4m3x2_to_f16x2(w[q] >> 16), f2);
+                  }
+                  if (e[i] == 0 || (cut && (key < u.key_lo || key >= u.key_hi)))
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) h[q] = 0u;
+                  uint8_t* row = s.kv[st] + (c >> 2) * Smem::kBlockBytes + r * 128;
+                  const int c0 = (c & 3) * 2;
+                  const uint4 a = make_uint4(h[0], h[1], h[2], h[3]),
+                              b = make_uint4(h[4], h[5], h[6], h[7]);
+                  // the upper block's lanes write their odd chunk first: the
+                  // blocks share banks
+                  const bool odd = (c >> 2) & 1;
+                  *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
+                  *reinterpret_cast<uint4*>(row + (((c0 + !odd) ^ (r & 7)) << 4)) = odd ? a : b;
+                }
               }
               fence_proxy_async_smem();
-              mbar_arrive(kv ? &s.v_full[st] : &s.k_full[st]);
-              mbar_arrive(&s.raw_empty[slot]);
+              mbar_arrive(&s.full[st]);
             }
           }
         }
@@ -657,7 +665,8 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
         float down = 1.f;
         if constexpr (kFp8) {
           // converted V comes after K and Q by the same threads
-          ok = many_warp_wait(&s.v_full[g & 1], (g >> 1) & 1, p.err, abort_flag);
+          ok = many_warp_wait(&s.full[(2 * g + 1) % kStages], (2 * g + 1) / kStages & 1, p.err,
+                              abort_flag);
           if (!ok) break;
           if (jj == 0 && kBf16) sl2 *= many_exp2_field(127 - s.qshift[units & 1][t * kTile + r]);
           // K was scaled by 2^(127 - kref + 7)
