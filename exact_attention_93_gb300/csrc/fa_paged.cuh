@@ -10,7 +10,9 @@
 // every SM, ragged batches stay balanced, and a CTA leaves at most two cut
 // pieces whatever the batch.  Cut pieces go to the workspace in fp32
 // (unnormalised O, maximum, sum) and paged_join_kernel adds them up in a fixed
-// order.
+// order.  Where no sequence of the table can be long (PagedLaunch::whole), units
+// stay whole instead, each with the CTA whose stretch it begins in, and nothing
+// is left to join.
 //
 // Weights.  The few-row kernel gives all units of a sequence the number of key
 // tiles that any of its queries sees, at least 1 (a sequence usually is one
@@ -177,7 +179,15 @@ __device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) 
         hi = min(hi, lo + step);
       }
       at.block = lo;
-      at.off = lo ? rem - w.before(p, lo) : rem;
+      const long long start = lo ? w.before(p, lo) : 0;
+      at.off = rem - start;
+      if (p.whole && at.off > 0) {  // the unit belongs to a CTA before this one
+        const long long rest = w.before(p, lo + 1) - rem;
+        at.pos += rest;
+        at.left = max(0LL, at.left - rest);
+        at.off = 0;
+        ++at.block;
+      }
       return at;
     }
     ahead += __shfl_sync(0xffffffffu, upto, 31);
@@ -238,7 +248,8 @@ struct WorkWalk {
     const int lo_tile = x.lo / kTile, hi_tile = (x.hi + kTile - 1) / kTile;
     const int weight = kMany ? kUnitCost + hi_tile - lo_tile : w.flat;
     const int off = static_cast<int>(at.off);
-    const int take = static_cast<int>(min(at.left, static_cast<long long>(weight - off)));
+    const int take =
+        p.whole ? weight : static_cast<int>(min(at.left, static_cast<long long>(weight - off)));
     x.whole = take == weight;
     x.slot = off > 0 ? 0 : 1;
     const int base = kMany ? lo_tile - kUnitCost : w.first;
@@ -324,6 +335,8 @@ __global__ void __launch_bounds__(kJoinThreads)
             continue;
           }
           ml[q] = p.part_ml[at + q];
+          // (of pieces without keys there is a maximum alone; what the loads
+          // below find is multiplied by nothing)
           const float* src = p.part_o + (at + q) * D + lane * kN;
           if constexpr (kN == 4) {
             const float4 v = *reinterpret_cast<const float4*>(src);
@@ -341,7 +354,8 @@ __global__ void __launch_bounds__(kJoinThreads)
           m[q] = m_new;
           l[q] = l[q] * a + ml[q].y * b;
 #pragma unroll
-          for (int e = 0; e < kN; ++e) o[q][e] = o[q][e] * a + x[q][e] * b;
+          for (int e = 0; e < kN; ++e)
+            o[q][e] = o[q][e] * a + (ml[q].x == -INFINITY ? 0.f : x[q][e] * b);
         }
       }
     }

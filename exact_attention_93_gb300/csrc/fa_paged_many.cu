@@ -549,58 +549,49 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
               const int base_e = max(kv ? ref[1] : ref[0], top);
               (kv ? ref[1] : ref[0]) = base_e;
               if (cv == 0) (kv ? s.vref : s.kref)[ring % kRefs] = base_e;
-              // D / 16 lanes share a row: 16 codes each.  A warp reads kBatch
-              // groups of rows before it writes any: in place, a row's raw
-              // bytes lie under its converted ones.
-              constexpr int kChunks = D / 16, kRowsPerWarp = 32 / kChunks;
-              constexpr int kWarps = kConverters / 32, kBatch = 4;
-              const int c = lane % kChunks;
-              const int rw = (warp - 11) * kRowsPerWarp + lane / kChunks;
+              // Eight lanes share a row, lane c with codes 8 c .. 8 c + 7 of each
+              // 64: they become chunk c of the row in that column block.  A
+              // warp reads kBatch groups of rows before it writes any: in
+              // place, a row's raw bytes lie under its converted ones.  Odd
+              // rows take the 64s in the other order, for the banks' sake.
+              constexpr int kPieces = D / 64, kBatch = 2, kStep = kConverters / 8;
+              const int c = lane & 7, r_first = (warp - 11) * 4 + (lane >> 3);
               const uint8_t* raw = s.raw(st);
 #pragma unroll 1
-              for (int r0 = rw; r0 - rw + (warp - 11) * kRowsPerWarp < kTile;
-                   r0 += kBatch * kWarps * kRowsPerWarp) {
-                uint4 v[kBatch];
-                int e[kBatch];
+              for (int r0 = r_first; (r0 & ~3) < kTile; r0 += kBatch * kStep) {
+                uint2 v[kBatch][kPieces];
+                uint32_t e[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                  const int r = r0 + i * kWarps * kRowsPerWarp;
-                  e[i] = 0;
-                  v[i] = make_uint4(0u, 0u, 0u, 0u);
-                  if (r < kTile) {
-                    v[i] = *reinterpret_cast<const uint4*>(
-                        D == 128 ? raw + r * 128 + ((c ^ (r & 7)) << 4)
-                                 : raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-                    e[i] = s.exps[st][r];
+                  const int r = min(r0 + i * kStep, kTile - 1);
+#pragma unroll
+                  for (int h = 0; h < kPieces; ++h) {
+                    const int x = (h ^ (r & (kPieces - 1))) * 8 + c;  // 8-byte piece of the row
+                    v[i][h] = *reinterpret_cast<const uint2*>(
+                        D == 128 ? raw + r * 128 + (((x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8
+                                 : raw + r * 64 + (((x >> 1) ^ ((r >> 1) & 3)) << 4) + (x & 1) * 8);
                   }
+                  e[i] = s.exps[st][r];
                 }
                 if constexpr (Smem::kInPlace) __syncwarp();
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                  const int r = r0 + i * kWarps * kRowsPerWarp, key = j * kTile + r;
-                  if (r >= kTile) continue;
+                  const int r = r0 + i * kStep, key = j * kTile + r;
+                  if (r >= kTile) break;
                   // 2^(e - ref + 7): codes stay below 448 * 128
-                  const float f = many_exp2_field(127 + e[i] - base_e + 7);
+                  const bool none = e[i] == 0 || (cut && (key < u.key_lo || key >= u.key_hi));
+                  const float f = none ? 0.f : many_exp2_field(134 + static_cast<int>(e[i]) - base_e);
                   const uint32_t f2 = pack2<false>(f, f);
-                  const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                  uint32_t h[8];
+                  uint8_t* row = s.kv[st] + r * 128 + ((c ^ (r & 7)) << 4);
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    h[2 * q] = mul_f16x2(e4m3x2_to_f16x2(w[q]), f2);
-                    h[2 * q + 1] = mul_f16x2(e4m3x2_to_f16x2(w[q] >> 16), f2);
+                  for (int h = 0; h < kPieces; ++h) {
+                    const uint32_t w0 = none ? 0u : v[i][h].x, w1 = none ? 0u : v[i][h].y;
+                    *reinterpret_cast<uint4*>(row + (h ^ (r & (kPieces - 1))) * Smem::kBlockBytes) =
+                        make_uint4(mul_f16x2(e4m3x2_to_f16x2(w0), f2),
+                                   mul_f16x2(e4m3x2_to_f16x2(w0 >> 16), f2),
+                                   mul_f16x2(e4m3x2_to_f16x2(w1), f2),
+                                   mul_f16x2(e4m3x2_to_f16x2(w1 >> 16), f2));
                   }
-                  if (e[i] == 0 || (cut && (key < u.key_lo || key >= u.key_hi)))
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) h[q] = 0u;
-                  uint8_t* row = s.kv[st] + (c >> 2) * Smem::kBlockBytes + r * 128;
-                  const int c0 = (c & 3) * 2;
-                  const uint4 a = make_uint4(h[0], h[1], h[2], h[3]),
-                              b = make_uint4(h[4], h[5], h[6], h[7]);
-                  // the upper block's lanes write their odd chunk first: the
-                  // blocks share banks
-                  const bool odd = (c >> 2) & 1;
-                  *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
-                  *reinterpret_cast<uint4*>(row + (((c0 + !odd) ^ (r & 7)) << 4)) = odd ? a : b;
                 }
               }
               fence_proxy_async_smem();
@@ -831,8 +822,10 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                              : reinterpret_cast<uint8_t*>(p.part_o + at * D);
         if (!mine) out = nullptr;
         const int cols = whole ? 64 : 32;  // columns of a piece
+        // (a cut piece without tiles leaves its maximum, -inf, alone)
+        const int end = whole || have ? D : 0;
 #pragma unroll 1
-        for (int c = 0; c < D; c += cols) {
+        for (int c = 0; c < end; c += cols) {
           uint4 w[8];
           auto take = [&](int col, auto&& put) {
             uint32_t o[32];
@@ -917,8 +910,7 @@ cudaError_t launch_many_t(const PagedLaunch& a, cudaStream_t s) {
   cudaError_t e = ensure_dynamic_smem(kern, smem, configured);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, static_cast<unsigned>(a.sms), ManyWarps<kFp8>::kThreads, smem, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_join<D, kBf16>(a, s);
+  return e != cudaSuccess || a.whole ? e : launch_join<D, kBf16>(a, s);
 }
 
 template <int D, bool kFp8>

@@ -15,6 +15,7 @@ namespace {
 constexpr long long kMaxBytes = 1ll << 40;  // every operand lies below this from its base
 constexpr int kMaxRows = 1 << 29;           // packed rows, keys of a sequence, window bounds
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kWholeKeysFew = 1024, kWholeKeysMany = 1024;
 
 bool aligned(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -312,6 +313,10 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
   a.tasks = reinterpret_cast<JoinTask*>(static_cast<uint8_t*>(workspace) + plan.o_bytes +
                                         plan.ml_bytes);
   a.block_rows = plan.block_rows;
+  // Below this many keys a sequence, cutting a unit and joining its pieces costs
+  // more than it saves.
+  a.whole = static_cast<long long>(batch->max_pages) * cache->page_size <=
+            (plan.many ? kWholeKeysMany : kWholeKeysFew);
   if (sm_count(&a.sms) != cudaSuccess) return FA_ERR_CUDA;
   a.err = device_error_word();
   if (!a.err) return FA_ERR_CUDA;
