@@ -29,13 +29,13 @@
 // loaded) may be anything, and 0 * NaN is NaN: a spare warp makes those rows of
 // a tile zeros before the P V product reads it.
 //
-// e4m3 caches: five warps convert each 8-bit tile to fp16 in shared
+// e4m3 caches: four warps convert each 8-bit tile to fp16 in shared
 // memory (exactly, relative to the largest row exponent so far, which scales
 // the scores, and O, in fp32), and bf16 queries to fp16 under a power-of-two
 // scale per row; both products then run in fp16.
 //
 // Warps: 0-3 softmax of tile A, 4-7 of tile B, 8 producer, 9 MMA issue, 10 the
-// units, 11 zeroing (12 warps), or 11-15 conversion (e4m3 caches, 16 warps).
+// units, 11 zeroing (12 warps), or 12-15 conversion (e4m3 caches, 16 warps).
 #include "fa_paged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"
@@ -45,12 +45,13 @@ namespace {
 
 // Threads, and registers per thread after the softmax warps have taken the
 // others': 12 warps launch with 168 (2 x 208 + 80 <= 3 x 168 on each
-// sub-partition), 16 with 128 (2 x 200 + 2 x 56 = 4 x 128).
+// sub-partition), 16 with 128 (2 x 192 + 2 x 64 = 4 x 128).
 template <bool kFp8>
 struct ManyWarps {
   static constexpr int kThreads = kFp8 ? 512 : 384;
-  static constexpr uint32_t kLow = kFp8 ? 56 : 80, kHigh = kFp8 ? 200 : 208;
-  static constexpr int kConverters = (kThreads - 352);  // threads of warps 11 ..
+  static constexpr uint32_t kLow = kFp8 ? 64 : 80, kHigh = kFp8 ? 192 : 208;
+  static constexpr int kFirst = kFp8 ? 12 : 11;  // zeroing or converting warps
+  static constexpr int kConverters = kThreads - 32 * kFirst;  // their threads
 };
 constexpr int kUnitRing = 4;
 // references of key and value exponents, one per key tile: a softmax group is
@@ -457,9 +458,9 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
         __syncwarp();
         if (!more) break;
       }
-    } else {
-      // ---------------------- zeroing (warp 11), or conversion (warps 11-15)
-      [[maybe_unused]] const int cv = tid - 352;  // 0 .. kConverters - 1
+    } else if (warp >= ManyWarps<kFp8>::kFirst) {
+      // ---------------------- zeroing (warp 11), or conversion (warps 12-15)
+      [[maybe_unused]] const int cv = tid - 32 * ManyWarps<kFp8>::kFirst;
       [[maybe_unused]] uint32_t units = 0;
       uint32_t ring = 0;
       [[maybe_unused]] uint32_t fixed = 0;  // bit st: parity of the next tile in raw_full[st]
@@ -551,42 +552,54 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
               if (cv == 0) (kv ? s.vref : s.kref)[ring % kRefs] = base_e;
               // Eight lanes share a row, lane c with codes 8 c .. 8 c + 7 of each
               // 64: they become chunk c of the row in that column block.  A
-              // warp reads kBatch groups of rows before it writes any: in
-              // place, a row's raw bytes lie under its converted ones.  Odd
-              // rows take the 64s in the other order, for the banks' sake.
-              constexpr int kPieces = D / 64, kBatch = 2, kStep = kConverters / 8;
-              const int c = lane & 7, r_first = (warp - 11) * 4 + (lane >> 3);
-              const uint8_t* raw = s.raw(st);
-#pragma unroll 1
-              for (int r0 = r_first; (r0 & ~3) < kTile; r0 += kBatch * kStep) {
+              // warp's rows are 16 apart, so that their swizzle is the same and
+              // every address a constant away from the first; it reads kBatch
+              // of them before it writes any: in place, a row's raw bytes lie
+              // under its converted ones.  Odd rows take the 64s in the other
+              // order, for the banks' sake.
+              constexpr int kPieces = D / 64, kBatch = 4, kStep = kConverters / 8;
+              const int c = lane & 7, r0 = (cv >> 5) * 4 + (lane >> 3);
+              const int flip = r0 & (kPieces - 1);
+              const uint8_t* from[kPieces];
+              uint8_t* to[kPieces];
+#pragma unroll
+              for (int h = 0; h < kPieces; ++h) {
+                const int x = (h ^ flip) * 8 + c;  // 8-byte piece of the raw row
+                from[h] = s.raw(st) + (x & 1) * 8 +
+                          (D == 128 ? r0 * 128 + (((x >> 1) ^ (r0 & 7)) << 4)
+                                    : r0 * 64 + (((x >> 1) ^ ((r0 >> 1) & 3)) << 4));
+                to[h] = s.kv[st] + (h ^ flip) * Smem::kBlockBytes + r0 * 128 +
+                        ((c ^ (r0 & 7)) << 4);
+              }
+#pragma unroll
+              for (int m0 = 0; m0 < kTile / kStep; m0 += kBatch) {
                 uint2 v[kBatch][kPieces];
                 uint32_t e[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                  const int r = min(r0 + i * kStep, kTile - 1);
 #pragma unroll
-                  for (int h = 0; h < kPieces; ++h) {
-                    const int x = (h ^ (r & (kPieces - 1))) * 8 + c;  // 8-byte piece of the row
-                    v[i][h] = *reinterpret_cast<const uint2*>(
-                        D == 128 ? raw + r * 128 + (((x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8
-                                 : raw + r * 64 + (((x >> 1) ^ ((r >> 1) & 3)) << 4) + (x & 1) * 8);
+                  for (int h = 0; h < kPieces; ++h)
+                    v[i][h] = *reinterpret_cast<const uint2*>(from[h] + (m0 + i) * kStep * D);
+                  e[i] = s.exps[st][r0 + (m0 + i) * kStep];
+                }
+                if (cut) {
+#pragma unroll
+                  for (int i = 0; i < kBatch; ++i) {
+                    const int key = j * kTile + r0 + (m0 + i) * kStep;
+                    if (key < u.key_lo || key >= u.key_hi) e[i] = 0;
                   }
-                  e[i] = s.exps[st][r];
                 }
                 if constexpr (Smem::kInPlace) __syncwarp();
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                  const int r = r0 + i * kStep, key = j * kTile + r;
-                  if (r >= kTile) break;
-                  // 2^(e - ref + 7): codes stay below 448 * 128
-                  const bool none = e[i] == 0 || (cut && (key < u.key_lo || key >= u.key_hi));
-                  const float f = none ? 0.f : many_exp2_field(134 + static_cast<int>(e[i]) - base_e);
+                  // 2^(e - ref + 7): codes stay below 448 * 128.  e = 0: zeros
+                  const float f =
+                      e[i] ? many_exp2_field(134 + static_cast<int>(e[i]) - base_e) : 0.f;
                   const uint32_t f2 = pack2<false>(f, f);
-                  uint8_t* row = s.kv[st] + r * 128 + ((c ^ (r & 7)) << 4);
 #pragma unroll
                   for (int h = 0; h < kPieces; ++h) {
-                    const uint32_t w0 = none ? 0u : v[i][h].x, w1 = none ? 0u : v[i][h].y;
-                    *reinterpret_cast<uint4*>(row + (h ^ (r & (kPieces - 1))) * Smem::kBlockBytes) =
+                    const uint32_t w0 = e[i] ? v[i][h].x : 0u, w1 = e[i] ? v[i][h].y : 0u;
+                    *reinterpret_cast<uint4*>(to[h] + (m0 + i) * kStep * 128) =
                         make_uint4(mul_f16x2(e4m3x2_to_f16x2(w0), f2),
                                    mul_f16x2(e4m3x2_to_f16x2(w0 >> 16), f2),
                                    mul_f16x2(e4m3x2_to_f16x2(w1), f2),
