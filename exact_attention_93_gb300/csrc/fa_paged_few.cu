@@ -11,9 +11,11 @@
 // one producer warp keeps a ring of K and V tiles (128 keys each) in flight by
 // TMA, page by page.
 //
-// Eight consumer warps share each tile, 16 keys each, with a running maximum,
-// sum and O of their own that are joined once per piece of work: no barrier
-// among them inside the key loop.  The products are turned around, S^T = K Q^T
+// Eight consumer warps in two groups take alternate tiles, 32 keys of a tile
+// each, with a running maximum, sum and O of their own that are joined once per
+// piece of work: no barrier among them inside the key loop, and two tiles of
+// dependent steps in flight.  (With every warp on the same tile, 16 keys each,
+// an e4m3 batch of 64 contexts took 176 us instead of the time below.)  The products are turned around, S^T = K Q^T
 // and O^T = V^T P^T, on mma.sync m16n8k16: keys and head columns fill the 16
 // rows, so the padding of the query side is to 8 rows, and the operands go
 // from shared memory to registers to the tensor core without a detour through
@@ -36,24 +38,26 @@ namespace {
 
 constexpr int kConsumers = 8;                        // warps
 constexpr int kFewThreads = (kConsumers + 1) * 32;   // and the producer
-constexpr int kSliceKeys = kTile / kConsumers;       // keys of a tile per warp
-constexpr int kRingBytes = 160 * 1024;
+constexpr int kGroups = 2, kGroupWarps = kConsumers / kGroups;
+constexpr int kSlices = kTile / kGroupWarps / 16;    // 16-key slices of a tile per warp
+constexpr int kRingBytes = 192 * 1024;
 
 template <int D, bool kFp8, int NB>
 struct FewSmem {
   static constexpr int kRowBytes = kFp8 ? D : 2 * D;
   static constexpr int kSlotBytes = kTile * kRowBytes;
-  static constexpr int kSlots = kRingBytes / kSlotBytes;  // K and V tiles alternate
+  // Each group of consumers has a ring of its own, through which the K and V of
+  // its tiles alternate: a slot's uses then follow one another in one group's
+  // sight, and none can be mistaken for the one before it.
+  static constexpr int kSlots = kRingBytes / kSlotBytes, kRing = kSlots / kGroups;
   static constexpr int kMergePitch = D + 4;
   static constexpr int kSteps = D / 16;
   alignas(1024) uint8_t ring[kSlots][kSlotBytes];
   alignas(16) uint8_t exps[kFp8 ? kSlots : 1][kTile];
-  // joining the warps' results, eight query rows at a time
-  alignas(16) float merge[kConsumers][8][kMergePitch];
+  // joining the warps' results: eight query rows of one group's warps at a time
+  alignas(16) float merge[kGroupWarps][8][kMergePitch];
   float m[kConsumers][8 * NB], l[kConsumers][8 * NB];
   float vscale[kConsumers];
-  // queries as operand fragments, where registers do not hold them
-  uint2 q[NB >= 4 ? kSteps : 1][NB >= 4 ? NB : 1][32];
   uint64_t full[kSlots], empty[kSlots];
   Place place;
   int abort_flag;
@@ -114,10 +118,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     paged_few_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
   using Smem = FewSmem<D, kFp8, NB>;
-  constexpr int kRows = 8 * NB, kRowBytes = Smem::kRowBytes, kSlots = Smem::kSlots;
+  constexpr int kRows = 8 * NB, kRowBytes = Smem::kRowBytes;
+  constexpr int kSlots = Smem::kSlots, kRing = Smem::kRing;
   constexpr int kSteps = Smem::kSteps;      // k16 steps over the head, and m16 blocks of V^T
   constexpr bool kMmaBf16 = kBf16 && !kFp8;  // type of the products
-  constexpr bool kQRegs = NB < 4;
   // weights are kept as 2^(s - m + kLift): fp16 ones reach up to 2^15 and stay
   // normal down to 2^-29 of the largest (e4m3: see pfac)
   constexpr float kLift = !kFp8 && !kBf16 ? 15.f : 0.f;
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (threadIdx.x == 32) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], kConsumers);
+      mbar_init(&s.empty[i], kGroupWarps);
     }
     s.abort_flag = 0;
     fence_barrier_init();
@@ -153,31 +157,29 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       tma_prefetch_desc(&p.map_k);
       tma_prefetch_desc(&p.map_v);
     }
-    uint32_t n = 0;  // slots filled
+    uint32_t tiles = 0;  // begun so far; tile number i belongs to group i % kGroups
+    uint32_t loads0 = 0, loads1 = 0;  // slots filled of each group's ring
     while (walk.next(p, x)) {
-      const int* table = p.r.table + x.b * p.r.table_stride;
-      // lane i < per_tile: the i-th box of a tile, if a visible key lies in it
-      auto page_of = [&](int tile) {
+      PageFeed feed;
+      feed.start(p, x.b, x.tile0, x.lo, x.hi);
+      for (int tile = x.tile0; tile < x.tile1; ++tile, ++tiles) {
         const int k0 = tile * kTile + lane * box_rows;
-        const bool wanted = lane < per_tile && tile < x.tile1 && k0 < x.hi && k0 + box_rows > x.lo;
-        return wanted ? table[k0 >> p.page_log2] : -2;
-      };
-      int page = page_of(x.tile0);
-      for (int tile = x.tile0; tile < x.tile1; ++tile) {
-        const int k0 = tile * kTile + lane * box_rows;
+        // lane i < per_tile: the i-th box of the tile, if a visible key lies in it
         const bool mine = lane < per_tile && k0 < x.hi && k0 + box_rows > x.lo;
         const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        const int next_page = page_of(tile + 1);
+        int page = feed.get(p, tile, k0);
         if (mine && (page < 0 || page >= p.pages)) {
           atomicExch(p.err, kDevErrBadIndex);
           page = p.pages;  // out of range for the tensor map: reads as zeros
         }
         const int row = k0 & (p.page_size - 1);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int slot = n % kSlots;
-          if (n >= kSlots) ring_wait(&s.empty[slot], (n / kSlots - 1) & 1, p.err, abort_flag);
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t n = 2 * (tiles / kGroups) + kv;  // in its group's ring
+          const int slot = static_cast<int>(tiles % kGroups) * kRing + n % kRing;
+          if (n >= kRing) ring_wait(&s.empty[slot], (n / kRing - 1) & 1, p.err, abort_flag);
           if (__any_sync(0xffffffffu, *abort_flag)) goto stopped;
+          (tiles % kGroups ? loads1 : loads0) += 1;
           if (lane == 0)
             mbar_arrive_expect_tx(&s.full[slot],
                                   boxes * box_rows * (kRowBytes + (kFp8 ? 1 : 0)));
@@ -197,7 +199,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
           }
         }
-        page = next_page;
       }
     }
   stopped:
@@ -205,20 +206,45 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // Copies in flight land before the CTA's shared memory goes away.
       int zero = 0;
       if (lane == 0)
-        for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
-          mbar_wait(&s.full[i % kSlots], (i / kSlots) & 1, p.err, &zero, 100000000ull);
+        for (int gr = 0; gr < kGroups; ++gr) {
+          const uint32_t loads = gr ? loads1 : loads0;
+          for (uint32_t n = loads > kRing ? loads - kRing : 0; n < loads; ++n)
+            mbar_wait(&s.full[gr * kRing + n % kRing], (n / kRing) & 1, p.err, &zero, 100000000ull);
+        }
     }
     __syncwarp();
   } else {
     // --------------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
-    uint32_t n = 0;  // slots consumed
+    const int group = warp / kGroupWarps;
+    const int slice0 = (warp % kGroupWarps) * kSlices * 16;  // this warp's first row of a tile
+    // This lane's offsets into a tile, for its first slice; the others lie 16
+    // rows on, with the same swizzle.  K as A operand (m16 x k16), V^T as A
+    // operand; e4m3: 16 key bytes are chunks 2 t + h of rows g and g + 8 (four
+    // steps of four columns each), values are D / 8 columns of rows 2 t and
+    // 2 t + 1 (and 8 on).
+    uint32_t koff[kFp8 ? 2 : 4], voff[kFp8 ? 2 : 4];
+#pragma unroll
+    for (int i = 0; i < (kFp8 ? 2 : 4); ++i) {
+      if constexpr (!kFp8) {
+        koff[i] = (slice0 + (lane & 15)) * 128 + (((i * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
+        voff[i] = (slice0 + (lane >> 4) * 8 + (lane & 7)) * 128 +
+                  (((i * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+      } else if constexpr (D == 128) {
+        koff[i] = (slice0 + g) * 128 + (((2 * t + i) ^ g) << 4);
+        voff[i] = (slice0 + 2 * t + i) * 128 + ((g ^ (2 * t + i)) << 4);
+      } else {
+        koff[i] = (slice0 + g) * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+        voff[i] = (slice0 + 2 * t + i) * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+      }
+    }
+    uint32_t tiles = 0;  // of the pieces before this one
     while (walk.next(p, x)) {
       const Seq& seq = walk.w.s;
       const int row0 = x.block * kRows;
       if (threadIdx.x == 0) p.tasks[blockIdx.x] = join_task(p, x, seq);
       // -- queries as B operands, and what each of this lane's columns sees
-      uint32_t qf[kQRegs ? NB : 1][kSteps][2];
+      uint32_t qf[NB][kSteps][2];
       float qscale[NB][2];
       {
         float mine[NB];  // scale of query row 8 nb + g
@@ -238,7 +264,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if constexpr (kFp8) {
               // a lane's 16 key bytes are four steps of four columns
               const uint2 v = src ? __ldg(reinterpret_cast<const uint2*>(
-                                        src + (kk >> 2) * 64 + 16 * t + 4 * (kk & 3)))
+                                        src + (D == 128 ? 32 * t + 4 * kk : 16 * t + 4 * kk)))
                                   : make_uint2(0u, 0u);
               f[kk][0] = v.x;
               f[kk][1] = v.y;
@@ -278,12 +304,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
 #pragma unroll
           for (int kk = 0; kk < kSteps; ++kk) {
-            if constexpr (kQRegs) {
-              qf[nb][kk][0] = f[kk][0];
-              qf[nb][kk][1] = f[kk][1];
-            } else if (kk % kConsumers == warp) {
-              s.q[kk][nb][lane] = make_uint2(f[kk][0], f[kk][1]);
-            }
+            qf[nb][kk][0] = f[kk][0];
+            qf[nb][kk][1] = f[kk][1];
           }
         }
 #pragma unroll
@@ -292,7 +314,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           for (int c = 0; c < 2; ++c)  // from the lanes of row 8 nb + 2 t + c
             qscale[nb][c] =
                 p.scale_log2 * __shfl_sync(0xffffffffu, mine[nb], (2 * t + c) * 4);
-        if constexpr (!kQRegs) named_bar_sync(1, kConsumers * 32);
       }
       int pos[NB][2];
       float slope[NB][2];
@@ -321,169 +342,175 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           for (int i = 0; i < 4; ++i) o[mb][nb][i] = 0.f;
       }
 
-      for (int tile = x.tile0; tile < x.tile1; ++tile, n += 2) {
-        const int ks = n % kSlots, vs = (n + 1) % kSlots;
-        const int k0 = tile * kTile + warp * kSliceKeys;  // this warp's keys k0 .. k0 + 15
+      for (int tile = x.tile0 + ((group - static_cast<int>(tiles)) & (kGroups - 1));
+           tile < x.tile1; tile += kGroups) {
+        const uint32_t n = 2 * ((tiles + static_cast<uint32_t>(tile - x.tile0)) / kGroups);
+        const int ks = group * kRing + n % kRing, vs = group * kRing + (n + 1) % kRing;
+        const int k0 = tile * kTile + slice0;  // this warp's first key
         // -- S^T = K Q^T
-        ring_wait(&s.full[ks], (n / kSlots) & 1, p.err, abort_flag);
+        ring_wait(&s.full[ks], (n / kRing) & 1, p.err, abort_flag);
         __syncwarp();
-        float acc[NB][4];
-        {
-          float half[4] = {0.f, 0.f, 0.f, 0.f};  // NB = 1: a second, independent chain
+        float acc[kSlices][NB][4];
+        float kfac[kSlices][2];
+#pragma unroll
+        for (int sl = 0; sl < kSlices; ++sl) {
+          // two independent chains of products per slice and eight queries
+          float half[NB][4];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
+            for (int i = 0; i < 4; ++i) acc[sl][nb][i] = half[nb][i] = 0.f;
           auto step = [&](int kk, const uint32_t (&a)[4]) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              uint32_t b0, b1;
-              if constexpr (kQRegs) {
-                b0 = qf[nb][kk][0];
-                b1 = qf[nb][kk][1];
-              } else {
-                const uint2 v = s.q[kk][nb][lane];
-                b0 = v.x;
-                b1 = v.y;
-              }
-              if (NB == 1 && (kk & 1))
-                mma16816<kMmaBf16>(half, a, b0, b1);
+              if (kk & 1)
+                mma16816<kMmaBf16>(half[nb], a, qf[nb][kk][0], qf[nb][kk][1]);
               else
-                mma16816<kMmaBf16>(acc[nb], a, b0, b1);
+                mma16816<kMmaBf16>(acc[sl][nb], a, qf[nb][kk][0], qf[nb][kk][1]);
             }
           };
           if constexpr (!kFp8) {
-            const int r = warp * kSliceKeys + (lane & 15);
-            const uint32_t base = smem_u32(s.ring[ks]) + r * 128;
+            const uint32_t base = smem_u32(s.ring[ks]) + sl * 16 * 128;
 #pragma unroll
             for (int kk = 0; kk < kSteps; ++kk) {
-              const int chunk = (kk & 3) * 2 + (lane >> 4);
               uint32_t a[4];
-              ldmatrix4(a, base + (kk >> 2) * kTile * 128 + ((chunk ^ (r & 7)) << 4));
+              ldmatrix4(a, base + koff[kk & 3] + (kk >> 2) * kTile * 128);
               step(kk, a);
             }
           } else {
-            // rows g and g + 8 of the slice, 16 bytes per 64 columns
-            constexpr int kHalves = D / 64;
-            uint4 k8[2][kHalves];
+            const uint8_t* base = s.ring[ks] + sl * 16 * kRowBytes;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = warp * kSliceKeys + g + 8 * i;
-              const uint8_t* row = s.ring[ks] + r * kRowBytes;
-              if constexpr (D == 128) {
-                // odd rows take their halves in the other order (the swizzle
-                // would put both rows' 64 bytes on the same banks)
-                const uint4 u = *reinterpret_cast<const uint4*>(
-                    row + (((t + ((g & 1) << 2)) ^ (r & 7)) << 4));
-                const uint4 v = *reinterpret_cast<const uint4*>(
-                    row + (((t + (((g & 1) ^ 1) << 2)) ^ (r & 7)) << 4));
-                k8[i][0] = (g & 1) ? v : u;
-                k8[i][kHalves - 1] = (g & 1) ? u : v;
-              } else {
-                k8[i][0] = *reinterpret_cast<const uint4*>(row + ((t ^ ((r >> 1) & 3)) << 4));
+            for (int h = 0; h < kSteps / 4; ++h) {
+              const uint4 lo = *reinterpret_cast<const uint4*>(base + koff[h]);
+              const uint4 hi = *reinterpret_cast<const uint4*>(base + koff[h] + 8 * kRowBytes);
+              const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t a[4] = {e4m3x2_to_f16x2(lw[w]), e4m3x2_to_f16x2(hw[w]),
+                                       e4m3x2_to_f16x2(lw[w] >> 16), e4m3x2_to_f16x2(hw[w] >> 16)};
+                step(4 * h + w, a);
               }
             }
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-              const uint4 &lo = k8[0][kk >> 2], &hi = k8[1][kk >> 2];
-              const uint32_t w0 = (kk & 3) == 0 ? lo.x : (kk & 3) == 1 ? lo.y
-                                  : (kk & 3) == 2 ? lo.z : lo.w;
-              const uint32_t w1 = (kk & 3) == 0 ? hi.x : (kk & 3) == 1 ? hi.y
-                                  : (kk & 3) == 2 ? hi.z : hi.w;
-              const uint32_t a[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w1),
-                                     e4m3x2_to_f16x2(w0 >> 16), e4m3x2_to_f16x2(w1 >> 16)};
-              step(kk, a);
-            }
+            for (int i = 0; i < 2; ++i)  // 2^(e - 127)
+              kfac[sl][i] = __uint_as_float(
+                  static_cast<uint32_t>(s.exps[ks][slice0 + sl * 16 + g + 8 * i]) << 23);
           }
-          if (NB == 1)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[0][i] += half[i];
-        }
-        float kfac[2] = {1.f, 1.f};
-        if constexpr (kFp8) {
-          kfac[0] = exp2_field(s.exps[ks][warp * kSliceKeys + g]);
-          kfac[1] = exp2_field(s.exps[ks][warp * kSliceKeys + g + 8]);
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[sl][nb][i] += half[nb][i];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.empty[ks]);
 
         // -- scores, maximum, weights
-        const bool masked = k0 < all_lo || k0 + kSliceKeys > all_hi;
+        const bool masked = k0 < all_lo || k0 + kSlices * 16 > all_hi;
         float alpha[NB][2];
         bool moved = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = i & 1, key = k0 + g + (i >> 1) * 8;
-            float z = acc[nb][i] * (kFp8 ? qscale[nb][c] * kfac[i >> 1] : qscale[nb][c]);
-            if (p.alibi)
-              z = fmaf(slope[nb][c], fabsf(static_cast<float>(key - pos[nb][c])), z);
-            if (masked) {
-              const bool seen = key < seq.len && (p.win_left < 0 || key >= pos[nb][c] - p.win_left) &&
-                                (p.win_right < 0 || key <= pos[nb][c] + p.win_right);
-              if (!seen) z = -INFINITY;
+          for (int sl = 0; sl < kSlices; ++sl)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float z = acc[sl][nb][i] * qscale[nb][i & 1];
+              if constexpr (kFp8) z *= kfac[sl][i >> 1];
+              acc[sl][nb][i] = z;
             }
-            acc[nb][i] = z;
+          if (p.alibi || masked) {
+#pragma unroll
+            for (int sl = 0; sl < kSlices; ++sl)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int c = i & 1, key = k0 + sl * 16 + g + (i >> 1) * 8;
+                float z = acc[sl][nb][i];
+                if (p.alibi)
+                  z = fmaf(slope[nb][c], fabsf(static_cast<float>(key - pos[nb][c])), z);
+                if (masked) {
+                  const bool seen = key < seq.len &&
+                                    (p.win_left < 0 || key >= pos[nb][c] - p.win_left) &&
+                                    (p.win_right < 0 || key <= pos[nb][c] + p.win_right);
+                  if (!seen) z = -INFINITY;
+                }
+                acc[sl][nb][i] = z;
+              }
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(acc[nb][c], acc[nb][c + 2]);
+            float top = m[nb][c];
+#pragma unroll
+            for (int sl = 0; sl < kSlices; ++sl)
+              top = fmax3(top, acc[sl][nb][c], acc[sl][nb][c + 2]);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float m_new = fmaxf(m[nb][c], top);
-            alpha[nb][c] = m_new > m[nb][c] ? ex2_approx(m[nb][c] - m_new) : 1.f;
-            moved |= m_new > m[nb][c];
-            m[nb][c] = m_new;
-            const float ref = m_new == -INFINITY ? 0.f : m_new - kLift;
-            acc[nb][c] = ex2_approx(acc[nb][c] - ref);
-            acc[nb][c + 2] = ex2_approx(acc[nb][c + 2] - ref);
-            l[nb][c] = fmaf(l[nb][c], alpha[nb][c], acc[nb][c] + acc[nb][c + 2]);
+            alpha[nb][c] = top > m[nb][c] ? ex2_approx(m[nb][c] - top) : 1.f;
+            moved |= top > m[nb][c];
+            m[nb][c] = top;
+            const float ref = top == -INFINITY ? 0.f : top - kLift;
+            float sum = 0.f;
+#pragma unroll
+            for (int sl = 0; sl < kSlices; ++sl) {
+              acc[sl][nb][c] = ex2_approx(acc[sl][nb][c] - ref);
+              acc[sl][nb][c + 2] = ex2_approx(acc[sl][nb][c + 2] - ref);
+              sum += acc[sl][nb][c] + acc[sl][nb][c + 2];
+            }
+            l[nb][c] = fmaf(l[nb][c], alpha[nb][c], sum);
           }
         }
 
         // -- O^T = O^T diag(alpha) + V^T P^T
-        ring_wait(&s.full[vs], ((n + 1) / kSlots) & 1, p.err, abort_flag);
+        ring_wait(&s.full[vs], ((n + 1) / kRing) & 1, p.err, abort_flag);
         __syncwarp();
-        const bool ragged = k0 < x.lo || k0 + kSliceKeys > x.hi;
+        const bool ragged = k0 < x.lo || k0 + kSlices * 16 > x.hi;
         if (ragged) {
           // rows outside the visible span hold anything: make them zeros
-          for (int r = 0; r < kSliceKeys; ++r)
+          for (int r = 0; r < kSlices * 16; ++r)
             if (k0 + r < x.lo || k0 + r >= x.hi)
               for (int i = lane; i < kRowBytes / 16; i += 32) {
                 const int blk = i >> 3;  // 128-byte column blocks
                 uint8_t* row = s.ring[vs] + blk * kTile * 128 +
-                               (warp * kSliceKeys + r) * (kRowBytes < 128 ? kRowBytes : 128);
+                               (slice0 + r) * (kRowBytes < 128 ? kRowBytes : 128);
                 *reinterpret_cast<uint4*>(row + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
               }
           fence_proxy_async_smem();
           __syncwarp();
         }
-        float pfac[2] = {1.f, 1.f};
         if constexpr (kFp8) {
-          int e[2];
+          uint32_t e[kSlices][2], top = 0;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int key = k0 + g + 8 * i;
-            e[i] = key >= x.lo && key < x.hi ? s.exps[vs][warp * kSliceKeys + g + 8 * i] : 0;
-          }
-          int top = max(e[0], e[1]);
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          if (top > vref) {
-            const float down = exp2_field(127 + vref - top);
+          for (int sl = 0; sl < kSlices; ++sl)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int key = k0 + sl * 16 + g + 8 * i;
+              e[sl][i] = s.exps[vs][slice0 + sl * 16 + g + 8 * i];
+              if (ragged && (key < x.lo || key >= x.hi)) e[sl][i] = 0;
+              top = max(top, e[sl][i]);
+            }
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (static_cast<int>(top) > vref) {
+            const float down = exp2_field(127 + vref - static_cast<int>(top));
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               alpha[nb][0] *= down;
               alpha[nb][1] *= down;
             }
             moved = true;
-            vref = top;
+            vref = static_cast<int>(top);
           }
-          pfac[0] = e[0] ? exp2_field(127 + e[0] - vref + 15) : 0.f;
-          pfac[1] = e[1] ? exp2_field(127 + e[1] - vref + 15) : 0.f;
+#pragma unroll
+          for (int sl = 0; sl < kSlices; ++sl)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float f =
+                  e[sl][i] ? exp2_field(127 + 15 + static_cast<int>(e[sl][i]) - vref) : 0.f;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                acc[sl][nb][2 * i] *= f;
+                acc[sl][nb][2 * i + 1] *= f;
+              }
+            }
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -493,66 +520,67 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[mb][nb][i] *= alpha[nb][i & 1];
         }
-        uint32_t pf[NB][2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int sl = 0; sl < kSlices; ++sl) {
+          uint32_t pf[NB][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            pf[nb][i] = transpose8x8(
-                pack2<kMmaBf16>(kFp8 ? acc[nb][2 * i] * pfac[i] : acc[nb][2 * i],
-                                kFp8 ? acc[nb][2 * i + 1] * pfac[i] : acc[nb][2 * i + 1]));
-        if constexpr (!kFp8) {
-          const int r = warp * kSliceKeys + (lane >> 4) * 8 + (lane & 7);
-          const uint32_t base = smem_u32(s.ring[vs]) + r * 128;
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int mb = 0; mb < kSteps; ++mb) {
-            const int chunk = (mb & 3) * 2 + ((lane >> 3) & 1);
-            uint32_t a[4];
-            ldmatrix4_trans(a, base + (mb >> 2) * kTile * 128 + ((chunk ^ (r & 7)) << 4));
+            for (int i = 0; i < 2; ++i)
+              pf[nb][i] =
+                  transpose8x8(pack2<kMmaBf16>(acc[sl][nb][2 * i], acc[sl][nb][2 * i + 1]));
+          if constexpr (!kFp8) {
+            const uint32_t base = smem_u32(s.ring[vs]) + sl * 16 * 128;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<kMmaBf16>(o[mb][nb], a, pf[nb][0], pf[nb][1]);
-          }
-        } else {
-          // keys 2t, 2t+1, 2t+8, 2t+9 of the slice, D / 8 columns each
-          constexpr int kWords = D / 32;
-          uint32_t v8[4][kWords];
+            for (int mb = 0; mb < kSteps; ++mb) {
+              uint32_t a[4];
+              ldmatrix4_trans(a, base + voff[mb & 3] + (mb >> 2) * kTile * 128);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = warp * kSliceKeys + 2 * t + (i & 1) + (i >> 1) * 8;
-            const uint8_t* row = s.ring[vs] + r * kRowBytes;
-            if constexpr (D == 128) {
-              const uint4 v = *reinterpret_cast<const uint4*>(row + ((g ^ (r & 7)) << 4));
-              v8[i][0] = v.x;
-              v8[i][1] = v.y;
-              v8[i][kWords - 2] = v.z;
-              v8[i][kWords - 1] = v.w;
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(
-                  row + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
-              v8[i][0] = v.x;
-              v8[i][1] = v.y;
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816<kMmaBf16>(o[mb][nb], a, pf[nb][0], pf[nb][1]);
             }
-          }
+          } else {
+            // keys 2t, 2t+1, 2t+8, 2t+9 of the slice, D / 8 columns each
+            constexpr int kWords = D / 32;
+            uint32_t v8[4][kWords];
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            const uint32_t x0 = __byte_perm(v8[0][w], v8[1][w], 0x5140),
-                           x1 = __byte_perm(v8[0][w], v8[1][w], 0x7362),
-                           y0 = __byte_perm(v8[2][w], v8[3][w], 0x5140),
-                           y1 = __byte_perm(v8[2][w], v8[3][w], 0x7362);
-            const uint32_t a0[4] = {e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(x0 >> 16),
-                                    e4m3x2_to_f16x2(y0), e4m3x2_to_f16x2(y0 >> 16)};
-            const uint32_t a1[4] = {e4m3x2_to_f16x2(x1), e4m3x2_to_f16x2(x1 >> 16),
-                                    e4m3x2_to_f16x2(y1), e4m3x2_to_f16x2(y1 >> 16)};
+            for (int i = 0; i < 4; ++i) {
+              const uint8_t* row =
+                  s.ring[vs] + voff[i & 1] + (sl * 16 + (i >> 1) * 8) * kRowBytes;
+              if constexpr (D == 128) {
+                const uint4 v = *reinterpret_cast<const uint4*>(row);
+                v8[i][0] = v.x;
+                v8[i][1] = v.y;
+                v8[i][kWords - 2] = v.z;
+                v8[i][kWords - 1] = v.w;
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(row);
+                v8[i][0] = v.x;
+                v8[i][1] = v.y;
+              }
+            }
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816<kMmaBf16>(o[2 * w][nb], a0, pf[nb][0], pf[nb][1]);
-              mma16816<kMmaBf16>(o[2 * w + 1][nb], a1, pf[nb][0], pf[nb][1]);
+            for (int w = 0; w < kWords; ++w) {
+              const uint32_t x0 = __byte_perm(v8[0][w], v8[1][w], 0x5140),
+                             x1 = __byte_perm(v8[0][w], v8[1][w], 0x7362),
+                             y0 = __byte_perm(v8[2][w], v8[3][w], 0x5140),
+                             y1 = __byte_perm(v8[2][w], v8[3][w], 0x7362);
+              const uint32_t a0[4] = {e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(x0 >> 16),
+                                      e4m3x2_to_f16x2(y0), e4m3x2_to_f16x2(y0 >> 16)};
+              const uint32_t a1[4] = {e4m3x2_to_f16x2(x1), e4m3x2_to_f16x2(x1 >> 16),
+                                      e4m3x2_to_f16x2(y1), e4m3x2_to_f16x2(y1 >> 16)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                mma16816<kMmaBf16>(o[2 * w][nb], a0, pf[nb][0], pf[nb][1]);
+                mma16816<kMmaBf16>(o[2 * w + 1][nb], a1, pf[nb][0], pf[nb][1]);
+              }
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.empty[vs]);
       }
+      tiles += static_cast<uint32_t>(max(0, x.tile1 - x.tile0));
 
       // -- join the warps: row q of each group of eight is summed by warp q
 #pragma unroll
@@ -571,32 +599,38 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (lane == 0) s.vscale[warp] = kFp8 ? exp2_field(vref - 15) : 1.f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-        for (int mb = 0; mb < kSteps; ++mb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // 16-bit: column 16 mb + g (+ 8); e4m3: column (D / 8) g + 2 mb (+ 1)
-            const int d = kFp8 ? (D / 8) * g + 2 * mb + (i >> 1) : 16 * mb + g + 8 * (i >> 1);
-            s.merge[warp][2 * t + (i & 1)][d] = o[mb][nb][i];
-          }
-        named_bar_sync(1, kConsumers * 32);
         const int r = nb * 8 + warp;
-        if (r < x.rows) {
-          float top = -INFINITY;
+        constexpr int kN = D / 32;
+        float top = -INFINITY, sum = 0.f, out[kN] = {};
 #pragma unroll
-          for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, s.m[w][r]);
+        for (int gr = 0; gr < kGroups; ++gr) {
+          if (group == gr)
+#pragma unroll
+            for (int mb = 0; mb < kSteps; ++mb)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // 16-bit: column 16 mb + g (+ 8); e4m3: column (D / 8) g + 2 mb (+ 1)
+                const int d = kFp8 ? (D / 8) * g + 2 * mb + (i >> 1) : 16 * mb + g + 8 * (i >> 1);
+                s.merge[warp % kGroupWarps][2 * t + (i & 1)][d] = o[mb][nb][i];
+              }
+          named_bar_sync(1, kConsumers * 32);
+          if (gr == 0)
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, s.m[w][r]);
           const float ref = top == -INFINITY ? 0.f : top;
-          constexpr int kN = D / 32;
-          float sum = 0.f, out[kN] = {};
 #pragma unroll
-          for (int w = 0; w < kConsumers; ++w) {
-            const float a = ex2_approx(s.m[w][r] - ref);
-            sum = fmaf(s.l[w][r], a, sum);
-            const float av = kFp8 ? a * s.vscale[w] : a;
+          for (int w = 0; w < kGroupWarps; ++w) {
+            const int from = gr * kGroupWarps + w;
+            const float a = ex2_approx(s.m[from][r] - ref);
+            sum = fmaf(s.l[from][r], a, sum);
+            const float av = kFp8 ? a * s.vscale[from] : a;
             const float* src = &s.merge[w][warp][lane * kN];
 #pragma unroll
             for (int e = 0; e < kN; ++e) out[e] = fmaf(src[e], av, out[e]);
           }
+          named_bar_sync(1, kConsumers * 32);
+        }
+        if (r < x.rows) {
           if (x.whole) {
             int token, head;
             row_of(p, row0, r, x.hk, token, head);
@@ -615,7 +649,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (lane == 0) p.part_ml[at] = make_float2(top, sum);
           }
         }
-        named_bar_sync(1, kConsumers * 32);
       }
     }
   }
@@ -635,9 +668,8 @@ cudaError_t launch_few_t(const PagedLaunch& a, cudaStream_t s) {
 
 template <int D, bool kFp8, bool kBf16>
 cudaError_t launch_few_n(const PagedLaunch& a, cudaStream_t s) {
-  return a.block_rows == 8    ? launch_few_t<D, kFp8, kBf16, 1>(a, s)
-         : a.block_rows == 16 ? launch_few_t<D, kFp8, kBf16, 2>(a, s)
-                            : launch_few_t<D, kFp8, kBf16, 4>(a, s);
+  return a.block_rows == 8 ? launch_few_t<D, kFp8, kBf16, 1>(a, s)
+                           : launch_few_t<D, kFp8, kBf16, 2>(a, s);
 }
 
 template <int D>
@@ -652,7 +684,7 @@ cudaError_t launch_few_d(const PagedLaunch& a, cudaStream_t s) {
 }  // namespace
 
 int paged_few_rows(long long rows, int batch) {
-  return rows <= 8LL * batch ? 8 : rows <= 16LL * batch ? 16 : 32;
+  return rows <= 8LL * batch ? 8 : 16;
 }
 
 cudaError_t launch_paged_few(const PagedLaunch& a, cudaStream_t s) {

@@ -240,14 +240,8 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
       bool stop = false;
       while (!stop && take_unit(s, taken++, u, p.err, abort_flag)) {
         if (u.first > u.last) continue;
-        const int* table = p.r.table + u.b * p.r.table_stride;
-        auto page_of = [&](int tile) {
-          const int k0 = tile * kTile + lane * box_rows;
-          const bool wanted =
-              lane < per_tile && tile <= u.last && k0 < u.key_hi && k0 + box_rows > u.key_lo;
-          return wanted ? table[k0 >> p.page_log2] : -2;
-        };
-        int page = page_of(u.first);
+        PageFeed feed;
+        feed.start(p, u.b, u.first, u.key_lo, u.key_hi);
         // Q once the last S product of the unit before has read it
         if (units > 0 && !many_warp_wait(&s.q_empty, (units - 1) & 1, p.err, abort_flag)) break;
         if (lane == 0) {
@@ -263,7 +257,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           const int k0 = j * kTile + lane * box_rows;
           const bool mine = lane < per_tile && k0 < u.key_hi && k0 + box_rows > u.key_lo;
           const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
-          const int next_page = page_of(j + 1);
+          int page = feed.get(p, j, k0);
           if (mine && (page < 0 || page >= p.pages)) {
             atomicExch(p.err, kDevErrBadIndex);
             page = p.pages;  // out of range for the tensor map: reads as zeros
@@ -306,7 +300,6 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
             ++n;
           }
           if (stop) break;
-          page = next_page;
         }
       }
       if (*abort_flag && lane == 0) {

@@ -15,7 +15,7 @@ namespace {
 constexpr long long kMaxBytes = 1ll << 40;  // every operand lies below this from its base
 constexpr int kMaxRows = 1 << 29;           // packed rows, keys of a sequence, window bounds
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWholeKeysFew = 1024, kWholeKeysMany = 1024;
+constexpr int kWholeKeysFew = 512, kWholeKeysMany = 1024;
 
 bool aligned(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -132,7 +132,7 @@ bool paged_plan(int batch, int total, int heads, int heads_k, int D, PagedPlan* 
   if (sm_count(&sms) != cudaSuccess) sms = 160;  // no device: sizes for the checks alone
   const int group = heads / heads_k;
   const long long all = static_cast<long long>(total) * group;
-  plan->many = all > 32LL * batch;
+  plan->many = all > 16LL * batch;
   plan->block_rows = plan->many ? paged_many_rows(group) : paged_few_rows(all, batch);
   const size_t rows = 2ull * sms * plan->block_rows;
   plan->o_bytes = round256(rows * D * sizeof(float));
