@@ -4,8 +4,8 @@
 //
 // Units.  A unit is one block of query rows (rows token * group +
 // head-in-group of one sequence) against one key head.  It walks tiles of 128
-// keys.  Units are laid end to end by their weights, sequence by sequence,
-// head by head, and each CTA takes an equal stretch of the whole, cutting
+// keys.  Units are laid end to end by their weights, key head by key head and
+// within a head sequence by sequence, and each CTA takes an equal stretch of the whole, cutting
 // units where the stretch ends: a long context over few rows is spread over
 // every SM, ragged batches stay balanced, and a CTA leaves at most two cut
 // pieces whatever the batch.  Cut pieces go to the workspace in fp32
@@ -13,6 +13,10 @@
 // order.  Where no sequence of the table can be long (PagedLaunch::whole), units
 // stay whole instead, each with the CTA whose stretch it begins in, and nothing
 // is left to join.
+//
+// Heads come first in that order because a token's rows of all heads lie side by
+// side: the CTAs of the heads then walk the same tokens at about the same time,
+// and what one leaves in an open DRAM page the others find there.
 //
 // Weights.  The few-row kernel gives all units of a sequence the number of key
 // tiles that any of its queries sees, at least 1 (a sequence usually is one
@@ -130,45 +134,44 @@ template <bool kMany>
 __device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) {
   const int lane = threadIdx.x & 31;
   Place at{};
-  // lane i keeps the work of one head of sequences i, and the first 32 stay
+  // lane i sums over sequences i, i + 32, ...; the first 32 stay at hand
   SeqWork<kMany> w;
-  long long head0 = 0;
+  long long seq0 = 0;
   for (int b = lane; b < p.r.batch; b += 32) {
     w.load(p, b, c == 0 ? p.err : nullptr);
-    const long long head = w.blocks ? w.before(p, w.blocks) : 0;
-    if (b == lane) head0 = head;
-    at.total += head * p.heads_k;
+    const long long mine = w.blocks ? w.before(p, w.blocks) : 0;
+    if (b == lane) seq0 = mine;
+    at.total += mine;
   }
-  at.total = warp_sum(at.total);
+  const long long head = warp_sum(at.total);  // the work of one key head
+  at.total = head * p.heads_k;
   at.pos = stretch(at.total, n, c);
   at.left = stretch(at.total, n, c + 1) - at.pos;
   if (at.left == 0) return at;
+  at.hk = static_cast<int>(at.pos / head);
+  const long long in = at.pos - at.hk * head;  // in that head's work
   long long ahead = 0;
   for (int b0 = 0; b0 < p.r.batch; b0 += 32) {
-    long long head = head0;
+    long long mine = seq0;
     if (b0 > 0) {
-      head = 0;
+      mine = 0;
       if (b0 + lane < p.r.batch) {
         w.load(p, b0 + lane);
-        if (w.blocks) head = w.before(p, w.blocks);
+        if (w.blocks) mine = w.before(p, w.blocks);
       }
     }
-    const long long mine = head * p.heads_k;
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += o;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, ahead + upto > at.pos);
+    const uint32_t past = __ballot_sync(0xffffffffu, ahead + upto > in);
     if (past) {
       const int src = __ffs(past) - 1;
       at.b = b0 + src;
-      const long long in = at.pos - ahead - __shfl_sync(0xffffffffu, upto - mine, src);
-      head = __shfl_sync(0xffffffffu, head, src);
+      const long long rem = in - ahead - __shfl_sync(0xffffffffu, upto - mine, src);
       w.load(p, at.b);
-      at.hk = static_cast<int>(in / head);
-      const long long rem = in - at.hk * head;
       // the last block whose predecessors weigh at most rem: 32 tries at once
       int lo = 0, hi = w.blocks;  // it is in [lo, hi)
       while (hi - lo > 1) {
@@ -228,13 +231,12 @@ struct WorkWalk {
       w.load(p, at.b);
       loaded = true;
     }
-    if (at.block >= w.blocks) {
+    while (at.block >= w.blocks) {  // (a sequence without rows has no blocks)
       at.block = 0;
-      ++at.hk;
-    }
-    while (at.hk >= p.heads_k || w.blocks == 0) {
-      at.hk = 0;
-      if (++at.b >= p.r.batch) return false;
+      if (++at.b >= p.r.batch) {
+        at.b = 0;
+        if (++at.hk >= p.heads_k) return false;
+      }
       w.load(p, at.b);
     }
     x.b = at.b;

@@ -8,8 +8,9 @@
 // multiply-adds per element (G query heads to a key head): at 8 bytes moved
 // per 1000 products the tensor cores idle and HBM is the bound.  So the kernel
 // is a stream: one CTA per SM walks its stretch of the work (fa_paged.cuh) and
-// one producer warp keeps a ring of K and V tiles (128 keys each) in flight by
-// TMA, page by page.
+// four producer warps keep rings of K and V tiles (128 keys each) in flight by
+// TMA, page by page.  (One warp took 0.3 us to issue a tile's boxes, which an
+// e4m3 cache streams in 0.4 us.)
 //
 // Eight consumer warps in two groups take alternate tiles, 32 keys of a tile
 // each, with a running maximum, sum and O of their own that are joined once per
@@ -36,8 +37,12 @@
 namespace fa {
 namespace {
 
-constexpr int kConsumers = 8;                        // warps
-constexpr int kFewThreads = (kConsumers + 1) * 32;   // and the producer
+constexpr int kConsumers = 8;                       // warps
+constexpr int kProducers = 4;                       // K and V of either group
+constexpr int kFewThreads = (kConsumers + kProducers) * 32;
+// registers: 12 warps launch with 168 each; 2 x 208 + 80 <= 3 x 168 on each
+// sub-partition
+constexpr uint32_t kFewLow = 80, kFewHigh = 208;
 constexpr int kGroups = 2, kGroupWarps = kConsumers / kGroups;
 constexpr int kSlices = kTile / kGroupWarps / 16;    // 16-key slices of a tile per warp
 constexpr int kRingBytes = 192 * 1024;
@@ -149,20 +154,22 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   WorkWalk<false> walk(s.place);
   Piece x;
 
-  if (warp == kConsumers) {
-    // ---------------------------------------------------------------- producer
+  if (warp >= kConsumers) {
+    // --------------------------------------------------------------- producers
+    setmaxnreg_dec<kFewLow>();
+    const int group = (warp - kConsumers) >> 1, kv = (warp - kConsumers) & 1;
+    const CUtensorMap* map = kv ? &p.map_v : &p.map_k;
+    const uint8_t* exps = kv ? p.v_exp : p.k_exp;
     const int box_rows = min(p.page_size, kTile);
     const int per_tile = kTile / box_rows;
-    if (lane == 0) {
-      tma_prefetch_desc(&p.map_k);
-      tma_prefetch_desc(&p.map_v);
-    }
-    uint32_t tiles = 0;  // begun so far; tile number i belongs to group i % kGroups
-    uint32_t loads0 = 0, loads1 = 0;  // slots filled of each group's ring
+    if (lane == 0) tma_prefetch_desc(map);
+    uint32_t tiles = 0;  // of the pieces before this one
+    uint32_t loads = 0;  // this warp's
     while (walk.next(p, x)) {
       PageFeed feed;
       feed.start(p, x.b, x.tile0, x.lo, x.hi);
-      for (int tile = x.tile0; tile < x.tile1; ++tile, ++tiles) {
+      for (int tile = x.tile0 + ((group - static_cast<int>(tiles)) & (kGroups - 1));
+           tile < x.tile1; tile += kGroups) {
         const int k0 = tile * kTile + lane * box_rows;
         // lane i < per_tile: the i-th box of the tile, if a visible key lies in it
         const bool mine = lane < per_tile && k0 < x.hi && k0 + box_rows > x.lo;
@@ -173,48 +180,44 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           page = p.pages;  // out of range for the tensor map: reads as zeros
         }
         const int row = k0 & (p.page_size - 1);
+        const uint32_t n = 2 * loads + kv;  // in the group's ring
+        const int slot = group * kRing + n % kRing;
+        if (n >= kRing) ring_wait(&s.empty[slot], (n / kRing - 1) & 1, p.err, abort_flag);
+        if (__any_sync(0xffffffffu, *abort_flag)) goto stopped;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&s.full[slot], boxes * box_rows * (kRowBytes + (kFp8 ? 1 : 0)));
+        __syncwarp();
+        if (mine) {
+          uint8_t* dst = s.ring[slot] + lane * box_rows * (kRowBytes < 128 ? kRowBytes : 128);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t n = 2 * (tiles / kGroups) + kv;  // in its group's ring
-          const int slot = static_cast<int>(tiles % kGroups) * kRing + n % kRing;
-          if (n >= kRing) ring_wait(&s.empty[slot], (n / kRing - 1) & 1, p.err, abort_flag);
-          if (__any_sync(0xffffffffu, *abort_flag)) goto stopped;
-          (tiles % kGroups ? loads1 : loads0) += 1;
-          if (lane == 0)
-            mbar_arrive_expect_tx(&s.full[slot],
-                                  boxes * box_rows * (kRowBytes + (kFp8 ? 1 : 0)));
-          __syncwarp();
-          if (mine) {
-            uint8_t* dst = s.ring[slot] + lane * box_rows * (kRowBytes < 128 ? kRowBytes : 128);
-#pragma unroll
-            for (int kb = 0; kb < (kRowBytes + 127) / 128; ++kb)
-              tma_load_4d(dst + kb * kTile * 128, kv ? &p.map_v : &p.map_k, &s.full[slot],
-                          kb * 64, row, x.hk, page);
-            if constexpr (kFp8) {
-              // (of a page that does not exist, any exponents will do)
-              const uint8_t* e = (kv ? p.v_exp : p.k_exp) +
-                                 (static_cast<long long>(page < p.pages ? page : 0) * p.heads_k +
-                                  x.hk) * p.page_size + row;
-              bulk_load(s.exps[slot] + lane * box_rows, e, box_rows, &s.full[slot]);
-            }
-          }
+          for (int kb = 0; kb < (kRowBytes + 127) / 128; ++kb)
+            tma_load_4d(dst + kb * kTile * 128, map, &s.full[slot], kb * 64, row, x.hk, page);
+          if constexpr (kFp8)  // (of a page that does not exist, any exponents will do)
+            bulk_load(s.exps[slot] + lane * box_rows,
+                      exps + (static_cast<long long>(page < p.pages ? page : 0) * p.heads_k +
+                              x.hk) * p.page_size + row,
+                      box_rows, &s.full[slot]);
         }
+        ++loads;
       }
+      tiles += static_cast<uint32_t>(max(0, x.tile1 - x.tile0));
     }
   stopped:
     if (*abort_flag) {
       // Copies in flight land before the CTA's shared memory goes away.
       int zero = 0;
       if (lane == 0)
-        for (int gr = 0; gr < kGroups; ++gr) {
-          const uint32_t loads = gr ? loads1 : loads0;
-          for (uint32_t n = loads > kRing ? loads - kRing : 0; n < loads; ++n)
-            mbar_wait(&s.full[gr * kRing + n % kRing], (n / kRing) & 1, p.err, &zero, 100000000ull);
+        for (uint32_t i = loads > kRing ? loads - kRing : 0; i < loads; ++i) {
+          const uint32_t n = 2 * i + kv;
+          if (n + kRing >= 2 * loads)  // (earlier ones have been read)
+            mbar_wait(&s.full[group * kRing + n % kRing], (n / kRing) & 1, p.err, &zero,
+                      100000000ull);
         }
     }
     __syncwarp();
   } else {
     // --------------------------------------------------------------- consumers
+    setmaxnreg_inc<kFewHigh>();
     const int g = lane >> 2, t = lane & 3;
     const int group = warp / kGroupWarps;
     const int slice0 = (warp % kGroupWarps) * kSlices * 16;  // this warp's first row of a tile

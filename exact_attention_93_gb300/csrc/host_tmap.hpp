@@ -37,7 +37,8 @@ inline bool make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType
                          uint64_t inner, uint64_t rows, uint64_t heads, uint64_t batches,
                          uint64_t row_stride, uint64_t head_stride, uint64_t batch_stride,
                          uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle,
-                         uint64_t elem_bytes = 2, uint32_t box_heads = 1) {
+                         uint64_t elem_bytes = 2, uint32_t box_heads = 1,
+                         CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[4] = {inner, rows, heads, batches};
@@ -46,7 +47,7 @@ inline bool make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType
   cuuint32_t box[4] = {box_inner, box_rows, box_heads, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, dtype, 4, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
