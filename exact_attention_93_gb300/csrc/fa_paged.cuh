@@ -46,7 +46,8 @@ __device__ __forceinline__ void visible_span(const PagedLaunch& p, const Seq& s,
 }
 
 // sum over i < n of floor((a i + b) / m), a and b not negative, by Euclid's
-// algorithm on (a, m).
+// algorithm on (a, m).  m starts at 128 and n below 2^23, so that a n + b, with
+// a and b reduced, fits 32 bits throughout.
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long sum = 0;
   while (n > 0) {
@@ -58,10 +59,10 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
       sum += static_cast<long long>(n) * (b / m);
       b %= m;
     }
-    const unsigned long long y = static_cast<unsigned long long>(a) * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
-    n = static_cast<uint32_t>(y / m);
-    b = static_cast<uint32_t>(y % m);
+    n = y / m;
+    b = y - n * m;
     const uint32_t t = m;
     m = a;
     a = t;
@@ -119,8 +120,18 @@ struct Place {
   long long total;
 };
 
+// a / b for a >= 0, b > 0; a 64-bit division is a long instruction sequence.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// floor(total c / n)
 __device__ __forceinline__ long long stretch(long long total, int n, int c) {
-  return total * c / n;
+  const long long q = divide(total, n);
+  const uint32_t r = static_cast<uint32_t>(total - q * n);
+  return q * c + r * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);
 }
 
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -148,7 +159,7 @@ __device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) 
   at.pos = stretch(at.total, n, c);
   at.left = stretch(at.total, n, c + 1) - at.pos;
   if (at.left == 0) return at;
-  at.hk = static_cast<int>(at.pos / head);
+  at.hk = static_cast<int>(divide(at.pos, head));
   const long long in = at.pos - at.hk * head;  // in that head's work
   long long ahead = 0;
   for (int b0 = 0; b0 < p.r.batch; b0 += 32) {
