@@ -351,7 +351,7 @@ constexpr int kJoinRows = 4, kJoinThreads = 64;
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_join_kernel(const __grid_constant__ PagedLaunch p) {
-  pdl_wait();
+  pdl_wait_and_release();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const JoinTask task = p.tasks[c];
   constexpr int kN = D / 32, kWarps = kJoinThreads / 32;

@@ -15,7 +15,7 @@ namespace {
 constexpr long long kMaxBytes = 1ll << 40;  // every operand lies below this from its base
 constexpr int kMaxRows = 1 << 29;           // packed rows, keys of a sequence, window bounds
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWholeKeysFew = 512, kWholeKeysMany = 1024;
+constexpr int kWholeKeysFew = 1536, kWholeKeysMany = 1024;
 
 bool aligned(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
