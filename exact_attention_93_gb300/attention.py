@@ -214,29 +214,13 @@ def flash_attn_paged_func(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
     headdim) (and the fp32 (nheads, total) log-sum-exp when return_lse).  A row
     that sees no key gets zeros and -inf; rows behind the last sequence are not
     written.  Forward only."""
-    if torch.is_grad_enabled() and q.requires_grad:
-        raise ValueError("attention over a cache has no backward: call under torch.no_grad()")
-    cache = fattn.kv_pages(k_pages, v_pages, k_exp, v_exp)
-    shape, heads_k = q.shape, k_pages.shape[2]
-    if len(shape) != 3 or q.stride(2) != 1 or shape[2] != k_pages.shape[3]:
-        raise ValueError("q must be a packed (total, nheads, headdim) tensor of the cache's "
-                         "headdim, which must be contiguous")
-    total, H, D = shape
-    if H % heads_k:
-        raise ValueError("nheads must be a multiple of the cache's heads")
-    if seqlens is None:
-        raise ValueError("seqlens is needed")
-    batch = fattn.ragged(block_table, cu_seqlens, seqlens, total)
-    n, opts = seqlens.shape[0], None
     if alibi_slopes is not None or window_size != (-1, -1):
-        window, alibi_slopes = _check_options(0.0, window_size, alibi_slopes, n, H)
-    device = fattn.one_device(q, k_pages, v_pages, block_table, cu_seqlens, seqlens, alibi_slopes)
-    if alibi_slopes is not None or window_size != (-1, -1):
-        opts = fattn.options(window, alibi_slopes)
-    with fattn.on_device(device):
-        o = torch.empty_like(q, memory_format=torch.contiguous_format)
-        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
-        fattn.fa_fwd_paged(q, o, lse, cache, batch, n, heads_k, opts,
-                           D ** -0.5 if softmax_scale is None else float(softmax_scale),
-                           bool(causal), fattn.raw_stream(device))
-    return (o, lse) if return_lse else o
+        window_size, alibi_slopes = _check_options(0.0, window_size, alibi_slopes,
+                                                   block_table.shape[0], q.shape[1])
+    got = fattn.bind().paged(
+        q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
+        q.shape[-1] ** -0.5 if softmax_scale is None else softmax_scale, causal, window_size[0],
+        window_size[1], alibi_slopes, k_exp, v_exp)
+    if type(got) is int:
+        fattn._check(got, "fa_fwd_paged")
+    return got if return_lse else got[0]

@@ -1,4 +1,5 @@
-"""Builds libfattn.so in-tree with nvcc for sm_103a.
+"""Builds libfattn.so in-tree with nvcc for sm_103a, and the small native module
+through which torch tensors reach part of it (g++, against the installed torch).
 
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library next to this file.  The CUDA runtime is linked statically and
@@ -20,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfattn.so")
+BIND = os.path.join(HERE, "_bind_torch.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve_api.cu",
            "fa_rotary.cu", "fa_cache.cu", "fa_paged_few.cu", "fa_paged_many.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,9 +44,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -65,15 +67,46 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bind = ex.submit(compile_bind)
         objs = list(ex.map(compile_one, SOURCES))
+        bind_obj, torch_lib = bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # the module finds libfattn.so beside itself, and torch's libraries in the
+    # process that imports it
+    tmp = BIND + f".tmp{os.getpid()}"
+    run(["g++", "-shared", "-o", tmp, bind_obj, "-L" + HERE, "-l:libfattn.so", "-L" + torch_lib,
+         "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"],
+        "link failed")
+    os.replace(tmp, BIND)
     return LIB
+
+
+def run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+
+
+def compile_bind():
+    """The object file of bind_torch.cpp, and where torch's libraries are."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD, "bind_torch.o")
+    run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I" + INCLUDE,
+         "-I" + sysconfig.get_path("include"), "-isystem", os.path.join(root, "include"),
+         "-isystem", os.path.join(cuda, "include"),
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-c", os.path.join(CSRC, "bind_torch.cpp"), "-o", obj], "g++ failed for bind_torch.cpp")
+    return obj, os.path.join(root, "lib")
 
 
 if __name__ == "__main__":

@@ -140,7 +140,7 @@ __global__ void __maxnreg__(kFewRegs)
     const Place at = warp_place<false>(p, gridDim.x, blockIdx.x);
     if (lane == 0) {
       s.place = at;
-      if (at.left == 0) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
+      if (at.left == 0 && !p.whole) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
     }
   }
   if (threadIdx.x == 32) {
@@ -247,7 +247,7 @@ __global__ void __maxnreg__(kFewRegs)
     while (walk.next(p, x)) {
       const Seq& seq = walk.w.s;
       const int row0 = x.block * kRows;
-      if (threadIdx.x == 0) p.tasks[blockIdx.x] = join_task(p, x, seq);
+      if (threadIdx.x == 0 && !p.whole) p.tasks[blockIdx.x] = join_task(p, x, seq);
       // -- queries as B operands, and what each of this lane's columns sees
       uint32_t qf[NB][kSteps][2];
       float qscale[NB][2];

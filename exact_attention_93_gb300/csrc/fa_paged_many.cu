@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
     } else if (warp == 10) {
       // -------------------------------------------------------------- units
       const Place at = warp_place<true>(p, gridDim.x, blockIdx.x);
-      if (lane == 0 && at.left == 0) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
+      if (lane == 0 && at.left == 0 && !p.whole) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
       WorkWalk<true> walk(at);
       Piece x;
       for (uint32_t n = 0;; ++n) {
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           v.hk = x.hk;
           v.slot = x.whole ? -1 : x.slot;
           v.valid = 1;
-          if (lane == 0) p.tasks[blockIdx.x] = join_task(p, x, q);
+          if (lane == 0 && !p.whole) p.tasks[blockIdx.x] = join_task(p, x, q);
         }
         const int slot = n % kUnitRing;
         if (n >= kUnitRing && !many_warp_wait(&s.unit_empty[slot], (n / kUnitRing - 1) & 1, p.err,

@@ -86,6 +86,7 @@ struct PagedLaunch {
   int alibi_bstride;
   int block_rows;   // query rows of a unit
   int whole;        // units are not cut
+  // unless whole:
   float* part_o;    // [2 sms][block_rows][D]
   float2* part_ml;  // [2 sms][block_rows]: maximum, sum
   JoinTask* tasks;  // [sms]

@@ -122,23 +122,27 @@ fa_status cache_rows(const fa_kv_pages* cache, const fa_ragged* batch, const int
 // Query rows per sequence and key head that the batch has on average decide
 // the kernel and its row blocks.
 struct PagedPlan {
-  bool many;
+  bool many, whole;
   int block_rows;
   size_t o_bytes, ml_bytes, total_bytes;
 };
 
-bool paged_plan(int batch, int total, int heads, int heads_k, int D, PagedPlan* plan) {
+void paged_plan(int batch, int total, int heads, int heads_k, int D, long long max_keys,
+                PagedPlan* plan) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) sms = 160;  // no device: sizes for the checks alone
   const int group = heads / heads_k;
   const long long all = static_cast<long long>(total) * group;
   plan->many = all > 16LL * batch;
   plan->block_rows = plan->many ? paged_many_rows(group) : paged_few_rows(all, batch);
-  const size_t rows = 2ull * sms * plan->block_rows;
+  // Below this many keys a sequence, cutting a unit and joining its pieces costs
+  // more than it saves.
+  plan->whole = max_keys <= (plan->many ? kWholeKeysMany : kWholeKeysFew);
+  const size_t rows = plan->whole ? 0 : 2ull * sms * plan->block_rows;
   plan->o_bytes = round256(rows * D * sizeof(float));
   plan->ml_bytes = round256(rows * sizeof(float2));
-  plan->total_bytes = plan->o_bytes + plan->ml_bytes + round256(32ull * sms);
-  return true;
+  plan->total_bytes =
+      plan->whole ? 0 : plan->o_bytes + plan->ml_bytes + round256(32ull * sms);
 }
 
 bool paged_sizes_ok(int batch, int total, int heads, int heads_k, int D) {
@@ -252,12 +256,16 @@ fa_status fa_cache_read(const fa_kv_pages* cache, const fa_ragged* batch, const 
                     launch_cache_read);
 }
 
-size_t fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k, int D) {
+fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k, int D,
+                                      long long max_keys, size_t* bytes) {
+  if (!bytes) return FA_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (!paged_sizes_ok(batch, total, heads, heads_k, D) || max_keys < 0) return FA_ERR_INVALID_ARG;
   PagedPlan plan;
-  if (!paged_sizes_ok(batch, total, heads, heads_k, D) ||
-      !paged_plan(batch, total, heads, heads_k, D, &plan))
-    return 0;
-  return plan.total_bytes;
+  paged_plan(batch, total, heads, heads_k, D, max_keys, &plan);
+  *bytes = plan.total_bytes;
+  return FA_OK;
 }
 
 fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void* o,
@@ -289,9 +297,11 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
       !packed_ok(o, o_token, o_head, batch->total, heads, D) || !aligned(lse, 4))
     return FA_ERR_INVALID_ARG;
   PagedPlan plan;
-  if (!paged_plan(batch->batch, batch->total, heads, cache->heads, D, &plan))
+  paged_plan(batch->batch, batch->total, heads, cache->heads, D,
+             static_cast<long long>(batch->max_pages) * cache->page_size, &plan);
+  if (plan.total_bytes &&
+      (!aligned(workspace, 256) || workspace_bytes < plan.total_bytes))
     return FA_ERR_INVALID_ARG;
-  if (!aligned(workspace, 256) || workspace_bytes < plan.total_bytes) return FA_ERR_INVALID_ARG;
   if (!page_map(&a.map_k, cache->k, cache, cache->k_page, cache->k_token, cache->k_head) ||
       !page_map(&a.map_v, cache->v, cache, cache->v_page, cache->v_token, cache->v_head))
     return FA_ERR_CUDA;
@@ -315,15 +325,14 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
   a.cache_elem = cache->type;
   a.elem = dtype;
   a.scale_log2 = scale * kLog2e;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.o_bytes);
-  a.tasks = reinterpret_cast<JoinTask*>(static_cast<uint8_t*>(workspace) + plan.o_bytes +
-                                        plan.ml_bytes);
+  if (!plan.whole) {
+    auto* base = static_cast<uint8_t*>(workspace);
+    a.part_o = reinterpret_cast<float*>(base);
+    a.part_ml = reinterpret_cast<float2*>(base + plan.o_bytes);
+    a.tasks = reinterpret_cast<JoinTask*>(base + plan.o_bytes + plan.ml_bytes);
+  }
   a.block_rows = plan.block_rows;
-  // Below this many keys a sequence, cutting a unit and joining its pieces costs
-  // more than it saves.
-  a.whole = static_cast<long long>(batch->max_pages) * cache->page_size <=
-            (plan.many ? kWholeKeysMany : kWholeKeysFew);
+  a.whole = plan.whole;
   if (sm_count(&a.sms) != cudaSuccess) return FA_ERR_CUDA;
   a.err = device_error_word();
   if (!a.err) return FA_ERR_CUDA;

@@ -8,11 +8,9 @@ missing or cannot load, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
-import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -111,7 +109,7 @@ def load(path: str | None = None):
             "fa_rotary": (i, [vp, vp, i, i, i, i, vp, vp, i, ll, f, i, i, i, vp]),
             "fa_cache_append": (i, [vp, vp, vp, ll, ll, vp, ll, ll, i, vp]),
             "fa_cache_read": (i, [vp, vp, vp, vp, ll, ll, vp, ll, ll, i, vp]),
-            "fa_fwd_paged_workspace_size": (sz, [i, i, i, i, i]),
+            "fa_fwd_paged_workspace_size": (i, [i, i, i, i, i, ll, ctypes.POINTER(sz)]),
             "fa_fwd_paged": (i, [vp, ll, ll, vp, ll, ll, vp, vp, vp, i, vp, f, i, i, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
@@ -450,180 +448,26 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, deterministic=False,
 
 
 # --------------------------------------------------------------------------
-# include/fattn_cache.h: rotary positions, the paged cache, attention over it
-#
-# These calls are made once per layer and token while generating, so their
-# marshalling is kept short: the C structs are packed as bytes (native
-# alignment), pointers are plain integers, and the current stream is asked for
-# as the raw handle.
+# include/fattn_cache.h: rotary positions, the paged cache, attention over it.
+# Its torch-facing calls (rotary.py, kvcache.py, attention.py) go through a small
+# native module, csrc/bind_torch.cpp; load() has the C entry points themselves.
 # --------------------------------------------------------------------------
 
-_pack_rotary_operand = struct.Struct("@PPi6q").pack  # fa_rotary_operand
-_pack_kv_pages = struct.Struct("@4P6q5i").pack       # fa_kv_pages
-_pack_ragged = struct.Struct("@PqiPPii").pack        # fa_ragged
-
-_ELEMS = None
+_bind = None
 
 
-def elem_code(dtype) -> int:
-    """fa_elem of a torch dtype."""
-    global _ELEMS
-    if _ELEMS is None:
-        torch = _torch()
-        _ELEMS = {torch.bfloat16: FA_ELEM_BF16, torch.float16: FA_ELEM_FP16,
-                  torch.float32: FA_ELEM_FP32, torch.float8_e4m3fn: FA_ELEM_E4M3}
-    code = _ELEMS.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return code
-
-
-def raw_stream(device: int, stream=None) -> int:
-    """The cudaStream_t of `stream`, or of the device's current stream."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(device)
-
-
-def on_device(device: int):
-    """A context in which `device` is the current device."""
-    torch = _torch()
-    if torch._C._cuda_getDevice() == device:
-        return _NOTHING
-    return torch.cuda.device(device)
-
-
-_NOTHING = contextlib.nullcontext()
-
-
-def one_device(first, *others) -> int:
-    """The CUDA device that all tensors (None is skipped) are on."""
-    device = first.get_device()
-    if device >= 0:
-        for t in others:
-            if t is not None and t.get_device() != device:
-                break
-        else:
-            return device
-    raise ValueError("libfattn takes CUDA tensors of one device only")
-
-
-def rotary_operand(x, y) -> bytes:
-    """fa_rotary_operand of (batch, seq, heads, D) tensors x -> y (or packed
-    (seq, heads, D) ones)."""
-    xs, ys = x.stride(), y.stride()
-    if xs[-1] != 1 or ys[-1] != 1:
-        raise ValueError("the head dimension D must be contiguous")
-    if len(xs) == 3:
-        return _pack_rotary_operand(x.data_ptr(), y.data_ptr(), x.shape[1], 0, xs[1], xs[0], 0,
-                                    ys[1], ys[0])
-    return _pack_rotary_operand(x.data_ptr(), y.data_ptr(), x.shape[2], xs[0], xs[2], xs[1],
-                                ys[0], ys[2], ys[1])
-
-
-def kv_pages(k_pages, v_pages, k_exp=None, v_exp=None) -> bytes:
-    """fa_kv_pages of (pages, page_size, heads, D) tensors, and for e4m3 ones
-    their (pages, heads, page_size) exponent bytes."""
-    shape, dtype = k_pages.shape, k_pages.dtype
-    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype != dtype:
-        raise ValueError("k_pages and v_pages must be (pages, page_size, heads, D) tensors of "
-                         "one shape and type")
-    pages, page_size, heads, dim = shape
-    ks, vs = k_pages.stride(), v_pages.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("the head dimension D must be contiguous")
-    code = elem_code(dtype)
-    ke = ve = 0
-    if code == FA_ELEM_E4M3:
-        for e in (k_exp, v_exp):
-            if (e is None or e.dtype != _torch().uint8 or e.shape != (pages, heads, page_size)
-                    or not e.is_contiguous() or e.device != k_pages.device):
-                raise ValueError("an e4m3 cache needs k_exp and v_exp: contiguous uint8 "
-                                 "(pages, heads, page_size) tensors on its device")
-        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
-    elif k_exp is not None or v_exp is not None:
-        raise ValueError("k_exp and v_exp belong to an e4m3 cache")
-    return _pack_kv_pages(k_pages.data_ptr(), v_pages.data_ptr(), ke, ve, ks[0], ks[1], ks[2],
-                          vs[0], vs[1], vs[2], pages, page_size, heads, dim, code)
-
-
-def ragged(block_table, cu_seqlens, seqlens, total: int) -> bytes:
-    """fa_ragged of a (batch, max_pages) table, (batch + 1) boundaries and
-    (batch) lengths (or None), int32 tensors."""
-    i32 = _torch().int32
-    shape, st = block_table.shape, block_table.stride()
-    if len(shape) != 2 or block_table.dtype != i32 or (st[1] != 1 and shape[1] > 1):
-        raise ValueError("block_table must be an int32 (batch, max_pages) tensor with "
-                         "contiguous rows")
-    batch, max_pages = shape
-    if (cu_seqlens.dtype != i32 or cu_seqlens.shape != (batch + 1,)
-            or not cu_seqlens.is_contiguous()):
-        raise ValueError("cu_seqlens must be a contiguous int32 (batch + 1) tensor")
-    lens = 0
-    if seqlens is not None:
-        if seqlens.dtype != i32 or seqlens.shape != (batch,) or not seqlens.is_contiguous():
-            raise ValueError("sequence lengths and starts must be contiguous int32 (batch) "
-                             "tensors")
-        lens = seqlens.data_ptr()
-    return _pack_ragged(block_table.data_ptr(), st[0] if batch > 1 else max(max_pages, st[0]),
-                        max_pages, cu_seqlens.data_ptr(), lens, batch, total)
-
-
-def fa_rotary(q: bytes, k, B: int, N: int, D: int, rotary_dim: int, inv_freq: int,
-              positions: int, position_bits: int, position_batch_stride: int, magnitude: float,
-              interleaved: bool, inverse: bool, elem: int, stream: int):
-    """fa_rotary: operands from rotary_operand (k may be None), device
-    pointers for inv_freq and positions (0: none), a raw stream."""
-    st = (_lib or load()).fa_rotary(q, k, B, N, D, rotary_dim, inv_freq, positions,
-                                    position_bits, position_batch_stride, magnitude, interleaved,
-                                    inverse, elem, stream)
-    if st:
-        _check(st, "fa_rotary")
-
-
-def fa_cache_append(cache: bytes, batch: bytes, k, v, stream: int):
-    """fa_cache_append of packed (total, heads, D) tensors k, v; cache and
-    batch from kv_pages and ragged."""
-    ks, vs = k.stride(), v.stride()
-    st = (_lib or load()).fa_cache_append(cache, batch, k.data_ptr(), ks[0], ks[1], v.data_ptr(),
-                                          vs[0], vs[1], elem_code(k.dtype), stream)
-    if st:
-        _check(st, "fa_cache_append")
-
-
-def fa_cache_read(cache: bytes, batch: bytes, starts, k, v, stream: int):
-    """fa_cache_read into packed (total, heads, D) tensors k, v; starts: an
-    int32 (batch) tensor or None."""
-    ks, vs = k.stride(), v.stride()
-    st = (_lib or load()).fa_cache_read(cache, batch,
-                                        None if starts is None else starts.data_ptr(),
-                                        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                                        elem_code(k.dtype), stream)
-    if st:
-        _check(st, "fa_cache_read")
-
-
-def fa_fwd_paged_workspace_size(batch: int, total: int, heads: int, heads_k: int, D: int) -> int:
-    return int(load().fa_fwd_paged_workspace_size(batch, total, heads, heads_k, D))
-
-
-def fa_fwd_paged(q, o, lse, cache: bytes, batch: bytes, sequences: int, heads_k: int, opts,
-                 scale: float, causal: bool, stream: int, workspace=None):
-    """fa_fwd_paged of packed (total, heads, D) tensors q, o and an fp32
-    (heads, total) lse; cache and batch (of `sequences` sequences) from
-    kv_pages and ragged; opts: FaOptions or None."""
-    lib = _lib or load()
-    total, heads, dim = q.shape
-    if workspace is None:
-        n = lib.fa_fwd_paged_workspace_size(sequences, total, heads, heads_k, dim)
-        if n == 0:
-            raise ValueError("invalid sizes for attention over a paged cache")
-        torch = _torch()
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    qs, os_ = q.stride(), o.stride()
-    st = lib.fa_fwd_paged(q.data_ptr(), qs[0], qs[1], o.data_ptr(), os_[0], os_[1],
-                          lse.data_ptr(), cache, batch, heads,
-                          None if opts is None else ctypes.addressof(opts), scale, causal,
-                          elem_code(q.dtype), workspace.data_ptr(), workspace.numel(), stream)
-    if st:
-        _check(st, "fa_fwd_paged")
+def bind():
+    """The native module of csrc/bind_torch.cpp (built with the library)."""
+    global _bind
+    if _bind is None:
+        load()
+        import importlib.machinery
+        import importlib.util
+        from . import build as _build
+        _torch()  # the module's symbols come from torch's libraries
+        loader = importlib.machinery.ExtensionFileLoader("_bind_torch", _build.BIND)
+        spec = importlib.util.spec_from_file_location("_bind_torch", _build.BIND, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _bind = module
+    return _bind

@@ -18,6 +18,8 @@ from . import fattn
 
 __all__ = ["alloc_kv_cache", "kv_cache_append", "kv_cache_read"]
 
+_ELEMS = {torch.bfloat16: fattn.FA_ELEM_BF16, torch.float16: fattn.FA_ELEM_FP16}
+
 
 def alloc_kv_cache(pages, page_size, nheads, headdim, dtype=torch.bfloat16, device="cuda"):
     """(k_pages, v_pages, k_exp, v_exp) of an empty cache, zeros; the exponent
@@ -38,15 +40,6 @@ def alloc_kv_cache(pages, page_size, nheads, headdim, dtype=torch.bfloat16, devi
             make(exp, torch.uint8), make(exp, torch.uint8))
 
 
-def _check_rows(k, v, k_pages):
-    shape, page = k.shape, k_pages.shape
-    if (len(shape) != 3 or shape != v.shape or shape[1:] != page[2:] or k.dtype != v.dtype
-            or k.stride(2) != 1 or v.stride(2) != 1):
-        raise ValueError(f"k and v must be packed (total, {page[2]}, {page[3]}) tensors of one "
-                         "type with the head dimension contiguous")
-    return shape[0]
-
-
 def kv_cache_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, k_exp=None,
                     v_exp=None):
     """Writes the packed new keys and values ((total, nheads, headdim), bf16 or
@@ -57,16 +50,10 @@ def kv_cache_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, k_
     own power-of-two scale, rounded to nearest even.  Rows of `total` behind the
     last sequence, and rows whose key would be negative, are not written.  The
     slots that one call writes must be distinct."""
-    if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad):
-        raise ValueError("the cache keeps no gradients: call under torch.no_grad()")
-    cache = fattn.kv_pages(k_pages, v_pages, k_exp, v_exp)
-    total = _check_rows(k, v, k_pages)
-    if seqlens is None:
-        raise ValueError("seqlens is needed")
-    batch = fattn.ragged(block_table, cu_seqlens, seqlens, total)
-    device = fattn.one_device(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens)
-    with fattn.on_device(device):
-        fattn.fa_cache_append(cache, batch, k, v, fattn.raw_stream(device))
+    status = fattn.bind().append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, k_exp,
+                                 v_exp)
+    if status:
+        fattn._check(status, "fa_cache_append")
 
 
 def kv_cache_read(k_pages, v_pages, block_table, cu_seqlens, total, starts=None, k_exp=None,
@@ -77,20 +64,9 @@ def kv_cache_read(k_pages, v_pages, block_table, cu_seqlens, total, starts=None,
     be, and to bf16, which holds every e4m3 row exactly.  out: a (k, v) pair to
     write into; rows behind the last sequence are left as they were
     (uninitialised without out)."""
-    cache = fattn.kv_pages(k_pages, v_pages, k_exp, v_exp)
-    if dtype is None:
-        dtype = torch.bfloat16 if k_pages.dtype == torch.float8_e4m3fn else k_pages.dtype
-    total = int(total)
-    if out is None:
-        # one allocation: [0] keys, [1] values
-        k, v = torch.empty((2, total, *k_pages.shape[2:]), dtype=dtype,
-                           device=k_pages.device).unbind()
-    else:
-        k, v = out
-        if _check_rows(k, v, k_pages) != total or k.dtype != dtype:
-            raise ValueError("out must hold `total` rows of dtype")
-    batch = fattn.ragged(block_table, cu_seqlens, starts, total)
-    device = fattn.one_device(k_pages, v_pages, k, v, block_table, cu_seqlens, starts)
-    with fattn.on_device(device):
-        fattn.fa_cache_read(cache, batch, starts, k, v, fattn.raw_stream(device))
-    return k, v
+    k, v = (None, None) if out is None else out
+    got = fattn.bind().read(k_pages, v_pages, block_table, cu_seqlens, total, starts, k_exp, v_exp,
+                            -1 if dtype is None else _ELEMS.get(dtype, fattn.FA_ELEM_FP32), k, v)
+    if type(got) is int:
+        fattn._check(got, "fa_cache_read")
+    return got

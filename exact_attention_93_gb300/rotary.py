@@ -54,43 +54,11 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     return freq.to(device), magnitude
 
 
-def _check(q, k, inv_freq, positions):
-    """Checks the arguments; the device they are on."""
-    shape = q.shape
-    if len(shape) not in (3, 4):
-        raise ValueError("expected (batch, seqlen, nheads, headdim) or packed "
-                         "(total, nheads, headdim) tensors")
-    if k is not None:
-        other = k.shape
-        if (len(other) != len(shape) or other[:-2] != shape[:-2] or other[-1] != shape[-1]
-                or k.dtype != q.dtype):
-            raise ValueError("q and k must agree in type and in every dimension but the heads")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous float64 (rotary_dim / 2) tensor")
-    if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise TypeError("positions must be int32 or int64")
-        if positions.shape != shape[-3:-2] and (len(shape) != 4 or positions.shape != shape[:2]):
-            raise ValueError("positions must have shape (seqlen,) or (batch, seqlen)")
-    return fattn.one_device(q, k, inv_freq, positions)
-
-
-def _turn(device, x, y, x2, y2, inv_freq, positions, magnitude, interleaved, inverse):
-    """Turns x into y, and x2 (unless it is None) into y2."""
-    shape = x.shape
-    B, N = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
-    bits, stride, at = 0, 0, 0
-    if positions is not None:
-        if positions.stride(-1) != 1:
-            positions = positions.contiguous()
-        bits, at = 32 if positions.dtype == torch.int32 else 64, positions.data_ptr()
-        stride = positions.stride(0) if positions.dim() == 2 else 0
-    a = fattn.rotary_operand(x, y)
-    b = None if x2 is None else fattn.rotary_operand(x2, y2)
-    with fattn.on_device(device):
-        fattn.fa_rotary(a, b, B, N, shape[-1], 2 * inv_freq.shape[0], inv_freq.data_ptr(), at,
-                        bits, stride, magnitude, interleaved, inverse, fattn.elem_code(x.dtype),
-                        fattn.raw_stream(device))
+def _call(*args):
+    out = fattn.bind().rotary(*args)
+    if type(out) is int:
+        fattn._check(out, "fa_rotary")
+    return out
 
 
 def _grad_operand(g):
@@ -103,29 +71,28 @@ def _grad_operand(g):
 
 class _Rotary(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, inv_freq, positions, magnitude, interleaved, device):
+    def forward(ctx, q, k, inv_freq, positions, magnitude, interleaved):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(inv_freq, positions)
-        ctx.magnitude, ctx.interleaved, ctx.device = magnitude, interleaved, device
-        yq = torch.empty_like(q, memory_format=torch.contiguous_format)
-        yk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
-        _turn(device, q, yq, k, yk, inv_freq, positions, magnitude, interleaved, False)
-        return yq, yk
+        ctx.magnitude, ctx.interleaved = magnitude, interleaved
+        out = _call(q, k, inv_freq, positions, magnitude, interleaved, False, False)
+        return (out, None) if k is None else out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq, dk):
         inv_freq, positions = ctx.saved_tensors
         grads = [_grad_operand(g) for g in (dq, dk) if g is not None]
-        if not grads:
-            return None, None, None, None, None, None, None
-        outs = [torch.empty_like(g, memory_format=torch.contiguous_format) for g in grads]
-        two = len(grads) > 1
-        _turn(ctx.device, grads[0], outs[0], grads[1] if two else None, outs[1] if two else None,
-              inv_freq, positions, ctx.magnitude, ctx.interleaved, True)
-        gq = outs[0] if dq is not None else None
-        gk = None if dk is None else outs[-1]
-        return gq, gk, None, None, None, None, None
+        out = [None, None]
+        if grads:
+            two = len(grads) > 1
+            got = _call(grads[0], grads[1] if two else None, inv_freq, positions, ctx.magnitude,
+                        ctx.interleaved, True, False)
+            if two:
+                out = got
+            else:
+                out[0 if dq is not None else 1] = got
+        return out[0], out[1], None, None, None, None
 
 
 def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0, inplace=False):
@@ -143,17 +110,8 @@ def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0
     Returns new tensors (q, k), or q alone when k is None.  Differentiable in q
     and k.  inplace=True writes over q and k instead and returns them; it is
     for inference and refuses tensors that need a gradient."""
-    device = _check(q, k, inv_freq, positions)
-    magnitude, interleaved = float(magnitude), bool(interleaved)
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
-        if inplace:
-            raise ValueError("inplace=True would overwrite tensors that need a gradient")
-        yq, yk = _Rotary.apply(q, k, inv_freq, positions, magnitude, interleaved, device)
+    if (not inplace and torch.is_grad_enabled()
+            and (q.requires_grad or (k is not None and k.requires_grad))):
+        yq, yk = _Rotary.apply(q, k, inv_freq, positions, magnitude, interleaved)
         return yq if k is None else (yq, yk)
-    if inplace:
-        yq, yk = q, k
-    else:
-        yq = torch.empty_like(q, memory_format=torch.contiguous_format)
-        yk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
-    _turn(device, q, yq, k, yk, inv_freq, positions, magnitude, interleaved, False)
-    return yq if k is None else (yq, yk)
+    return _call(q, k, inv_freq, positions, magnitude, interleaved, False, inplace)

@@ -130,8 +130,14 @@ fa_status fa_cache_read(const fa_kv_pages* cache, const fa_ragged* batch, const 
                         void* k, long long k_token, long long k_head, void* v, long long v_token,
                         long long v_head, fa_elem dtype, void* stream);
 
-/* Workspace bytes fa_fwd_paged needs (0 for invalid sizes). */
-size_t fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k, int D);
+/*
+ * Workspace bytes that fa_fwd_paged needs for these sizes, max_keys being
+ * max_pages * page_size of its batch and cache.  Zero where it needs none
+ * (short tables: no sequence's work is divided); otherwise room for the partial
+ * results that are joined at the end.
+ */
+fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k, int D,
+                                      long long max_keys, size_t* bytes);
 
 /*
  * Exact attention of packed new tokens over the paged cache (which already
@@ -152,8 +158,8 @@ size_t fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k,
  *   lse      fp32 [heads][total].
  *   options  NULL, or window and ALiBi as for fa_fwd_ex (slopes [heads] or
  *            [batch][heads]); block_mask must be NULL.
- *   workspace  fa_fwd_paged_workspace_size bytes, 256-byte aligned.  Calls that
- *            may overlap on the GPU need one each.
+ *   workspace  fa_fwd_paged_workspace_size bytes, 256-byte aligned (NULL when
+ *            that is zero).  Calls that may overlap on the GPU need one each.
  *
  * Keys and values beyond a sequence's length, and pages that no visible key
  * lies in, are not looked at, whatever they hold.  Inside the span of keys that

@@ -1,11 +1,34 @@
 """Plain 64-bit forms of rotary positions, the paged cache and attention over
-it, on the CPU, and ragged batches to test with."""
+it, on the CPU, ragged batches to test with, and the C structs of
+include/fattn_cache.h."""
+import ctypes
 import math
 
 import torch
 
+from exact_attention_93_gb300 import fattn
+
 EPS = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 E4M3 = torch.float8_e4m3fn
+
+
+# the structs of include/fattn_cache.h
+class KvPages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp")] + [
+        (n, ctypes.c_longlong) for n in ("k_page", "k_token", "k_head", "v_page", "v_token",
+                                         "v_head")] + [
+        (n, ctypes.c_int) for n in ("pages", "page_size", "heads", "head_dim", "type")]
+
+
+class Ragged(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
+                ("max_pages", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("batch", ctypes.c_int), ("total", ctypes.c_int)]
+
+
+class RotaryOperand(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("xs", fattn.FaStrides), ("ys", fattn.FaStrides)]
 
 
 def rotary(x, pos, inv_freq, interleaved=False, magnitude=1.0, inverse=False):

@@ -1,4 +1,5 @@
 """Attention of new tokens over a paged cache against 64 bits, on the GPU."""
+import ctypes
 import math
 
 import pytest
@@ -62,9 +63,11 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])  # wide tables: work may be cut and joined
 @pytest.mark.parametrize("rows,ctx,H,Hk,D,page,dtype,fp8", CASES)
-def test_causal(rows, ctx, H, Hk, D, page, dtype, fp8):
-    b = R.Batch(rows, ctx, Hk, D, page, dtype, fp8, seed=len(rows) + H)
+def test_causal(rows, ctx, H, Hk, D, page, dtype, fp8, wide):
+    b = R.Batch(rows, ctx, Hk, D, page, dtype, fp8, seed=len(rows) + H,
+                spare_cols=200 if wide else 2)
     q, o, lse = run(b, H)
     check(b, H, q, o, lse)
 
@@ -72,9 +75,10 @@ def test_causal(rows, ctx, H, Hk, D, page, dtype, fp8):
 @pytest.mark.parametrize("causal,window", [(False, (-1, -1)), (True, (0, -1)), (True, (40, 7)),
                                            (False, (100, 3)), (False, (-1, 20)), (True, (2000, 0))])
 @pytest.mark.parametrize("fp8,D", [(False, 128), (True, 64)])
-@pytest.mark.parametrize("rows", [[1, 1, 1], [3, 90, 17], [300, 5, 129]])
-def test_windows(causal, window, fp8, D, rows):
-    b = R.Batch(rows, [1000, 150, 0], 2, D, 32, BF, fp8, seed=3)
+@pytest.mark.parametrize("rows,spare", [([1, 1, 1], 2), ([1, 1, 1], 90), ([3, 90, 17], 90),
+                                        ([300, 5, 129], 2)])
+def test_windows(causal, window, fp8, D, rows, spare):
+    b = R.Batch(rows, [1000, 150, 0], 2, D, 32, BF, fp8, seed=3, spare_cols=spare)
     q, o, lse = run(b, 8, causal=causal, window=window)
     check(b, 8, q, o, lse, causal=causal, window=window)
 
@@ -93,24 +97,42 @@ def test_alibi(per_batch, fp8, rows):
 
 @pytest.mark.parametrize("rows", [[1, 1, 2, 1], [40, 3, 200, 1]])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_rows_without_keys_and_rows_behind_the_last_sequence(rows, fp8):
+@pytest.mark.parametrize("spare", [1, 200])
+def test_rows_without_keys_and_rows_behind_the_last_sequence(rows, fp8, spare):
     # sequences shorter than their rows: the first rows sit before key 0
-    b = R.Batch(rows, [-1, -3, -1, 0], 2, 128, 16, BF, fp8, seed=2, tail=5)
+    b = R.Batch(rows, [-1, -3, -1, 0], 2, 128, 16, BF, fp8, seed=2, tail=5, spare_cols=spare)
     H = 4
     g = torch.Generator().manual_seed(1)
     q = torch.randn(b.total, H, 128, generator=g).to(BF)
     k, v, table, cu, lens, kw = b.gpu()
     o = torch.full((b.total, H, 128), 7.0, dtype=BF, device="cuda")
     lse = torch.full((H, b.total), 7.0, device="cuda")
-    fattn.fa_fwd_paged(q.cuda(), o, lse, fattn.kv_pages(k, v, **kw),
-                       fattn.ragged(table, cu, lens, b.total), len(rows), 2, None, 128 ** -0.5,
-                       True, fattn.raw_stream(0))
+    call_c(q.cuda(), o, lse, k, v, table, cu, lens, **kw)
     torch.cuda.synchronize()
     assert fattn_error() == fattn.FA_OK
     check(b, H, q, o.cpu(), lse.cpu())
     n = sum(rows)
     assert (o[n:] == 7).all() and (lse[:, n:] == 7).all()
     assert (o[0] == 0).all() and (lse[:, 0] == -math.inf).all()
+
+
+def call_c(q, o, lse, k, v, table, cu, lens, k_exp=None, v_exp=None):
+    """fa_fwd_paged itself, on results of the caller's."""
+    lib, total, H, D = fattn.load(), *q.shape
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    code = {BF: 0, HF: 1, R.E4M3: 3}
+    c = R.KvPages(ptr(k), ptr(v), ptr(k_exp), ptr(v_exp), *k.stride()[:3], *v.stride()[:3],
+                  *k.shape, code[k.dtype])
+    r = R.Ragged(ptr(table), table.stride(0), table.shape[1], ptr(cu), ptr(lens), len(lens), total)
+    n = ctypes.c_size_t()
+    assert lib.fa_fwd_paged_workspace_size(len(lens), total, H, k.shape[2], D,
+                                           table.shape[1] * k.shape[1], ctypes.byref(n)) == 0
+    ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    st = lib.fa_fwd_paged(ptr(q), *q.stride()[:2], ptr(o), *o.stride()[:2], ptr(lse),
+                          ctypes.addressof(c), ctypes.addressof(r), H, None, D ** -0.5, 1,
+                          code[q.dtype], ptr(ws) if n.value else None, n.value,
+                          torch.cuda.current_stream().cuda_stream)
+    assert st == fattn.FA_OK
 
 
 def test_strided_operands_and_other_page_orders():

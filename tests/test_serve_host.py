@@ -9,27 +9,10 @@ import pytest
 import torch
 
 from exact_attention_93_gb300 import attention, build, fattn, kvcache, rotary
+from paged_ref import KvPages, Ragged, RotaryOperand
 
 FAKE = 1 << 20  # aligned and never dereferenced: every call below fails its checks first
 INV, UNS = fattn.FA_ERR_INVALID_ARG, fattn.FA_ERR_UNSUPPORTED
-
-
-class KvPages(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp")] + [
-        (n, ctypes.c_longlong) for n in ("k_page", "k_token", "k_head", "v_page", "v_token",
-                                         "v_head")] + [
-        (n, ctypes.c_int) for n in ("pages", "page_size", "heads", "head_dim", "type")]
-
-
-class Ragged(ctypes.Structure):
-    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
-                ("max_pages", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
-                ("seqlens", ctypes.c_void_p), ("batch", ctypes.c_int), ("total", ctypes.c_int)]
-
-
-class RotaryOperand(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
-                ("xs", fattn.FaStrides), ("ys", fattn.FaStrides)]
 
 
 @pytest.fixture(scope="module")
@@ -113,7 +96,7 @@ def test_rows_and_null_structs(lib):
 
 def paged(lib, heads=4, scale=0.125, opts=None, ws=FAKE, ws_bytes=1 << 30, q=FAKE, q_token=256,
           o=FAKE, lse=FAKE):
-    c, b = pages(), ragged()
+    c, b = pages(), ragged(max_pages=1000, table_stride=1000)
     return lib.fa_fwd_paged(q, q_token, 64, o, 256, 64, lse, ctypes.addressof(c),
                             ctypes.addressof(b), heads,
                             None if opts is None else ctypes.addressof(opts), scale, 1, 0, ws,
@@ -134,27 +117,18 @@ def test_paged_arguments(lib, kw, status):
     assert paged(lib, **kw) == status
 
 
-def test_packed_structs_match_the_c_layout():
-    kp, vp, ke, ve = kvcache.alloc_kv_cache(3, 16, 2, 64, torch.float8_e4m3fn, device="cpu")
-    c = KvPages.from_buffer_copy(fattn.kv_pages(kp, vp, ke, ve).ljust(ctypes.sizeof(KvPages)))
-    assert (c.k, c.v, c.k_exp, c.v_exp) == tuple(x.data_ptr() for x in (kp, vp, ke, ve))
-    assert (c.k_page, c.k_token, c.k_head) == (2048, 128, 64) == (c.v_page, c.v_token, c.v_head)
-    assert (c.pages, c.page_size, c.heads, c.head_dim, c.type) == (3, 16, 2, 64, 3)
-    table, cu, lens = torch.zeros(2, 5, dtype=torch.int32), i32(0, 1, 4), i32(1, 3)
-    b = Ragged.from_buffer_copy(fattn.ragged(table, cu, lens, 4).ljust(ctypes.sizeof(Ragged)))
-    assert (b.block_table, b.cu_seqlens, b.seqlens) == tuple(x.data_ptr() for x in (table, cu, lens))
-    assert (b.table_stride, b.max_pages, b.batch, b.total) == (5, 5, 2, 4)
-    x, y = t(1, 4, 2, 64), t(1, 4, 2, 64)
-    o = RotaryOperand.from_buffer_copy(fattn.rotary_operand(x, y))
-    assert (o.x, o.y, o.heads) == (x.data_ptr(), y.data_ptr(), 2)
-    assert (o.xs.batch, o.xs.head, o.xs.seq) == (512, 64, 128) == (o.ys.batch, o.ys.head, o.ys.seq)
-
-
 def test_workspace_size(lib):
-    size = lib.fa_fwd_paged_workspace_size
-    assert size(1, 1, 8, 2, 64) > 0 and size(1, 1, 8, 2, 64) % 256 == 0
-    for bad in ((0, 1, 8, 2, 64), (1, 1, 8, 3, 64), (1, 1, 8, 2, 96), (1, -1, 8, 2, 64)):
-        assert size(*bad) == 0
+    n = ctypes.c_size_t()
+    size = lambda *a: (lib.fa_fwd_paged_workspace_size(*a, ctypes.byref(n)), n.value)  # noqa: E731
+    st, long = size(1, 1, 8, 2, 64, 1 << 20)
+    assert st == fattn.FA_OK and long > 0 and long % 256 == 0
+    assert size(1, 1, 8, 2, 64, 16) == (fattn.FA_OK, 0)  # short tables need none
+    assert size(1, 1000, 8, 2, 64, 1 << 20)[1] > long    # more rows, larger blocks
+    for bad, want in (((0, 1, 8, 2, 64, 16), INV), ((1, 1, 8, 3, 64, 16), INV),
+                      ((1, 1, 8, 2, 96, 16), UNS), ((1, -1, 8, 2, 64, 16), INV),
+                      ((1, 1, 8, 2, 64, -1), INV)):
+        assert size(*bad) == (want, 0)
+    assert lib.fa_fwd_paged_workspace_size(1, 1, 8, 2, 64, 16, None) == INV
 
 
 def rot(lib, B=1, N=4, D=64, r=64, freq=FAKE, pos=None, bits=0, stride=0, mag=1.0, dtype=0, x=FAKE,
@@ -214,8 +188,14 @@ def test_python_refusals():
         kvcache.kv_cache_append(x, x, kp, vp, table, cu.long(), lens)
     with pytest.raises(ValueError):
         kvcache.kv_cache_append(x, x, kp, vp, table, cu, i32(3, 3))
-    with pytest.raises(ValueError):
+    with pytest.raises(TypeError):
         kvcache.kv_cache_append(x, x, kp, vp, table, cu, None)
+    with pytest.raises(TypeError):
+        kvcache.kv_cache_append(x, "x", kp, vp, table, cu, lens)
+    with pytest.raises(TypeError):  # neither bf16 nor fp16
+        kvcache.kv_cache_read(kp, vp, table, cu, 3, dtype=torch.float32)
+    with pytest.raises(ValueError):  # a result of another size
+        kvcache.kv_cache_read(kp, vp, table, cu, 3, out=(t(2, 2, 64), t(2, 2, 64)))
     with pytest.raises(ValueError):  # exponents with a 16-bit cache, and an e4m3 one without
         kvcache.kv_cache_append(x, x, *args, k_exp=torch.zeros(2, 2, 16, dtype=torch.uint8))
     k8, v8, ke, ve = kvcache.alloc_kv_cache(2, 16, 2, 64, torch.float8_e4m3fn, device="cpu")
