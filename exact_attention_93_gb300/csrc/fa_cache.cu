@@ -14,7 +14,11 @@
 // values of one token: D / 8 lanes hold a head's row, 8 elements (16 bytes of
 // 16-bit rows) each, kUnroll rows in flight per lane; the row loads are issued
 // before the page lookup (sequence, length, page: three dependent loads), which
-// they hide.
+// they hide.  Many warps with little each hide those loads best: four tokens a
+// warp took 10 % longer, one lookup for a block of tokens and a barrier 30 %.
+// What is left beside the bytes is instruction issue, so a row's maximum is
+// taken on packed 16-bit magnitudes (ordered like their values), and rows that
+// hold infinities or NaN take a path of their own.
 #include "fa_ragged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"
@@ -93,37 +97,42 @@ __global__ void __launch_bounds__(kCacheThreads)
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.c.p[w]) + at.row +
                                     h * p.c.head[w] + sub * 8) = v[u];
       } else {
-        float f[8];
-        unpack8<kBf16>(v[u], f);
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = fabsf(f[i]);
-          top = fmaxf(top, a < INFINITY ? a : 0.f);  // (false for NaN)
-        }
+        const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t halves = __vmaxu2(__vmaxu2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu),
+                                   __vmaxu2(x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu));
 #pragma unroll
         for (int m = 1; m < kLanes; m <<= 1)
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        const uint32_t bits = __float_as_uint(top);
-        int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-        e = max(e, 1);  // a finite maximum keeps e below 248
+          halves = __vmaxu2(halves, __shfl_xor_sync(0xffffffffu, halves, m));
+        uint32_t top = max(halves & 0xffffu, halves >> 16);
+        const bool zeros = top == 0;
+        constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;
+        if (top >= kInf) {  // the same for all lanes of the row
+          top = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t m = (x[i >> 1] >> ((i & 1) * 16)) & 0x7fffu;
+            top = m < kInf ? max(top, m) : top;
+          }
+          const uint32_t row = ((1u << kLanes) - 1u) << (slot * kLanes);
+#pragma unroll
+          for (int m = 1; m < kLanes; m <<= 1) top = max(top, __shfl_xor_sync(row, top, m));
+        }
+        // the smallest 2^(e - 127) with top <= 448 * 2^(e - 127); a finite
+        // maximum keeps e below 248
+        const uint32_t bits = __float_as_uint(unpack2<kBf16>(top).x);
+        const int e = max(
+            static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), 1);
         const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        const uint2 code = make_uint2(
-            pack2_e4m3(f[0] * inv, f[1] * inv) | pack2_e4m3(f[2] * inv, f[3] * inv) << 16,
-            pack2_e4m3(f[4] * inv, f[5] * inv) | pack2_e4m3(f[6] * inv, f[7] * inv) << 16);
-        // a row without finite nonzero values is marked as zeros, unless it holds
-        // infinities or NaN, which keep the smallest scale
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) odd |= !(fabsf(f[i]) < INFINITY);
-#pragma unroll
-        for (int m = 1; m < kLanes; m <<= 1) odd |= __shfl_xor_sync(0xffffffffu, odd, m) != 0;
+        float f[8];
+        unpack8<kBf16>(v[u], f);
         if (h < p.c.heads) {
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.c.p[w]) + at.row + h * p.c.head[w] +
-                                    sub * 8) = code;
+                                    sub * 8) = make_uint2(
+              pack2_e4m3(f[0] * inv, f[1] * inv) | pack2_e4m3(f[2] * inv, f[3] * inv) << 16,
+              pack2_e4m3(f[4] * inv, f[5] * inv) | pack2_e4m3(f[6] * inv, f[7] * inv) << 16);
           if (sub == 0)
             p.c.exp[w][at.exp + static_cast<long long>(h) * p.c.page_size] =
-                static_cast<uint8_t>(top > 0.f || odd ? e : 0);
+                static_cast<uint8_t>(zeros ? 0 : e);
         }
       }
     }

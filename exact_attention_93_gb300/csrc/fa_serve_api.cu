@@ -15,7 +15,7 @@ namespace {
 constexpr long long kMaxBytes = 1ll << 40;  // every operand lies below this from its base
 constexpr int kMaxRows = 1 << 29;           // packed rows, keys of a sequence, window bounds
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWholeKeysFew = 1536, kWholeKeysMany = 1024;
+constexpr int kWholeKeysFew = 1536, kWholeKeysMany = 1536;
 
 bool aligned(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -332,7 +332,12 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
     a.tasks = reinterpret_cast<JoinTask*>(base + plan.o_bytes + plan.ml_bytes);
   }
   a.block_rows = plan.block_rows;
-  a.whole = plan.whole;
+  // (a window bounds what a unit walks as well as the table does)
+  const long long unit_keys =
+      a.win_left < 0 || a.win_right < 0
+          ? kMaxRows
+          : static_cast<long long>(a.win_left) + a.win_right + plan.block_rows / a.group + kTile;
+  a.whole = plan.whole || unit_keys <= (plan.many ? kWholeKeysMany : kWholeKeysFew);
   if (sm_count(&a.sms) != cudaSuccess) return FA_ERR_CUDA;
   a.err = device_error_word();
   if (!a.err) return FA_ERR_CUDA;
