@@ -191,14 +191,14 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
   if (tid == 0) {
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 1);
-    mbar_init(&s.q_ready, kConverters);
+    mbar_init(&s.q_ready, kConverters / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 128);
       mbar_init(&s.o_done[i], 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.full[i], kFp8 ? kConverters : 1);
+      mbar_init(&s.full[i], kFp8 ? kConverters / 32 : 1);
       mbar_init(&s.empty[i], 1);
       mbar_init(&s.raw_full[i], 1);
     }
@@ -520,10 +520,15 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
               }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&s.q_ready);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.q_ready);
           }
           ++units;
-          int ref[2] = {0, 0};  // largest key, value exponent of the piece so far
+          // Two warps convert K tiles and two V tiles, side by side.  All four
+          // see every tile land and arrive for it, so that V's barrier covers
+          // what the others have written for its key tile too.
+          const int my_kv = (warp - ManyWarps<kFp8>::kFirst) >> 1;
+          uint32_t ref = 0;  // largest exponent of the piece's keys, or values, so far
           for (int j = u.first; ok && j <= u.last; ++j, ++ring) {
             const bool cut = u.ragged(j);
 #pragma unroll 1
@@ -532,26 +537,34 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
               const int st = n % kStages;
               ok = many_warp_wait(&s.raw_full[st], (n / kStages) & 1, p.err, abort_flag);
               if (!ok) break;
-              int top = 0;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int r = lane * 4 + i, key = j * kTile + r;
-                if (key >= u.key_lo && key < u.key_hi)
-                  top = max(top, static_cast<int>(s.exps[st][r]));
+              if (kv != my_kv) {
+                if (lane == 0) mbar_arrive(&s.full[st]);
+                continue;
               }
-              top = __reduce_max_sync(0xffffffffu, top);
-              const int base_e = max(kv ? ref[1] : ref[0], top);
-              (kv ? ref[1] : ref[0]) = base_e;
-              if (cv == 0) (kv ? s.vref : s.kref)[ring % kRefs] = base_e;
+              {
+                uint32_t four = reinterpret_cast<const uint32_t*>(s.exps[st])[lane];
+                if (cut) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int key = j * kTile + lane * 4 + i;
+                    if (key < u.key_lo || key >= u.key_hi) four &= ~(0xffu << (8 * i));
+                  }
+                }
+                const uint32_t top = max(max(four & 0xffu, (four >> 8) & 0xffu),
+                                         max((four >> 16) & 0xffu, four >> 24));
+                ref = max(ref, __reduce_max_sync(0xffffffffu, top));
+              }
+              const int base_e = static_cast<int>(ref);
+              if ((cv & 63) == 0) (kv ? s.vref : s.kref)[ring % kRefs] = base_e;
               // Eight lanes share a row, lane c with codes 8 c .. 8 c + 7 of each
               // 64: they become chunk c of the row in that column block.  A
-              // warp's rows are 16 apart, so that their swizzle is the same and
+              // warp's rows are 8 apart, so that their swizzle is the same and
               // every address a constant away from the first; it reads kBatch
               // of them before it writes any: in place, a row's raw bytes lie
               // under its converted ones.  Odd rows take the 64s in the other
               // order, for the banks' sake.
-              constexpr int kPieces = D / 64, kBatch = 4, kStep = kConverters / 8;
-              const int c = lane & 7, r0 = (cv >> 5) * 4 + (lane >> 3);
+              constexpr int kPieces = D / 64, kBatch = 4, kStep = 8;
+              const int c = lane & 7, r0 = (warp & 1) * 4 + (lane >> 3);
               const int flip = r0 & (kPieces - 1);
               const uint8_t* from[kPieces];
               uint8_t* to[kPieces];
@@ -564,21 +577,21 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                 to[h] = s.kv[st] + (h ^ flip) * Smem::kBlockBytes + r0 * 128 +
                         ((c ^ (r0 & 7)) << 4);
               }
-#pragma unroll
-              for (int m0 = 0; m0 < kTile / kStep; m0 += kBatch) {
+#pragma unroll 1
+              for (int m = 0; m < kTile / kStep; m += kBatch) {
                 uint2 v[kBatch][kPieces];
                 uint32_t e[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
 #pragma unroll
                   for (int h = 0; h < kPieces; ++h)
-                    v[i][h] = *reinterpret_cast<const uint2*>(from[h] + (m0 + i) * kStep * D);
-                  e[i] = s.exps[st][r0 + (m0 + i) * kStep];
+                    v[i][h] = *reinterpret_cast<const uint2*>(from[h] + (m + i) * kStep * D);
+                  e[i] = s.exps[st][r0 + (m + i) * kStep];
                 }
                 if (cut) {
 #pragma unroll
                   for (int i = 0; i < kBatch; ++i) {
-                    const int key = j * kTile + r0 + (m0 + i) * kStep;
+                    const int key = j * kTile + r0 + (m + i) * kStep;
                     if (key < u.key_lo || key >= u.key_hi) e[i] = 0;
                   }
                 }
@@ -592,7 +605,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
 #pragma unroll
                   for (int h = 0; h < kPieces; ++h) {
                     const uint32_t w0 = e[i] ? v[i][h].x : 0u, w1 = e[i] ? v[i][h].y : 0u;
-                    *reinterpret_cast<uint4*>(to[h] + (m0 + i) * kStep * 128) =
+                    *reinterpret_cast<uint4*>(to[h] + (m + i) * kStep * 128) =
                         make_uint4(mul_f16x2(e4m3x2_to_f16x2(w0), f2),
                                    mul_f16x2(e4m3x2_to_f16x2(w0 >> 16), f2),
                                    mul_f16x2(e4m3x2_to_f16x2(w1), f2),
@@ -601,7 +614,8 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                 }
               }
               fence_proxy_async_smem();
-              mbar_arrive(&s.full[st]);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s.full[st]);
             }
           }
         }
