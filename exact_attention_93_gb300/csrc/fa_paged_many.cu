@@ -716,10 +716,22 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
         }
         const bool masked = k0 < all_first || k0 + kTile - 1 > all_last;
         if (masked) {
-          const int cf = first - k0, cl = last - k0;  // visible columns cf .. cl
+          // visible columns cf .. cl of this row; 32 columns at a time, as a
+          // warp's rows agree about most of them
+          const int cf = first - k0, cl = last - k0;
 #pragma unroll
-          for (int c = 0; c < kTile; ++c)
-            if (c < cf || c > cl) sv[c] = -INFINITY;
+          for (int c = 0; c < kTile; c += 32) {
+            if (__any_sync(0xffffffffu, cl < c + 31)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e > cl) sv[c + e] = -INFINITY;
+            }
+            if (p.win_left >= 0 && __any_sync(0xffffffffu, cf > c)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e < cf) sv[c + e] = -INFINITY;
+            }
+          }
         }
         float mxs[8];
 #pragma unroll
@@ -835,72 +847,61 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           else
             p.part_ml[at] = make_float2(m, l);
         }
-        // this row's 128-byte pieces in the output: D / 64 of 16-bit elements,
-        // D / 32 of fp32
+        // This row's 128-byte pieces in the output: D / 64 of 16-bit elements,
+        // D / 32 of fp32.  (The loops stay rolled: unrolled, the epilogue spent
+        // most of its 2.5 us waiting for its own instructions.)
         uint8_t* out = whole ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) +
                                                           row * p.o_token + head * p.o_head)
                              : reinterpret_cast<uint8_t*>(p.part_o + at * D);
         if (!mine) out = nullptr;
-        const int cols = whole ? 64 : 32;  // columns of a piece
         // (a cut piece without tiles leaves its maximum, -inf, alone)
-        const int end = whole || have ? D : 0;
+        const int chunks = whole || have ? D / 32 : 0;
 #pragma unroll 1
-        for (int c = 0; c < end; c += cols) {
-          uint4 w[8];
-          auto take = [&](int col, auto&& put) {
-            uint32_t o[32];
-            if (have) {
-              tmem_ld32(tO + lane_off + col, o);
-              tmem_ld_wait();
-            } else {
+        for (int c = 0; c < chunks; ++c) {  // 32 columns
+          uint32_t o[32];
+          if (have) {
+            tmem_ld32(tO + lane_off + c * 32, o);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0u;
-            }
-            put(o);
-          };
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+          // 16-bit: half a piece, fp32: a whole one
+          const int half = whole ? (c & 1) * 4 : 0, n = whole ? 4 : 8;
           if (whole) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              take(c + h * 32, [&](const uint32_t(&o)[32]) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  uint32_t pk[4];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    pk[e] = pack2<kBf16>(__uint_as_float(o[8 * q + 2 * e]) * scale,
-                                         __uint_as_float(o[8 * q + 2 * e + 1]) * scale);
-                  w[h * 4 + q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
-              });
-          } else {
-            take(c, [&](const uint32_t(&o)[32]) {
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                w[q] = make_uint4(__float_as_uint(__uint_as_float(o[4 * q]) * scale),
-                                  __float_as_uint(__uint_as_float(o[4 * q + 1]) * scale),
-                                  __float_as_uint(__uint_as_float(o[4 * q + 2]) * scale),
-                                  __float_as_uint(__uint_as_float(o[4 * q + 3]) * scale));
-            });
+            for (int e = 0; e < 16; ++e)
+              o[e] = pack2<kBf16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
           }
           if constexpr (kFp8) {
-            if (mine)
+            if (mine) {
 #pragma unroll
-              for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(out + q * 16) = w[q];
+              for (int q = 0; q < 8; ++q)
+                if (q < n)
+                  *reinterpret_cast<uint4*>(out + (half + q) * 16) =
+                      make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
           } else {
             // through shared memory, so that eight lanes write a row's 128 bytes
-            uint8_t* mine_at = s.stage[warp] + lane * 128;
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<uint4*>(mine_at + ((q ^ (lane & 7)) << 4)) = w[q];
+              if (q < n)
+                *reinterpret_cast<uint4*>(s.stage[warp] + lane * 128 +
+                                          (((half + q) ^ (lane & 7)) << 4)) =
+                    make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+          if (whole && !(c & 1)) continue;  // the piece's other half comes next
+          if constexpr (!kFp8) {
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = i * 4 + (lane >> 3), q = lane & 7;
+#pragma unroll 2
+            for (int rr = lane >> 3; rr < 32; rr += 4) {
               uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(
                   0xffffffffu, reinterpret_cast<unsigned long long>(out), rr));
-              const uint4 v =
-                  *reinterpret_cast<const uint4*>(s.stage[warp] + rr * 128 + ((q ^ (rr & 7)) << 4));
-              if (dst) *reinterpret_cast<uint4*>(dst + q * 16) = v;
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  s.stage[warp] + rr * 128 + (((lane ^ rr) & 7) << 4));
+              if (dst) *reinterpret_cast<uint4*>(dst + (lane & 7) * 16) = v;
             }
             __syncwarp();
           }
