@@ -854,6 +854,14 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                                                           row * p.o_token + head * p.o_head)
                              : reinterpret_cast<uint8_t*>(p.part_o + at * D);
         if (!mine) out = nullptr;
+        // the rows this lane writes 16 bytes of: rr = lane / 8 + 4 i
+        unsigned long long rows[kFp8 ? 1 : 8];
+        if constexpr (!kFp8) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            rows[i] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out),
+                                  (lane >> 3) + 4 * i);
+        }
         // (a cut piece without tiles leaves its maximum, -inf, alone)
         const int chunks = whole || have ? D / 32 : 0;
 #pragma unroll 1
@@ -895,17 +903,22 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           if (whole && !(c & 1)) continue;  // the piece's other half comes next
           if constexpr (!kFp8) {
             __syncwarp();
-#pragma unroll 2
-            for (int rr = lane >> 3; rr < 32; rr += 4) {
-              uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(
-                  0xffffffffu, reinterpret_cast<unsigned long long>(out), rr));
-              const uint4 v = *reinterpret_cast<const uint4*>(
-                  s.stage[warp] + rr * 128 + (((lane ^ rr) & 7) << 4));
-              if (dst) *reinterpret_cast<uint4*>(dst + (lane & 7) * 16) = v;
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = (lane >> 3) + 4 * i;
+              v[i] = *reinterpret_cast<const uint4*>(s.stage[warp] + rr * 128 +
+                                                     (((lane ^ rr) & 7) << 4));
             }
+            const int piece = whole ? c >> 1 : c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (rows[i])
+                *reinterpret_cast<uint4*>(rows[i] + piece * 128 + (lane & 7) * 16) = v[i];
             __syncwarp();
+          } else {
+            out += 128;
           }
-          if (mine) out += 128;
         }
       }
       if (u.first <= u.last) ++units;
