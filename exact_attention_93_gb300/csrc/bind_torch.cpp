@@ -15,11 +15,13 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
 #include <climits>
 #include <optional>
+#include <vector>
 
 #include "fattn_cache.h"
 
@@ -126,13 +128,111 @@ fa_rotary_operand rotary_operand(const at::Tensor& x, const at::Tensor& y) {
   return o;
 }
 
-// rotary(q, k, inv_freq, positions, magnitude, interleaved, inverse, inplace)
+// How a rotation is done, apart from the tensors turned.
+struct Rotation {
+  at::Tensor freq, pos;  // pos may be undefined
+  double magnitude;
+  bool interleaved, inverse;
+};
+
+// Turns x into y, and x2 (when defined) into y2.
+fa_status turn(const at::Tensor& x, const at::Tensor& y, const at::Tensor& x2,
+               const at::Tensor& y2, const Rotation& r, const Device& device) {
+  const int64_t dim = x.dim(), B = dim == 4 ? x.size(0) : 1, N = x.size(dim - 3);
+  need(B <= INT_MAX && N <= INT_MAX, "tensors too large");
+  const fa_rotary_operand a = rotary_operand(x, y);
+  fa_rotary_operand b;
+  if (x2.defined()) b = rotary_operand(x2, y2);
+  const bool pos = r.pos.defined();
+  return fa_rotary(&a, x2.defined() ? &b : nullptr, static_cast<int>(B), static_cast<int>(N),
+                   static_cast<int>(x.size(dim - 1)), static_cast<int>(2 * r.freq.size(0)),
+                   r.freq.const_data_ptr<double>(), pos ? r.pos.const_data_ptr() : nullptr,
+                   !pos ? 0 : r.pos.scalar_type() == at::kInt ? 32 : 64,
+                   pos && r.pos.dim() == 2 ? r.pos.stride(0) : 0,
+                   static_cast<float>(r.magnitude), r.interleaved, r.inverse,
+                   static_cast<fa_elem>(elem(x.scalar_type())), device.stream());
+}
+
+// What the C ABI refuses inside autograd.
+void check(fa_status st) {
+  TORCH_CHECK(st == FA_OK, "fa_rotary failed: ", fa_status_string(st), " (", static_cast<int>(st),
+              ")");
+}
+
+// The incoming gradient as the kernels need it: D contiguous, 16-byte aligned
+// rows.  Anything else is copied once.
+at::Tensor grad_operand(const at::Tensor& g) {
+  if (!g.defined()) return g;
+  bool ok = g.stride(-1) == 1 && reinterpret_cast<uintptr_t>(g.const_data_ptr()) % 16 == 0;
+  for (int64_t i = 0; i + 1 < g.dim(); ++i) ok = ok && g.stride(i) % 8 == 0;
+  return ok ? g : g.contiguous();
+}
+
+// A rotation's gradient is the rotation back, with the same magnitude; it is
+// linear, so its own gradient is a rotation again.  kTensors: one or two tensors
+// turned (autograd takes no undefined ones).
+template <int kTensors>
+struct RotaryFunction : torch::autograd::Function<RotaryFunction<kTensors>> {
+  static torch::autograd::variable_list run(torch::autograd::AutogradContext* ctx,
+                                            const at::Tensor& q, const at::Tensor& k,
+                                            const Rotation& r) {
+    ctx->set_materialize_grads(false);
+    ctx->save_for_backward({r.freq, r.pos});
+    ctx->saved_data["magnitude"] = r.magnitude;
+    ctx->saved_data["interleaved"] = r.interleaved;
+    ctx->saved_data["inverse"] = r.inverse;
+    return rotated(q, k, r);
+  }
+  static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx,
+                                                const at::Tensor& q, const Rotation& r) {
+    return run(ctx, q, at::Tensor(), r);
+  }
+  static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx,
+                                                const at::Tensor& q, const at::Tensor& k,
+                                                const Rotation& r) {
+    return run(ctx, q, k, r);
+  }
+  static torch::autograd::variable_list rotated(const at::Tensor& q, const at::Tensor& k,
+                                                const Rotation& r) {
+    const Device device({&q, &k, &r.freq, &r.pos});
+    const at::Tensor yq = like(q), yk = k.defined() ? like(k) : k;
+    check(turn(q, yq, k, yk, r, device));
+    if (!k.defined()) return {yq};
+    return {yq, yk};
+  }
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                 torch::autograd::variable_list grads);
+};
+
+template <int kTensors>
+torch::autograd::variable_list RotaryFunction<kTensors>::backward(
+    torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grads) {
+  const auto saved = ctx->get_saved_variables();
+  const Rotation r{saved[0], saved[1], ctx->saved_data["magnitude"].toDouble(),
+                   ctx->saved_data["interleaved"].toBool(),
+                   !ctx->saved_data["inverse"].toBool()};
+  std::vector<at::Tensor> have;
+  for (const at::Tensor& g : grads)
+    if (g.defined()) have.push_back(grad_operand(g));
+  torch::autograd::variable_list out(kTensors + 1), got;
+  if (have.empty()) return out;
+  if (c10::GradMode::is_enabled())
+    got = have.size() == 1 ? RotaryFunction<1>::apply(have[0], r)
+                           : RotaryFunction<2>::apply(have[0], have[1], r);
+  else
+    got = rotated(have[0], have.size() == 1 ? at::Tensor() : have[1], r);
+  for (size_t i = 0, n = 0; i < grads.size(); ++i)
+    if (grads[i].defined()) out[i] = got[n++];
+  return out;
+}
+
+// rotary(q, k, inv_freq, positions, magnitude, interleaved, inplace)
 PyObject* rotary(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q must be a tensor");
   const at::Tensor k = maybe(a[1], "k must be a tensor or None");
-  const at::Tensor& freq = tensor(a[2], "inv_freq must be a tensor");
-  at::Tensor pos = maybe(a[3], "positions must be a tensor or None");
-  const bool inplace = truth(a[7]);
+  Rotation r{tensor(a[2], "inv_freq must be a tensor"),
+             maybe(a[3], "positions must be a tensor or None"), number(a[4]), truth(a[5]), false};
+  const bool inplace = truth(a[6]);
   const int64_t dim = q.dim();
   need(dim == 3 || dim == 4,
        "expected (batch, seqlen, nheads, headdim) or packed (total, nheads, headdim) tensors");
@@ -140,36 +240,27 @@ PyObject* rotary(PyObject* const* a) {
     need(k.dim() == dim && k.size(0) == q.size(0) && (dim == 3 || k.size(1) == q.size(1)) &&
              k.size(dim - 1) == q.size(dim - 1) && k.scalar_type() == q.scalar_type(),
          "q and k must agree in type and in every dimension but the heads");
-  need(freq.scalar_type() == at::kDouble && freq.dim() == 1 && freq.is_contiguous(),
+  need(r.freq.scalar_type() == at::kDouble && r.freq.dim() == 1 && r.freq.is_contiguous(),
        "inv_freq must be a contiguous float64 (rotary_dim / 2) tensor");
   const int64_t B = dim == 4 ? q.size(0) : 1, N = q.size(dim - 3);
-  int bits = 0;
-  if (pos.defined()) {
-    if (pos.scalar_type() != at::kInt && pos.scalar_type() != at::kLong)
+  if (r.pos.defined()) {
+    if (r.pos.scalar_type() != at::kInt && r.pos.scalar_type() != at::kLong)
       throw Refuse{PyExc_TypeError, "positions must be int32 or int64"};
-    bits = pos.scalar_type() == at::kInt ? 32 : 64;
-    need((pos.dim() == 1 && pos.size(0) == N) ||
-             (dim == 4 && pos.dim() == 2 && pos.size(0) == B && pos.size(1) == N),
+    need((r.pos.dim() == 1 && r.pos.size(0) == N) ||
+             (dim == 4 && r.pos.dim() == 2 && r.pos.size(0) == B && r.pos.size(1) == N),
          "positions must have shape (seqlen,) or (batch, seqlen)");
   }
-  const Device device({&q, &k, &freq, &pos});
-  if (inplace) {
-    no_grad(q, "inplace=True would overwrite tensors that need a gradient");
-    no_grad(k, "inplace=True would overwrite tensors that need a gradient");
+  const Device device({&q, &k, &r.freq, &r.pos});
+  if (r.pos.defined() && N > 1 && r.pos.stride(-1) != 1) r.pos = r.pos.contiguous();
+  const bool grad =
+      c10::GradMode::is_enabled() && (q.requires_grad() || (k.defined() && k.requires_grad()));
+  if (grad) {
+    need(!inplace, "inplace=True would overwrite tensors that need a gradient");
+    auto y = k.defined() ? RotaryFunction<2>::apply(q, k, r) : RotaryFunction<1>::apply(q, r);
+    return k.defined() ? pair(std::move(y[0]), std::move(y[1])) : wrap(std::move(y[0]));
   }
-  if (pos.defined() && N > 1 && pos.stride(-1) != 1) pos = pos.contiguous();
-  need(B <= INT_MAX && N <= INT_MAX, "tensors too large");
-  const at::Tensor yq = inplace ? q : like(q);
-  const at::Tensor yk = !k.defined() || inplace ? k : like(k);
-  const fa_rotary_operand oq = rotary_operand(q, yq);
-  fa_rotary_operand ok;
-  if (k.defined()) ok = rotary_operand(k, yk);
-  const fa_status st = fa_rotary(
-      &oq, k.defined() ? &ok : nullptr, static_cast<int>(B), static_cast<int>(N),
-      static_cast<int>(q.size(dim - 1)), static_cast<int>(2 * freq.size(0)),
-      freq.const_data_ptr<double>(), pos.defined() ? pos.const_data_ptr() : nullptr, bits,
-      pos.defined() && pos.dim() == 2 ? pos.stride(0) : 0, static_cast<float>(number(a[4])),
-      truth(a[5]), truth(a[6]), static_cast<fa_elem>(elem(q.scalar_type())), device.stream());
+  const at::Tensor yq = inplace ? q : like(q), yk = !k.defined() || inplace ? k : like(k);
+  const fa_status st = turn(q, yq, k, yk, r, device);
   if (st != FA_OK) return status(st);
   return k.defined() ? pair(yq, yk) : wrap(yq);
 }
@@ -388,7 +479,7 @@ PyMethodDef method(const char* name) {
                      METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method<rotary, 8>("rotary"), method<append, 9>("append"),
+PyMethodDef methods[] = {method<rotary, 7>("rotary"), method<append, 9>("append"),
                          method<read, 11>("read"), method<paged, 13>("paged"),
                          {nullptr, nullptr, 0, nullptr}};
 

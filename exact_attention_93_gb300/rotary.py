@@ -54,47 +54,6 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     return freq.to(device), magnitude
 
 
-def _call(*args):
-    out = fattn.bind().rotary(*args)
-    if type(out) is int:
-        fattn._check(out, "fa_rotary")
-    return out
-
-
-def _grad_operand(g):
-    """The incoming gradient as the kernels need it: D contiguous, 16-byte
-    aligned rows.  Anything else is copied once (argument marshalling)."""
-    if g.stride(-1) != 1 or any(s % 8 for s in g.stride()[:-1]) or g.data_ptr() % 16:
-        g = g.contiguous()
-    return g
-
-
-class _Rotary(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, inv_freq, positions, magnitude, interleaved):
-        ctx.set_materialize_grads(False)
-        ctx.save_for_backward(inv_freq, positions)
-        ctx.magnitude, ctx.interleaved = magnitude, interleaved
-        out = _call(q, k, inv_freq, positions, magnitude, interleaved, False, False)
-        return (out, None) if k is None else out
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dq, dk):
-        inv_freq, positions = ctx.saved_tensors
-        grads = [_grad_operand(g) for g in (dq, dk) if g is not None]
-        out = [None, None]
-        if grads:
-            two = len(grads) > 1
-            got = _call(grads[0], grads[1] if two else None, inv_freq, positions, ctx.magnitude,
-                        ctx.interleaved, True, False)
-            if two:
-                out = got
-            else:
-                out[0 if dq is not None else 1] = got
-        return out[0], out[1], None, None, None, None
-
-
 def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0, inplace=False):
     """q and k (k may be None) with the first 2 * len(inv_freq) elements of
     every head turned by position, the others unchanged: (batch, seqlen,
@@ -108,10 +67,9 @@ def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0
     when interleaved.  Rotated elements are multiplied by magnitude.
 
     Returns new tensors (q, k), or q alone when k is None.  Differentiable in q
-    and k.  inplace=True writes over q and k instead and returns them; it is
+    and k (the gradient is the rotation back), any number of times.  inplace=True writes over q and k instead and returns them; it is
     for inference and refuses tensors that need a gradient."""
-    if (not inplace and torch.is_grad_enabled()
-            and (q.requires_grad or (k is not None and k.requires_grad))):
-        yq, yk = _Rotary.apply(q, k, inv_freq, positions, magnitude, interleaved)
-        return yq if k is None else (yq, yk)
-    return _call(q, k, inv_freq, positions, magnitude, interleaved, False, inplace)
+    out = fattn.bind().rotary(q, k, inv_freq, positions, magnitude, interleaved, inplace)
+    if type(out) is int:
+        fattn._check(out, "fa_rotary")
+    return out

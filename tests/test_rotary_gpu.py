@@ -167,3 +167,32 @@ def test_non_finite_values_stay_in_their_pair():
 def test_empty():
     freq, _ = rotary.rotary_frequencies(64)
     assert rotary.rotary_func(torch.zeros(2, 0, 4, 64, device="cuda"), None, freq).shape == (2, 0, 4, 64)
+
+
+def test_second_derivative():
+    # the gradient is linear in what comes in: its own gradient is the rotation
+    freq, _ = rotary.rotary_frequencies(64)
+    x = torch.randn(1, 5, 2, 64, device="cuda", requires_grad=True)
+    w = torch.randn(1, 5, 2, 64, device="cuda", requires_grad=True)
+    y = rotary.rotary_func(x, None, freq, magnitude=2.0)
+    gx, = torch.autograd.grad(y, (x,), (w,), create_graph=True)
+    v = torch.randn_like(x)
+    gw, = torch.autograd.grad(gx, (w,), (v,))
+    ref = R.rotary(v.cpu(), torch.arange(5)[None], freq.cpu(), magnitude=2.0)
+    assert ((gw.cpu().double() - ref).abs() <= 2.0 ** -20 * 2 * 8).all()
+
+
+def test_backward_on_another_stream_and_leaf_accumulation():
+    freq, _ = rotary.rotary_frequencies(64)
+    x = torch.randn(2, 9, 3, 64, device="cuda", requires_grad=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y, z = rotary.rotary_func(x, x[:, :, :1], freq)
+        (y.sum() + 2 * z.sum()).backward()
+    torch.cuda.current_stream().wait_stream(s)
+    one = torch.ones(2, 9, 3, 64)
+    pos = torch.arange(9).expand(2, 9)
+    ref = R.rotary(one, pos, freq.cpu(), inverse=True)
+    ref[:, :, :1] += 2 * R.rotary(one[:, :, :1], pos, freq.cpu(), inverse=True)
+    assert ((x.grad.cpu().double() - ref).abs() <= 2.0 ** -20 * 8).all()
