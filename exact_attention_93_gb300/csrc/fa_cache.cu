@@ -16,7 +16,8 @@
 // before the page lookup (sequence, length, page: three dependent loads), which
 // they hide.  Many warps with little each hide those loads best: four tokens a
 // warp took 10 % longer, one lookup for a block of tokens and a barrier 30 %.
-// What is left beside the bytes is instruction issue, so a row's maximum is
+// With at most kUnroll heads each lane group takes a token of its own instead of
+// every kRows-th head of one.  What is left beside the bytes is instruction issue, so a row's maximum is
 // taken on packed 16-bit magnitudes (ordered like their values), and rows that
 // hold infinities or NaN take a path of their own.
 #include "fa_ragged.cuh"
@@ -59,41 +60,42 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-template <int D, bool kBf16, bool kFp8>
+template <int D, bool kBf16, bool kFp8, bool kFewHeads>
 __global__ void __launch_bounds__(kCacheThreads)
     cache_append_kernel(const __grid_constant__ CacheLaunch p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kStep = kFewHeads ? 1 : kRows;
   const long long item = blockIdx.x * (kCacheThreads / 32LL) + (threadIdx.x >> 5);
-  const int w = static_cast<int>(item & 1), row = static_cast<int>(item >> 1);
-  if (row >= p.r.total) return;
+  const int w = static_cast<int>(item & 1);
+  const long long first = (item >> 1) * (kFewHeads ? kRows : 1);
+  if (first >= p.r.total) return;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, slot = lane / kLanes;
+  const int row = static_cast<int>(first) + (kFewHeads ? slot : 0);
+  const int h_first = kFewHeads ? 0 : slot, heads = row < p.r.total ? p.c.heads : 0;
   const uint16_t* src = static_cast<const uint16_t*>(p.rows[w]) + row * p.row_token[w] + sub * 8;
   Slot at{0, 0, false};
-  for (int h0 = slot; h0 - slot < p.c.heads; h0 += kRows * kUnroll) {
+  for (int h0 = h_first; h0 - h_first < p.c.heads; h0 += kStep * kUnroll) {
     uint4 v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * kRows;
-      v[u] = h < p.c.heads ? __ldg(reinterpret_cast<const uint4*>(src + h * p.row_head[w]))
+      const int h = h0 + u * kStep;
+      v[u] = h < heads ? __ldg(reinterpret_cast<const uint4*>(src + h * p.row_head[w]))
                            : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (h0 == slot) {
-      const int b = warp_find_seq(p.r.cu, p.r.batch, row);
-      if (b < 0) return;  // behind the last sequence
-      const int c0 = p.r.cu[b], c1 = p.r.cu[b + 1];
-      const long long pos = static_cast<long long>(p.r.lens[b]) - c1 + row;
-      at = find_slot(p, w, b, pos);
-      if (!at.ok) {
-        // no slot for this row; a sequence shorter than its rows is the caller's right
-        if ((pos >= 0 || c1 < c0) && lane == 0) atomicExch(p.err, kDevErrBadIndex);
-        return;
+    if (h0 == h_first) {
+      const int b = warp_find_seq(p.r.cu, p.r.batch, static_cast<int>(first), row);
+      if (b >= 0 && row < p.r.total) {  // (not behind the last sequence)
+        const int c0 = p.r.cu[b], c1 = p.r.cu[b + 1];
+        const long long pos = static_cast<long long>(p.r.lens[b]) - c1 + row;
+        at = find_slot(p, w, b, pos);
+        // no slot: a sequence shorter than its rows is the caller's right
+        if (!at.ok && (pos >= 0 || c1 < c0) && sub == 0) atomicExch(p.err, kDevErrBadIndex);
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * kRows;
+      const int h = h0 + u * kStep;
       if constexpr (!kFp8) {
-        if (h < p.c.heads)
+        if (at.ok && h < heads)
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.c.p[w]) + at.row +
                                     h * p.c.head[w] + sub * 8) = v[u];
       } else {
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kCacheThreads)
         const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
         float f[8];
         unpack8<kBf16>(v[u], f);
-        if (h < p.c.heads) {
+        if (at.ok && h < heads) {
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.c.p[w]) + at.row + h * p.c.head[w] +
                                     sub * 8) = make_uint2(
               pack2_e4m3(f[0] * inv, f[1] * inv) | pack2_e4m3(f[2] * inv, f[3] * inv) << 16,
@@ -139,26 +141,28 @@ __global__ void __launch_bounds__(kCacheThreads)
   }
 }
 
-template <int D, bool kBf16, bool kFp8>
+template <int D, bool kBf16, bool kFp8, bool kFewHeads>
 __global__ void __launch_bounds__(kCacheThreads)
     cache_read_kernel(const __grid_constant__ CacheLaunch p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kStep = kFewHeads ? 1 : kRows;
   const long long item = blockIdx.x * (kCacheThreads / 32LL) + (threadIdx.x >> 5);
-  const int w = static_cast<int>(item & 1), row = static_cast<int>(item >> 1);
-  if (row >= p.r.total) return;
+  const int w = static_cast<int>(item & 1);
+  const long long first = (item >> 1) * (kFewHeads ? kRows : 1);
+  if (first >= p.r.total) return;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, slot = lane / kLanes;
-  const int b = warp_find_seq(p.r.cu, p.r.batch, row);
-  if (b < 0) return;  // behind the last sequence
+  const int row = static_cast<int>(first) + (kFewHeads ? slot : 0);
+  const int b = warp_find_seq(p.r.cu, p.r.batch, static_cast<int>(first), row);
+  if (b < 0 || row >= p.r.total) return;  // behind the last sequence
   const long long pos = (p.r.lens ? p.r.lens[b] : 0LL) + row - p.r.cu[b];
   const Slot at = find_slot(p, w, b, pos);
-  if (!at.ok && lane == 0) atomicExch(p.err, kDevErrBadIndex);
+  if (!at.ok && sub == 0) atomicExch(p.err, kDevErrBadIndex);
   uint16_t* dst = static_cast<uint16_t*>(p.rows[w]) + row * p.row_token[w] + sub * 8;
-  for (int h0 = slot; h0 < p.c.heads; h0 += kRows * kUnroll) {
+  for (int h0 = kFewHeads ? 0 : slot; h0 < p.c.heads; h0 += kStep * kUnroll) {
     uint4 v[kUnroll];
     uint32_t e[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * kRows;
+      const int h = h0 + u * kStep;
       v[u] = make_uint4(0u, 0u, 0u, 0u);
       e[u] = 0u;
       if (!at.ok || h >= p.c.heads) continue;
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(kCacheThreads)
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * kRows;
+      const int h = h0 + u * kStep;
       if (h >= p.c.heads) continue;
       if constexpr (kFp8) {
         const float scale = __uint_as_float(e[u] << 23);
@@ -194,35 +198,46 @@ __global__ void __launch_bounds__(kCacheThreads)
 }
 
 template <typename K>
-cudaError_t launch_rows(K kern, const CacheLaunch& a, cudaStream_t s) {
-  const long long per_block = kCacheThreads / 32;
-  const long long blocks = (2LL * a.r.total + per_block - 1) / per_block;
-  kern<<<static_cast<unsigned>(blocks), kCacheThreads, 0, s>>>(a);
+cudaError_t launch_rows(K kern, K few_heads, const CacheLaunch& a, cudaStream_t s) {
+  const bool few = a.c.heads <= kUnroll;
+  const long long tokens = few ? 32 / (a.c.D / 8) : 1, per_block = kCacheThreads / 32;
+  const long long items = 2 * ((a.r.total + tokens - 1) / tokens);
+  const long long blocks = (items + per_block - 1) / per_block;
+  (few ? few_heads : kern)<<<static_cast<unsigned>(blocks), kCacheThreads, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+template <int D, bool kBf16, bool kFp8>
+cudaError_t append_t(const CacheLaunch& a, cudaStream_t s) {
+  return launch_rows(cache_append_kernel<D, kBf16, kFp8, false>,
+                     cache_append_kernel<D, kBf16, kFp8, true>, a, s);
+}
+
+template <int D, bool kBf16, bool kFp8>
+cudaError_t read_t(const CacheLaunch& a, cudaStream_t s) {
+  return launch_rows(cache_read_kernel<D, kBf16, kFp8, false>,
+                     cache_read_kernel<D, kBf16, kFp8, true>, a, s);
 }
 
 }  // namespace
 
+// (a 16-bit cache's rows are copied, whichever type they are)
 cudaError_t launch_cache_append(const CacheLaunch& a, cudaStream_t s) {
   const bool fp8 = a.c.elem == kElemE4m3, bf16 = a.elem == kElemBf16;
   if (a.c.D == 64)
-    return !fp8 ? launch_rows(cache_append_kernel<64, true, false>, a, s)
-           : bf16 ? launch_rows(cache_append_kernel<64, true, true>, a, s)
-                  : launch_rows(cache_append_kernel<64, false, true>, a, s);
-  return !fp8 ? launch_rows(cache_append_kernel<128, true, false>, a, s)
-         : bf16 ? launch_rows(cache_append_kernel<128, true, true>, a, s)
-                : launch_rows(cache_append_kernel<128, false, true>, a, s);
+    return !fp8 ? append_t<64, true, false>(a, s)
+           : bf16 ? append_t<64, true, true>(a, s) : append_t<64, false, true>(a, s);
+  return !fp8 ? append_t<128, true, false>(a, s)
+         : bf16 ? append_t<128, true, true>(a, s) : append_t<128, false, true>(a, s);
 }
 
 cudaError_t launch_cache_read(const CacheLaunch& a, cudaStream_t s) {
   const bool fp8 = a.c.elem == kElemE4m3, bf16 = a.elem == kElemBf16;
   if (a.c.D == 64)
-    return !fp8 ? launch_rows(cache_read_kernel<64, true, false>, a, s)
-           : bf16 ? launch_rows(cache_read_kernel<64, true, true>, a, s)
-                  : launch_rows(cache_read_kernel<64, false, true>, a, s);
-  return !fp8 ? launch_rows(cache_read_kernel<128, true, false>, a, s)
-         : bf16 ? launch_rows(cache_read_kernel<128, true, true>, a, s)
-                : launch_rows(cache_read_kernel<128, false, true>, a, s);
+    return !fp8 ? read_t<64, true, false>(a, s)
+           : bf16 ? read_t<64, true, true>(a, s) : read_t<64, false, true>(a, s);
+  return !fp8 ? read_t<128, true, false>(a, s)
+         : bf16 ? read_t<128, true, true>(a, s) : read_t<128, false, true>(a, s);
 }
 
 }  // namespace fa

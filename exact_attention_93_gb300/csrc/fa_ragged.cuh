@@ -10,19 +10,22 @@
 namespace fa {
 
 // The sequence of packed row `row`, or -1 when it belongs to none (before
-// cu[0], or from cu[batch] on).  The whole warp calls it with one row: each
-// step samples 32 boundaries at once, so 1024 sequences take two dependent
-// loads.
-__device__ __forceinline__ int warp_find_seq(const int* __restrict__ cu, int batch, int row) {
+// cu[0], or from cu[batch] on).  The lanes' rows ascend and lie close together:
+// the whole warp looks for `first`, the least of them, sampling 32 boundaries at
+// a step, so that 1024 sequences take two dependent loads, and each lane goes on
+// from there.
+__device__ __forceinline__ int warp_find_seq(const int* __restrict__ cu, int batch, int first,
+                                             int row) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = batch;  // the number of b in 1 .. batch with cu[b] <= row is in [lo, hi]
   while (lo < hi) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + (lane + 1) * step - 1;
-    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && cu[1 + min(i, batch - 1)] <= row));
+    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && cu[1 + min(i, batch - 1)] <= first));
     lo += n * step;
     hi = min(hi, lo + step - 1);
   }
+  while (lo < batch && cu[lo + 1] <= row) ++lo;
   return lo < batch && cu[0] <= row ? lo : -1;
 }
 
