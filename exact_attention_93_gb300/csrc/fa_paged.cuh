@@ -344,67 +344,72 @@ __device__ __forceinline__ void store16(uint16_t* dst, const float (&o)[kN], flo
 // Adds up the units that several CTAs worked on.  Block (c, y) takes a share of
 // the rows of the unit that CTA c began and did not finish; its pieces are CTA
 // c's second partial result and the first ones of the CTAs after it.  A warp's
-// lanes are the D columns; it adds kJoinRows rows side by side, as the loads'
-// latency is all this costs.
-constexpr int kJoinRows = 4, kJoinThreads = 64;
+// lanes are the D columns of kRowsAtOnce rows, kPieces pieces of which it loads
+// side by side: the loads' latency is all this costs.  A long context over few
+// rows has up to a hundred pieces of a handful of rows, a prompt two or three
+// pieces of 256.
+constexpr int kJoinThreads = 64;
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, int kRowsAtOnce, int kPieces>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_join_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const JoinTask task = p.tasks[c];
   constexpr int kN = D / 32, kWarps = kJoinThreads / 32;
-  const int step = gridDim.y * kWarps * kJoinRows;
-  for (int r0 = (blockIdx.y * kWarps + warp) * kJoinRows; r0 < task.rows; r0 += step) {
-    float m[kJoinRows], l[kJoinRows] = {}, o[kJoinRows][kN] = {};
+  const int step = gridDim.y * kWarps * kRowsAtOnce;
+  for (int r0 = (blockIdx.y * kWarps + warp) * kRowsAtOnce; r0 < task.rows; r0 += step) {
+    float m[kRowsAtOnce], l[kRowsAtOnce] = {}, o[kRowsAtOnce][kN] = {};
 #pragma unroll
-    for (int q = 0; q < kJoinRows; ++q) m[q] = -INFINITY;
+    for (int q = 0; q < kRowsAtOnce; ++q) m[q] = -INFINITY;
     // up to 32 CTAs at a time: lane i knows whether CTA first + i had work
     for (int first = c; first <= task.last; first += 32) {
       uint32_t live = __ballot_sync(
           0xffffffffu, first + lane <= task.last && p.tasks[min(first + lane, task.last)].rows >= 0);
       while (live) {
-        const int i = first + __ffs(live) - 1;
-        live &= live - 1;
-        const long long at = (2LL * i + (i == c ? 1 : 0)) * p.block_rows + r0;
-        float2 ml[kJoinRows];
-        float x[kJoinRows][kN];
+        float2 ml[kPieces][kRowsAtOnce];
+        float x[kPieces][kRowsAtOnce][kN];
 #pragma unroll
-        for (int q = 0; q < kJoinRows; ++q) {
-          if (r0 + q >= task.rows) {
-            ml[q] = make_float2(-INFINITY, 0.f);
+        for (int k = 0; k < kPieces; ++k) {
+          const bool some = live != 0;
+          const int i = first + (some ? __ffs(live) - 1 : 0);
+          live &= live - 1;
+          const long long at = (2LL * i + (i == c ? 1 : 0)) * p.block_rows + r0;
 #pragma unroll
-            for (int e = 0; e < kN; ++e) x[q][e] = 0.f;
-            continue;
-          }
-          ml[q] = p.part_ml[at + q];
-          // (of pieces without keys there is a maximum alone; what the loads
-          // below find is multiplied by nothing)
-          const float* src = p.part_o + (at + q) * D + lane * kN;
-          if constexpr (kN == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            x[q][0] = v.x; x[q][1] = v.y; x[q][2] = v.z; x[q][3] = v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            x[q][0] = v.x; x[q][1] = v.y;
+          for (int q = 0; q < kRowsAtOnce; ++q) {
+            const bool valid = some && r0 + q < task.rows;
+            ml[k][q] = valid ? p.part_ml[at + q] : make_float2(-INFINITY, 0.f);
+            // (of pieces without keys there is a maximum alone, -inf; what this
+            // finds there is not used)
+            const float* src = p.part_o + (at + q) * D + lane * kN;
+            if constexpr (kN == 4) {
+              const float4 v = valid ? *reinterpret_cast<const float4*>(src)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+              x[k][q][0] = v.x; x[k][q][1] = v.y; x[k][q][2] = v.z; x[k][q][3] = v.w;
+            } else {
+              const float2 v =
+                  valid ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
+              x[k][q][0] = v.x; x[k][q][1] = v.y;
+            }
           }
         }
 #pragma unroll
-        for (int q = 0; q < kJoinRows; ++q) {
-          const float m_new = fmaxf(m[q], ml[q].x);
-          const float ref = m_new == -INFINITY ? 0.f : m_new;
-          const float a = ex2_approx(m[q] - ref), b = ex2_approx(ml[q].x - ref);
-          m[q] = m_new;
-          l[q] = l[q] * a + ml[q].y * b;
+        for (int k = 0; k < kPieces; ++k)
 #pragma unroll
-          for (int e = 0; e < kN; ++e)
-            o[q][e] = o[q][e] * a + (ml[q].x == -INFINITY ? 0.f : x[q][e] * b);
-        }
+          for (int q = 0; q < kRowsAtOnce; ++q) {
+            const float m_new = fmaxf(m[q], ml[k][q].x);
+            const float ref = m_new == -INFINITY ? 0.f : m_new;
+            const float a = ex2_approx(m[q] - ref), b = ex2_approx(ml[k][q].x - ref);
+            m[q] = m_new;
+            l[q] = l[q] * a + ml[k][q].y * b;
+#pragma unroll
+            for (int e = 0; e < kN; ++e)
+              o[q][e] = o[q][e] * a + (ml[k][q].x == -INFINITY ? 0.f : x[k][q][e] * b);
+          }
       }
     }
 #pragma unroll
-    for (int q = 0; q < kJoinRows; ++q) {
+    for (int q = 0; q < kRowsAtOnce; ++q) {
       if (r0 + q >= task.rows) continue;
       int token, head;
       row_of(p, task.first_row, r0 + q, task.hk, token, head);
@@ -421,7 +426,9 @@ __global__ void __launch_bounds__(kJoinThreads)
 template <int D, bool kBf16>
 cudaError_t launch_join(const PagedLaunch& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int rows = kJoinThreads / 32 * kJoinRows;
+  // few rows in a block: many pieces at a time; many rows: some of each
+  const bool few = a.block_rows <= 16;
+  const int rows = kJoinThreads / 32 * (few ? 1 : 2);
   cfg.gridDim = dim3(static_cast<unsigned>(a.sms),
                      static_cast<unsigned>((a.block_rows + rows - 1) / rows));
   cfg.blockDim = dim3(kJoinThreads);
@@ -431,7 +438,8 @@ cudaError_t launch_join(const PagedLaunch& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16>, a);
+  return few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, 1, 8>, a)
+             : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, 2, 2>, a);
 }
 
 }  // namespace fa
