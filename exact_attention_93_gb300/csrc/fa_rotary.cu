@@ -28,7 +28,10 @@ namespace fa {
 namespace {
 
 constexpr int kRotThreads = 128;
-constexpr int kUnroll = 4;  // heads in flight per lane group
+// Heads in flight per lane group: 128 bytes a lane.  (fp32: 28.0 us with four,
+// 26.2 with two, 1860 tokens of 72 heads of 128.)
+template <int kElem>
+constexpr int kUnroll = kElem == kElemFp32 ? 2 : 4;
 
 // Sine and cosine of turn32 * 2^-32 turns (Taylor series about the nearest
 // quarter turn; the remainder is at most pi/4, where the first terms left
@@ -133,10 +136,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     const long long token = item / head_groups;
     const int hg = static_cast<int>(item - token * head_groups);
     const long long b = token / p.N, n = token - b * p.N;
-    const int h_first = hg * (kSlots * kUnroll) + slot;
-    Vec8<kElem> v0[kUnroll], v1[kUnroll];
+    const int h_first = hg * (kSlots * kUnroll<kElem>) + slot;
+    Vec8<kElem> v0[kUnroll<kElem>], v1[kUnroll<kElem>];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kUnroll<kElem>; ++u) {
       const int h = h_first + u * kSlots;
       if (h < all) {
         const int w = h >= p.heads[0];
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
       cs[j] = __shfl_sync(0xffffffffu, mc[j % kShare], from);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kUnroll<kElem>; ++u) {
       const int h = h_first + u * kSlots;
       if (h >= all) continue;
       if (rotates) {
@@ -206,14 +209,18 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
 
 template <int D, int kElem, bool kInterleaved>
 cudaError_t launch_rotary_t(const RotaryLaunch& a, cudaStream_t s) {
-  constexpr int kHeads = 32 / (D / 16) * kUnroll;  // heads of one work item
+  constexpr int kHeads = 32 / (D / 16) * kUnroll<kElem>;  // heads of one work item
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const int groups = (a.heads[0] + a.heads[1] + kHeads - 1) / kHeads;
   const long long items = static_cast<long long>(a.B) * a.N * groups;
   const long long per_block = kRotThreads / 32;
-  const long long blocks = (items + per_block - 1) / per_block, most = 16LL * sms;
+  const long long blocks = (items + per_block - 1) / per_block;
+  // Blocks stay for several items, as each first turns inv_freq into fractions of
+  // a turn in fp64; but few enough items that they end together (65536 tokens of
+  // 16 heads: 86.5 us with 16 blocks per SM, 80.5 with 64, 83.6 with one item each).
+  const long long most = 64LL * sms;
   rotary_kernel<D, kElem, kInterleaved>
       <<<static_cast<unsigned>(blocks < most ? blocks : most), kRotThreads, 0, s>>>(a, groups, items);
   return cudaGetLastError();
