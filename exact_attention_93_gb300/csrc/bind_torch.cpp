@@ -110,6 +110,12 @@ void no_grad(const at::Tensor& t, const char* what) {
   need(!(t.defined() && t.requires_grad() && c10::GradMode::is_enabled()), what);
 }
 
+// What torch's own in-place operations do: autograd then notices that a tensor it
+// saved has changed.
+void written(const at::Tensor& t) {
+  if (t.defined()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 fa_rotary_operand rotary_operand(const at::Tensor& x, const at::Tensor& y) {
   const auto xs = x.strides(), ys = y.strides();
   need(xs.back() == 1 && ys.back() == 1, "the head dimension D must be contiguous");
@@ -250,6 +256,7 @@ PyObject* rotary(PyObject* const* a) {
              (dim == 4 && r.pos.dim() == 2 && r.pos.size(0) == B && r.pos.size(1) == N),
          "positions must have shape (seqlen,) or (batch, seqlen)");
   }
+  need(!r.freq.requires_grad(), "inv_freq gets no gradient: detach it");
   const Device device({&q, &k, &r.freq, &r.pos});
   if (r.pos.defined() && N > 1 && r.pos.stride(-1) != 1) r.pos = r.pos.contiguous();
   const bool grad =
@@ -260,6 +267,12 @@ PyObject* rotary(PyObject* const* a) {
     return k.defined() ? pair(std::move(y[0]), std::move(y[1])) : wrap(std::move(y[0]));
   }
   const at::Tensor yq = inplace ? q : like(q), yk = !k.defined() || inplace ? k : like(k);
+  if (inplace) {
+    need(!k.defined() || k.numel() == 0 || k.const_data_ptr() != q.const_data_ptr(),
+         "q and k would be written over each other");
+    written(q);
+    written(k);
+  }
   const fa_status st = turn(q, yq, k, yk, r, device);
   if (st != FA_OK) return status(st);
   return k.defined() ? pair(yq, yk) : wrap(yq);
@@ -351,6 +364,7 @@ PyObject* append(PyObject* const* a) {
   const fa_kv_pages c = kv_pages(kp, vp, ke, ve);
   const fa_ragged r = ragged(table, cu, lens, k.size(0));
   const Device device({&k, &v, &kp, &vp, &table, &cu, &lens, &ke, &ve});
+  for (const at::Tensor* t : {&kp, &vp, &ke, &ve}) written(*t);
   const fa_status st = fa_cache_append(&c, &r, k.const_data_ptr(), k.stride(0), k.stride(1),
                                        v.const_data_ptr(), v.stride(0), v.stride(1),
                                        static_cast<fa_elem>(elem(k.scalar_type())),
@@ -378,7 +392,8 @@ PyObject* read(PyObject* const* a) {
     throw Refuse{PyExc_TypeError, "unsupported dtype; use bfloat16 or float16"};
   at::Tensor k = maybe(a[9], "out must be a pair of tensors"),
              v = maybe(a[10], "out must be a pair of tensors");
-  if (k.defined()) {
+  if (k.defined() || v.defined()) {
+    need(k.defined() && v.defined(), "out must be a pair of tensors");
     check_rows(k, v, kp);
     no_grad(k, "out must not need a gradient");
     no_grad(v, "out must not need a gradient");
@@ -386,7 +401,10 @@ PyObject* read(PyObject* const* a) {
          "out must hold `total` rows of dtype");
   }
   const Device device({&kp, &vp, &table, &cu, &starts, &ke, &ve, &k, &v});
-  if (!k.defined()) {
+  if (k.defined()) {
+    written(k);
+    written(v);
+  } else {
     const auto opt = kp.options().requires_grad(false).dtype(out_elem == FA_ELEM_BF16 ? at::kBFloat16
                                                                                     : at::kHalf);
     k = at::empty({total, kp.size(2), kp.size(3)}, opt);
@@ -411,7 +429,7 @@ PyObject* paged(PyObject* const* a) {
   const at::Tensor slopes = maybe(a[10], "alibi_slopes must be a tensor or None"),
                    ke = maybe(a[11], "k_exp must be a tensor or None"),
                    ve = maybe(a[12], "v_exp must be a tensor or None");
-  for (const at::Tensor* t : {&q, &kp, &vp})
+  for (const at::Tensor* t : {&q, &kp, &vp, &slopes})
     no_grad(*t, "attention over a cache has no backward: call under torch.no_grad()");
   const fa_kv_pages c = kv_pages(kp, vp, ke, ve);
   need(q.dim() == 3 && q.stride(2) == 1 && q.size(2) == c.head_dim,

@@ -86,7 +86,8 @@ struct SeqWork {
   int first;   // few rows: the first key tile
   __device__ __forceinline__ void load(const PagedLaunch& p, int b, uint32_t* err = nullptr) {
     s = load_seq(p.r, p.page_log2, b, err);
-    blocks = (s.rows * p.group + p.block_rows - 1) / p.block_rows;
+    const int rows = s.rows * p.group;
+    blocks = rows < p.min_rows || rows > p.max_rows ? 0 : (rows + p.block_rows - 1) / p.block_rows;
     if constexpr (!kMany) {
       int lo, hi;
       visible_span(p, s, 0, s.rows, lo, hi);
@@ -289,8 +290,7 @@ __device__ __forceinline__ JoinTask join_task(const PagedLaunch& p, const Piece&
 }
 
 // The pages of a piece's tiles, for a producer warp: 32 table entries at a time,
-// the next 32 on their way.  (One tile's entries at a time cost a load's latency,
-// about 0.8 us, for every tile: an e4m3 batch of 64 contexts read 3.5 TB/s.)
+// the next 32 on their way, so that no tile waits for a load of its entries.
 struct PageFeed {
   const int* table;
   int first;       // page index that lane 0's entry belongs to

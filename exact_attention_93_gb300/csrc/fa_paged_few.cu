@@ -688,9 +688,7 @@ cudaError_t launch_few_d(const PagedLaunch& a, cudaStream_t s) {
 
 }  // namespace
 
-int paged_few_rows(long long rows, int batch) {
-  return rows <= 8LL * batch ? 8 : 16;
-}
+int paged_few_rows(double rows) { return rows <= 8 ? 8 : 16; }
 
 cudaError_t launch_paged_few(const PagedLaunch& a, cudaStream_t s) {
   return a.D == 64 ? launch_few_d<64>(a, s) : launch_few_d<128>(a, s);

@@ -85,6 +85,7 @@ struct PagedLaunch {
   const float* alibi;
   int alibi_bstride;
   int block_rows;   // query rows of a unit
+  int min_rows, max_rows;  // sequences of other numbers of rows (tokens x group) are left out
   int whole;        // units are not cut
   // unless whole:
   float* part_o;    // [2 sms][block_rows][D]
@@ -94,9 +95,9 @@ struct PagedLaunch {
   uint32_t* err;
 };
 
-// Query rows (tokens x group) of a block of the few-row kernel, by the mean
-// number of rows a sequence has, and of the many-row kernel.
-int paged_few_rows(long long rows, int batch);
+// Query rows (tokens x group) of a block of the few-row kernel, for sequences of
+// `rows` rows on average, and of the many-row kernel.
+int paged_few_rows(double rows);
 int paged_many_rows(int group);
 cudaError_t launch_paged_many(const PagedLaunch& a, cudaStream_t s);
 cudaError_t launch_paged_few(const PagedLaunch& a, cudaStream_t s);

@@ -1,6 +1,8 @@
 // fa_serve_api.cu -- the C ABI of include/fattn_cache.h: argument checks, TMA
 // descriptor set-up, workspace layout and kernel launches.  No arithmetic of
 // the operators lives here.
+#include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -15,6 +17,9 @@ namespace {
 constexpr long long kMaxBytes = 1ll << 40;  // every operand lies below this from its base
 constexpr int kMaxRows = 1 << 29;           // packed rows, keys of a sequence, window bounds
 constexpr float kLog2e = 1.4426950408889634f;
+// Keys up to which units stay whole.  (us, cut and whole: one sequence of 1000
+// keys 9.9 and 9.6, of 1500 10.8 and 11.9, 8 of 1000 13.7 and 10.4; prompts of
+// 4 x 300 tokens 28.2 and 16.9, of 1500 tokens 39.4 and 31.9.)
 constexpr int kWholeKeysFew = 1536, kWholeKeysMany = 1536;
 
 bool aligned(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -34,6 +39,14 @@ bool strides_ok(const long long* st, const long long* extent, int n, int D, int 
     last += static_cast<double>(extent[i] - 1) * st[i];
   }
   return last * es < static_cast<double>(kMaxBytes);
+}
+
+// An operand that is written: every index has elements of its own (strides below
+// a row would let rows share them).
+bool apart(const long long* st, const long long* extent, int n, int D) {
+  for (int i = 0; i < n; ++i)
+    if (extent[i] > 1 && st[i] < D) return false;
+  return true;
 }
 
 fa_status check_batch(const fa_ragged* b, bool lens_needed) {
@@ -87,13 +100,25 @@ Ragged ragged_of(const fa_ragged* b, const int* lens) {
 fa_status cache_rows(const fa_kv_pages* cache, const fa_ragged* batch, const int* lens,
                      const void* k, long long k_token, long long k_head, const void* v,
                      long long v_token, long long v_head, fa_elem dtype, void* stream,
-                     cudaError_t (*launch)(const CacheLaunch&, cudaStream_t)) {
+                     bool append) {
   fa_status st;
   if ((st = check_pages(cache, batch, dtype)) != FA_OK) return st;
   if (batch->total == 0) return FA_OK;
   if (!packed_ok(k, k_token, k_head, batch->total, cache->heads, cache->head_dim) ||
       !packed_ok(v, v_token, v_head, batch->total, cache->heads, cache->head_dim))
     return FA_ERR_INVALID_ARG;
+  const long long pages[3] = {cache->pages, cache->page_size, cache->heads};
+  const long long rows[2] = {batch->total, cache->heads};
+  const long long st_k[3] = {cache->k_page, cache->k_token, cache->k_head};
+  const long long st_v[3] = {cache->v_page, cache->v_token, cache->v_head};
+  const long long st_rk[2] = {k_token, k_head}, st_rv[2] = {v_token, v_head};
+  const int D = cache->head_dim;
+  const bool distinct =
+      append ? cache->k != cache->v &&
+                   (cache->type != FA_ELEM_E4M3 || cache->k_exp != cache->v_exp) &&
+                   apart(st_k, pages, 3, D) && apart(st_v, pages, 3, D)
+             : k != v && apart(st_rk, rows, 2, D) && apart(st_rv, rows, 2, D);
+  if (!distinct) return FA_ERR_INVALID_ARG;
   CacheLaunch a{};
   a.c = Pages{{cache->k, cache->v},
               {cache->k_exp, cache->v_exp},
@@ -116,33 +141,65 @@ fa_status cache_rows(const fa_kv_pages* cache, const fa_ragged* batch, const int
   a.elem = dtype;
   a.err = device_error_word();
   if (!a.err) return FA_ERR_CUDA;
+  const auto launch = append ? launch_cache_append : launch_cache_read;
   return launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// Query rows per sequence and key head that the batch has on average decide
-// the kernel and its row blocks.
-struct PagedPlan {
+// One launch of a call: the few-row or the many-row kernel over the sequences of
+// min_rows to max_rows query rows (tokens x group).
+struct PagedPart {
   bool many, whole;
-  int block_rows;
+  int block_rows, min_rows, max_rows;
+};
+
+struct PagedPlan {
+  int parts;
+  PagedPart part[2];
   size_t o_bytes, ml_bytes, total_bytes;
 };
 
-void paged_plan(int batch, int total, int heads, int heads_k, int D, long long max_keys,
-                PagedPlan* plan) {
+// Which kernel a call takes.  The lengths are on the device; what the host knows
+// is the mean.  (us, few-row and many-row kernel, 32 / 8 heads of 128, contexts
+// up to 16000 keys, 16-bit and e4m3: 64 sequences of 2 tokens, 8 rows, 147 and
+// 161, 94 and 195; of 4 tokens, 16 rows, 160 and 162, 162 and 197; of 8 tokens,
+// 32 rows, 16-bit, 968 with a few-row kernel of 32 rows and 208.)
+//
+// Single tokens may come together with a chunk of a prompt.  Where that is likely
+// (the sequences cannot be equally long, and one of them could be) and there are
+// enough single tokens for it to pay, each kernel takes its own sequences; a
+// launch that finds none costs 15 us.  (Few rows alone, many rows alone, both: 256
+// single tokens and a chunk of 512 over 4000 keys 561, 350 and 299, e4m3 701, 446
+// and 242; 256 and 100 259, 291 and 283, e4m3 239, 375 and 219; 64 and 512 260,
+// 195 and 198, e4m3 328, 251 and 153; 64 and 64 157, 165 and 186, e4m3 113, 205
+// and 139; 8 and 200, e4m3, 53, 25 and 35.)
+constexpr int kFewRows = 16, kMixedMean = 512;
+constexpr int mixed_batch(bool fp8) { return fp8 ? 32 : 128; }
+constexpr int mixed_longest(bool fp8) { return fp8 ? 384 : 768; }
+
+PagedPlan paged_plan(int batch, int total, int heads, int heads_k, int D, long long max_keys,
+                     bool fp8) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) sms = 160;  // no device: sizes for the checks alone
   const int group = heads / heads_k;
-  const long long all = static_cast<long long>(total) * group;
-  plan->many = all > 16LL * batch;
-  plan->block_rows = plan->many ? paged_many_rows(group) : paged_few_rows(all, batch);
-  // Below this many keys a sequence, cutting a unit and joining its pieces costs
-  // more than it saves.
-  plan->whole = max_keys <= (plan->many ? kWholeKeysMany : kWholeKeysFew);
-  const size_t rows = plan->whole ? 0 : 2ull * sms * plan->block_rows;
-  plan->o_bytes = round256(rows * D * sizeof(float));
-  plan->ml_bytes = round256(rows * sizeof(float2));
-  plan->total_bytes =
-      plan->whole ? 0 : plan->o_bytes + plan->ml_bytes + round256(32ull * sms);
+  const double mean = static_cast<double>(total) * group / batch;
+  // rows of the longest sequence when the others are single tokens
+  const long long longest = (static_cast<long long>(total) - batch + 1) * group;
+  const bool mixed = total % batch != 0 && batch >= mixed_batch(fp8) && group <= kFewRows &&
+                     mean <= kMixedMean && longest > mixed_longest(fp8);
+  PagedPlan plan{};
+  size_t rows = 0;
+  auto add = [&](bool many, int block_rows, int min_rows, int max_rows) {
+    const bool whole = max_keys <= (many ? kWholeKeysMany : kWholeKeysFew);
+    plan.part[plan.parts++] = PagedPart{many, whole, block_rows, min_rows, max_rows};
+    if (!whole) rows = std::max(rows, size_t(2) * sms * block_rows);
+  };
+  if (mixed || mean <= kFewRows)
+    add(false, paged_few_rows(mixed ? group : mean), 0, mixed ? kFewRows : INT_MAX);
+  if (mixed || mean > kFewRows) add(true, paged_many_rows(group), mixed ? kFewRows + 1 : 0, INT_MAX);
+  plan.o_bytes = round256(rows * D * sizeof(float));
+  plan.ml_bytes = round256(rows * sizeof(float2));
+  plan.total_bytes = rows ? plan.o_bytes + plan.ml_bytes + round256(32ull * sms) : 0;
+  return plan;
 }
 
 bool paged_sizes_ok(int batch, int total, int heads, int heads_k, int D) {
@@ -156,8 +213,8 @@ bool page_map(CUtensorMap* m, const void* base, const fa_kv_pages* c, long long 
               long long token, long long head) {
   const bool fp8 = c->type == FA_ELEM_E4M3;
   // A row is followed by another head's, which another CTA wants at another
-  // time: fetching more than the row wasted half the HBM bandwidth (e4m3,
-  // D = 128: 3.5 TB/s of keys and values).
+  // time: fetching 256 bytes for rows of 128 took 182 us where 128 took 161
+  // (64 contexts of 256 to 16000 keys, e4m3, D = 128).
   const int row = c->head_dim * (fp8 ? 1 : 2);
   const CUtensorMapL2promotion promotion = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                            : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
@@ -213,8 +270,7 @@ fa_status fa_rotary(const fa_rotary_operand* q, const fa_rotary_operand* k, int 
       return FA_ERR_INVALID_ARG;
     if (t->x == t->y && (xs[0] != ys[0] || xs[1] != ys[1] || xs[2] != ys[2]))
       return FA_ERR_INVALID_ARG;
-    for (int d = 0; d < 3; ++d)  // an output element of its own for every index
-      if (extent[d] > 1 && ys[d] < D) return FA_ERR_INVALID_ARG;
+    if (!apart(ys, extent, 3, D) || (i == 1 && t->y == a.y[0])) return FA_ERR_INVALID_ARG;
     a.x[i] = t->x;
     a.y[i] = t->y;
     a.xs[i] = RowStrides{t->xs.batch, t->xs.head, t->xs.seq};
@@ -243,7 +299,7 @@ fa_status fa_cache_append(const fa_kv_pages* cache, const fa_ragged* batch, cons
   const fa_status st = check_batch(batch, true);
   if (st != FA_OK) return st;
   return cache_rows(cache, batch, batch->seqlens, k, k_token, k_head, v, v_token, v_head, dtype,
-                    stream, launch_cache_append);
+                    stream, true);
 }
 
 fa_status fa_cache_read(const fa_kv_pages* cache, const fa_ragged* batch, const int* starts,
@@ -253,7 +309,7 @@ fa_status fa_cache_read(const fa_kv_pages* cache, const fa_ragged* batch, const 
   if (st != FA_OK) return st;
   if (starts && !aligned(starts, 4)) return FA_ERR_INVALID_ARG;
   return cache_rows(cache, batch, starts, k, k_token, k_head, v, v_token, v_head, dtype, stream,
-                    launch_cache_read);
+                    false);
 }
 
 fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k, int D,
@@ -262,9 +318,9 @@ fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads
   *bytes = 0;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
   if (!paged_sizes_ok(batch, total, heads, heads_k, D) || max_keys < 0) return FA_ERR_INVALID_ARG;
-  PagedPlan plan;
-  paged_plan(batch, total, heads, heads_k, D, max_keys, &plan);
-  *bytes = plan.total_bytes;
+  for (const bool fp8 : {false, true})  // whatever the cache holds
+    *bytes = std::max(
+        *bytes, paged_plan(batch, total, heads, heads_k, D, max_keys, fp8).total_bytes);
   return FA_OK;
 }
 
@@ -296,9 +352,12 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
   if (!packed_ok(q, q_token, q_head, batch->total, heads, D) ||
       !packed_ok(o, o_token, o_head, batch->total, heads, D) || !aligned(lse, 4))
     return FA_ERR_INVALID_ARG;
-  PagedPlan plan;
-  paged_plan(batch->batch, batch->total, heads, cache->heads, D,
-             static_cast<long long>(batch->max_pages) * cache->page_size, &plan);
+  const long long extent[2] = {batch->total, heads}, o_st[2] = {o_token, o_head};
+  if (o == q || !apart(o_st, extent, 2, D)) return FA_ERR_INVALID_ARG;
+  const PagedPlan plan =
+      paged_plan(batch->batch, batch->total, heads, cache->heads, D,
+                 static_cast<long long>(batch->max_pages) * cache->page_size,
+                 cache->type == FA_ELEM_E4M3);
   if (plan.total_bytes &&
       (!aligned(workspace, 256) || workspace_bytes < plan.total_bytes))
     return FA_ERR_INVALID_ARG;
@@ -325,24 +384,17 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
   a.cache_elem = cache->type;
   a.elem = dtype;
   a.scale_log2 = scale * kLog2e;
-  if (!plan.whole) {
+  if (plan.total_bytes) {
     auto* base = static_cast<uint8_t*>(workspace);
     a.part_o = reinterpret_cast<float*>(base);
     a.part_ml = reinterpret_cast<float2*>(base + plan.o_bytes);
     a.tasks = reinterpret_cast<JoinTask*>(base + plan.o_bytes + plan.ml_bytes);
   }
-  a.block_rows = plan.block_rows;
-  // (a window bounds what a unit walks as well as the table does)
-  const long long unit_keys =
-      a.win_left < 0 || a.win_right < 0
-          ? kMaxRows
-          : static_cast<long long>(a.win_left) + a.win_right + plan.block_rows / a.group + kTile;
-  a.whole = plan.whole || unit_keys <= (plan.many ? kWholeKeysMany : kWholeKeysFew);
   if (sm_count(&a.sms) != cudaSuccess) return FA_ERR_CUDA;
   a.err = device_error_word();
   if (!a.err) return FA_ERR_CUDA;
   // {D, heads, total}: a box is the heads of one key head for a tile's tokens
-  if (plan.many &&
+  if (plan.part[plan.parts - 1].many &&
       !make_tmap_4d(&a.map_q, q,
                     dtype == FA_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
@@ -352,8 +404,21 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
                     static_cast<uint32_t>(a.group), CU_TENSOR_MAP_SWIZZLE_128B, 2,
                     static_cast<uint32_t>(kTile / a.group)))
     return FA_ERR_CUDA;
-  const auto launch = plan.many ? launch_paged_many : launch_paged_few;
-  return launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  for (int i = 0; i < plan.parts; ++i) {  // one after the other: they share the workspace
+    const PagedPart& part = plan.part[i];
+    a.block_rows = part.block_rows;
+    a.min_rows = part.min_rows;
+    a.max_rows = part.max_rows;
+    // (a window bounds what a unit walks as well as the table does)
+    const long long unit_keys =
+        a.win_left < 0 || a.win_right < 0
+            ? kMaxRows
+            : static_cast<long long>(a.win_left) + a.win_right + a.block_rows / a.group + kTile;
+    a.whole = part.whole || unit_keys <= (part.many ? kWholeKeysMany : kWholeKeysFew);
+    const auto launch = part.many ? launch_paged_many : launch_paged_few;
+    if (launch(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
 }
 
 }  // extern "C"

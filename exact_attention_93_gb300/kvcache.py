@@ -49,7 +49,8 @@ def kv_cache_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, k_
     1,).  A 16-bit cache has the rows' type; an e4m3 one gets each row at its
     own power-of-two scale, rounded to nearest even.  Rows of `total` behind the
     last sequence, and rows whose key would be negative, are not written.  The
-    slots that one call writes must be distinct."""
+    slots that one call writes must be distinct, and k_pages and v_pages must not
+    overlap (they may be interleaved views of one tensor)."""
     status = fattn.bind().append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, k_exp,
                                  v_exp)
     if status:

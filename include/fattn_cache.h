@@ -29,7 +29,8 @@ typedef enum { FA_ELEM_BF16 = 0, FA_ELEM_FP16 = 1, FA_ELEM_FP32 = 2, FA_ELEM_E4M
 /*
  * One operand of fa_rotary: [batch][seq][head][D] elements at x + b*xs.batch +
  * n*xs.seq + h*xs.head + d, written to y with the strides ys.  y == x (with
- * equal strides) rotates in place; otherwise x and y must not overlap.
+ * equal strides) rotates in place; otherwise x and y must not overlap, and the
+ * two operands' y never do.
  * Strides are non-negative and keep every 8 elements 16-byte aligned
  * (multiples of 8; of 4 for fp32).
  */
@@ -112,8 +113,9 @@ typedef struct {
  * smallest power of two 2^(e - 127), 1 <= e <= 254, with which the row's
  * largest finite magnitude is at most 448; values are rounded to nearest even,
  * infinities become +-448 * 2^(e - 127), NaN stays NaN.
- * Rows whose position is negative or beyond the table, or whose page is not in
- * 0 .. pages - 1, are not written.  The slots that one call writes must be
+ * The cache's strides are at least D where there is more than one of a kind, and
+ * k and v (and their exponents) do not overlap.  Rows whose position is negative
+ * or beyond the table, or whose page is not in 0 .. pages - 1, are not written.  The slots that one call writes must be
  * distinct; a slot that two rows share holds either one's bytes.
  */
 fa_status fa_cache_append(const fa_kv_pages* cache, const fa_ragged* batch, const void* k,
@@ -124,7 +126,8 @@ fa_status fa_cache_append(const fa_kv_pages* cache, const fa_ragged* batch, cons
  * Reads cached rows back: packed row i of sequence b gets key starts[b] + i
  * (starts NULL: key i), as k and v in `dtype` (bf16 or fp16; a 16-bit cache's
  * own type).  Rows outside the table, or of a page outside 0 .. pages - 1, read
- * as zeros.  batch->seqlens is not used.
+ * as zeros.  batch->seqlens is not used.  k and v do not overlap, and their
+ * strides are at least D where there is more than one of a kind.
  */
 fa_status fa_cache_read(const fa_kv_pages* cache, const fa_ragged* batch, const int* starts,
                         void* k, long long k_token, long long k_head, void* v, long long v_token,
@@ -155,6 +158,8 @@ fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads
  *   q, o     [total][heads][D] in `dtype` (bf16 or fp16; a 16-bit cache's own
  *            type), element strides token / head, multiples of 8, 16-byte
  *            aligned.
+ *            o does not overlap q, and its strides are at least D where there
+ *            is more than one of a kind.
  *   lse      fp32 [heads][total].
  *   options  NULL, or window and ALiBi as for fa_fwd_ex (slopes [heads] or
  *            [batch][heads]); block_mask must be NULL.
@@ -166,6 +171,11 @@ fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads
  * some query of a row block sees, a NaN or infinity in a value reaches every
  * query of that block (its weight 0 times NaN is NaN), as in the dense product.
  * Deterministic: the same inputs give bit-identical outputs.
+ *
+ * Under an e4m3 cache the products run on fp16 numbers under powers of two: a
+ * row of q under its own, keys and values relative to the largest row exponent
+ * among those that a row block walks.  Rows up to 2^22 below that lose nothing;
+ * what is 2^40 below counts as zeros.
  */
 fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void* o,
                        long long o_token, long long o_head, float* lse, const fa_kv_pages* cache,

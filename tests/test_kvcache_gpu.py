@@ -187,3 +187,112 @@ def test_a_decoder_layer_from_prompt_to_tokens():
         # and the rows went in turned by their positions
         want = R.rotary(x[s][0][None], torch.arange(n)[None], freq.cpu())[0]
         assert ((q.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("cache_dtype,D", [(BF, 128), (E4, 128), (E4, 64)])
+def test_chunks_and_tokens_attend_to_what_the_cache_reads_back(cache_dtype, D):
+    """A prompt in chunks beside sequences that generate, an idle one among
+    them: each step attends to exactly the keys and values read back."""
+    g = torch.Generator().manual_seed(7)
+    H, Hk, page = 6, 3, 32
+    freq, _ = rotary.rotary_frequencies(D)
+    kp, vp, ke, ve = kvcache.alloc_kv_cache(60, page, Hk, D, cache_dtype)
+    table = torch.randperm(60, generator=g)[:4 * 12].view(4, 12).to(torch.int32).cuda()
+    kw = dict(k_exp=ke, v_exp=ve)
+    done = [0, 0, 0, 0]
+    for new in ([70, 3, 0, 20], [150, 1, 1, 0], [9, 1, 1, 1], [1, 1, 0, 1]):
+        q, k, v = (torch.randn(sum(new), h, D, generator=g).to(BF).cuda() for h in (H, Hk, Hk))
+        pos = torch.cat([torch.arange(d, d + n) for d, n in zip(done, new)]).cuda()
+        ctx, done = done, [d + n for d, n in zip(done, new)]
+        cu = torch.tensor([0] + new).cumsum(0).to(torch.int32).cuda()
+        lens = torch.tensor(done, dtype=torch.int32).cuda()
+        q, k = rotary.rotary_func(q, k, freq, positions=pos)
+        kvcache.kv_cache_append(k, v, kp, vp, table, cu, lens, **kw)
+        o, lse = attention.flash_attn_paged_func(q, kp, vp, table, cu, lens, return_lse=True, **kw)
+        every = torch.tensor([0] + done).cumsum(0).to(torch.int32).cuda()
+        kr, vr = kvcache.kv_cache_read(kp, vp, table, every, sum(done), **kw)
+        torch.cuda.synchronize()
+        assert fattn.fa_device_error() == fattn.FA_OK
+        b = R.Batch(new, ctx, Hk, D, page, BF, False)
+        b.k, b.v = ([t.cpu().double() for t in x.split(done)] for x in (kr, vr))
+        ref, rl, A, S = R.attention(b, q.cpu(), D ** -0.5)
+        tol_o, tol_l = R.attention_bounds(ref, rl, A, S, BF, R.EPS[BF], D)
+        assert ((o.cpu().double() - ref).abs() <= tol_o).all()
+        assert ((lse.cpu().double() - rl).abs() <= tol_l).all()
+
+
+@pytest.mark.parametrize("cache_dtype", [BF, E4])
+def test_append_and_read_in_a_graph_on_another_stream(cache_dtype):
+    b, (kp, vp, ke, ve), k, v = setup([3, 20, 1], [30, 0, 5], 2, 64, 16, cache_dtype, BF)
+    table, cu, lens = b.table.cuda(), b.cu.cuda(), b.len_t.cuda()
+    starts = torch.tensor([30, 0, 5], dtype=torch.int32, device="cuda")
+    kd, vd = k.cuda(), v.cuda()
+    out = torch.zeros_like(kd), torch.zeros_like(vd)
+
+    def step():
+        kvcache.kv_cache_append(kd, vd, kp, vp, table, cu, lens, k_exp=ke, v_exp=ve)
+        kvcache.kv_cache_read(kp, vp, table, cu, b.total, starts=starts, k_exp=ke, v_exp=ve,
+                              dtype=BF, out=out)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    first = [t.clone() for t in out]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    n = sum(b.rows)
+    for swap in (True, False):
+        kd.copy_(v if swap else k)
+        vd.copy_(k if swap else v)
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = first[::-1] if swap else first
+        assert torch.equal(out[0][:n], want[0][:n]) and torch.equal(out[1][:n], want[1][:n])
+    assert fattn.fa_device_error() == fattn.FA_OK
+
+
+def test_written_tensors_are_seen_by_autograd():
+    b, (kp, vp, ke, ve), k, v = setup([3, 2], [0, 5], 2, 64, 16, BF, BF)
+    table, cu, lens = b.table.cuda(), b.cu.cuda(), b.len_t.cuda()
+    w = torch.ones(64, device="cuda", dtype=BF, requires_grad=True)
+    y = (kp * w).sum()  # saves kp
+    kvcache.kv_cache_append(k.cuda(), v.cuda(), kp, vp, table, cu, lens)
+    with pytest.raises(RuntimeError):
+        y.backward()
+
+
+def test_overlapping_results_are_refused():
+    b, (kp, vp, ke, ve), k, v = setup([3, 2], [0, 5], 2, 64, 16, BF, BF)
+    table, cu, lens = b.table.cuda(), b.cu.cuda(), b.len_t.cuda()
+    kd, vd = k.cuda(), v.cuda()
+    with pytest.raises(fattn.FattnError):
+        kvcache.kv_cache_append(kd, vd, kp, kp, table, cu, lens)
+    one = kp[:, :, :1].expand(-1, -1, 2, -1)
+    with pytest.raises(fattn.FattnError):
+        kvcache.kv_cache_append(kd, vd, one, vp, table, cu, lens)
+    with pytest.raises(fattn.FattnError):
+        kvcache.kv_cache_read(kp, vp, table, cu, b.total, out=(kd, kd))
+    with pytest.raises(fattn.FattnError):
+        kvcache.kv_cache_read(kp, vp, table, cu, b.total, out=(kd, vd[:1].expand(b.total, -1, -1)))
+    both = torch.zeros(kp.shape[0], 2, *kp.shape[1:], device="cuda", dtype=BF)  # interleaved pages
+    kvcache.kv_cache_append(kd, vd, both[:, 0], both[:, 1], table, cu, lens)
+    kvcache.kv_cache_append(kd, vd, kp, vp, table, cu, lens)
+    assert torch.equal(both[:, 0], kp) and torch.equal(both[:, 1], vp)
+
+
+def test_a_batch_without_rows():
+    b, (kp, vp, ke, ve), k, v = setup([0, 0], [4, 0], 2, 64, 16, BF, BF)
+    table, cu, lens = b.table.cuda(), b.cu.cuda(), b.len_t.cuda()
+    none = torch.zeros(0, 2, 64, device="cuda", dtype=BF)
+    kvcache.kv_cache_append(none, none, kp, vp, table, cu, lens)
+    ko, vo = kvcache.kv_cache_read(kp, vp, table, cu, 0)
+    o, lse = attention.flash_attn_paged_func(torch.zeros(0, 6, 64, device="cuda", dtype=BF), kp, vp,
+                                             table, cu, lens, return_lse=True)
+    torch.cuda.synchronize()
+    assert ko.shape == vo.shape == (0, 2, 64) and o.shape == (0, 6, 64) and lse.shape == (6, 0)
+    assert not kp.any() and not vp.any() and fattn.fa_device_error() == fattn.FA_OK

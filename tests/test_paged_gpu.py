@@ -212,6 +212,22 @@ def test_same_bits_twice_on_streams_and_in_graphs(rows):
             assert torch.equal(out[0], want[i][0]) and torch.equal(out[1], want[i][1])
 
 
+@pytest.mark.parametrize("spare", [2, 200])  # units whole, and cut and joined
+@pytest.mark.parametrize("fp8,D,H,Hk,dtype", [(False, 128, 8, 2, BF), (True, 128, 8, 2, BF),
+                                              (True, 64, 6, 6, HF), (False, 64, 16, 1, HF)])
+def test_single_tokens_beside_a_chunk(fp8, D, H, Hk, dtype, spare):
+    rows = [1] * 11 + [790] + [0, 1, 2, 4, 5, 16, 17] + [1] * 130 + [3]
+    ctx = [(i * 97) % 700 for i in range(len(rows))]
+    b = R.Batch(rows, ctx, Hk, D, 16, dtype, fp8, seed=4, spare_cols=spare)
+    q, o, lse = run(b, H)
+    check(b, H, q, o, lse)
+    q, o, lse = run(b, H, causal=False, window=(60, 5))
+    check(b, H, q, o, lse, causal=False, window=(60, 5))
+    q, again, lse2 = run(b, H, causal=False, window=(60, 5))
+    n = sum(b.rows)
+    assert torch.equal(o[:n], again[:n]) and torch.equal(lse[:, :n], lse2[:, :n])
+
+
 def test_many_short_sequences():
     n = 700
     lens = [(i * 37) % 90 for i in range(n)]

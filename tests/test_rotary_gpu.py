@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import paged_ref as R
-from exact_attention_93_gb300 import rotary
+from exact_attention_93_gb300 import fattn, rotary
 
 pytestmark = pytest.mark.gpu
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -196,3 +196,26 @@ def test_backward_on_another_stream_and_leaf_accumulation():
     ref = R.rotary(one, pos, freq.cpu(), inverse=True)
     ref[:, :, :1] += 2 * R.rotary(one[:, :, :1], pos, freq.cpu(), inverse=True)
     assert ((x.grad.cpu().double() - ref).abs() <= 2.0 ** -20 * 8).all()
+
+
+def test_in_place_refusals_and_versions():
+    freq, _ = rotary.rotary_frequencies(64)
+    x = torch.randn(2, 9, 3, 64, device="cuda")
+    keep = x.clone()
+    with pytest.raises(ValueError):  # both results in one place
+        rotary.rotary_func(x, x, freq, inplace=True)
+    with pytest.raises(ValueError):
+        rotary.rotary_func(x.requires_grad_(), None, freq, inplace=True)
+    x = x.detach()
+    with pytest.raises(fattn.FattnError):  # heads that share their elements
+        rotary.rotary_func(x[:, :, :1].expand(-1, -1, 3, -1), None, freq, inplace=True)
+    assert torch.equal(x, keep)
+    a, b = rotary.rotary_func(x, x, freq)  # two results: allowed
+    assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        rotary.rotary_func(x, None, freq.clone().requires_grad_())
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    y = (x * w).sum()  # saves x
+    rotary.rotary_func(x, None, freq, inplace=True)
+    with pytest.raises(RuntimeError):
+        y.backward()

@@ -90,6 +90,12 @@ def test_rows_and_null_structs(lib):
     n = ragged(seqlens=None)
     assert lib.fa_cache_append(pc, ctypes.addressof(n), FAKE, 128, 64, FAKE, 128, 64, 0,
                                None) == INV
+    e = pages(v=2 * FAKE, v_head=0)  # heads, or keys and values, that share elements
+    assert lib.fa_cache_append(ctypes.addressof(e), pb, FAKE, 128, 64, FAKE, 128, 64, 0,
+                               None) == INV
+    assert lib.fa_cache_append(pc, pb, FAKE, 128, 64, FAKE, 128, 64, 0, None) == INV
+    assert lib.fa_cache_read(pc, pb, None, FAKE, 128, 64, FAKE, 128, 64, 0, None) == INV
+    assert lib.fa_cache_read(pc, pb, None, FAKE, 0, 64, 2 * FAKE, 128, 64, 0, None) == INV
     z = ragged(total=0)  # nothing to do, nothing to check the rows of
     assert lib.fa_cache_append(pc, ctypes.addressof(z), None, 0, 0, None, 0, 0, 0, None) == 0
 
@@ -107,7 +113,7 @@ def paged(lib, heads=4, scale=0.125, opts=None, ws=FAKE, ws_bytes=1 << 30, q=FAK
     (dict(heads=3), INV), (dict(heads=0), INV), (dict(heads=2 * 129), INV),
     (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(ws=None), INV),
     (dict(ws=FAKE + 128), INV), (dict(ws_bytes=64), INV), (dict(q=FAKE + 2), INV),
-    (dict(q_token=252), INV), (dict(o=None), INV), (dict(lse=FAKE + 1), INV),
+    (dict(q_token=252), INV), (dict(o=None), INV), (dict(o=FAKE), INV), (dict(lse=FAKE + 1), INV),
     (dict(opts=fattn.FaOptions(-2, 0, None, 0, None, 0)), INV),
     (dict(opts=fattn.FaOptions(0, -2, None, 0, None, 0)), INV),
     (dict(opts=fattn.FaOptions(-1, -1, FAKE + 2, 0, None, 0)), INV),
@@ -124,6 +130,8 @@ def test_workspace_size(lib):
     assert st == fattn.FA_OK and long > 0 and long % 256 == 0
     assert size(1, 1, 8, 2, 64, 16) == (fattn.FA_OK, 0)  # short tables need none
     assert size(1, 1000, 8, 2, 64, 1 << 20)[1] > long    # more rows, larger blocks
+    # single tokens, and with a chunk among them: either kernel's blocks fit
+    assert size(200, 200, 8, 2, 64, 1 << 20)[1] < size(200, 701, 8, 2, 64, 1 << 20)[1]
     for bad, want in (((0, 1, 8, 2, 64, 16), INV), ((1, 1, 8, 3, 64, 16), INV),
                       ((1, 1, 8, 2, 96, 16), UNS), ((1, -1, 8, 2, 64, 16), INV),
                       ((1, 1, 8, 2, 64, -1), INV)):
@@ -196,6 +204,8 @@ def test_python_refusals():
         kvcache.kv_cache_read(kp, vp, table, cu, 3, dtype=torch.float32)
     with pytest.raises(ValueError):  # a result of another size
         kvcache.kv_cache_read(kp, vp, table, cu, 3, out=(t(2, 2, 64), t(2, 2, 64)))
+    with pytest.raises(ValueError):  # half a result
+        kvcache.kv_cache_read(kp, vp, table, cu, 3, out=(t(3, 2, 64), None))
     with pytest.raises(ValueError):  # exponents with a 16-bit cache, and an e4m3 one without
         kvcache.kv_cache_append(x, x, *args, k_exp=torch.zeros(2, 2, 16, dtype=torch.uint8))
     k8, v8, ke, ve = kvcache.alloc_kv_cache(2, 16, 2, 64, torch.float8_e4m3fn, device="cpu")
