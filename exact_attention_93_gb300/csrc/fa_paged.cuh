@@ -5,10 +5,10 @@
 // Units.  A unit is one block of query rows (rows token * group +
 // head-in-group of one sequence) against one key head.  It walks tiles of 128
 // keys.  Units are laid end to end by their weights, key head by key head and
-// within a head sequence by sequence, and each CTA takes an equal stretch of the whole, cutting
-// units where the stretch ends: a long context over few rows is spread over
-// every SM, ragged batches stay balanced, and a CTA leaves at most two cut
-// pieces whatever the batch.  Cut pieces go to the workspace in fp32
+// within a head sequence by sequence, and each CTA takes an equal stretch of the
+// whole, cutting units where the stretch ends: a long context over few rows is
+// spread over every SM, ragged batches stay balanced, and a CTA leaves at most two
+// cut pieces whatever the batch.  Cut pieces go to the workspace in fp32
 // (unnormalised O, maximum, sum) and paged_join_kernel adds them up in a fixed
 // order.  Where no sequence of the table can be long (PagedLaunch::whole), units
 // stay whole instead, each with the CTA whose stretch it begins in, and nothing

@@ -16,12 +16,14 @@
 // each, with a running maximum, sum and O of their own that are joined once per
 // piece of work: no barrier among them inside the key loop, and two tiles of
 // dependent steps in flight.  (With every warp on the same tile, 16 keys each,
-// an e4m3 batch of 64 contexts took 176 us instead of the time below.)  The products are turned around, S^T = K Q^T
-// and O^T = V^T P^T, on mma.sync m16n8k16: keys and head columns fill the 16
-// rows, so the padding of the query side is to 8 rows, and the operands go
-// from shared memory to registers to the tensor core without a detour through
-// tensor memory, which a tile of 8 columns would not fill.  P^T moves from the
-// accumulator to the operand layout by an in-register 8 x 8 transpose.
+// an e4m3 batch of 64 contexts took 9 % longer; three groups of four warps, with
+// one producer each, gained nothing there and lost 20 % on 128 shorter contexts.)
+// The products are turned around, S^T = K Q^T and O^T = V^T P^T, on mma.sync
+// m16n8k16: keys and head columns fill the 16 rows, so the padding of the query
+// side is to 8 rows, and the operands go from shared memory to registers to the
+// tensor core without a detour through tensor memory, which a tile of 8 columns
+// would not fill.  P^T moves from the accumulator to the operand layout by an
+// in-register 8 x 8 transpose.
 //
 // e4m3 caches.  Codes convert exactly to fp16 in registers, so an 8-bit cache
 // costs half the HBM bytes and no precision beyond its own: q is scaled by a
@@ -30,6 +32,14 @@
 // P' = 2^(s - m) * 2^(e_v - R + 15), at most 2^15.  The order of the head
 // columns (keys) and of columns and keys (values) inside an operand is chosen
 // so that a lane reads 16 contiguous bytes.
+//
+// Measured (32 query and 8 key heads): 64 contexts of 256 to 16000 keys, D = 128,
+// 16-bit 193 us, 6.4 TB/s of keys and values, 94 % of the measured copy rate;
+// D = 64 110 us, 5.6 TB/s.  e4m3, D = 128, 122 us, 5.1 TB/s (the same stream
+// without its products 107 us, of which 13 are the start and the joining), and
+// D = 64 87 us, where the conversions bound it (the stream alone 62).  One
+// context of 1000 keys 9.6 us, of 4000 13 to 15, of 32000 31 to 37: launch, the
+// look at the batch, and the joining of the pieces.
 #include "fa_paged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"
@@ -57,7 +67,10 @@ struct FewSmem {
   // its tiles alternate: a slot's uses then follow one another in one group's
   // sight, and none can be mistaken for the one before it.
   static constexpr int kSlots = kRingBytes / kSlotBytes, kRing = kSlots / kGroups;
-  static constexpr int kMergePitch = D + 4;
+  // a row of the joining buffer: 16-bit, its columns; e4m3, where a lane holds
+  // columns (D / 8) g + 2 mb and the next of every block mb, pair mb of lane group g
+  // at 2 (10 mb + g): stores of pairs and loads of a lane's columns meet no bank twice
+  static constexpr int kMergePitch = kFp8 ? D / 16 * 20 + 4 : D + 4;
   static constexpr int kSteps = D / 16;
   alignas(1024) uint8_t ring[kSlots][kSlotBytes];
   alignas(16) uint8_t exps[kFp8 ? kSlots : 1][kTile];
@@ -613,10 +626,15 @@ __global__ void __maxnreg__(kFewRegs)
 #pragma unroll
             for (int mb = 0; mb < kSteps; ++mb)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                // 16-bit: column 16 mb + g (+ 8); e4m3: column (D / 8) g + 2 mb (+ 1)
-                const int d = kFp8 ? (D / 8) * g + 2 * mb + (i >> 1) : 16 * mb + g + 8 * (i >> 1);
-                s.merge[warp % kGroupWarps][2 * t + (i & 1)][d] = o[mb][nb][i];
+              for (int c = 0; c < 2; ++c) {
+                float* row = s.merge[warp % kGroupWarps][2 * t + c];
+                if constexpr (kFp8) {
+                  *reinterpret_cast<float2*>(row + 2 * (10 * mb + g)) =
+                      make_float2(o[mb][nb][c], o[mb][nb][c + 2]);
+                } else {
+                  row[16 * mb + g] = o[mb][nb][c];
+                  row[16 * mb + g + 8] = o[mb][nb][c + 2];
+                }
               }
           named_bar_sync(1, kConsumers * 32);
           if (gr == 0)
@@ -629,9 +647,16 @@ __global__ void __maxnreg__(kFewRegs)
             const float a = ex2_approx(s.m[from][r] - ref);
             sum = fmaf(s.l[from][r], a, sum);
             const float av = kFp8 ? a * s.vscale[from] : a;
-            const float* src = &s.merge[w][warp][lane * kN];
+            const float* src = s.merge[w][warp];
 #pragma unroll
-            for (int e = 0; e < kN; ++e) out[e] = fmaf(src[e], av, out[e]);
+            for (int e = 0; e < kN; e += 2) {  // columns lane * kN + e and the next
+              constexpr int kPairs = D / 16;   // of a lane group's columns
+              const int pair = (lane * kN + e) / 2;
+              const float2 v = *reinterpret_cast<const float2*>(
+                  src + (kFp8 ? 2 * (10 * (pair % kPairs) + pair / kPairs) : 2 * pair));
+              out[e] = fmaf(v.x, av, out[e]);
+              out[e + 1] = fmaf(v.y, av, out[e + 1]);
+            }
           }
           named_bar_sync(1, kConsumers * 32);
         }

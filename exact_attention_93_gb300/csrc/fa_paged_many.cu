@@ -36,6 +36,14 @@
 //
 // Warps: 0-3 softmax of tile A, 4-7 of tile B, 8 producer, 9 MMA issue, 10 the
 // units, 11 zeroing (12 warps), or 12-15 conversion (e4m3 caches, 16 warps).
+//
+// Measured (D = 128, 32 query and 8 key heads, bf16): a prompt of 8192 tokens
+// 380 us, 1447 TFLOP/s, tensor pipe 61 % active (the dense forward over 32 heads
+// 416 us); 32768 tokens of 8 heads 1443 us, 1524 TFLOP/s (dense 1378); four
+// prompts of 9429 tokens in all 227 us; four chunks of 137 tokens over 20000 keys
+// 189 us.  Beside its key tiles a unit costs about 3 us (reading O out, filling
+// the pipeline again) and a call about 10.  e4m3: 497 and 229 us for the first
+// and the last: the four converting warps are the slowest stage.
 #include "fa_paged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"

@@ -19,6 +19,10 @@
 // 512 / D heads at a time.  The angles of a lane's 8 pairs depend on the
 // token alone and serve all of its heads; the lane groups of a warp compute
 // a share of them each and exchange them by shuffles.
+//
+// Measured: 65536 tokens of 16 heads of 128, bf16, 80.7 us, 6.65 TB/s, 98 % of
+// the measured copy rate; 5003 tokens of 40 heads 18 us; 32 tokens of 40 heads
+// 3.2 us.
 #include <type_traits>
 
 #include "fa_serve.h"

@@ -195,7 +195,8 @@ PagedPlan paged_plan(int batch, int total, int heads, int heads_k, int D, long l
   };
   if (mixed || mean <= kFewRows)
     add(false, paged_few_rows(mixed ? group : mean), 0, mixed ? kFewRows : INT_MAX);
-  if (mixed || mean > kFewRows) add(true, paged_many_rows(group), mixed ? kFewRows + 1 : 0, INT_MAX);
+  if (mixed || mean > kFewRows)
+    add(true, paged_many_rows(group), mixed ? kFewRows + 1 : 0, INT_MAX);
   plan.o_bytes = round256(rows * D * sizeof(float));
   plan.ml_bytes = round256(rows * sizeof(float2));
   plan.total_bytes = rows ? plan.o_bytes + plan.ml_bytes + round256(32ull * sms) : 0;
@@ -212,9 +213,9 @@ bool paged_sizes_ok(int batch, int total, int heads, int heads_k, int D) {
 bool page_map(CUtensorMap* m, const void* base, const fa_kv_pages* c, long long page,
               long long token, long long head) {
   const bool fp8 = c->type == FA_ELEM_E4M3;
-  // A row is followed by another head's, which another CTA wants at another
-  // time: fetching 256 bytes for rows of 128 took 182 us where 128 took 161
-  // (64 contexts of 256 to 16000 keys, e4m3, D = 128).
+  // A row is followed by another head's, which another CTA wants: fetching 256
+  // bytes for rows of 128 gains nothing with 8 heads (122 and 120 us for 64 contexts
+  // of 256 to 16000 keys, e4m3, D = 128) and loses with 3 (61 and 67).
   const int row = c->head_dim * (fp8 ? 1 : 2);
   const CUtensorMapL2promotion promotion = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                            : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
