@@ -146,8 +146,7 @@ __global__ void __maxnreg__(kFewRegs)
   // normal down to 2^-29 of the largest (e4m3: see pfac)
   constexpr float kLift = !kFp8 && !kBf16 ? 15.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
-  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                     ~uintptr_t(1023));
+  Smem& s = *reinterpret_cast<Smem*>(smem_raw + (-smem_u32(smem_raw) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     const Place at = warp_place<false>(p, gridDim.x, blockIdx.x);

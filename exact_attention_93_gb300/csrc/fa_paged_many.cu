@@ -191,8 +191,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
   constexpr float kThreshold = 8.0f;
   constexpr int kPOffset = kMmaBf16 ? 0 : kFp8 ? 4 : 6;
   extern __shared__ uint8_t smem_raw[];
-  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                     ~uintptr_t(1023));
+  Smem& s = *reinterpret_cast<Smem*>(smem_raw + (-smem_u32(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile_tokens = p.block_rows / p.group / 2, tile_rows = tile_tokens * p.group;
   constexpr int kConverters = ManyWarps<kFp8>::kConverters, kStages = Smem::kStages;
