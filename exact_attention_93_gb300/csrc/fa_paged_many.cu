@@ -44,6 +44,8 @@
 // 189 us.  Beside its key tiles a unit costs about 3 us (reading O out, filling
 // the pipeline again) and a call about 10.  e4m3: 497 and 229 us for the first
 // and the last: the four converting warps are the slowest stage.
+#include <type_traits>
+
 #include "fa_paged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"
@@ -584,42 +586,52 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                 to[h] = s.kv[st] + (h ^ flip) * Smem::kBlockBytes + r0 * 128 +
                         ((c ^ (r0 & 7)) << 4);
               }
+              // Factors 2^(e - ref + 7), which keep codes below 448 * 128, as fp16
+              // pairs: this lane's are of rows 8 (lane >> 2) + (lane & 3) of the
+              // warp's fours, and 64 on.  e = 0 (and rows to leave out) make
+              // zeros whatever the codes; -0 stands for that.
+              uint32_t f2[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int r = (warp & 1) * 4 + (lane & 3) + (lane >> 2) * kStep + i * 64;
+                const int key = j * kTile + r, e = s.exps[st][r];
+                const float f = many_exp2_field(134 + e - base_e);
+                f2[i] = e == 0 || (cut && (key < u.key_lo || key >= u.key_hi)) ? 0x80008000u
+                                                                              : pack2<false>(f, f);
+              }
+              const bool empty =
+                  __any_sync(0xffffffffu, f2[0] == 0x80008000u || f2[1] == 0x80008000u);
+              auto rows = [&](auto some_empty) {
 #pragma unroll 1
-              for (int m = 0; m < kTile / kStep; m += kBatch) {
-                uint2 v[kBatch][kPieces];
-                uint32_t e[kBatch];
+                for (int m = 0; m < kTile / kStep; m += kBatch) {
+                  uint2 v[kBatch][kPieces];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
+                  for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-                  for (int h = 0; h < kPieces; ++h)
-                    v[i][h] = *reinterpret_cast<const uint2*>(from[h] + (m + i) * kStep * D);
-                  e[i] = s.exps[st][r0 + (m + i) * kStep];
-                }
-                if (cut) {
+                    for (int h = 0; h < kPieces; ++h)
+                      v[i][h] = *reinterpret_cast<const uint2*>(from[h] + (m + i) * kStep * D);
+                  if constexpr (Smem::kInPlace) __syncwarp();
 #pragma unroll
                   for (int i = 0; i < kBatch; ++i) {
-                    const int key = j * kTile + r0 + (m + i) * kStep;
-                    if (key < u.key_lo || key >= u.key_hi) e[i] = 0;
+                    const uint32_t f = __shfl_sync(0xffffffffu, m < 8 ? f2[0] : f2[1],
+                                                   ((m + i) & 7) * 4 + (lane >> 3));
+#pragma unroll
+                    for (int h = 0; h < kPieces; ++h) {
+                      uint32_t w0 = v[i][h].x, w1 = v[i][h].y;
+                      if (some_empty && f == 0x80008000u) w0 = w1 = 0u;
+                      *reinterpret_cast<uint4*>(to[h] + (m + i) * kStep * 128) =
+                          make_uint4(mul_f16x2(e4m3x2_to_f16x2(w0), f),
+                                     mul_f16x2(e4m3x2_to_f16x2(w0 >> 16), f),
+                                     mul_f16x2(e4m3x2_to_f16x2(w1), f),
+                                     mul_f16x2(e4m3x2_to_f16x2(w1 >> 16), f));
+                    }
                   }
                 }
-                if constexpr (Smem::kInPlace) __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                  // 2^(e - ref + 7): codes stay below 448 * 128.  e = 0: zeros
-                  const float f =
-                      e[i] ? many_exp2_field(134 + static_cast<int>(e[i]) - base_e) : 0.f;
-                  const uint32_t f2 = pack2<false>(f, f);
-#pragma unroll
-                  for (int h = 0; h < kPieces; ++h) {
-                    const uint32_t w0 = e[i] ? v[i][h].x : 0u, w1 = e[i] ? v[i][h].y : 0u;
-                    *reinterpret_cast<uint4*>(to[h] + (m + i) * kStep * 128) =
-                        make_uint4(mul_f16x2(e4m3x2_to_f16x2(w0), f2),
-                                   mul_f16x2(e4m3x2_to_f16x2(w0 >> 16), f2),
-                                   mul_f16x2(e4m3x2_to_f16x2(w1), f2),
-                                   mul_f16x2(e4m3x2_to_f16x2(w1 >> 16), f2));
-                  }
-                }
-              }
+              };
+              if (empty)
+                rows(std::true_type{});
+              else
+                rows(std::false_type{});
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) mbar_arrive(&s.full[st]);
