@@ -34,11 +34,11 @@
 // so that a lane reads 16 contiguous bytes.
 //
 // Measured (32 query and 8 key heads): 64 contexts of 256 to 16000 keys, D = 128,
-// 16-bit 193 us, 6.4 TB/s of keys and values, 94 % of the measured copy rate;
-// D = 64 110 us, 5.6 TB/s.  e4m3, D = 128, 122 us, 5.1 TB/s (the same stream
+// 16-bit 188 us, 6.6 TB/s of keys and values, 97 % of the measured copy rate;
+// D = 64 108 us, 5.7 TB/s.  e4m3, D = 128, 116 us, 5.35 TB/s (the same stream
 // without its products 107 us, of which 13 are the start and the joining), and
-// D = 64 87 us, where the conversions bound it (the stream alone 62).  One
-// context of 1000 keys 9.6 us, of 4000 13 to 15, of 32000 31 to 37: launch, the
+// D = 64 82 us, where the conversions bound it (the stream alone 62).  One
+// context of 1000 keys 9.3 us, of 4000 12 to 15, of 32000 30 to 35: launch, the
 // look at the batch, and the joining of the pieces.
 #include "fa_paged.cuh"
 #include "fa_serve.h"

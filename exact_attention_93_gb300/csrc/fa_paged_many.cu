@@ -38,12 +38,15 @@
 // units, 11 zeroing (12 warps), or 12-15 conversion (e4m3 caches, 16 warps).
 //
 // Measured (D = 128, 32 query and 8 key heads, bf16): a prompt of 8192 tokens
-// 380 us, 1447 TFLOP/s, tensor pipe 61 % active (the dense forward over 32 heads
-// 416 us); 32768 tokens of 8 heads 1443 us, 1524 TFLOP/s (dense 1378); four
+// 381 us, 1442 TFLOP/s, tensor pipe 61 % active (the dense forward over 32 heads
+// 415 us); 32768 tokens of 8 heads 1447 us, 1520 TFLOP/s (dense 1381); four
 // prompts of 9429 tokens in all 227 us; four chunks of 137 tokens over 20000 keys
-// 189 us.  Beside its key tiles a unit costs about 3 us (reading O out, filling
-// the pipeline again) and a call about 10.  e4m3: 497 and 229 us for the first
-// and the last: the four converting warps are the slowest stage.
+// 188 us.  Beside its key tiles a unit costs about 3 us (reading O out, filling
+// the pipeline again) and a call about 10.  e4m3: 464 and 208 us for the first
+// and the last.  There registers are the limit: 16 warps share what 12 have in
+// the 16-bit kernel, and a split with more for the softmax or more for the
+// conversion made both slower (200 / 56: 481 us, 184 / 72: 482).  Queries take 25
+// us of the 464, a unit's rows being converted before its first product.
 #include <type_traits>
 
 #include "fa_paged.cuh"

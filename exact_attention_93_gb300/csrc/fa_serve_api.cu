@@ -160,18 +160,18 @@ struct PagedPlan {
 
 // Which kernel a call takes.  The lengths are on the device; what the host knows
 // is the mean.  (us, few-row and many-row kernel, 32 / 8 heads of 128, contexts
-// up to 16000 keys, 16-bit and e4m3: 64 sequences of 2 tokens, 8 rows, 147 and
-// 161, 94 and 195; of 4 tokens, 16 rows, 160 and 162, 162 and 197; of 8 tokens,
-// 32 rows, 16-bit, 968 with a few-row kernel of 32 rows and 208.)
+// up to 16000 keys, 16-bit and e4m3: 64 sequences of 2 tokens, 8 rows, 146 and
+// 160, 92 and 184; of 4 tokens, 16 rows, 156 and 162, 142 and 185.  Blocks of 32
+// rows in the few-row kernel spilled: 968 us for 8 tokens, 207 in the other.)
 //
 // Single tokens may come together with a chunk of a prompt.  Where that is likely
 // (the sequences cannot be equally long, and one of them could be) and there are
 // enough single tokens for it to pay, each kernel takes its own sequences; a
 // launch that finds none costs 15 us.  (Few rows alone, many rows alone, both: 256
-// single tokens and a chunk of 512 over 4000 keys 561, 350 and 299, e4m3 701, 446
-// and 242; 256 and 100 259, 291 and 283, e4m3 239, 375 and 219; 64 and 512 260,
-// 195 and 198, e4m3 328, 251 and 153; 64 and 64 157, 165 and 186, e4m3 113, 205
-// and 139; 8 and 200, e4m3, 53, 25 and 35.)
+// single tokens and a chunk of 512 over 4000 keys 447, 346 and 298, e4m3 609, 411
+// and 227; 256 and 100 252, 283 and 278, e4m3 219, 347 and 205; 64 and 512 218,
+// 192 and 195, e4m3 289, 230 and 149; 64 and 64 153, 163 and 185, e4m3 104, 190
+// and 135; 8 and 200, e4m3, 45, 24 and 32.)
 constexpr int kFewRows = 16, kMixedMean = 512;
 constexpr int mixed_batch(bool fp8) { return fp8 ? 32 : 128; }
 constexpr int mixed_longest(bool fp8) { return fp8 ? 384 : 768; }
@@ -214,8 +214,8 @@ bool page_map(CUtensorMap* m, const void* base, const fa_kv_pages* c, long long 
               long long token, long long head) {
   const bool fp8 = c->type == FA_ELEM_E4M3;
   // A row is followed by another head's, which another CTA wants: fetching 256
-  // bytes for rows of 128 gains nothing with 8 heads (122 and 120 us for 64 contexts
-  // of 256 to 16000 keys, e4m3, D = 128) and loses with 3 (61 and 67).
+  // bytes for rows of 128 gained 2 % with 8 heads (122 and 120 us for 64 contexts
+  // of 256 to 16000 keys, e4m3, D = 128) and lost 10 % with 3 (61 and 67).
   const int row = c->head_dim * (fp8 ? 1 : 2);
   const CUtensorMapL2promotion promotion = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                            : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
