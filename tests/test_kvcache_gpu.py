@@ -296,3 +296,47 @@ def test_a_batch_without_rows():
     torch.cuda.synchronize()
     assert ko.shape == vo.shape == (0, 2, 64) and o.shape == (0, 6, 64) and lse.shape == (6, 0)
     assert not kp.any() and not vp.any() and fattn.fa_device_error() == fattn.FA_OK
+
+
+def test_inference_mode():
+    with torch.inference_mode():
+        b, (kp, vp, ke, ve), k, v = setup([3, 2], [0, 5], 2, 64, 16, E4, BF)
+        table, cu, lens = b.table.cuda(), b.cu.cuda(), b.len_t.cuda()
+        freq, _ = rotary.rotary_frequencies(64)
+        q = torch.randn(5, 4, 64, device="cuda").to(BF)
+        want = rotary.rotary_func(q, None, freq)
+        assert rotary.rotary_func(q, None, freq, inplace=True) is q and torch.equal(q, want)
+        kvcache.kv_cache_append(k.cuda(), v.cuda(), kp, vp, table, cu, lens, k_exp=ke, v_exp=ve)
+        o = attention.flash_attn_paged_func(q, kp, vp, table, cu, lens, k_exp=ke, v_exp=ve)
+        assert torch.isfinite(o).all() and fattn.fa_device_error() == fattn.FA_OK
+
+
+def test_two_threads():
+    """Calls from two threads on streams of their own give what one gives."""
+    import threading
+    b, (kp, vp, ke, ve), k, v = setup([1] * 6, [100, 900, 2500, 0, 40, 600], 2, 128, 16, E4, BF)
+    kw = dict(k_exp=ke, v_exp=ve)
+    table, cu, lens = b.table.cuda(), b.cu.cuda(), b.len_t.cuda()
+    ends = torch.tensor([0] + b.lens).cumsum(0).to(torch.int32).cuda()
+    g = torch.Generator().manual_seed(1)
+    kk, vv = (torch.randn(sum(b.lens), 2, 128, generator=g).to(BF).cuda() for _ in range(2))
+    kvcache.kv_cache_append(kk, vv, kp, vp, table, ends, lens, **kw)
+    wide = torch.nn.functional.pad(table, (0, 200), value=-1)  # work may be cut and joined
+    qs = [torch.randn(6, 8, 128, generator=g).to(BF).cuda() for _ in range(2)]
+    want = [attention.flash_attn_paged_func(q, kp, vp, wide, cu, lens, **kw) for q in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i].append(attention.flash_attn_paged_func(qs[i], kp, vp, wide, cu, lens, **kw))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20 and all(torch.equal(o, want[i]) for o in got[i])
