@@ -95,6 +95,25 @@ __global__ void __launch_bounds__(kCacheThreads)
         if (!at.ok && (pos >= 0 || c1 < c0) && sub == 0) atomicExch(p.err, kDevErrBadIndex);
       }
     }
+    // the rows' largest magnitudes, two rows to a word
+    [[maybe_unused]] uint32_t tops[kUnroll / 2];
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int i = 0; i < kUnroll / 2; ++i) {
+        uint32_t half[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint4& x = v[2 * i + j];
+          half[j] = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                             __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+        }
+        tops[i] = __vmaxu2(__byte_perm(half[0], half[1], 0x5410),
+                           __byte_perm(half[0], half[1], 0x7632));
+#pragma unroll
+        for (int m = 1; m < kLanes; m <<= 1)
+          tops[i] = __vmaxu2(tops[i], __shfl_xor_sync(0xffffffffu, tops[i], m));
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * kStep;
@@ -104,12 +123,7 @@ __global__ void __launch_bounds__(kCacheThreads)
                                     h * p.c.head[w] + sub * 8) = v[u];
       } else {
         const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        uint32_t halves = __vmaxu2(__vmaxu2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu),
-                                   __vmaxu2(x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu));
-#pragma unroll
-        for (int m = 1; m < kLanes; m <<= 1)
-          halves = __vmaxu2(halves, __shfl_xor_sync(0xffffffffu, halves, m));
-        uint32_t top = max(halves & 0xffffu, halves >> 16);
+        uint32_t top = (tops[u >> 1] >> ((u & 1) * 16)) & 0xffffu;
         const bool zeros = top == 0;
         constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;
         if (top >= kInf) {  // the same for all lanes of the row
