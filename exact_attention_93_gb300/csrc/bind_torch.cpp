@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -106,7 +107,17 @@ PyObject* status(fa_status s) { return PyLong_FromLong(static_cast<long>(s)); }
 
 at::Tensor like(const at::Tensor& x) { return at::empty(x.sizes(), x.options().requires_grad(false)); }
 
+// Forward-mode differentiation gives a tensor a tangent whether or not it needs a
+// gradient; none of these calls makes one for its results.
+void no_tangent(const at::Tensor& t) {
+  TORCH_CHECK_NOT_IMPLEMENTED(
+      !t.defined() || !c10::AutogradState::get_tls_state().get_fw_grad_mode() ||
+          !t._fw_grad(/*level=*/0).defined(),
+      "forward-mode differentiation is not supported: the tangent would be lost");
+}
+
 void no_grad(const at::Tensor& t, const char* what) {
+  no_tangent(t);
   need(!(t.defined() && t.requires_grad() && c10::GradMode::is_enabled()), what);
 }
 
@@ -222,6 +233,7 @@ torch::autograd::variable_list RotaryFunction<kTensors>::backward(
     if (g.defined()) have.push_back(grad_operand(g));
   torch::autograd::variable_list out(kTensors + 1), got;
   if (have.empty()) return out;
+  for (const at::Tensor& g : have) no_tangent(g);
   if (c10::GradMode::is_enabled())
     got = have.size() == 1 ? RotaryFunction<1>::apply(have[0], r)
                            : RotaryFunction<2>::apply(have[0], have[1], r);
@@ -257,6 +269,7 @@ PyObject* rotary(PyObject* const* a) {
          "positions must have shape (seqlen,) or (batch, seqlen)");
   }
   need(!r.freq.requires_grad(), "inv_freq gets no gradient: detach it");
+  for (const at::Tensor* t : {&q, &k, static_cast<const at::Tensor*>(&r.freq)}) no_tangent(*t);
   const Device device({&q, &k, &r.freq, &r.pos});
   if (r.pos.defined() && N > 1 && r.pos.stride(-1) != 1) r.pos = r.pos.contiguous();
   const bool grad =
@@ -384,6 +397,8 @@ PyObject* read(PyObject* const* a) {
   const at::Tensor starts = maybe(a[5], "starts must be a tensor or None"),
                    ke = maybe(a[6], "k_exp must be a tensor or None"),
                    ve = maybe(a[7], "v_exp must be a tensor or None");
+  no_tangent(kp);
+  no_tangent(vp);
   const fa_kv_pages c = kv_pages(kp, vp, ke, ve);
   const fa_ragged r = ragged(table, cu, starts, total);
   const int asked = static_cast<int>(integer(a[8]));

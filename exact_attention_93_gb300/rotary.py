@@ -67,7 +67,8 @@ def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0
     when interleaved.  Rotated elements are multiplied by magnitude.
 
     Returns new tensors (q, k), or q alone when k is None.  Differentiable in q
-    and k (the gradient is the rotation back), any number of times.
+    and k (the gradient is the rotation back), any number of times; tensors with
+    a forward-mode tangent are refused.
     inplace=True writes over q and k instead and returns them; it is for
     inference, refuses tensors that need a gradient, and q and k must not
     overlap.  (A backward pass can be captured into a CUDA graph while no eager

@@ -1,0 +1,170 @@
+"""The serving calls at the ends of their ranges, on the GPU: gradients and
+tangents as autograd hands them over, rows marked as zeros, the smallest and
+most different row scales of an e4m3 cache, rows without keys, scales of zero
+and below, many query heads to a key head, infinities and NaN in visible places."""
+import math
+
+import pytest
+import torch
+
+import paged_ref as R
+from exact_attention_93_gb300 import attention, fattn, kvcache, rotary
+
+pytestmark = pytest.mark.gpu
+BF, HF, E4 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+def slot(b, s, j):
+    """Where key j of sequence s of a batch lives."""
+    return int(b.table[s, j // b.page]), j % b.page
+
+
+def refresh(b):
+    """The batch's 64-bit keys and values, read anew from an e4m3 cache's bytes."""
+    for w, to in ((0, b.k), (1, b.v)):
+        for s, n in enumerate(b.lens):
+            pages = b.table[s, :-(-n // b.page)].long()
+            e = b.exp[w][pages].permute(0, 2, 1).flatten(0, 1)[:n, :, None]
+            code = b.pool[w].view(torch.uint8)[pages].view(E4).float().double().flatten(0, 1)[:n]
+            to[s] = torch.where(e > 0, torch.ldexp(code, e.int() - 127), 0.0)
+
+
+def shift_exponents(b, w, s, by):
+    """Adds by (keys,) to the exponent bytes of the keys' (w = 0) or values' (w = 1) rows."""
+    for j in range(b.lens[s]):
+        pg, off = slot(b, s, j)
+        e = b.exp[w, pg, :, off].int()
+        b.exp[w, pg, :, off] = torch.where(e > 0, (e + int(by[j])).clamp(1, 248), 0).to(torch.uint8)
+
+
+def queries(b, H, seed=5, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(b.total, H, b.D, generator=g) * scale).to(b.dtype)
+
+
+def attend(b, q, *, scale=None, causal=True, window=(-1, -1), slopes=None, error=fattn.FA_OK):
+    k, v, table, cu, lens, kw = b.gpu()
+    o, lse = attention.flash_attn_paged_func(q.cuda(), k, v, table, cu, lens, softmax_scale=scale,
+                                             causal=causal, window_size=window, alibi_slopes=slopes,
+                                             return_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert fattn.fa_device_error() == error
+    return o.cpu(), lse.cpu()
+
+
+def reference(b, q, scale, causal=True, window=(-1, -1), without=None):
+    """o, lse in 64 bits, and how far each may be off; without: a (sequence, key, key
+    head) left out.
+
+    Scores are fp32 sums of D products, scaled: off by (D + 8) 2^-24 of S, the
+    largest sum of magnitudes, and the exponential by 2^-21; o takes that twice
+    (weights and their sum) times A = sum P |v|.  Weights in bf16 are off by 2^-8
+    of themselves; in fp16 by 2^-11, and below 2^-18 of the largest by 2^-29 of it
+    at most.  Joining, and the sums, 2^-20.  Over an e4m3 cache, R being a
+    sequence's largest exponent byte:
+      few rows: weight * 2^(e - R) below 2^-29 is off by 2^-40 at most, that is
+        by 448 * 2^(R - 127) * 2^-40 of a value;
+      many rows: keys and values below 2^(R - 22) are off by 2^-32 * 2^(R - 127),
+        those of 2^(R - 32) and below are zeros."""
+    H, G = q.shape[1], q.shape[1] // b.heads_k
+    few = b.total * G <= 16 * len(b.rows)
+    fp16 = b.fp8 or b.dtype == HF
+    os_, ls, tos, tls, at = [], [], [], [], 0
+    for s, n in enumerate(b.rows):
+        L = b.lens[s]
+        x = q[at:at + n].double()
+        at += n
+        k, v = b.k[s].repeat_interleave(G, 1), b.v[s].repeat_interleave(G, 1)
+        left_out = torch.zeros(H, 1, L, dtype=torch.bool)
+        if without and without[0] == s:
+            left_out[without[2] * G:(without[2] + 1) * G, :, without[1]] = True
+            k = k.masked_fill(left_out[:, 0].t()[..., None], 0.0)
+        d = torch.arange(L)[None, :] - (L - n + torch.arange(n))[:, None]
+        seen = torch.ones_like(d, dtype=torch.bool)
+        if causal:
+            seen &= d <= 0
+        if window[0] >= 0:
+            seen &= d >= -window[0]
+        if window[1] >= 0:
+            seen &= d <= window[1]
+        z = (torch.einsum("ihd,jhd->hij", x, k) * scale).masked_fill(~seen | left_out, -math.inf)
+        lse = torch.logsumexp(z, -1) if L else torch.full((H, n), -math.inf, dtype=torch.float64)
+        p = torch.exp(z - torch.where(lse == -math.inf, 0.0, lse)[..., None])
+        o = torch.einsum("hij,jhd->ihd", p, v)
+        ev, ek = torch.zeros_like(v), torch.zeros_like(k)  # errors of the operands
+        flat = 0.0                                         # of each value that is seen
+        if b.fp8 and L:
+            e = [torch.stack([b.exp[w, slot(b, s, j)[0], :, slot(b, s, j)[1]] for j in range(L)])
+                 .int().repeat_interleave(G, 1)[..., None] for w in (0, 1)]
+            top = [int(t.max()) for t in e]
+            if few:
+                flat = 448 * 2.0 ** (top[1] - 127 - 40)
+            else:
+                for t, err, val, R_ in zip(e, (ek, ev), (k, v), top):
+                    low = torch.where(t <= R_ - 22, 2.0 ** (R_ - 127 - 32), 0.0)
+                    err += torch.where(t <= R_ - 32, val.abs(), low)
+        mag = torch.einsum("ihd,jhd->hij", x.abs(), k.abs()) * abs(scale)
+        off = torch.einsum("ihd,jhd->hij", x.abs(), ek) * abs(scale)
+        S, dk = (t.masked_fill(~seen, 0.0).amax(-1) if L else torch.zeros(H, n).double()
+                 for t in (mag, off))
+        ds = (b.D + 8) * 2.0 ** -24 * S + 2.0 ** -21 + dk
+        A = torch.einsum("hij,jhd->ihd", p, v.abs())
+        some = torch.einsum("hij,jhd->ihd", seen.double().expand_as(p), v.abs())
+        count = seen.sum(-1).double()[:, None, None]
+        u, p_eps = R.EPS[b.dtype], 2.0 ** -11 if fp16 else 2.0 ** -8
+        tos.append(1.01 * u * o.abs() + (1.01 * p_eps + 2 * ds.t()[..., None] + 2.0 ** -20) * A
+                   + (2.0 ** -29 if fp16 else 0.0) * some + count * flat
+                   + torch.einsum("hij,jhd->ihd", p, ev)
+                   + (2.0 ** -133 if b.dtype == BF else 2.0 ** -24))
+        tls.append(ds + 2.0 ** -20 + 2.0 ** -22 * torch.where(torch.isfinite(lse), lse.abs(), 0.0))
+        os_.append(o)
+        ls.append(lse)
+    return torch.cat(os_), torch.cat(ls, 1), torch.cat(tos), torch.cat(tls, 1)
+
+
+def compare(b, q, o, lse, scale=None, **kw):
+    ro, rl, to, tl = reference(b, q[:sum(b.rows)], b.D ** -0.5 if scale is None else scale, **kw)
+    n = sum(b.rows)
+    o, lse = o[:n].double(), lse[:, :n].double()
+    assert torch.equal(lse == -math.inf, rl == -math.inf)
+    fin = torch.isfinite(rl)
+    assert ((lse - rl).abs()[fin] <= tl[fin]).all(), (lse - rl).abs()[fin].max()
+    bad = ~((o - ro).abs() <= to)
+    assert not bad.any(), (bad.nonzero()[:5], ((o - ro).abs() / to).nan_to_num(9e9).max())
+
+
+# ---- tangents and gradients
+
+def test_forward_mode_is_refused():
+    """A tangent is never dropped: each call that has none to give refuses its input."""
+    freq, _ = rotary.rotary_frequencies(64)
+    x, t = torch.randn(2, 3, 9, 2, 64, device="cuda").to(BF)
+    b = R.Batch([3, 2], [5, 0], 2, 64, 16, BF, False)
+    k, v, table, cu, lens, _ = b.gpu()
+    q = queries(b, 4).cuda()
+    new = torch.randn(5, 2, 64, device="cuda").to(BF)
+    keep = k.clone()
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual
+        for grad in (torch.enable_grad(), torch.no_grad()):
+            with grad:
+                for call in (
+                        lambda: rotary.rotary_func(dual(x, t), None, freq),
+                        lambda: rotary.rotary_func(x, dual(x, t), freq),
+                        lambda: rotary.rotary_func(dual(x, t), None, freq, inplace=True),
+                        lambda: rotary.rotary_func(x, None, dual(freq, freq)),
+                        lambda: attention.flash_attn_paged_func(dual(q, q), k, v, table, cu, lens),
+                        lambda: attention.flash_attn_paged_func(q, dual(k, k), v, table, cu, lens),
+                        lambda: kvcache.kv_cache_append(dual(new, new), new, k, v, table, cu, lens),
+                        lambda: kvcache.kv_cache_append(new, new, k, dual(v, v), table, cu, lens),
+                        lambda: kvcache.kv_cache_read(dual(k, k), v, table, cu, 5)):
+                    with pytest.raises(NotImplementedError):
+                        call()
+    assert torch.equal(k.view(torch.int16), keep.view(torch.int16))
+    rotary.rotary_func(x, x, freq)  # and without tangents it runs
+    # a gradient that carries a tangent
+    y = rotary.rotary_func(x.requires_grad_(), None, freq)
+    with torch.autograd.forward_ad.dual_level():
+        for create in (False, True):
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(y, (x,), (dual(t, t),), create_graph=create, retain_graph=True)
