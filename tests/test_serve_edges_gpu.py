@@ -168,3 +168,26 @@ def test_forward_mode_is_refused():
         for create in (False, True):
             with pytest.raises(NotImplementedError):
                 torch.autograd.grad(y, (x,), (dual(t, t),), create_graph=create, retain_graph=True)
+
+
+# ---- rows marked as zeros
+
+@pytest.mark.parametrize("D,H,Hk,dtype", [(128, 8, 2, BF), (64, 6, 6, HF), (64, 16, 2, BF)])
+@pytest.mark.parametrize("rows,spare", [([1, 1, 1], 2), ([1, 2, 2], 200), ([40, 3, 140], 2),
+                                        ([40, 3, 140], 200)])
+def test_rows_marked_as_zeros(D, H, Hk, dtype, rows, spare):
+    """e = 0 makes a row of zeros, whatever codes lie under it."""
+    b = R.Batch(rows, [300, 20, 1000], Hk, D, 16, dtype, True, seed=D + H, spare_cols=spare)
+    g = torch.Generator().manual_seed(1)
+    for w in range(2):
+        for s, n in enumerate(b.lens):
+            for j in range(n):
+                pg, off = slot(b, s, j)
+                none = torch.rand(Hk, generator=g) < (1.0 if s == 1 else 0.2)
+                b.exp[w, pg, none, off] = 0
+                b.pool[w].view(torch.uint8)[pg, off, none] = 0x7f  # NaN
+    refresh(b)
+    q = queries(b, H)
+    o, lse = attend(b, q)
+    compare(b, q, o, lse)
+    assert (o[rows[0]:rows[0] + rows[1]] == 0).all()
