@@ -77,7 +77,7 @@ struct FewSmem {
   // joining the warps' results: eight query rows of one group's warps at a time
   alignas(16) float merge[kGroupWarps][8][kMergePitch];
   float m[kConsumers][8 * NB], l[kConsumers][8 * NB];
-  float vscale[kConsumers];
+  int vref[kConsumers];
   uint64_t full[kSlots], empty[kSlots];
   Place place;
   int abort_flag;
@@ -348,7 +348,7 @@ __global__ void __maxnreg__(kFewRegs)
       const int all_hi = p.win_right < 0 ? seq.len : min(seq.len, seq.pos0 + x.t0 + p.win_right + 1);
 
       float m[NB][2], l[NB][2], o[kSteps][NB][4];
-      int vref = 0;  // R: the largest value exponent so far
+      int vref = 16;  // R: the largest value exponent so far, or 16: 2^(R - 142) stays normal
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         m[nb][0] = m[nb][1] = -INFINITY;
@@ -462,9 +462,11 @@ __global__ void __maxnreg__(kFewRegs)
           for (int sl = 0; sl < kSlices; ++sl)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float z = acc[sl][nb][i] * qscale[nb][i & 1];
-              if constexpr (kFp8) z *= kfac[sl][i >> 1];
-              acc[sl][nb][i] = z;
+              // (the powers of two first: beside small keys a query may be so large
+              // that its product alone leaves the range)
+              const float f =
+                  kFp8 ? qscale[nb][i & 1] * kfac[sl][i >> 1] : qscale[nb][i & 1];
+              acc[sl][nb][i] *= f;
             }
           if (p.alibi || masked) {
 #pragma unroll
@@ -655,12 +657,13 @@ __global__ void __maxnreg__(kFewRegs)
             s.l[warp][nb * 8 + 2 * t + c] = sum;
           }
         }
-      if (lane == 0) s.vscale[warp] = kFp8 ? exp2_field(vref - 15) : 1.f;
+      if (lane == 0) s.vref[warp] = vref;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int r = nb * 8 + warp;
         constexpr int kN = D / 32;
         float top = -INFINITY, sum = 0.f, out[kN] = {};
+        [[maybe_unused]] int vtop = 0;
 #pragma unroll
         for (int gr = 0; gr < kGroups; ++gr) {
           if (group == gr)
@@ -680,14 +683,17 @@ __global__ void __maxnreg__(kFewRegs)
           named_bar_sync(1, kConsumers * 32);
           if (gr == 0)
 #pragma unroll
-            for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, s.m[w][r]);
+            for (int w = 0; w < kConsumers; ++w) {
+              top = fmaxf(top, s.m[w][r]);
+              if constexpr (kFp8) vtop = max(vtop, s.vref[w]);
+            }
           const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
           for (int w = 0; w < kGroupWarps; ++w) {
             const int from = gr * kGroupWarps + w;
             const float a = ex2_approx(s.m[from][r] - ref);
             sum = fmaf(s.l[from][r], a, sum);
-            const float av = kFp8 ? a * s.vscale[from] : a;
+            const float av = kFp8 ? a * exp2_field(127 + s.vref[from] - vtop) : a;
             const float* src = s.merge[w][warp];
 #pragma unroll
             for (int e = 0; e < kN; e += 2) {  // columns lane * kN + e and the next
@@ -700,6 +706,11 @@ __global__ void __maxnreg__(kFewRegs)
             }
           }
           named_bar_sync(1, kConsumers * 32);
+        }
+        if constexpr (kFp8) {
+          const float back = exp2_field(vtop - 15);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) out[e] *= back;
         }
         if (r < x.rows) {
           if (x.whole) {

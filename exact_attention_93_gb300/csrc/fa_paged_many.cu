@@ -540,7 +540,10 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           // see every tile land and arrive for it, so that V's barrier covers
           // what the others have written for its key tile too.
           const int my_kv = (warp - ManyWarps<kFp8>::kFirst) >> 1;
-          uint32_t ref = 0;  // largest exponent of the piece's keys, or values, so far
+          // Largest exponent of the piece's keys, or values, so far, or 12: 2^(ref - 11
+          // - 127), by which the results are scaled back, stays a normal number.  (Rows
+          // of exponent 1 lose nothing under it.)
+          uint32_t ref = 12;
           for (int j = u.first; ok && j <= u.last; ++j, ++ring) {
             const bool cut = u.ragged(j);
 #pragma unroll 1
@@ -853,7 +856,10 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
       if (t == 0 || u.two(tile_tokens)) {
         // O in tensor memory is 2^kPOffset (e4m3: and 2^(127 + 7 - vbase)) times
         // the sum of weights times values
-        const float back = many_exp2_field((kFp8 ? vbase - 7 : 127) - kPOffset);
+        // (of small values in two steps, as the first divides by a sum of many weights)
+        const bool small = kFp8 && vbase < 64;
+        const float back =
+            many_exp2_field((kFp8 ? vbase - 7 + (small ? 64 : 0) : 127) - kPOffset);
         const float per = lo == 0.f ? 0.f : back / lo;
         const bool whole = u.slot < 0;
         // partial results are divided by their sum as rounded and multiplied by
@@ -898,6 +904,11 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+          if (small) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * many_exp2_field(127 - 64));
+          }
           // 16-bit: half a piece, fp32: a whole one
           const int half = whole ? (c & 1) * 4 : 0, n = whole ? 4 : 8;
           if (whole) {

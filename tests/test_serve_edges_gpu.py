@@ -191,3 +191,36 @@ def test_rows_marked_as_zeros(D, H, Hk, dtype, rows, spare):
     o, lse = attend(b, q)
     compare(b, q, o, lse)
     assert (o[rows[0]:rows[0] + rows[1]] == 0).all()
+
+
+# ---- the smallest row scales
+
+@pytest.mark.parametrize("top", [1, 9, 15, 30])
+@pytest.mark.parametrize("D,H,Hk", [(128, 8, 2), (64, 6, 6)])
+@pytest.mark.parametrize("rows,spare", [([1, 1, 1], 2), ([1, 2, 2], 200), ([40, 3, 140], 2),
+                                        ([40, 3, 140], 200)])
+def test_smallest_value_scales(top, D, H, Hk, rows, spare):
+    """Values near 2^-117 and up come out as such, not as zeros."""
+    b = R.Batch(rows, [300, 20, 1000], Hk, D, 32, BF, True, seed=D, spare_cols=spare)
+    for s, n in enumerate(b.lens):
+        most = max(int(b.exp[1, slot(b, s, j)[0], :, slot(b, s, j)[1]].max()) for j in range(n))
+        shift_exponents(b, 1, s, [top - most] * n)
+    refresh(b)
+    q = queries(b, H)
+    o, lse = attend(b, q)
+    compare(b, q, o, lse)
+    assert (o != 0).any()
+
+
+@pytest.mark.parametrize("top", [4, 20])
+@pytest.mark.parametrize("rows,spare", [([1, 2, 2], 2), ([40, 3, 140], 200)])
+@pytest.mark.parametrize("D,H,Hk", [(128, 8, 2), (64, 6, 6)])
+def test_smallest_key_scales_under_the_largest_queries(top, D, H, Hk, rows, spare):
+    b = R.Batch(rows, [300, 20, 1000], Hk, D, 32, BF, True, seed=D, spare_cols=spare)
+    for s, n in enumerate(b.lens):
+        most = max(int(b.exp[0, slot(b, s, j)[0], :, slot(b, s, j)[1]].max()) for j in range(n))
+        shift_exponents(b, 0, s, [top - most] * n)
+    refresh(b)
+    q = queries(b, H, scale=2.0 ** (119 - top))  # scores of a few units
+    o, lse = attend(b, q)
+    compare(b, q, o, lse)
