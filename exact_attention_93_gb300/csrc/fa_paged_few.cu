@@ -717,6 +717,10 @@ __global__ void __maxnreg__(kFewRegs)
             int token, head;
             row_of(p, row0, r, x.hk, token, head);
             const long long row = seq.start + token;
+            if (sum == 0.f) {  // no key: zeros, also where other rows saw a NaN value
+#pragma unroll
+              for (int e = 0; e < kN; ++e) out[e] = 0.f;
+            }
             store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head +
                                lane * kN,
                            out, sum == 0.f ? 0.f : 1.f / sum);

@@ -904,6 +904,10 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+          if (lo == 0.f) {  // no key: zeros, also where other rows saw a NaN value
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
           if (small) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)

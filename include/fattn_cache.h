@@ -169,7 +169,8 @@ fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads
  * Keys and values beyond a sequence's length, and pages that no visible key
  * lies in, are not looked at, whatever they hold.  Inside the span of keys that
  * some query of a row block sees, a NaN or infinity in a value reaches every
- * query of that block (its weight 0 times NaN is NaN), as in the dense product.
+ * query of that block that sees any key (its weight 0 times NaN is NaN), as in
+ * the dense product.
  * Deterministic: the same inputs give bit-identical outputs.
  *
  * Under an e4m3 cache the products run on fp16 numbers under powers of two: a

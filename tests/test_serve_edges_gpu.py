@@ -224,3 +224,22 @@ def test_smallest_key_scales_under_the_largest_queries(top, D, H, Hk, rows, spar
     q = queries(b, H, scale=2.0 ** (119 - top))  # scores of a few units
     o, lse = attend(b, q)
     compare(b, q, o, lse)
+
+
+# ---- rows without keys
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,rows,spare", [(64, [3, 1], 2), (128, [2, 1], 200), (64, [90, 40], 2),
+                                          (128, [90, 40], 200)])
+def test_rows_without_keys_beside_values_that_are_not_finite(fp8, D, rows, spare):
+    """A row that sees no key gets zeros, also where rows of its block see a NaN."""
+    b = R.Batch(rows, [-1, 40], 2, D, 16, BF, fp8, spare_cols=spare)
+    pg, off = slot(b, 0, 0)
+    if fp8:
+        b.pool[1].view(torch.uint8)[pg, off] = 0x7f
+    else:
+        b.pool[1, pg, off] = math.nan
+    o, lse = attend(b, queries(b, 4))
+    assert (o[0] == 0).all() and (lse[:, 0] == -math.inf).all()
+    assert torch.isnan(o[1:rows[0]]).all() and torch.isfinite(lse[:, 1:]).all()
+    assert torch.isfinite(o[rows[0]:]).all()
