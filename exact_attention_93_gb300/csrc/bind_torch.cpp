@@ -177,12 +177,13 @@ void check(fa_status st) {
 }
 
 // The incoming gradient as the kernels need it: D contiguous, 16-byte aligned
-// rows.  Anything else is copied once.
+// rows.  Anything else is copied once (a contiguous one too, where it begins at an
+// odd address: contiguous() would return it as it is).
 at::Tensor grad_operand(const at::Tensor& g) {
   if (!g.defined()) return g;
   bool ok = g.stride(-1) == 1 && reinterpret_cast<uintptr_t>(g.const_data_ptr()) % 16 == 0;
   for (int64_t i = 0; i + 1 < g.dim(); ++i) ok = ok && g.stride(i) % 8 == 0;
-  return ok ? g : g.contiguous();
+  return ok ? g : g.clone(at::MemoryFormat::Contiguous);
 }
 
 // A rotation's gradient is the rotation back, with the same magnitude; it is

@@ -243,3 +243,29 @@ def test_rows_without_keys_beside_values_that_are_not_finite(fp8, D, rows, spare
     assert (o[0] == 0).all() and (lse[:, 0] == -math.inf).all()
     assert torch.isnan(o[1:rows[0]]).all() and torch.isfinite(lse[:, 1:]).all()
     assert torch.isfinite(o[rows[0]:]).all()
+
+
+# ---- gradients at addresses that are no multiple of 16
+
+def misaligned(shape, dtype):
+    n = math.prod(shape)
+    t = torch.randn(n + 1, device="cuda").to(dtype)[1:].view(shape)
+    assert t.is_contiguous() and t.data_ptr() % 16
+    return t
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_misaligned_gradient_of_rotary(dtype):
+    freq, _ = rotary.rotary_frequencies(64)
+    x, z = (torch.randn(2, 9, h, 64, device="cuda").to(dtype).requires_grad_() for h in (3, 1))
+    y, u = rotary.rotary_func(x, z, freq)
+    dy, du = misaligned(y.shape, dtype), misaligned(u.shape, dtype)
+    want = torch.autograd.grad((y, u), (x, z), (dy.clone(), du.clone()), retain_graph=True)
+    got = torch.autograd.grad((y, u), (x, z), (dy, du), retain_graph=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # as a join behind an odd offset leaves it
+    one = torch.ones(1, device="cuda", dtype=dtype)
+    w = torch.randn(1 + y.numel(), device="cuda").to(dtype)
+    gx, = torch.autograd.grad((torch.cat((one, y.flatten())) * w).sum(), (x,), retain_graph=True)
+    wx, = torch.autograd.grad(y, (x,), (w[1:].clone().view_as(y),))
+    assert torch.equal(gx, wx)
