@@ -59,9 +59,10 @@ def _bnhd(t) -> fattn.FaStrides:
 
 def _grad_operand(g):
     """The incoming gradient as the kernels need it: D contiguous, 16-byte
-    aligned rows.  Anything else is copied once (argument marshalling)."""
+    aligned rows.  Anything else is copied once (argument marshalling), a
+    contiguous one at an odd address too, which contiguous() returns as it is."""
     if g.stride(-1) != 1 or any(s % 8 for s in g.stride()[:-1]) or g.data_ptr() % 16:
-        g = g.contiguous()
+        g = g.clone(memory_format=torch.contiguous_format)
     return g
 
 

@@ -269,3 +269,13 @@ def test_misaligned_gradient_of_rotary(dtype):
     gx, = torch.autograd.grad((torch.cat((one, y.flatten())) * w).sum(), (x,), retain_graph=True)
     wx, = torch.autograd.grad(y, (x,), (w[1:].clone().view_as(y),))
     assert torch.equal(gx, wx)
+
+
+def test_misaligned_gradient_of_dense_attention():
+    q, k, v = (torch.randn(1, 200, 2, 64, device="cuda").to(BF).requires_grad_() for _ in range(3))
+    o = attention.flash_attn_func(q, k, v, causal=True, deterministic=True)
+    do = misaligned(o.shape, BF)
+    want = torch.autograd.grad(o, (q, k, v), (do.clone(),), retain_graph=True)
+    got = torch.autograd.grad(o, (q, k, v), (do,))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
