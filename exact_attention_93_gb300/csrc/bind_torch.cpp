@@ -160,7 +160,7 @@ fa_status turn(const at::Tensor& x, const at::Tensor& y, const at::Tensor& x2,
   const fa_rotary_operand a = rotary_operand(x, y);
   fa_rotary_operand b;
   if (x2.defined()) b = rotary_operand(x2, y2);
-  const bool pos = r.pos.defined();
+  const bool pos = r.pos.defined() && r.pos.numel() > 0;  // (no tokens: no address either)
   return fa_rotary(&a, x2.defined() ? &b : nullptr, static_cast<int>(B), static_cast<int>(N),
                    static_cast<int>(x.size(dim - 1)), static_cast<int>(2 * r.freq.size(0)),
                    r.freq.const_data_ptr<double>(), pos ? r.pos.const_data_ptr() : nullptr,

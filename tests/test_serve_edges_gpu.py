@@ -279,3 +279,20 @@ def test_misaligned_gradient_of_dense_attention():
     got = torch.autograd.grad(o, (q, k, v), (do,))
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ---- no tokens
+
+@pytest.mark.parametrize("shape,pos", [((2, 0, 4, 64), (0,)), ((2, 0, 4, 64), (2, 0)),
+                                       ((0, 5, 4, 64), (0, 5)), ((0, 4, 64), (0,))])
+@pytest.mark.parametrize("bits", [torch.int32, torch.int64])
+def test_rotary_of_no_tokens_with_positions(shape, pos, bits):
+    freq, _ = rotary.rotary_frequencies(64)
+    x = torch.zeros(shape, device="cuda", requires_grad=True)
+    p = torch.zeros(pos, dtype=bits, device="cuda")
+    y = rotary.rotary_func(x, None, freq, positions=p)
+    assert y.shape == x.shape
+    gx, = torch.autograd.grad(y.sum(), (x,))
+    assert gx.shape == x.shape
+    with torch.no_grad():
+        assert rotary.rotary_func(x, x, freq, positions=p)[1].shape == x.shape
