@@ -1,5 +1,6 @@
-"""Builds libfattn.so in-tree with nvcc for sm_103a, and the small native module
-through which torch tensors reach part of it (g++, against the installed torch).
+"""Builds libfattn.so in-tree with nvcc for sm_103a, and, where torch is installed,
+the small native module through which its tensors reach part of the library (g++,
+against that torch).  The library alone needs no torch.
 
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library next to this file.  The CUDA runtime is linked statically and
@@ -10,6 +11,7 @@ there; nothing can run).
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -44,47 +46,67 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+    """Whether libfattn.so is there and newer than its sources."""
+    if not os.path.exists(LIB):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    t = os.path.getmtime(LIB)
+    return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def have_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
+def bind_up_to_date() -> bool:
+    """The same for the native module."""
+    if not os.path.exists(BIND):
+        return False
+    t = os.path.getmtime(BIND)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile (if needed) and return the path of libfattn.so."""
-    if not force and up_to_date():
+    """Compiles (if needed) the library and the native module, which is left out where
+    there is no torch, and returns the path of libfattn.so."""
+    want_lib = force or not up_to_date()
+    want_bind = have_torch() and (force or not bind_up_to_date())
+    if not want_lib and not want_bind:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    cc = nvcc()
-
-    def compile_one(src):
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [cc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            sys.stderr.write(r.stdout + r.stderr)
-        return obj
-
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bind = ex.submit(compile_bind)
-        objs = list(ex.map(compile_one, SOURCES))
-        bind_obj, torch_lib = bind.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
+        bind = ex.submit(compile_bind) if want_bind else None
+        if want_lib:
+            link_library(list(ex.map(lambda src: compile_one(src, verbose, extra), SOURCES)))
+        if want_bind:
+            link_bind(*bind.result())
+    return LIB
+
+
+def compile_one(src, verbose, extra):
+    obj = os.path.join(BUILD, src.replace(".cu", ".o"))
+    cmd = [nvcc(), *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        sys.stderr.write(r.stdout + r.stderr)
+    return obj
+
+
+def link_library(objs):
+    tmp = LIB + f".tmp{os.getpid()}"
+    run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], "link failed")
     os.replace(tmp, LIB)
+
+
+def link_bind(obj, torch_lib):
     # the module finds libfattn.so beside itself, and torch's libraries in the
     # process that imports it
     tmp = BIND + f".tmp{os.getpid()}"
-    run(["g++", "-shared", "-o", tmp, bind_obj, "-L" + HERE, "-l:libfattn.so", "-L" + torch_lib,
+    run(["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:libfattn.so", "-L" + torch_lib,
          "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"],
         "link failed")
     os.replace(tmp, BIND)
-    return LIB
 
 
 def run(cmd, what):

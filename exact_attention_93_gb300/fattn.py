@@ -457,7 +457,7 @@ _bind = None
 
 
 def bind():
-    """The native module of csrc/bind_torch.cpp (built with the library)."""
+    """The native module of csrc/bind_torch.cpp (built with the library, or now)."""
     global _bind
     if _bind is None:
         load()
@@ -465,6 +465,8 @@ def bind():
         import importlib.util
         from . import build as _build
         _torch()  # the module's symbols come from torch's libraries
+        if not _build.bind_up_to_date():
+            _build.build()
         loader = importlib.machinery.ExtensionFileLoader("_bind_torch", _build.BIND)
         spec = importlib.util.spec_from_file_location("_bind_torch", _build.BIND, loader=loader)
         module = importlib.util.module_from_spec(spec)

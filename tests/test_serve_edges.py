@@ -1,9 +1,15 @@
 """What the serving calls refuse on the host, beyond shapes and types, and how
 their native module is built.  No kernel runs here."""
+import os
+import shutil
+import stat
+import subprocess
+import sys
+
 import pytest
 import torch
 
-from exact_attention_93_gb300 import attention, kvcache, rotary
+from exact_attention_93_gb300 import attention, build, kvcache, rotary
 
 
 def small():
@@ -29,3 +35,55 @@ def test_tangents_are_refused():
                              lambda: attention.flash_attn_paged_func(d(q), kp, vp, table, cu, lens)):
                     with pytest.raises(NotImplementedError):
                         call()
+
+
+# ---- building, with compilers that only write down what they are asked for
+
+@pytest.fixture
+def tree(tmp_path):
+    """A copy of the sources beside an nvcc and a g++ that make empty files."""
+    package = tmp_path / "exact_attention_93_gb300"
+    package.mkdir()
+    for f in ("__init__.py", "build.py"):
+        shutil.copy(os.path.join(build.HERE, f), package)
+    shutil.copytree(build.CSRC, package / "csrc")
+    shutil.copytree(build.INCLUDE, tmp_path / "include")
+    (tmp_path / "bin").mkdir()
+    for name in ("nvcc", "g++"):
+        tool = tmp_path / "bin" / name
+        tool.write_text(f"""#!/bin/sh
+echo {name} "$@" >> {tmp_path}/calls
+[ -e {tmp_path}/no-{name} ] && exit 1
+while [ $# -gt 0 ]; do [ "$1" = -o ] && : > "$2"; shift; done
+exit 0
+""")
+        tool.chmod(tool.stat().st_mode | stat.S_IEXEC)
+    return tmp_path
+
+
+def run_in(tree, code):
+    env = {**os.environ, "PATH": f"{tree}/bin:{os.environ['PATH']}", "PYTHONPATH": str(tree)}
+    r = subprocess.run([sys.executable, "-c", code], cwd=tree, env=env, capture_output=True, text=True)
+    calls = tree / "calls"
+    lines = calls.read_text().splitlines() if calls.exists() else []
+    calls.unlink(missing_ok=True)
+    return r, [x.split()[0] for x in lines]
+
+
+def test_the_library_is_built_without_torch(tree):
+    code = "import sys; sys.modules['torch'] = None; from exact_attention_93_gb300 import build as b; b.build()"
+    r, calls = run_in(tree, code)
+    assert r.returncode == 0, r.stderr
+    assert (tree / "exact_attention_93_gb300/libfattn.so").exists() and set(calls) == {"nvcc"}
+    assert run_in(tree, code)[1] == []  # and is then up to date
+    r, calls = run_in(tree, "from exact_attention_93_gb300 import build as b; b.build()")
+    assert r.returncode == 0, r.stderr  # with torch the native module follows alone
+    assert (tree / "exact_attention_93_gb300/_bind_torch.so").exists() and set(calls) == {"g++"}
+
+
+def test_the_library_is_built_where_the_native_module_is_not(tree):
+    (tree / "no-g++").touch()
+    r, _ = run_in(tree, "from exact_attention_93_gb300 import build as b; b.build()")
+    assert r.returncode != 0 and "g++ failed" in r.stderr
+    assert (tree / "exact_attention_93_gb300/libfattn.so").exists()
+    assert not (tree / "exact_attention_93_gb300/_bind_torch.so").exists()
