@@ -16,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -24,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfattn.so")
 BIND = os.path.join(HERE, "_bind_torch.so")
+BIND_STAMP = os.path.join(BUILD, "bind_torch.stamp")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve_api.cu",
            "fa_rotary.cu", "fa_cache.cu", "fa_paged_few.cu", "fa_paged_many.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -57,8 +59,28 @@ def have_torch() -> bool:
     return importlib.util.find_spec("torch") is not None
 
 
+def torch_version() -> str:
+    """The installed torch's own account of its build (version, CUDA, commit), read
+    without importing it."""
+    root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    with open(os.path.join(root, "version.py")) as f:
+        return f"{root}\n{f.read()}"
+
+
+def bind_stamp() -> str:
+    """What the native module is bound to beside its sources."""
+    return f"{sysconfig.get_config_var('SOABI')}\n{torch_version()}"
+
+
 def bind_up_to_date() -> bool:
-    """The same for the native module."""
+    """The same for the native module, and whether torch and Python are those it was
+    built with."""
+    try:
+        with open(BIND_STAMP) as f:
+            if f.read() != bind_stamp():
+                return False
+    except OSError:
+        return False
     if not os.path.exists(BIND):
         return False
     t = os.path.getmtime(BIND)
@@ -107,6 +129,8 @@ def link_bind(obj, torch_lib):
          "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"],
         "link failed")
     os.replace(tmp, BIND)
+    with open(BIND_STAMP, "w") as f:
+        f.write(bind_stamp())
 
 
 def run(cmd, what):
@@ -117,8 +141,6 @@ def run(cmd, what):
 
 def compile_bind():
     """The object file of bind_torch.cpp, and where torch's libraries are."""
-    import sysconfig
-
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))

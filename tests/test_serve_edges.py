@@ -87,3 +87,15 @@ def test_the_library_is_built_where_the_native_module_is_not(tree):
     assert r.returncode != 0 and "g++ failed" in r.stderr
     assert (tree / "exact_attention_93_gb300/libfattn.so").exists()
     assert not (tree / "exact_attention_93_gb300/_bind_torch.so").exists()
+
+
+def test_the_native_module_follows_torch_and_python(tree):
+    get, code = "from exact_attention_93_gb300 import build as b; ", "b.build()"
+    assert set(run_in(tree, get + code)[1]) == {"nvcc", "g++"}
+    assert run_in(tree, get + code)[1] == []
+    other = get + "b.torch_version = lambda: '0.0'; "
+    assert set(run_in(tree, other + code)[1]) == {"g++"}
+    assert run_in(tree, other + code)[1] == []
+    assert set(run_in(tree, get + code)[1]) == {"g++"}  # and back
+    other = get + "import sysconfig as s; s.get_config_var = lambda n: 'cpython-399'; "
+    assert set(run_in(tree, other + code)[1]) == {"g++"}
