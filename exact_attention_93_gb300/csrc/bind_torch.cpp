@@ -398,8 +398,8 @@ PyObject* read(PyObject* const* a) {
   const at::Tensor starts = maybe(a[5], "starts must be a tensor or None"),
                    ke = maybe(a[6], "k_exp must be a tensor or None"),
                    ve = maybe(a[7], "v_exp must be a tensor or None");
-  no_tangent(kp);
-  no_tangent(vp);
+  for (const at::Tensor* t : {&kp, &vp})
+    no_grad(*t, "the cache keeps no gradients: call under torch.no_grad()");
   const fa_kv_pages c = kv_pages(kp, vp, ke, ve);
   const fa_ragged r = ragged(table, cu, starts, total);
   const int asked = static_cast<int>(integer(a[8]));

@@ -37,6 +37,15 @@ def test_tangents_are_refused():
                         call()
 
 
+def test_reading_a_cache_that_needs_gradients_is_refused():
+    _, _, kp, vp, (table, cu, _) = small()
+    for pages in ((kp.clone().requires_grad_(), vp), (kp, vp.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="no gradients"):  # they would be lost
+            kvcache.kv_cache_read(*pages, table, cu, 3)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # allowed, but for the device
+            kvcache.kv_cache_read(*pages, table, cu, 3)
+
+
 # ---- building, with compilers that only write down what they are asked for
 
 @pytest.fixture
