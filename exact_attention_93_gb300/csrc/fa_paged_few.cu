@@ -23,15 +23,20 @@
 // side is to 8 rows, and the operands go from shared memory to registers to the
 // tensor core without a detour through tensor memory, which a tile of 8 columns
 // would not fill.  P^T moves from the accumulator to the operand layout by an
-// in-register 8 x 8 transpose.
+// in-register 8 x 8 transpose.  The tensor cores take P in 16 bits, so weights are
+// rounded (by 2^-8 of themselves at most in bf16, 2^-11 in fp16), each on its own;
+// O is divided by the sum of the unrounded ones.
 //
 // e4m3 caches.  Codes convert exactly to fp16 in registers, so an 8-bit cache
 // costs half the HBM bytes and no precision beyond its own: q is scaled by a
 // power of two per row to fit fp16, key exponents scale the scores in fp32,
 // and value exponents go into P relative to the largest one seen so far, R:
-// P' = 2^(s - m) * 2^(e_v - R + 15), at most 2^15.  The order of the head
-// columns (keys) and of columns and keys (values) inside an operand is chosen
-// so that a lane reads 16 contiguous bytes.
+// P' = 2^(s - m) * 2^(e_v - R + 15), at most 2^15.  Weights and exponents share
+// fp16's range that way: P' is normal down to a product of 2^-29.  (Scaling V
+// instead would leave the range to each, at a multiply for every value; with the
+// rows' magnitudes within some 2^10 of one another, weights keep their 11 bits down
+// to 2^-19.)  The order of the head columns (keys) and of columns and keys (values)
+// inside an operand is chosen so that a lane reads 16 contiguous bytes.
 //
 // Measured (32 query and 8 key heads): 64 contexts of 256 to 16000 keys, D = 128,
 // 16-bit 188 us, 6.6 TB/s of keys and values, 97 % of the measured copy rate;

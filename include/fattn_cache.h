@@ -173,10 +173,22 @@ fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads
  * the dense product.
  * Deterministic: the same inputs give bit-identical outputs.
  *
- * Under an e4m3 cache the products run on fp16 numbers under powers of two: a
- * row of q under its own, keys and values relative to the largest row exponent
- * among those that a row block walks.  Rows up to 2^22 below that lose nothing;
- * what is 2^40 below counts as zeros.
+ * Weights are rounded to q's type before they multiply the values (fp16 ones keep
+ * 11 bits down to 2^-20 of the largest), over an e4m3 cache to fp16; all sums are
+ * fp32.
+ *
+ * Under an e4m3 cache the products run on fp16 numbers under powers of two, a row
+ * of q under its own.  What that costs goes by the kernel that a sequence takes.
+ * With e a row's exponent byte and R the largest among those (of keys, of values)
+ * that a row block has walked:
+ *   - up to 16 rows (tokens x G; the mean over the batch, or the sequence's own
+ *     where single tokens come beside a chunk of a prompt): keys lose nothing; a
+ *     weight times 2^(e - R) is rounded to 11 bits down to 2^-29, and off by 2^-40
+ *     at most below.
+ *   - more rows: keys and values with e >= R - 22 lose nothing, those with e > R -
+ *     32 are off by 2^-32 * 2^(R - 127) at most, others count as zeros; weights are
+ *     rounded to 11 bits down to 2^-18 of the largest, and off by 2^-29 of it at
+ *     most below.
  */
 fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void* o,
                        long long o_token, long long o_head, float* lse, const fa_kv_pages* cache,

@@ -296,3 +296,84 @@ def test_rotary_of_no_tokens_with_positions(shape, pos, bits):
     assert gx.shape == x.shape
     with torch.no_grad():
         assert rotary.rotary_func(x, x, freq, positions=p)[1].shape == x.shape
+
+
+# ---- row scales that differ
+
+def climbs(n, kind):
+    """Exponents added to the rows of n keys, tile by tile of 128."""
+    tile = torch.arange(n) // 128
+    if kind == "up 5":
+        return tile * 5
+    if kind == "up 12":
+        return (tile * 12).clamp(max=60)
+    if kind == "up 20":
+        return (tile * 20).clamp(max=80)
+    if kind == "down":
+        return 60 - (tile * 12).clamp(max=60)
+    if kind == "last":
+        return torch.where(torch.arange(n) == n - 1, 25, 0)
+    return (tile * 7) % 40  # up and down
+
+
+@pytest.mark.parametrize("kind", ["up 5", "up 12", "up 20", "down", "last", "both ways"])
+@pytest.mark.parametrize("D,H,Hk,dtype", [(128, 8, 2, BF), (64, 6, 6, BF), (128, 4, 4, HF)])
+@pytest.mark.parametrize("rows,spare", [([1, 1, 1], 2), ([1, 2, 2], 200), ([40, 3, 140], 2),
+                                        ([40, 3, 140], 200)])
+def test_value_scales_that_climb_and_fall(kind, D, H, Hk, dtype, rows, spare):
+    b = R.Batch(rows, [900, 20, 1300], Hk, D, 64, dtype, True, seed=D, spare_cols=spare)
+    for s, n in enumerate(b.lens):
+        shift_exponents(b, 1, s, climbs(n, kind) - 70 * (dtype == HF))
+    refresh(b)
+    q = queries(b, H)
+    compare(b, q, *attend(b, q))
+    window = (300, 0)  # the largest rows are hidden from some queries
+    compare(b, q, *attend(b, q, causal=False, window=window), causal=False, window=window)
+
+
+@pytest.mark.parametrize("kind", ["up 5", "down", "last", "both ways"])
+@pytest.mark.parametrize("D,H,Hk", [(128, 8, 2), (64, 6, 6)])
+@pytest.mark.parametrize("rows,spare", [([1, 2, 2], 2), ([40, 3, 140], 200)])
+def test_key_scales_that_climb_and_fall(kind, D, H, Hk, rows, spare):
+    b = R.Batch(rows, [900, 20, 1300], Hk, D, 64, BF, True, seed=D, spare_cols=spare)
+    for s, n in enumerate(b.lens):
+        shift_exponents(b, 0, s, climbs(n, kind))
+    refresh(b)
+    q = queries(b, H)
+    scale = D ** -0.5 * 2.0 ** -int(climbs(max(b.lens), kind).max())
+    compare(b, q, *attend(b, q, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("below", [15, 22, 27, 31, 32, 40])
+@pytest.mark.parametrize("D,H,Hk", [(128, 8, 2), (64, 6, 6)])
+@pytest.mark.parametrize("rows", [[1, 2, 2], [40, 3, 140]])
+def test_one_row_far_above_the_others(below, D, H, Hk, rows):
+    """Keys and values 2^below under one row, which has next to no weight."""
+    b = R.Batch(rows, [300, 20, 1000], Hk, D, 64, BF, True, seed=D)
+    q = queries(b, H)
+    for s, n in enumerate(b.lens):
+        by = torch.full((n,), -below)
+        by[0] = 0
+        shift_exponents(b, 1, s, by)
+        pg, off = slot(b, s, 0)  # key 0: -112 in column 0, where the queries hold 4
+        b.pool[0].view(torch.uint8)[pg, off, :, 0] = 0xfe
+        b.exp[0, pg, :, off] = 125
+    q[:, :, 0] = 4
+    refresh(b)
+    compare(b, q, *attend(b, q))
+
+
+@pytest.mark.parametrize("first", [1, 128, 200])
+@pytest.mark.parametrize("rows,spare", [([1, 2, 2], 200), ([40, 3, 140], 2), ([40, 3, 140], 200)])
+@pytest.mark.parametrize("D,H,Hk", [(128, 8, 2), (64, 6, 6)])
+def test_zeros_first(first, rows, spare, D, H, Hk):
+    b = R.Batch(rows, [900, 200, 1300], Hk, D, 16, BF, True, seed=D, spare_cols=spare)
+    for w in range(2):
+        for s in range(3):
+            for j in range(min(first, b.lens[s])):
+                pg, off = slot(b, s, j)
+                b.exp[w, pg, :, off] = 0
+                b.pool[w].view(torch.uint8)[pg, off] = 0
+    refresh(b)
+    q = queries(b, H)
+    compare(b, q, *attend(b, q))
