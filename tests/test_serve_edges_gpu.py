@@ -377,3 +377,14 @@ def test_zeros_first(first, rows, spare, D, H, Hk):
     refresh(b)
     q = queries(b, H)
     compare(b, q, *attend(b, q))
+
+
+# ---- weights over an e4m3 cache are fp16 for any number of rows
+
+@pytest.mark.parametrize("rows,ctx,H,Hk,D", [([33, 1, 64], [5, 900, 64], 3, 1, 128),
+                                             ([300, 5, 129], [1000, 150, 0], 8, 2, 64),
+                                             ([700, 300], [0, 650], 16, 4, 128)])
+def test_weights_of_many_rows_over_e4m3(rows, ctx, H, Hk, D):
+    b = R.Batch(rows, ctx, Hk, D, 32, BF, True, seed=4)
+    q = queries(b, H)
+    compare(b, q, *attend(b, q))
