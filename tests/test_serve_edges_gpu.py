@@ -388,3 +388,145 @@ def test_weights_of_many_rows_over_e4m3(rows, ctx, H, Hk, D):
     b = R.Batch(rows, ctx, Hk, D, 32, BF, True, seed=4)
     q = queries(b, H)
     compare(b, q, *attend(b, q))
+
+
+# ---- scales, heads, pages
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.2, 1.5])
+@pytest.mark.parametrize("fp8,D,dtype", [(False, 128, BF), (True, 64, BF), (False, 64, HF),
+                                         (True, 128, HF)])
+@pytest.mark.parametrize("rows,spare", [([1, 2, 1], 200), ([60, 1, 200], 2), ([60, 1, 200], 200)])
+def test_softmax_scales(scale, fp8, D, dtype, rows, spare):
+    b = R.Batch(rows, [900, 0, 300], 2, D, 32, dtype, fp8, seed=3, spare_cols=spare)
+    q = queries(b, 8)
+    compare(b, q, *attend(b, q, scale=scale), scale=scale)
+    window = (150, 3)
+    compare(b, q, *attend(b, q, scale=scale, causal=False, window=window), scale=scale,
+            causal=False, window=window)
+
+
+@pytest.mark.parametrize("group", [17, 24, 40, 64, 65, 100, 127, 128])
+@pytest.mark.parametrize("fp8,D,Hk", [(False, 128, 1), (True, 64, 2), (False, 64, 2),
+                                      (True, 128, 1)])
+@pytest.mark.parametrize("rows,spare", [([1, 1, 1], 2), ([1, 0, 2], 200), ([9, 40, 1], 200)])
+def test_many_heads_to_a_key_head(group, fp8, D, Hk, rows, spare):
+    b = R.Batch(rows, [700, 0, 130], Hk, D, 16, BF, fp8, seed=group, tail=2, spare_cols=spare)
+    q = queries(b, group * Hk)
+    compare(b, q, *attend(b, q))
+    window = (50, -1)
+    compare(b, q, *attend(b, q, window=window), window=window)
+
+
+def test_sequences_that_share_pages():
+    """A common beginning lies in the cache once; single tokens and chunks read it."""
+    for rows in ([1, 1, 1], [70, 3, 30]):
+        b = R.Batch(rows, [400, 400, 400], 2, 64, 16, BF, False, seed=2)
+        shared = 320  # keys
+        for s in (1, 2):
+            b.table[s, :shared // 16] = b.table[0, :shared // 16]
+            b.k[s][:shared], b.v[s][:shared] = b.k[0][:shared], b.v[0][:shared]
+        q = queries(b, 8)
+        compare(b, q, *attend(b, q))
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_offsets_beyond_32_bits(dtype):
+    """A cache of more than 2^32 elements: its last pages are written, read and attended to."""
+    Hk, D, page = 8, 128, 256
+    pages = (1 << 32) // (Hk * D * page) + 40
+    cache = kvcache.alloc_kv_cache(pages, page, Hk, D, dtype)
+    kp, vp, ke, ve = cache
+    kw = dict(k_exp=ke, v_exp=ve)
+    b = R.Batch([300, 1, 2], [0, 600, 20], Hk, D, page, BF, False, seed=1, poison=False)
+    table = (pages - 1 - b.table.clamp(0, 30)).cuda()
+    cu = torch.tensor([0] + b.lens).cumsum(0).to(torch.int32).cuda()
+    lens = b.len_t.cuda()
+    k, v = (torch.cat(t).to(BF).cuda() for t in (b.k, b.v))
+    kvcache.kv_cache_append(k, v, kp, vp, table, cu, lens, **kw)
+    kr, vr = kvcache.kv_cache_read(kp, vp, table, cu, sum(b.lens), **kw)
+    want = [R.quantise(t.cpu())[0].to(BF) if dtype == E4 else t.cpu() for t in (k, v)]
+    assert torch.equal(kr.cpu(), want[0]) and torch.equal(vr.cpu(), want[1])
+    b.k, b.v = (list(t.double().split(b.lens)) for t in want)
+    for rows in ([300, 1, 2], [1, 1, 1]):
+        b.rows, b.total = rows, sum(rows)
+        q = queries(b, 16)
+        o = attention.flash_attn_paged_func(q.cuda(), kp, vp, table, torch.tensor(
+            [0] + rows).cumsum(0).to(torch.int32).cuda(), lens, **kw).cpu()
+        ref, lse, A, S = R.attention(b, q, D ** -0.5)
+        tol, _ = R.attention_bounds(ref, lse, A, S, BF, R.EPS[BF], D)
+        assert ((o.double() - ref).abs() <= tol).all()
+    assert fattn.fa_device_error() == fattn.FA_OK
+
+
+# ---- infinities and NaN that are visible
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,rows,spare", [(128, [1, 1, 2], 2), (64, [1, 1, 2], 200),
+                                          (128, [70, 3, 200], 2), (64, [70, 3, 200], 200)])
+def test_values_that_are_not_finite(fp8, D, rows, spare):
+    b = R.Batch(rows, [300, 20, 1000], 2, D, 16, BF, fp8, seed=6, spare_cols=spare)
+    q = queries(b, 8)
+    clean, clean_lse = attend(b, q)
+    # NaN in column 5 of key 250 of sequence 0, key head 1; infinity in column 9
+    pg, off = slot(b, 0, 250)
+    if fp8:
+        b.pool[1].view(torch.uint8)[pg, off, 1, 5] = 0x7f
+    else:
+        b.pool[1, pg, off, 1, 5] = math.nan
+        b.pool[1, pg, off, 1, 9] = -math.inf
+    o, lse = attend(b, q)
+    n = rows[0]
+    assert torch.equal(lse, clean_lse)
+    assert torch.isnan(o[:n, 4:, 5]).all()
+    if not fp8:
+        assert (o[:n, 4:, 9] == -math.inf).all()
+    o[:n, 4:, 5], o[:n, 4:, 9] = clean[:n, 4:, 5], clean[:n, 4:, 9]
+    assert torch.equal(o, clean)
+
+
+@pytest.mark.parametrize("what", ["nan", "inf"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,rows,spare", [(128, [3, 1, 2], 2), (64, [3, 1, 1], 200),
+                                          (128, [70, 3, 200], 2), (64, [70, 3, 200], 200)])
+def test_keys_that_are_not_finite(what, fp8, D, rows, spare):
+    if fp8 and what == "inf":
+        return  # e4m3 has none
+    b = R.Batch(rows, [300, 20, 1000], 2, D, 16, BF, fp8, seed=6, spare_cols=spare)
+    q = queries(b, 8)
+    clean, clean_lse = attend(b, q)
+    n, at = rows[0], b.lens[0] - rows[0] + rows[0] // 2  # visible to the last rows alone
+    pg, off = slot(b, 0, at)
+    if fp8:
+        b.pool[0].view(torch.uint8)[pg, off, 1, 5] = 0x7f
+    else:
+        b.pool[0, pg, off, 1, 5] = math.nan if what == "nan" else math.inf
+    o, lse = attend(b, q)
+    see = torch.zeros(b.total, 8, dtype=torch.bool)
+    see[rows[0] // 2:n, 4:] = True
+    if what == "inf":  # a score of -inf is a weight of zero, one of +inf makes NaN
+        up = q[:, :, 5] > 0
+        ro, rl, to, tl = reference(b, q, D ** -0.5, without=(0, at, 1))
+        low = see & ~up
+        assert ((o.double() - ro).abs() <= to)[low].all()
+        assert ((lse.double() - rl).abs() <= tl)[low.t()].all()
+        see_nan = see & up
+    else:
+        see_nan = see
+        assert torch.isnan(lse[see.t()]).all()
+    assert torch.isnan(o[see_nan]).all()
+    assert torch.equal(o[~see], clean[~see]) and torch.equal(lse[~see.t()], clean_lse[~see.t()])
+
+
+@pytest.mark.parametrize("fp8,D", [(False, 128), (True, 64), (True, 128)])
+@pytest.mark.parametrize("rows,spare", [([3, 1, 2], 200), ([70, 3, 200], 2)])
+def test_queries_that_are_not_finite(fp8, D, rows, spare):
+    b = R.Batch(rows, [300, 20, 1000], 2, D, 16, BF, fp8, seed=6, spare_cols=spare)
+    q = queries(b, 8)
+    clean, clean_lse = attend(b, q)
+    bad = torch.zeros(b.total, 8, dtype=torch.bool)
+    for token, head, value in ((0, 0, math.nan), (1, 5, math.inf), (rows[0], 7, -math.inf)):
+        q[token, head, 3] = value
+        bad[token, head] = True
+    o, lse = attend(b, q)
+    assert torch.isnan(o[bad]).all()
+    assert torch.equal(o[~bad], clean[~bad]) and torch.equal(lse[~bad.t()], clean_lse[~bad.t()])
