@@ -207,8 +207,8 @@ def flash_attn_paged_func(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
     seqlens[b] (int32, (batch,)).  Row i of sequence b sits at position
     seqlens[b] - rows(b) + i.  k_pages, v_pages: (pages, page_size, nheads_k,
     headdim) of q's type, or e4m3 with k_exp and v_exp; nheads is a multiple of
-    nheads_k, and nheads / nheads_k query heads share a key head.  block_table:
-    int32 (batch, max_pages).
+    nheads_k, and nheads / nheads_k query heads (128 at most) share a key head.
+    block_table: int32 (batch, max_pages).
 
     causal, window_size and alibi_slopes ((nheads,) or (batch, nheads)) as for
     flash_attn_func, in positions of the sequence.  Returns (total, nheads,

@@ -45,9 +45,11 @@ __device__ __forceinline__ void visible_span(const PagedLaunch& p, const Seq& s,
   if (lo >= hi) lo = hi = 0;
 }
 
-// sum over i < n of floor((a i + b) / m), a and b not negative, by Euclid's
-// algorithm on (a, m).  m starts at 128 and n below 2^23, so that a n + b, with
-// a and b reduced, fits 32 bits throughout.
+// sum over i < n of floor((a i + b) / m), a and b not negative: the lattice points
+// under a line, counted by the reciprocity of such sums (Graham, Knuth and Patashnik,
+// Concrete Mathematics, section 3.5), which takes (a, m) through the steps of Euclid's
+// algorithm.  m starts at 128 and n below 2^23, so that a n + b, with a and b reduced,
+// fits 32 bits throughout.
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long sum = 0;
   while (n > 0) {

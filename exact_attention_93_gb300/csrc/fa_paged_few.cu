@@ -40,11 +40,15 @@
 //
 // Measured (32 query and 8 key heads): 64 contexts of 256 to 16000 keys, D = 128,
 // 16-bit 188 us, 6.6 TB/s of keys and values, 97 % of the measured copy rate;
-// D = 64 108 us, 5.7 TB/s.  e4m3, D = 128, 116 us, 5.35 TB/s (the same stream
+// D = 64 108 us, 5.7 TB/s.  e4m3, D = 128, 118 us, 5.3 TB/s (the same stream
 // without its products 107 us, of which 13 are the start and the joining), and
-// D = 64 82 us, where the conversions bound it (the stream alone 62).  One
-// context of 1000 keys 9.3 us, of 4000 12 to 15, of 32000 30 to 35: launch, the
-// look at the batch, and the joining of the pieces.
+// D = 64 84 us, where the conversions bound it (the stream alone 62).  Sixteen rows (4
+// tokens a sequence) take half as long again as eight over an e4m3 cache, a tenth
+// longer over a 16-bit one: the second eight columns double the products, softmax and
+// transposes of each warp's chain, which over e4m3 is nearly as long as the stream
+// already with eight.  One context of 1000 keys 9 to 12 us, by the machine, of 4000 12
+// to 15, of 32000 30 to 37: launch, the look at the batch, and the joining of the
+// pieces.
 #include "fa_paged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"

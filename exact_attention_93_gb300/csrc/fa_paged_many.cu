@@ -42,11 +42,14 @@
 // 415 us); 32768 tokens of 8 heads 1447 us, 1520 TFLOP/s (dense 1381); four
 // prompts of 9429 tokens in all 227 us; four chunks of 137 tokens over 20000 keys
 // 188 us.  Beside its key tiles a unit costs about 3 us (reading O out, filling
-// the pipeline again) and a call about 10.  e4m3: 464 and 208 us for the first
-// and the last.  There registers are the limit: 16 warps share what 12 have in
-// the 16-bit kernel, and a split with more for the softmax or more for the
-// conversion made both slower (200 / 56: 481 us, 184 / 72: 482).  Queries take 25
-// us of the 464, a unit's rows being converted before its first product.
+// the pipeline again) and a call about 10.  e4m3: 466 and 208 us for the first
+// and the last.  (With other inputs in every call 412 and 197, e4m3 479 and 217.)
+// There registers are the limit: 16 warps share what 12 have in the 16-bit kernel,
+// and a split with more for the softmax or more for the conversion made both slower
+// (200 / 56: 481 us, 184 / 72: 482).  Queries take 25 us of the 466, a unit's rows
+// being converted before its first product.  The chunks are at half the tensor rate:
+// 4 x 137 rows of a key head are two full blocks and one of 36 rows for each, and
+// that one walks every key with one query tile and nothing to alternate with.
 #include <type_traits>
 
 #include "fa_paged.cuh"

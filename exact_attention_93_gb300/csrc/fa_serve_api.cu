@@ -19,7 +19,9 @@ constexpr int kMaxRows = 1 << 29;           // packed rows, keys of a sequence, 
 constexpr float kLog2e = 1.4426950408889634f;
 // Keys up to which units stay whole.  (us, cut and whole: one sequence of 1000
 // keys 9.9 and 9.6, of 1500 10.8 and 11.9, 8 of 1000 13.7 and 10.4; prompts of
-// 4 x 300 tokens 28.2 and 16.9, of 1500 tokens 39.4 and 31.9.)
+// 4 x 300 tokens 28.2 and 16.9, of 1500 tokens 39.4 and 31.9.)  The keys alone decide,
+// and with fewer units than SMs whole units leave some without work: 9 chunks of 1 to
+// 500 tokens under a window of 1000, 72 units, take 35 us; cut, they were not measured.
 constexpr int kWholeKeysFew = 1536, kWholeKeysMany = 1536;
 
 bool aligned(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -165,13 +167,16 @@ struct PagedPlan {
 // rows in the few-row kernel spilled: 968 us for 8 tokens, 207 in the other.)
 //
 // Single tokens may come together with a chunk of a prompt.  Where that is likely
-// (the sequences cannot be equally long, and one of them could be) and there are
-// enough single tokens for it to pay, each kernel takes its own sequences; a
-// launch that finds none costs 15 us.  (Few rows alone, many rows alone, both: 256
+// (the sequences cannot be equally long, as total is no multiple of batch, and one of
+// them could be) and there are enough single tokens for it to pay, each kernel takes
+// its own sequences; a launch that finds none costs 15 us.  (Few rows alone, many rows alone, both: 256
 // single tokens and a chunk of 512 over 4000 keys 447, 346 and 298, e4m3 609, 411
 // and 227; 256 and 100 252, 283 and 278, e4m3 219, 347 and 205; 64 and 512 218,
 // 192 and 195, e4m3 289, 230 and 149; 64 and 64 153, 163 and 185, e4m3 104, 190
-// and 135; 8 and 200, e4m3, 45, 24 and 32.)
+// and 135; 8 and 200, e4m3, 45, 24 and 32.)  Unequal sequences whose rows happen to
+// divide evenly are not seen, as equal ones (a few drafted tokens each) are the far
+// likelier reason: 255 single tokens and a chunk of 513 over 4000 keys each take 741 us
+// in e4m3, 256 and 512 464 (16-bit 696 and 691).
 constexpr int kFewRows = 16, kMixedMean = 512;
 constexpr int mixed_batch(bool fp8) { return fp8 ? 32 : 128; }
 constexpr int mixed_longest(bool fp8) { return fp8 ? 384 : 768; }

@@ -74,8 +74,8 @@ fa_status fa_rotary(const fa_rotary_operand* q, const fa_rotary_operand* k, int 
  *
  * An e4m3 cache holds for each (page, head, token) row an exponent byte e in
  * k_exp / v_exp, contiguous [pages][heads][page_size], 16-byte aligned: the
- * row's values are code * 2^(e - 127); e = 0 marks a row of zeros (a cache of
- * zero bytes reads as zeros).
+ * row's values are code * 2^(e - 127), 1 <= e <= 254; e = 0 marks a row of zeros,
+ * whatever its codes (a cache of zero bytes reads as zeros).
  */
 typedef struct {
   void *k, *v;
@@ -95,6 +95,9 @@ typedef struct {
  * sequence b in the cache, its rows of the packed array (the newest tokens)
  * included.  All int32 on the device.  A sequence may have no rows, or a
  * length of zero.
+ *
+ * batch, max_pages and the cache's pages are at least 1, total at most 2^29, and so
+ * is max_pages * page_size.
  */
 typedef struct {
   const int* block_table;
@@ -152,8 +155,8 @@ fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads
  * for row r of sequence b at position p = seqlens[b] - rows(b) + (r -
  * cu_seqlens[b]), over the keys j < seqlens[b] inside p - window_left ..
  * p + window_right (options; -1: no bound), with causal != 0 also j <= p.
- * G = heads / cache->heads query heads share a key head.  A row that sees no
- * key gets o = 0 and lse = -inf.
+ * G = heads / cache->heads query heads, 128 at most, share a key head; total *
+ * heads is below 2^30.  A row that sees no key gets o = 0 and lse = -inf.
  *
  *   q, o     [total][heads][D] in `dtype` (bf16 or fp16; a 16-bit cache's own
  *            type), element strides token / head, multiples of 8, 16-byte
