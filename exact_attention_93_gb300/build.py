@@ -25,7 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfattn.so")
 BIND = os.path.join(HERE, "_bind_torch.so")
-BIND_STAMP = os.path.join(BUILD, "bind_torch.stamp")
+BIND_STAMP = os.path.join(HERE, "_bind_torch.stamp")  # goes where the module goes
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve_api.cu",
            "fa_rotary.cu", "fa_cache.cu", "fa_paged_few.cu", "fa_paged_many.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -64,7 +64,9 @@ def kv_cache_read(k_pages, v_pages, block_table, cu_seqlens, total, starts=None,
     dtype (bf16 or fp16) defaults to a 16-bit cache's own type, which it must
     be, and to bf16, which holds every e4m3 row exactly.  out: a (k, v) pair to
     write into; rows behind the last sequence are left as they were
-    (uninitialised without out)."""
+    (uninitialised without out).  The cache keeps no gradients: outside
+    torch.no_grad(), tensors that need one are refused, here as in
+    kv_cache_append."""
     k, v = (None, None) if out is None else out
     got = fattn.bind().read(k_pages, v_pages, block_table, cu_seqlens, total, starts, k_exp, v_exp,
                             -1 if dtype is None else _ELEMS.get(dtype, fattn.FA_ELEM_FP32), k, v)

@@ -106,5 +106,7 @@ def test_the_native_module_follows_torch_and_python(tree):
     assert set(run_in(tree, other + code)[1]) == {"g++"}
     assert run_in(tree, other + code)[1] == []
     assert set(run_in(tree, get + code)[1]) == {"g++"}  # and back
+    shutil.rmtree(tree / "exact_attention_93_gb300/_build")  # the built files alone, as copied
+    assert run_in(tree, get + code)[1] == []
     other = get + "import sysconfig as s; s.get_config_var = lambda n: 'cpython-399'; "
     assert set(run_in(tree, other + code)[1]) == {"g++"}
