@@ -18,7 +18,7 @@ the v1 -> v3 table of "FlashAttention 深入" list), with per-(batch, head)
 descale factors; it has no backward.  flash_attn_paged_func is the forward of
 new tokens (one each while generating, chunks or whole prompts) over a paged
 key/value cache (kvcache.py), with grouped heads and packed sequences of
-different lengths.
+different lengths, which may share prefixes.
 """
 from __future__ import annotations
 
@@ -197,7 +197,8 @@ def flash_attn_fp8_func(q, k, v, softmax_scale=None, causal=False, window_size=(
 
 def flash_attn_paged_func(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
                           softmax_scale=None, causal=True, window_size=(-1, -1),
-                          alibi_slopes=None, k_exp=None, v_exp=None, return_lse=False):
+                          alibi_slopes=None, k_exp=None, v_exp=None, return_lse=False,
+                          cu_groups=None, shared_pages=None):
     """Attention of packed new tokens over a paged cache that already holds
     their keys and values (kvcache.kv_cache_append).
 
@@ -214,14 +215,22 @@ def flash_attn_paged_func(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
     flash_attn_func, in positions of the sequence.  Returns (total, nheads,
     headdim) (and the fp32 (nheads, total) log-sum-exp when return_lse).  A row
     that sees no key gets zeros and -inf; rows behind the last sequence are not
-    written.  Forward only."""
+    written.  Forward only.
+
+    Sequences that share their first pages (answers to one prompt, requests under one
+    system prompt) can say so: cu_groups (int32 (groups + 1,)) makes sequences
+    cu_groups[g] .. cu_groups[g + 1] - 1 a group, whose rows of block_table agree in their
+    first shared_pages[g] entries (int32 (groups,)).  Those keys are then walked once for
+    the group instead of once for each sequence; the results are the same up to rounding.
+    No more pages are shared than lie before every new token of the group.  For causal
+    attention without window and biases."""
     if alibi_slopes is not None or window_size != (-1, -1):
         window_size, alibi_slopes = _check_options(0.0, window_size, alibi_slopes,
                                                    block_table.shape[0], q.shape[1])
     got = fattn.bind().paged(
         q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
         q.shape[-1] ** -0.5 if softmax_scale is None else softmax_scale, causal, window_size[0],
-        window_size[1], alibi_slopes, k_exp, v_exp)
+        window_size[1], alibi_slopes, k_exp, v_exp, cu_groups, shared_pages)
     if type(got) is int:
         fattn._check(got, "fa_fwd_paged")
     return got if return_lse else got[0]

@@ -27,7 +27,8 @@ LIB = os.path.join(HERE, "libfattn.so")
 BIND = os.path.join(HERE, "_bind_torch.so")
 BIND_STAMP = os.path.join(HERE, "_bind_torch.stamp")  # goes where the module goes
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve_api.cu",
-           "fa_rotary.cu", "fa_cache.cu", "fa_paged_few.cu", "fa_paged_many.cu"]
+           "fa_rotary.cu", "fa_cache.cu", "fa_paged_few.cu", "fa_paged_many.cu",
+           "fa_decoder_api.cu", "fa_norm_rotary.cu", "fa_tables.cu", "fa_paged_shared.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

@@ -1,5 +1,6 @@
-// bind_torch.cpp -- the Python entry to include/fattn_cache.h: checks torch
-// tensors, allocates the results and calls the C ABI of libfattn.so.
+// bind_torch.cpp -- the Python entry to include/fattn_cache.h and
+// include/fattn_decoder.h: checks torch tensors, allocates the results and calls the
+// C ABI of libfattn.so.
 //
 // These calls are made for every layer and token while generating, when the
 // kernels take a few microseconds: the same marshalling written in Python over
@@ -21,10 +22,12 @@
 #include <torch/csrc/utils/object_ptr.h>
 
 #include <climits>
+#include <cstring>
 #include <optional>
+#include <string>
 #include <vector>
 
-#include "fattn_cache.h"
+#include "fattn_decoder.h"
 
 namespace {
 
@@ -150,7 +153,66 @@ struct Rotation {
   at::Tensor freq, pos;  // pos may be undefined
   double magnitude;
   bool interleaved, inverse;
+  std::string axis;  // of each pair; empty: one axis, and pos without a dimension for it
+  int axes = 1;
+
+  // Of (b, n) of x's tokens.
+  fa_positions positions() const {
+    fa_positions p{nullptr, 0, axes, 0, 0, reinterpret_cast<const unsigned char*>(axis.data())};
+    if (!pos.defined() || pos.numel() == 0) return p;  // (no tokens: no address either)
+    const int64_t lead = axis.empty() ? 0 : 1;
+    p.positions = pos.const_data_ptr();
+    p.bits = pos.scalar_type() == at::kInt ? 32 : 64;
+    p.axis_stride = lead ? pos.stride(0) : 0;
+    p.batch_stride = pos.dim() == lead + 2 ? pos.stride(lead) : 0;
+    return p;
+  }
+  void save(torch::autograd::AutogradContext* ctx) const {
+    ctx->saved_data["magnitude"] = magnitude;
+    ctx->saved_data["interleaved"] = interleaved;
+    ctx->saved_data["inverse"] = inverse;
+    ctx->saved_data["axis"] = axis;
+    ctx->saved_data["axes"] = axes;
+  }
+  static Rotation saved(torch::autograd::AutogradContext* ctx, const at::Tensor& freq,
+                        const at::Tensor& pos) {
+    return Rotation{freq,
+                    pos,
+                    ctx->saved_data["magnitude"].toDouble(),
+                    ctx->saved_data["interleaved"].toBool(),
+                    ctx->saved_data["inverse"].toBool(),
+                    ctx->saved_data["axis"].toStringRef(),
+                    static_cast<int>(ctx->saved_data["axes"].toInt())};
+  }
 };
+
+// sections (None, or how many pairs each axis gets) and their order as the axis of
+// each of `pairs` pairs.
+void read_sections(PyObject* sections, PyObject* order, int64_t pairs, Rotation& r) {
+  const char* name = PyUnicode_Check(order) ? PyUnicode_AsUTF8(order) : nullptr;
+  const bool turns = name && !std::strcmp(name, "turns");
+  need(turns || (name && !std::strcmp(name, "blocks")),
+       "section_order must be \"blocks\" or \"turns\"");
+  if (sections == Py_None) return;
+  THPObjectPtr items(PySequence_Fast(sections, "sections must be a sequence of integers"));
+  if (!items) throw python_error();
+  const Py_ssize_t axes = PySequence_Fast_GET_SIZE(items.get());
+  need(axes >= 1 && axes <= 8, "sections must name 1 to 8 axes");
+  int64_t left[8], all = 0;
+  for (Py_ssize_t i = 0; i < axes; ++i) {
+    left[i] = integer(PySequence_Fast_GET_ITEM(items.get(), i));
+    need(left[i] >= 0 && left[i] <= pairs, "sections must add up to the pairs of inv_freq");
+    all += left[i];
+  }
+  need(all == pairs && pairs > 0, "sections must add up to the pairs of inv_freq");
+  r.axes = static_cast<int>(axes);
+  while (static_cast<int64_t>(r.axis.size()) < pairs)
+    for (Py_ssize_t i = 0; i < axes; ++i) {  // a round: all of an axis, or one of each
+      const int64_t n = turns ? std::min<int64_t>(left[i], 1) : left[i];
+      r.axis.append(static_cast<size_t>(n), static_cast<char>(i));
+      left[i] -= n;
+    }
+}
 
 // Turns x into y, and x2 (when defined) into y2.
 fa_status turn(const at::Tensor& x, const at::Tensor& y, const at::Tensor& x2,
@@ -160,19 +222,17 @@ fa_status turn(const at::Tensor& x, const at::Tensor& y, const at::Tensor& x2,
   const fa_rotary_operand a = rotary_operand(x, y);
   fa_rotary_operand b;
   if (x2.defined()) b = rotary_operand(x2, y2);
-  const bool pos = r.pos.defined() && r.pos.numel() > 0;  // (no tokens: no address either)
-  return fa_rotary(&a, x2.defined() ? &b : nullptr, static_cast<int>(B), static_cast<int>(N),
-                   static_cast<int>(x.size(dim - 1)), static_cast<int>(2 * r.freq.size(0)),
-                   r.freq.const_data_ptr<double>(), pos ? r.pos.const_data_ptr() : nullptr,
-                   !pos ? 0 : r.pos.scalar_type() == at::kInt ? 32 : 64,
-                   pos && r.pos.dim() == 2 ? r.pos.stride(0) : 0,
-                   static_cast<float>(r.magnitude), r.interleaved, r.inverse,
-                   static_cast<fa_elem>(elem(x.scalar_type())), device.stream());
+  const fa_positions pos = r.positions();
+  return fa_rotary_axes(&a, x2.defined() ? &b : nullptr, static_cast<int>(B), static_cast<int>(N),
+                        static_cast<int>(x.size(dim - 1)), static_cast<int>(2 * r.freq.size(0)),
+                        r.freq.const_data_ptr<double>(), &pos, static_cast<float>(r.magnitude),
+                        r.interleaved, r.inverse, static_cast<fa_elem>(elem(x.scalar_type())),
+                        device.stream());
 }
 
 // What the C ABI refuses inside autograd.
-void check(fa_status st) {
-  TORCH_CHECK(st == FA_OK, "fa_rotary failed: ", fa_status_string(st), " (", static_cast<int>(st),
+void check(fa_status st, const char* what = "fa_rotary") {
+  TORCH_CHECK(st == FA_OK, what, " failed: ", fa_status_string(st), " (", static_cast<int>(st),
               ")");
 }
 
@@ -196,9 +256,7 @@ struct RotaryFunction : torch::autograd::Function<RotaryFunction<kTensors>> {
                                             const Rotation& r) {
     ctx->set_materialize_grads(false);
     ctx->save_for_backward({r.freq, r.pos});
-    ctx->saved_data["magnitude"] = r.magnitude;
-    ctx->saved_data["interleaved"] = r.interleaved;
-    ctx->saved_data["inverse"] = r.inverse;
+    r.save(ctx);
     return rotated(q, k, r);
   }
   static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx,
@@ -226,9 +284,8 @@ template <int kTensors>
 torch::autograd::variable_list RotaryFunction<kTensors>::backward(
     torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grads) {
   const auto saved = ctx->get_saved_variables();
-  const Rotation r{saved[0], saved[1], ctx->saved_data["magnitude"].toDouble(),
-                   ctx->saved_data["interleaved"].toBool(),
-                   !ctx->saved_data["inverse"].toBool()};
+  Rotation r = Rotation::saved(ctx, saved[0], saved[1]);
+  r.inverse = !r.inverse;
   std::vector<at::Tensor> have;
   for (const at::Tensor& g : grads)
     if (g.defined()) have.push_back(grad_operand(g));
@@ -245,13 +302,14 @@ torch::autograd::variable_list RotaryFunction<kTensors>::backward(
   return out;
 }
 
-// rotary(q, k, inv_freq, positions, magnitude, interleaved, inplace)
-PyObject* rotary(PyObject* const* a) {
-  const at::Tensor& q = tensor(a[0], "q must be a tensor");
-  const at::Tensor k = maybe(a[1], "k must be a tensor or None");
-  Rotation r{tensor(a[2], "inv_freq must be a tensor"),
-             maybe(a[3], "positions must be a tensor or None"), number(a[4]), truth(a[5]), false};
-  const bool inplace = truth(a[6]);
+// Checks q, k (may be undefined) and how they are turned, the latter from the
+// arguments inv_freq, positions, magnitude, interleaved, sections and section_order.
+Rotation rotation(const at::Tensor& q, const at::Tensor& k, PyObject* freq, PyObject* positions,
+                  PyObject* magnitude, PyObject* interleaved, PyObject* sections,
+                  PyObject* order) {
+  Rotation r{tensor(freq, "inv_freq must be a tensor"),
+             maybe(positions, "positions must be a tensor or None"), number(magnitude),
+             truth(interleaved), false, {}, 1};
   const int64_t dim = q.dim();
   need(dim == 3 || dim == 4,
        "expected (batch, seqlen, nheads, headdim) or packed (total, nheads, headdim) tensors");
@@ -261,33 +319,250 @@ PyObject* rotary(PyObject* const* a) {
          "q and k must agree in type and in every dimension but the heads");
   need(r.freq.scalar_type() == at::kDouble && r.freq.dim() == 1 && r.freq.is_contiguous(),
        "inv_freq must be a contiguous float64 (rotary_dim / 2) tensor");
-  const int64_t B = dim == 4 ? q.size(0) : 1, N = q.size(dim - 3);
+  read_sections(sections, order, r.freq.size(0), r);
+  const int64_t B = dim == 4 ? q.size(0) : 1, N = q.size(dim - 3), lead = r.axis.empty() ? 0 : 1;
+  need(!lead || r.pos.defined(), "sections need positions");
   if (r.pos.defined()) {
     if (r.pos.scalar_type() != at::kInt && r.pos.scalar_type() != at::kLong)
       throw Refuse{PyExc_TypeError, "positions must be int32 or int64"};
-    need((r.pos.dim() == 1 && r.pos.size(0) == N) ||
-             (dim == 4 && r.pos.dim() == 2 && r.pos.size(0) == B && r.pos.size(1) == N),
-         "positions must have shape (seqlen,) or (batch, seqlen)");
+    const int64_t rest = r.pos.dim() - lead;
+    const bool fits = (rest == 1 && r.pos.size(lead) == N) ||
+                      (dim == 4 && rest == 2 && r.pos.size(lead) == B && r.pos.size(lead + 1) == N);
+    if (lead)
+      need(fits && r.pos.size(0) == r.axes,
+           "with sections, positions must have shape (axes, seqlen) or (axes, batch, seqlen)");
+    else
+      need(fits, "positions must have shape (seqlen,) or (batch, seqlen)");
   }
   need(!r.freq.requires_grad(), "inv_freq gets no gradient: detach it");
-  for (const at::Tensor* t : {&q, &k, static_cast<const at::Tensor*>(&r.freq)}) no_tangent(*t);
-  const Device device({&q, &k, &r.freq, &r.pos});
   if (r.pos.defined() && N > 1 && r.pos.stride(-1) != 1) r.pos = r.pos.contiguous();
-  const bool grad =
-      c10::GradMode::is_enabled() && (q.requires_grad() || (k.defined() && k.requires_grad()));
-  if (grad) {
+  return r;
+}
+
+bool wants_grad(const at::Tensor& t) { return t.defined() && t.requires_grad(); }
+
+void apart(const at::Tensor& q, const at::Tensor& k) {
+  need(!k.defined() || k.numel() == 0 || k.const_data_ptr() != q.const_data_ptr(),
+       "q and k would be written over each other");
+}
+
+// rotary(q, k, inv_freq, positions, magnitude, interleaved, inplace, sections, order)
+PyObject* rotary(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q must be a tensor");
+  const at::Tensor k = maybe(a[1], "k must be a tensor or None");
+  const Rotation r = rotation(q, k, a[2], a[3], a[4], a[5], a[7], a[8]);
+  const bool inplace = truth(a[6]);
+  for (const at::Tensor* t : {&q, &k, &r.freq}) no_tangent(*t);
+  const Device device({&q, &k, &r.freq, &r.pos});
+  if (c10::GradMode::is_enabled() && (wants_grad(q) || wants_grad(k))) {
     need(!inplace, "inplace=True would overwrite tensors that need a gradient");
     auto y = k.defined() ? RotaryFunction<2>::apply(q, k, r) : RotaryFunction<1>::apply(q, r);
     return k.defined() ? pair(std::move(y[0]), std::move(y[1])) : wrap(std::move(y[0]));
   }
   const at::Tensor yq = inplace ? q : like(q), yk = !k.defined() || inplace ? k : like(k);
   if (inplace) {
-    need(!k.defined() || k.numel() == 0 || k.const_data_ptr() != q.const_data_ptr(),
-         "q and k would be written over each other");
+    apart(q, k);
     written(q);
     written(k);
   }
   const fa_status st = turn(q, yq, k, yk, r, device);
+  if (st != FA_OK) return status(st);
+  return k.defined() ? pair(yq, yk) : wrap(yq);
+}
+
+// Norm and rotation of one or two tensors.  Undefined tensors stand for what is absent;
+// autograd takes none, and gets empty ones instead.
+struct Norm {
+  Rotation r;
+  double eps;
+  bool grad_wq, grad_wk;  // weights that need a gradient
+};
+
+at::Tensor present(const at::Tensor& t, const at::Tensor& like) {
+  return t.defined() ? t : at::empty({0}, like.options().requires_grad(false));
+}
+
+at::Tensor absent(const at::Tensor& t) { return t.dim() == 1 && t.size(0) == 0 ? at::Tensor() : t; }
+
+fa_elem weight_elem(const at::Tensor& x, const at::Tensor& wq, const at::Tensor& wk) {
+  const at::Tensor& w = wq.defined() ? wq : wk;
+  return static_cast<fa_elem>(elem((w.defined() ? w : x).scalar_type()));
+}
+
+const void* address(const at::Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
+
+fa_status normed(const at::Tensor& q, const at::Tensor& yq, const at::Tensor& k,
+                 const at::Tensor& yk, const at::Tensor& wq, const at::Tensor& wk, const Norm& n,
+                 const Device& device) {
+  const int64_t dim = q.dim(), B = dim == 4 ? q.size(0) : 1, N = q.size(dim - 3);
+  need(B <= INT_MAX && N <= INT_MAX, "tensors too large");
+  const fa_rotary_operand a = rotary_operand(q, yq);
+  fa_rotary_operand b;
+  if (k.defined()) b = rotary_operand(k, yk);
+  const fa_positions pos = n.r.positions();
+  return fa_qk_norm_rotary(&a, k.defined() ? &b : nullptr, address(wq), address(wk),
+                           weight_elem(q, wq, wk), static_cast<float>(n.eps), static_cast<int>(B),
+                           static_cast<int>(N), static_cast<int>(q.size(dim - 1)),
+                           static_cast<int>(2 * n.r.freq.size(0)),
+                           n.r.freq.const_data_ptr<double>(), &pos,
+                           static_cast<float>(n.r.magnitude), n.r.interleaved,
+                           static_cast<fa_elem>(elem(q.scalar_type())), device.stream());
+}
+
+// The gradients of x and of its weight (undefined where not wanted), for one or two
+// tensors x with the gradients g of their results.
+struct NormOperand {
+  at::Tensor x, g, w, dx, dw;
+};
+
+void norm_gradients(std::vector<NormOperand>& ops, const Norm& n) {
+  const at::Tensor none;
+  const bool two = ops.size() > 1;
+  NormOperand &a = ops[0], &b = ops[two ? 1 : 0];
+  const Device device({&a.x, &a.g, &a.w, two ? &b.x : &none, two ? &b.g : &none,
+                       two ? &b.w : &none, &n.r.freq, &n.r.pos});
+  fa_rotary_operand o[2];
+  fa_strides gs[2] = {};
+  for (size_t i = 0; i < ops.size(); ++i) {
+    ops[i].g = grad_operand(ops[i].g);
+    ops[i].dx = like(ops[i].x);
+    o[i] = rotary_operand(ops[i].x, ops[i].dx);
+    gs[i] = rotary_operand(ops[i].g, ops[i].dx).xs;
+  }
+  const at::Tensor& x = a.x;
+  const int64_t dim = x.dim(), B = dim == 4 ? x.size(0) : 1, N = x.size(dim - 3), D = x.size(dim - 1);
+  size_t bytes = 0;
+  check(fa_qk_norm_rotary_bwd_workspace_size(static_cast<int>(D), &bytes), "fa_qk_norm_rotary_bwd");
+  const at::Tensor ws = at::empty({static_cast<int64_t>(bytes)},
+                                  x.options().requires_grad(false).dtype(at::kByte));
+  const fa_positions pos = n.r.positions();
+  check(fa_qk_norm_rotary_bwd(
+            &o[0], two ? &o[1] : nullptr, a.g.const_data_ptr(), gs[0],
+            two ? b.g.const_data_ptr() : nullptr, gs[1], address(a.w),
+            two ? address(b.w) : nullptr, a.dw.defined() ? a.dw.data_ptr() : nullptr,
+            two && b.dw.defined() ? b.dw.data_ptr() : nullptr,
+            weight_elem(x, a.w, two ? b.w : none), static_cast<float>(n.eps), static_cast<int>(B),
+            static_cast<int>(N), static_cast<int>(D), static_cast<int>(2 * n.r.freq.size(0)),
+            n.r.freq.const_data_ptr<double>(), &pos, static_cast<float>(n.r.magnitude),
+            n.r.interleaved, static_cast<fa_elem>(elem(x.scalar_type())), ws.data_ptr(), bytes,
+            device.stream()),
+        "fa_qk_norm_rotary_bwd");
+}
+
+// (dq, dk, dq_weight, dk_weight), undefined where there is nothing.
+torch::autograd::variable_list norm_backward(const at::Tensor& gq, const at::Tensor& gk,
+                                             const at::Tensor& q, const at::Tensor& k,
+                                             const at::Tensor& wq, const at::Tensor& wk,
+                                             const Norm& n) {
+  std::vector<NormOperand> ops;
+  if (gq.defined()) ops.push_back({q, gq, wq, {}, n.grad_wq ? like(wq) : at::Tensor()});
+  if (gk.defined()) ops.push_back({k, gk, wk, {}, n.grad_wk ? like(wk) : at::Tensor()});
+  torch::autograd::variable_list out(4);
+  if (ops.empty()) return out;
+  norm_gradients(ops, n);
+  size_t i = 0;
+  if (gq.defined()) {
+    out[0] = ops[i].dx;
+    out[2] = ops[i++].dw;
+  }
+  if (gk.defined()) {
+    out[1] = ops[i].dx;
+    out[3] = ops[i].dw;
+  }
+  return out;
+}
+
+// The gradients as a function of their own, which has none: differentiating twice is
+// an error instead of a wrong result.
+struct NormGradient : torch::autograd::Function<NormGradient> {
+  static torch::autograd::variable_list forward(torch::autograd::AutogradContext*,
+                                                const at::Tensor& gq, const at::Tensor& gk,
+                                                const at::Tensor& q, const at::Tensor& k,
+                                                const at::Tensor& wq, const at::Tensor& wk,
+                                                const Norm& n) {
+    auto out = norm_backward(absent(gq), absent(gk), q, absent(k), absent(wq), absent(wk), n);
+    for (at::Tensor& t : out) t = present(t, q);
+    return out;
+  }
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext*,
+                                                 torch::autograd::variable_list) {
+    TORCH_CHECK_NOT_IMPLEMENTED(false,
+                                "qk_norm_rotary_func is differentiable once: its gradients have "
+                                "none of their own");
+  }
+};
+
+struct NormFunction : torch::autograd::Function<NormFunction> {
+  static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx,
+                                                const at::Tensor& q, const at::Tensor& k,
+                                                const at::Tensor& wq, const at::Tensor& wk,
+                                                const Norm& n) {
+    ctx->set_materialize_grads(false);
+    ctx->save_for_backward({n.r.freq, n.r.pos, q, k, wq, wk});
+    n.r.save(ctx);
+    ctx->saved_data["eps"] = n.eps;
+    ctx->saved_data["grad_wq"] = n.grad_wq;
+    ctx->saved_data["grad_wk"] = n.grad_wk;
+    const at::Tensor k2 = absent(k), w1 = absent(wq), w2 = absent(wk);
+    const Device device({&q, &k2, &w1, &w2, &n.r.freq, &n.r.pos});
+    const at::Tensor yq = like(q), yk = k2.defined() ? like(k2) : k2;
+    check(normed(q, yq, k2, yk, w1, w2, n, device), "fa_qk_norm_rotary");
+    if (!k2.defined()) return {yq};
+    return {yq, yk};
+  }
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                 torch::autograd::variable_list grads) {
+    const auto saved = ctx->get_saved_variables();
+    const Norm n{Rotation::saved(ctx, saved[0], saved[1]), ctx->saved_data["eps"].toDouble(),
+                 ctx->saved_data["grad_wq"].toBool(), ctx->saved_data["grad_wk"].toBool()};
+    const at::Tensor gq = grads[0], gk = grads.size() > 1 ? grads[1] : at::Tensor();
+    const at::Tensor &q = saved[2], &k = saved[3], &wq = saved[4], &wk = saved[5];
+    for (const at::Tensor& g : {gq, gk}) no_tangent(g);
+    torch::autograd::variable_list out(5);
+    if (!gq.defined() && !gk.defined()) return out;
+    auto got = c10::GradMode::is_enabled()
+                   ? NormGradient::apply(present(gq, q), present(gk, q), q, k, wq, wk, n)
+                   : norm_backward(gq, gk, q, absent(k), absent(wq), absent(wk), n);
+    for (size_t i = 0; i < got.size(); ++i)
+      if (got[i].defined()) out[i] = absent(got[i]);
+    return out;
+  }
+};
+
+// norm_rotary(q, k, q_weight, k_weight, inv_freq, positions, eps, magnitude, interleaved,
+//             inplace, sections, order)
+PyObject* norm_rotary(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q must be a tensor");
+  const at::Tensor k = maybe(a[1], "k must be a tensor or None"),
+                   wq = maybe(a[2], "q_weight must be a tensor or None"),
+                   wk = maybe(a[3], "k_weight must be a tensor or None");
+  Norm n{rotation(q, k, a[4], a[5], a[7], a[8], a[10], a[11]), number(a[6]), wants_grad(wq),
+         wants_grad(wk)};
+  const bool inplace = truth(a[9]);
+  need(k.defined() || !wk.defined(), "k_weight belongs to k");
+  for (const at::Tensor* w : {&wq, &wk})
+    if (w->defined())
+      need(w->dim() == 1 && w->size(0) == q.size(-1) && w->is_contiguous() &&
+               (w->scalar_type() == q.scalar_type() || w->scalar_type() == at::kFloat),
+           "weights must be contiguous (headdim,) tensors of q's type or float32");
+  need(!wq.defined() || !wk.defined() || wq.scalar_type() == wk.scalar_type(),
+       "q_weight and k_weight must be of one type");
+  for (const at::Tensor* t : {&q, &k, &wq, &wk, static_cast<const at::Tensor*>(&n.r.freq)})
+    no_tangent(*t);
+  const Device device({&q, &k, &wq, &wk, &n.r.freq, &n.r.pos});
+  if (c10::GradMode::is_enabled() &&
+      (wants_grad(q) || wants_grad(k) || wants_grad(wq) || wants_grad(wk))) {
+    need(!inplace, "inplace=True would overwrite what the gradients need");
+    auto y = NormFunction::apply(q, present(k, q), present(wq, q), present(wk, q), n);
+    return k.defined() ? pair(std::move(y[0]), std::move(y[1])) : wrap(std::move(y[0]));
+  }
+  const at::Tensor yq = inplace ? q : like(q), yk = !k.defined() || inplace ? k : like(k);
+  if (inplace) {
+    apart(q, k);
+    written(q);
+    written(k);
+  }
+  const fa_status st = normed(q, yq, k, yk, wq, wk, n, device);
   if (st != FA_OK) return status(st);
   return k.defined() ? pair(yq, yk) : wrap(yq);
 }
@@ -433,8 +708,139 @@ PyObject* read(PyObject* const* a) {
   return pair(k, v);
 }
 
+const int* int32s(const at::Tensor& t, int64_t n, const char* what) {
+  need(t.scalar_type() == at::kInt && t.dim() == 1 && t.size(0) == n && t.is_contiguous(), what);
+  return t.const_data_ptr<int>();
+}
+
+void check_table(const at::Tensor& table, const at::Tensor& free_pages) {
+  need(table.dim() == 2 && table.scalar_type() == at::kInt &&
+           (table.size(1) <= 1 || table.stride(1) == 1) && table.size(0) <= INT_MAX &&
+           table.size(1) <= INT_MAX &&
+           (table.size(0) <= 1 || table.stride(0) >= table.size(1)),
+       "block_table must be an int32 (batch, max_pages) tensor with contiguous rows");
+  need(free_pages.dim() == 1 && free_pages.scalar_type() == at::kInt &&
+           free_pages.is_contiguous() && free_pages.size(0) <= INT_MAX,
+       "free_pages must be a contiguous int32 tensor");
+}
+
+constexpr const char* kBatchInts =
+    "new_tokens, seqlens and keep_pages must be contiguous int32 (batch,) tensors";
+constexpr const char* kOneInt = "free_count must be an int32 (1,) tensor";
+
+int size_of_page(PyObject* o) {
+  const long long v = integer(o);
+  need(v >= 16 && v <= 256 && (v & (v - 1)) == 0, "page_size must be 16, 32, 64, 128 or 256");
+  return static_cast<int>(v);
+}
+
+// reserve(new_tokens, seqlens, block_table, free_pages, free_count, page_size, total, inplace)
+PyObject* reserve(PyObject* const* a) {
+  const at::Tensor &fresh = tensor(a[0], "new_tokens must be a tensor"),
+                   &lens = tensor(a[1], "seqlens must be a tensor"),
+                   &table = tensor(a[2], "block_table must be a tensor"),
+                   &pages = tensor(a[3], "free_pages must be a tensor"),
+                   &count = tensor(a[4], "free_count must be a tensor");
+  check_table(table, pages);
+  const int64_t batch = table.size(0);
+  fa_reserve r{};
+  r.new_tokens = int32s(fresh, batch, kBatchInts);
+  r.seqlens = int32s(lens, batch, kBatchInts);
+  r.free_count = int32s(count, 1, kOneInt);
+  r.page_size = size_of_page(a[5]);
+  const long long total = integer(a[6]);
+  need(total >= 0 && total <= INT_MAX, "total must not be negative");
+  const bool inplace = truth(a[7]);
+  const Device device({&fresh, &lens, &table, &pages, &count});
+  const auto opt = fresh.options().requires_grad(false);
+  const at::Tensor cu = at::empty({batch + 1}, opt), positions = at::empty({total}, opt),
+                   slots = at::empty({total}, opt.dtype(at::kLong)), missing = at::empty({1}, opt),
+                   lens_out = inplace ? lens : at::empty({batch}, opt),
+                   count_out = inplace ? count : at::empty({1}, opt);
+  r.block_table = table.data_ptr<int>();
+  r.table_stride = batch > 1 ? table.stride(0) : std::max(table.size(1), table.stride(0));
+  r.max_pages = static_cast<int>(table.size(1));
+  r.free_pages = pages.const_data_ptr<int>();
+  r.capacity = static_cast<int>(pages.size(0));
+  r.batch = static_cast<int>(batch);
+  r.total = static_cast<int>(total);
+  r.cu_seqlens = cu.data_ptr<int>();
+  r.seqlens_out = lens_out.data_ptr<int>();
+  r.positions = positions.data_ptr<int>();
+  r.slots = reinterpret_cast<long long*>(slots.data_ptr<int64_t>());
+  r.free_count_out = count_out.data_ptr<int>();
+  r.missing = missing.data_ptr<int>();
+  written(table);
+  if (inplace) {
+    written(lens);
+    written(count);
+  }
+  const fa_status st = fa_cache_reserve(&r, device.stream());
+  if (st != FA_OK) return status(st);
+  THPObjectPtr out(PyTuple_New(6));
+  if (!out) throw python_error();
+  Py_ssize_t i = 0;
+  for (const at::Tensor* t : {&cu, &lens_out, &positions, &slots, &count_out, &missing})
+    PyTuple_SET_ITEM(out.get(), i++, wrap(*t));
+  return out.release();
+}
+
+// release(done, seqlens, block_table, free_pages, free_count, page_size, keep_pages)
+PyObject* release(PyObject* const* a) {
+  const at::Tensor &done = tensor(a[0], "done must be a tensor"),
+                   &lens = tensor(a[1], "seqlens must be a tensor"),
+                   &table = tensor(a[2], "block_table must be a tensor"),
+                   &pages = tensor(a[3], "free_pages must be a tensor"),
+                   &count = tensor(a[4], "free_count must be a tensor");
+  const at::Tensor keep = maybe(a[6], "keep_pages must be a tensor or None");
+  check_table(table, pages);
+  const int64_t batch = table.size(0);
+  need((done.scalar_type() == at::kBool || done.scalar_type() == at::kByte) && done.dim() == 1 &&
+           done.size(0) == batch && done.is_contiguous(),
+       "done must be a contiguous bool or uint8 (batch,) tensor");
+  int32s(lens, batch, kBatchInts);
+  int32s(count, 1, kOneInt);
+  const int* kept = keep.defined() ? int32s(keep, batch, kBatchInts) : nullptr;
+  const int page_size = size_of_page(a[5]);
+  const Device device({&done, &lens, &table, &pages, &count, &keep});
+  for (const at::Tensor* t : {&lens, &pages, &count}) written(*t);
+  const fa_status st = fa_cache_release(
+      static_cast<const unsigned char*>(done.const_data_ptr()), lens.data_ptr<int>(), kept,
+      table.const_data_ptr<int>(),
+      batch > 1 ? table.stride(0) : std::max(table.size(1), table.stride(0)),
+      static_cast<int>(table.size(1)), pages.data_ptr<int>(), static_cast<int>(pages.size(0)),
+      count.data_ptr<int>(), static_cast<int>(batch), page_size, device.stream());
+  if (st != FA_OK) return status(st);
+  Py_RETURN_NONE;
+}
+
+// write(k, v, k_pages, v_pages, slots, k_exp, v_exp)
+PyObject* write(PyObject* const* a) {
+  const at::Tensor &k = tensor(a[0], "k must be a tensor"), &v = tensor(a[1], "v must be a tensor"),
+                   &kp = tensor(a[2], "k_pages must be a tensor"),
+                   &vp = tensor(a[3], "v_pages must be a tensor"),
+                   &slots = tensor(a[4], "slots must be a tensor");
+  const at::Tensor ke = maybe(a[5], "k_exp must be a tensor or None"),
+                   ve = maybe(a[6], "v_exp must be a tensor or None");
+  for (const at::Tensor* t : {&k, &v, &kp, &vp})
+    no_grad(*t, "the cache keeps no gradients: call under torch.no_grad()");
+  check_rows(k, v, kp);
+  need(slots.scalar_type() == at::kLong && slots.dim() == 1 && slots.size(0) == k.size(0) &&
+           slots.is_contiguous() && k.size(0) <= INT_MAX,
+       "slots must be a contiguous int64 (total,) tensor");
+  const fa_kv_pages c = kv_pages(kp, vp, ke, ve);
+  const Device device({&k, &v, &kp, &vp, &slots, &ke, &ve});
+  for (const at::Tensor* t : {&kp, &vp, &ke, &ve}) written(*t);
+  const fa_status st = fa_cache_write(
+      &c, reinterpret_cast<const long long*>(slots.const_data_ptr<int64_t>()),
+      static_cast<int>(k.size(0)), k.const_data_ptr(), k.stride(0), k.stride(1), v.const_data_ptr(),
+      v.stride(0), v.stride(1), static_cast<fa_elem>(elem(k.scalar_type())), device.stream());
+  if (st != FA_OK) return status(st);
+  Py_RETURN_NONE;
+}
+
 // paged(q, k_pages, v_pages, block_table, cu_seqlens, seqlens, scale, causal, window_left,
-//       window_right, alibi_slopes, k_exp, v_exp)
+//       window_right, alibi_slopes, k_exp, v_exp, cu_groups, shared_pages)
 PyObject* paged(PyObject* const* a) {
   const at::Tensor &q = tensor(a[0], "q must be a tensor"),
                    &kp = tensor(a[1], "k_pages must be a tensor"),
@@ -444,7 +850,9 @@ PyObject* paged(PyObject* const* a) {
                    &lens = tensor(a[5], "seqlens must be a tensor");
   const at::Tensor slopes = maybe(a[10], "alibi_slopes must be a tensor or None"),
                    ke = maybe(a[11], "k_exp must be a tensor or None"),
-                   ve = maybe(a[12], "v_exp must be a tensor or None");
+                   ve = maybe(a[12], "v_exp must be a tensor or None"),
+                   cu_groups = maybe(a[13], "cu_groups must be a tensor or None"),
+                   shared = maybe(a[14], "shared_pages must be a tensor or None");
   for (const at::Tensor* t : {&q, &kp, &vp, &slopes})
     no_grad(*t, "attention over a cache has no backward: call under torch.no_grad()");
   const fa_kv_pages c = kv_pages(kp, vp, ke, ve);
@@ -466,12 +874,27 @@ PyObject* paged(PyObject* const* a) {
     opt.alibi_slopes = slopes.const_data_ptr<float>();
     opt.alibi_per_batch = slopes.dim() == 2;
   }
-  const Device device({&q, &kp, &vp, &table, &cu, &lens, &slopes, &ke, &ve});
+  const bool grouped = cu_groups.defined();
+  const bool causal = truth(a[7]);
+  need(grouped == shared.defined(), "cu_groups and shared_pages go together");
+  int groups = 0;
+  if (grouped) {
+    need(causal && opt.window_left == -1 && opt.window_right == -1 && !slopes.defined(),
+         "cu_groups are for causal attention without window and alibi_slopes");
+    need(shared.dim() == 1 && shared.size(0) <= r.batch,
+         "there must be at most as many groups as sequences");
+    groups = static_cast<int>(shared.size(0));
+    int32s(shared, groups, "shared_pages must be a contiguous int32 (groups,) tensor");
+    int32s(cu_groups, groups + 1, "cu_groups must be a contiguous int32 (groups + 1,) tensor");
+  }
+  const Device device({&q, &kp, &vp, &table, &cu, &lens, &slopes, &ke, &ve, &cu_groups, &shared});
   const int D = c.head_dim, H = static_cast<int>(heads);
+  const long long max_keys = static_cast<long long>(r.max_pages) * c.page_size;
   size_t bytes = 0;
-  fa_status st = fa_fwd_paged_workspace_size(r.batch, r.total, H, c.heads, D,
-                                             static_cast<long long>(r.max_pages) * c.page_size,
-                                             &bytes);
+  fa_status st =
+      grouped ? fa_fwd_paged_shared_workspace_size(r.batch, r.total, H, c.heads, D, max_keys,
+                                                   groups, &bytes)
+              : fa_fwd_paged_workspace_size(r.batch, r.total, H, c.heads, D, max_keys, &bytes);
   if (st != FA_OK) return status(st);
   const at::Tensor o = like(q);
   const at::Tensor lse = at::empty({heads, total}, q.options().requires_grad(false).dtype(at::kFloat));
@@ -479,11 +902,18 @@ PyObject* paged(PyObject* const* a) {
   if (bytes)
     ws = at::empty({static_cast<int64_t>(bytes)},
                    q.options().requires_grad(false).dtype(at::kByte));
-  st = fa_fwd_paged(q.const_data_ptr(), q.stride(0), q.stride(1), o.data_ptr(), o.stride(0),
-                    o.stride(1), lse.data_ptr<float>(), &c, &r, H, &opt,
-                    static_cast<float>(number(a[6])), truth(a[7]),
-                    static_cast<fa_elem>(elem(q.scalar_type())), bytes ? ws.data_ptr() : nullptr,
-                    bytes, device.stream());
+  const float scale = static_cast<float>(number(a[6]));
+  const fa_elem type = static_cast<fa_elem>(elem(q.scalar_type()));
+  void* const room = bytes ? ws.data_ptr() : nullptr;
+  if (grouped)
+    st = fa_fwd_paged_shared(q.const_data_ptr(), q.stride(0), q.stride(1), o.data_ptr(),
+                             o.stride(0), o.stride(1), lse.data_ptr<float>(), &c, &r,
+                             cu_groups.const_data_ptr<int>(), shared.const_data_ptr<int>(), groups,
+                             H, scale, type, room, bytes, device.stream());
+  else
+    st = fa_fwd_paged(q.const_data_ptr(), q.stride(0), q.stride(1), o.data_ptr(), o.stride(0),
+                      o.stride(1), lse.data_ptr<float>(), &c, &r, H, &opt, scale, causal, type,
+                      room, bytes, device.stream());
   if (st != FA_OK) return status(st);
   return pair(o, lse);
 }
@@ -513,8 +943,10 @@ PyMethodDef method(const char* name) {
                      METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method<rotary, 7>("rotary"), method<append, 9>("append"),
-                         method<read, 11>("read"), method<paged, 13>("paged"),
+PyMethodDef methods[] = {method<rotary, 9>("rotary"),   method<norm_rotary, 12>("norm_rotary"),
+                         method<append, 9>("append"),   method<write, 7>("write"),
+                         method<read, 11>("read"),      method<reserve, 8>("reserve"),
+                         method<release, 7>("release"), method<paged, 15>("paged"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind_torch", nullptr, -1, methods,

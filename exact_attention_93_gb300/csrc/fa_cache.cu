@@ -122,7 +122,15 @@ __global__ void __launch_bounds__(kCacheThreads)
                             : make_uint4(0u, 0u, 0u, 0u);
       }
     }
-    if (h0 == h_first) {
+    if (h0 == h_first && p.slots) {
+      if (row < p.r.total) {
+        const long long slot = p.slots[row], page = slot >> p.c.page_log2;
+        ok = slot >= 0 && page < p.c.pages;
+        at[0] = Slot(p, 0, static_cast<int>(page), slot);
+        at[1] = Slot(p, 1, static_cast<int>(page), slot);
+        if (!ok && slot >= 0 && sub == 0) atomicExch(p.err, kDevErrBadIndex);
+      }
+    } else if (h0 == h_first) {
       const int b = warp_find_seq(p.r.cu, p.r.batch, static_cast<int>(first), row);
       if (b >= 0 && row < p.r.total) {  // (not behind the last sequence)
         const int c0 = p.r.cu[b], c1 = p.r.cu[b + 1];

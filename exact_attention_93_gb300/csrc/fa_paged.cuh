@@ -301,7 +301,8 @@ struct PageFeed {
   __device__ __forceinline__ int load(int i) const { return i >= lo && i <= hi ? table[i] : -1; }
   __device__ __forceinline__ void start(const PagedLaunch& p, int b, int tile, int key_lo,
                                         int key_hi) {
-    table = p.r.table + b * p.r.table_stride;
+    table = p.r.table + (p.r.rows ? p.r.rows[b] : b) * p.r.table_stride +
+            (p.r.skip ? p.r.skip[b] : 0);
     first = (tile * kTile) >> p.page_log2;
     lo = key_lo >> p.page_log2;
     hi = (key_hi - 1) >> p.page_log2;
@@ -341,6 +342,26 @@ __device__ __forceinline__ void store16(uint16_t* dst, const float (&o)[kN], flo
   } else {
     *reinterpret_cast<uint32_t*>(dst) = pack2<kBf16>(o[0] * scale, o[1] * scale);
   }
+}
+
+template <int kN>
+__device__ __forceinline__ void store32(float* dst, const float (&o)[kN], float scale) {
+  if constexpr (kN == 4)
+    *reinterpret_cast<float4*>(dst) =
+        make_float4(o[0] * scale, o[1] * scale, o[2] * scale, o[3] * scale);
+  else
+    *reinterpret_cast<float2*>(dst) = make_float2(o[0] * scale, o[1] * scale);
+}
+
+// A lane's columns of a finished row, in the type that the call asks for.
+template <int D, bool kBf16, int kN>
+__device__ __forceinline__ void store_row(const PagedLaunch& p, long long row, int head, int column,
+                                          const float (&o)[kN], float scale) {
+  if (p.o32)
+    store32(p.o32 + (row * p.heads + head) * D + column, o, scale);
+  else
+    store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head + column, o,
+                   scale);
 }
 
 // Adds up the units that several CTAs worked on.  Block (c, y) takes a share of
@@ -416,8 +437,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       int token, head;
       row_of(p, task.first_row, r0 + q, task.hk, token, head);
       const long long row = task.start + token;
-      store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head + lane * kN,
-                     o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
+      store_row<D, kBf16>(p, row, head, lane * kN, o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
       if (lane == 0)
         p.lse[static_cast<long long>(head) * p.r.total + row] =
             l[q] == 0.f ? -INFINITY : (m[q] + lg2_approx(l[q])) * kPagedLn2;

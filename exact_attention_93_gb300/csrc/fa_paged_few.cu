@@ -730,9 +730,7 @@ __global__ void __maxnreg__(kFewRegs)
 #pragma unroll
               for (int e = 0; e < kN; ++e) out[e] = 0.f;
             }
-            store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head +
-                               lane * kN,
-                           out, sum == 0.f ? 0.f : 1.f / sum);
+            store_row<D, kBf16>(p, row, head, lane * kN, out, sum == 0.f ? 0.f : 1.f / sum);
             if (lane == 0)
               p.lse[static_cast<long long>(head) * p.r.total + row] =
                   sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kPagedLn2;

@@ -881,9 +881,11 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
         // This row's 128-byte pieces in the output: D / 64 of 16-bit elements,
         // D / 32 of fp32.  (The loops stay rolled: unrolled, the epilogue spent
         // most of its 2.5 us waiting for its own instructions.)
-        uint8_t* out = whole ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) +
-                                                          row * p.o_token + head * p.o_head)
-                             : reinterpret_cast<uint8_t*>(p.part_o + at * D);
+        const bool narrow = whole && !p.o32;
+        uint8_t* out = narrow ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) +
+                                                           row * p.o_token + head * p.o_head)
+                       : whole ? reinterpret_cast<uint8_t*>(p.o32 + (row * p.heads + head) * D)
+                               : reinterpret_cast<uint8_t*>(p.part_o + at * D);
         if (!mine) out = nullptr;
         // the rows this lane writes 16 bytes of: rr = lane / 8 + 4 i
         unsigned long long rows[kFp8 ? 1 : 8];
@@ -917,8 +919,8 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
               o[e] = __float_as_uint(__uint_as_float(o[e]) * many_exp2_field(127 - 64));
           }
           // 16-bit: half a piece, fp32: a whole one
-          const int half = whole ? (c & 1) * 4 : 0, n = whole ? 4 : 8;
-          if (whole) {
+          const int half = narrow ? (c & 1) * 4 : 0, n = narrow ? 4 : 8;
+          if (narrow) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               o[e] = pack2<kBf16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
@@ -940,7 +942,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
                                           (((half + q) ^ (lane & 7)) << 4)) =
                     make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
-          if (whole && !(c & 1)) continue;  // the piece's other half comes next
+          if (narrow && !(c & 1)) continue;  // the piece's other half comes next
           if constexpr (!kFp8) {
             __syncwarp();
             uint4 v[8];
@@ -950,7 +952,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
               v[i] = *reinterpret_cast<const uint4*>(s.stage[warp] + rr * 128 +
                                                      (((lane ^ rr) & 7) << 4));
             }
-            const int piece = whole ? c >> 1 : c;
+            const int piece = narrow ? c >> 1 : c;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (rows[i])

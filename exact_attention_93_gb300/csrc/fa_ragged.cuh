@@ -43,6 +43,7 @@ __device__ __forceinline__ Seq load_seq(const Ragged& r, int page_log2, int b, u
   s.rows = min(max(c1, s.start), r.total) - s.start;
   const long long most = static_cast<long long>(r.max_pages) << page_log2;
   s.len = static_cast<int>(min(static_cast<long long>(max(n, 0)), most));
+  if (r.skip) s.len -= r.skip[b] << page_log2;
   s.pos0 = s.len - s.rows;
   if (err && (n < 0 || n > most || c0 < 0 || c1 < c0 || c1 > r.total))
     atomicExch(err, kDevErrBadIndex);

@@ -27,6 +27,10 @@ struct RotaryLaunch {
   long long position_bstride;
   float magnitude;
   int interleaved, inverse, elem;
+  // more than one axis: pair i takes its position from row axis[i] of the positions
+  int position_axes;
+  long long position_astride;
+  uint8_t axis[64];
 };
 
 cudaError_t launch_rotary(const RotaryLaunch& a, cudaStream_t s);
@@ -39,6 +43,9 @@ struct Ragged {
   const int* cu;
   const int* lens;  // append, attention: lengths; read: first positions (may be null)
   int batch, total;
+  // Attention over a part of the keys: the first skip[b] pages of sequence b are left
+  // out; a group of sequences as one reads the table's row rows[g].  Either may be null.
+  const int *skip, *rows;
 };
 
 // Strides in elements of the cache's type.
@@ -55,6 +62,7 @@ struct CacheLaunch {
   void* rows[2];  // packed keys, values
   long long row_token[2], row_head[2];
   int elem;  // of the packed rows
+  const long long* slots;  // append: where each row goes; null: by table and lengths
   uint32_t* err;
 };
 
@@ -75,6 +83,7 @@ struct PagedLaunch {
   void* o;
   long long o_token, o_head;
   float* lse;  // [heads][total]
+  float* o32;  // or null: O goes here in fp32, [total][heads][D], instead of o
   const uint8_t *k_exp, *v_exp;
   Ragged r;
   int heads, heads_k, group, D;
@@ -101,5 +110,30 @@ int paged_few_rows(double rows);
 int paged_many_rows(int group);
 cudaError_t launch_paged_many(const PagedLaunch& a, cudaStream_t s);
 cudaError_t launch_paged_few(const PagedLaunch& a, cudaStream_t s);
+
+// Attention over prefixes that sequences share (fa_paged_shared.cu): what makes
+// groups of sequences look like sequences, and the joining of the two parts.
+struct SharedSetup {
+  Ragged r;
+  const int *cu_groups, *shared_pages;
+  int groups, page_log2;
+  int *cu, *lens, *rows;  // of the groups as sequences: [groups + 1], [groups], [groups]
+  int* skip;              // [batch]
+  uint32_t* err;
+};
+
+struct SharedJoin {
+  const float *o1, *o2, *lse1, *lse2;  // the shared part, the own part
+  const int* cu_groups;                // packed rows of the groups, [groups + 1]
+  int groups;
+  const int* cu;
+  int batch, total, heads, D, elem;
+  void* o;
+  long long o_token, o_head;
+  float* lse;
+};
+
+cudaError_t launch_shared_setup(const SharedSetup& a, cudaStream_t s);
+cudaError_t launch_shared_join(const SharedJoin& a, cudaStream_t s);
 
 }  // namespace fa

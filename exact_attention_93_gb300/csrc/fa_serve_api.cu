@@ -1,21 +1,20 @@
-// fa_serve_api.cu -- the C ABI of include/fattn_cache.h: argument checks, TMA
-// descriptor set-up, workspace layout and kernel launches.  No arithmetic of
-// the operators lives here.
+// fa_serve_api.cu -- the C ABI of include/fattn_cache.h, and attention over shared
+// prefixes of include/fattn_decoder.h: argument checks, TMA descriptor set-up,
+// workspace layout and kernel launches.  No arithmetic of the operators lives here.
 #include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 
+#include "fa_checks.h"
 #include "fa_internal.h"
 #include "fa_serve.h"
-#include "fattn_cache.h"
+#include "fattn_decoder.h"
 #include "host_tmap.hpp"
 
 namespace fa {
 namespace {
 
-constexpr long long kMaxBytes = 1ll << 40;  // every operand lies below this from its base
-constexpr int kMaxRows = 1 << 29;           // packed rows, keys of a sequence, window bounds
 constexpr float kLog2e = 1.4426950408889634f;
 // Keys up to which units stay whole.  (us, cut and whole: one sequence of 1000
 // keys 9.9 and 9.6, of 1500 10.8 and 11.9, 8 of 1000 13.7 and 10.4; prompts of
@@ -23,129 +22,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 // and with fewer units than SMs whole units leave some without work: 9 chunks of 1 to
 // 500 tokens under a window of 1000, 72 units, take 35 us; cut, they were not measured.
 constexpr int kWholeKeysFew = 1536, kWholeKeysMany = 1536;
-
-bool aligned(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-
-int elem_bytes(int elem) { return elem == FA_ELEM_FP32 ? 4 : elem == FA_ELEM_E4M3 ? 1 : 2; }
-
-bool is16(int elem) { return elem == FA_ELEM_BF16 || elem == FA_ELEM_FP16; }
-
-// Strides of one operand: non-negative, `unit`-byte multiples, and the last
-// element below kMaxBytes.
-bool strides_ok(const long long* st, const long long* extent, int n, int D, int es, int unit) {
-  double last = D;
-  for (int i = 0; i < n; ++i) {
-    if (st[i] < 0 || (st[i] * es) % unit != 0 || st[i] > kMaxBytes) return false;
-    last += static_cast<double>(extent[i] - 1) * st[i];
-  }
-  return last * es < static_cast<double>(kMaxBytes);
-}
-
-// An operand that is written: every index has elements of its own (strides below
-// a row would let rows share them).
-bool apart(const long long* st, const long long* extent, int n, int D) {
-  for (int i = 0; i < n; ++i)
-    if (extent[i] > 1 && st[i] < D) return false;
-  return true;
-}
-
-fa_status check_batch(const fa_ragged* b, bool lens_needed) {
-  if (!b || b->batch < 1 || b->total < 0 || b->total > kMaxRows || b->max_pages < 1)
-    return FA_ERR_INVALID_ARG;
-  if (!aligned(b->block_table, 4) || !aligned(b->cu_seqlens, 4) || b->table_stride < b->max_pages)
-    return FA_ERR_INVALID_ARG;
-  if (lens_needed && !aligned(b->seqlens, 4)) return FA_ERR_INVALID_ARG;
-  return FA_OK;
-}
-
-fa_status check_pages(const fa_kv_pages* c, const fa_ragged* b, fa_elem dtype) {
-  if (!c) return FA_ERR_INVALID_ARG;
-  if (c->head_dim != 64 && c->head_dim != 128) return FA_ERR_UNSUPPORTED;
-  if (!is16(dtype) || (!is16(c->type) && c->type != FA_ELEM_E4M3)) return FA_ERR_UNSUPPORTED;
-  if (is16(c->type) && c->type != static_cast<int>(dtype)) return FA_ERR_UNSUPPORTED;
-  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
-    return FA_ERR_UNSUPPORTED;
-  if (c->pages < 1 || c->heads < 1 || c->heads > 65535) return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(b->max_pages) * c->page_size > kMaxRows) return FA_ERR_INVALID_ARG;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID_ARG;
-  if (c->type == FA_ELEM_E4M3 && (!aligned(c->k_exp, 16) || !aligned(c->v_exp, 16)))
-    return FA_ERR_INVALID_ARG;
-  const long long extent[3] = {c->pages, c->page_size, c->heads};
-  const long long ks[3] = {c->k_page, c->k_token, c->k_head};
-  const long long vs[3] = {c->v_page, c->v_token, c->v_head};
-  const int es = elem_bytes(c->type);
-  if (!strides_ok(ks, extent, 3, c->head_dim, es, 16) ||
-      !strides_ok(vs, extent, 3, c->head_dim, es, 16))
-    return FA_ERR_INVALID_ARG;
-  return FA_OK;
-}
-
-// A packed [total][heads][D] operand of 16-bit elements.
-bool packed_ok(const void* p, long long token, long long head, int total, int heads, int D) {
-  const long long extent[2] = {total, heads}, st[2] = {token, head};
-  return aligned(p, 16) && strides_ok(st, extent, 2, D, 2, 16);
-}
-
-int log2_of(int x) {
-  int n = 0;
-  while ((1 << n) < x) ++n;
-  return n;
-}
-
-Ragged ragged_of(const fa_ragged* b, const int* lens) {
-  return Ragged{b->block_table, b->table_stride, b->max_pages, b->cu_seqlens, lens, b->batch,
-                b->total};
-}
-
-fa_status cache_rows(const fa_kv_pages* cache, const fa_ragged* batch, const int* lens,
-                     const void* k, long long k_token, long long k_head, const void* v,
-                     long long v_token, long long v_head, fa_elem dtype, void* stream,
-                     bool append) {
-  fa_status st;
-  if ((st = check_pages(cache, batch, dtype)) != FA_OK) return st;
-  if (batch->total == 0) return FA_OK;
-  if (!packed_ok(k, k_token, k_head, batch->total, cache->heads, cache->head_dim) ||
-      !packed_ok(v, v_token, v_head, batch->total, cache->heads, cache->head_dim))
-    return FA_ERR_INVALID_ARG;
-  const long long pages[3] = {cache->pages, cache->page_size, cache->heads};
-  const long long rows[2] = {batch->total, cache->heads};
-  const long long st_k[3] = {cache->k_page, cache->k_token, cache->k_head};
-  const long long st_v[3] = {cache->v_page, cache->v_token, cache->v_head};
-  const long long st_rk[2] = {k_token, k_head}, st_rv[2] = {v_token, v_head};
-  const int D = cache->head_dim;
-  const bool distinct =
-      append ? cache->k != cache->v &&
-                   (cache->type != FA_ELEM_E4M3 || cache->k_exp != cache->v_exp) &&
-                   apart(st_k, pages, 3, D) && apart(st_v, pages, 3, D)
-             : k != v && apart(st_rk, rows, 2, D) && apart(st_rv, rows, 2, D);
-  if (!distinct) return FA_ERR_INVALID_ARG;
-  CacheLaunch a{};
-  a.c = Pages{{cache->k, cache->v},
-              {cache->k_exp, cache->v_exp},
-              {cache->k_page, cache->v_page},
-              {cache->k_token, cache->v_token},
-              {cache->k_head, cache->v_head},
-              cache->pages,
-              cache->page_size,
-              log2_of(cache->page_size),
-              cache->heads,
-              cache->head_dim,
-              cache->type};
-  a.r = ragged_of(batch, lens);
-  a.rows[0] = const_cast<void*>(k);
-  a.rows[1] = const_cast<void*>(v);
-  a.row_token[0] = k_token;
-  a.row_token[1] = v_token;
-  a.row_head[0] = k_head;
-  a.row_head[1] = v_head;
-  a.elem = dtype;
-  a.err = device_error_word();
-  if (!a.err) return FA_ERR_CUDA;
-  const auto launch = append ? launch_cache_append : launch_cache_read;
-  return launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
-}
 
 // One launch of a call: the few-row or the many-row kernel over the sequences of
 // min_rows to max_rows query rows (tokens x group).
@@ -239,109 +115,25 @@ bool page_map(CUtensorMap* m, const void* base, const fa_kv_pages* c, long long 
       fp8 ? 1 : 2, 1, promotion);
 }
 
-}  // namespace
-}  // namespace fa
-
-using namespace fa;
-
-extern "C" {
-
-fa_status fa_rotary(const fa_rotary_operand* q, const fa_rotary_operand* k, int B, int N, int D,
-                    int rotary_dim, const double* inv_freq, const void* positions,
-                    int position_bits, long long position_batch_stride, float magnitude,
-                    int interleaved, int inverse, fa_elem dtype, void* stream) {
-  if (!q || B < 0 || N < 0 || B > kMaxRows || N > kMaxRows) return FA_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
-  if (!is16(dtype) && dtype != FA_ELEM_FP32) return FA_ERR_UNSUPPORTED;
-  if (rotary_dim < 16 || rotary_dim > D || rotary_dim % 16) return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(B) * N > (1ll << 40)) return FA_ERR_INVALID_ARG;
-  if (!aligned(inv_freq, 8) || !std::isfinite(magnitude)) return FA_ERR_INVALID_ARG;
-  if (positions ? (position_bits != 32 && position_bits != 64) ||
-                      !aligned(positions, position_bits / 8) || position_batch_stride < 0
-                : position_bits != 0)
-    return FA_ERR_INVALID_ARG;
-  RotaryLaunch a{};
-  const fa_rotary_operand* ops[2] = {q, k};
-  for (int i = 0; i < 2; ++i) {
-    const fa_rotary_operand* t = ops[i];
-    if (!t) continue;
-    if (t->heads < 1 || t->heads > 65535) return FA_ERR_INVALID_ARG;
-    if (B == 0 || N == 0) continue;
-    const long long extent[3] = {B, t->heads, N};
-    const long long xs[3] = {t->xs.batch, t->xs.head, t->xs.seq};
-    const long long ys[3] = {t->ys.batch, t->ys.head, t->ys.seq};
-    const int es = elem_bytes(dtype);
-    if (!aligned(t->x, 16) || !aligned(t->y, 16) || !strides_ok(xs, extent, 3, D, es, 16) ||
-        !strides_ok(ys, extent, 3, D, es, 16))
-      return FA_ERR_INVALID_ARG;
-    if (t->x == t->y && (xs[0] != ys[0] || xs[1] != ys[1] || xs[2] != ys[2]))
-      return FA_ERR_INVALID_ARG;
-    if (!apart(ys, extent, 3, D) || (i == 1 && t->y == a.y[0])) return FA_ERR_INVALID_ARG;
-    a.x[i] = t->x;
-    a.y[i] = t->y;
-    a.xs[i] = RowStrides{t->xs.batch, t->xs.head, t->xs.seq};
-    a.ys[i] = RowStrides{t->ys.batch, t->ys.head, t->ys.seq};
-    a.heads[i] = t->heads;
-  }
-  if (B == 0 || N == 0) return FA_OK;
-  a.B = B;
-  a.N = N;
-  a.D = D;
-  a.rotary = rotary_dim;
-  a.inv_freq = inv_freq;
-  a.positions = positions;
-  a.position_bits = position_bits;
-  a.position_bstride = position_batch_stride;
-  a.magnitude = magnitude;
-  a.interleaved = interleaved != 0;
-  a.inverse = inverse != 0;
-  a.elem = dtype;
-  return launch_rotary(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+PagedPlan plan_of(const PagedLaunch& a, const Ragged& r) {
+  return paged_plan(r.batch, r.total, a.heads, a.heads_k, a.D,
+                    static_cast<long long>(r.max_pages) * a.page_size, a.cache_elem == kElemE4m3);
 }
 
-fa_status fa_cache_append(const fa_kv_pages* cache, const fa_ragged* batch, const void* k,
-                          long long k_token, long long k_head, const void* v, long long v_token,
-                          long long v_head, fa_elem dtype, void* stream) {
-  const fa_status st = check_batch(batch, true);
-  if (st != FA_OK) return st;
-  return cache_rows(cache, batch, batch->seqlens, k, k_token, k_head, v, v_token, v_head, dtype,
-                    stream, true);
-}
+bool plan_many(const PagedPlan& plan) { return plan.part[plan.parts - 1].many; }
 
-fa_status fa_cache_read(const fa_kv_pages* cache, const fa_ragged* batch, const int* starts,
-                        void* k, long long k_token, long long k_head, void* v, long long v_token,
-                        long long v_head, fa_elem dtype, void* stream) {
-  const fa_status st = check_batch(batch, false);
-  if (st != FA_OK) return st;
-  if (starts && !aligned(starts, 4)) return FA_ERR_INVALID_ARG;
-  return cache_rows(cache, batch, starts, k, k_token, k_head, v, v_token, v_head, dtype, stream,
-                    false);
-}
-
-fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k, int D,
-                                      long long max_keys, size_t* bytes) {
-  if (!bytes) return FA_ERR_INVALID_ARG;
-  *bytes = 0;
-  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
-  if (!paged_sizes_ok(batch, total, heads, heads_k, D) || max_keys < 0) return FA_ERR_INVALID_ARG;
-  for (const bool fp8 : {false, true})  // whatever the cache holds
-    *bytes = std::max(
-        *bytes, paged_plan(batch, total, heads, heads_k, D, max_keys, fp8).total_bytes);
-  return FA_OK;
-}
-
-fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void* o,
-                       long long o_token, long long o_head, float* lse, const fa_kv_pages* cache,
-                       const fa_ragged* batch, int heads, const fa_options* options, float scale,
-                       int causal, fa_elem dtype, void* workspace, size_t workspace_bytes,
-                       void* stream) {
+// Checks the arguments of attention over pages, and fills all of the kernels' but what
+// comes from the device and the workspace.
+fa_status paged_arguments(PagedLaunch& a, const void* q, long long q_token, long long q_head,
+                          void* o, long long o_token, long long o_head, float* lse,
+                          const fa_kv_pages* cache, const fa_ragged* batch, int heads,
+                          const fa_options* options, float scale, int causal, fa_elem dtype) {
   fa_status st;
   if ((st = check_batch(batch, true)) != FA_OK) return st;
   if ((st = check_pages(cache, batch, dtype)) != FA_OK) return st;
   if (!paged_sizes_ok(batch->batch, batch->total, heads, cache->heads, cache->head_dim) ||
       !std::isfinite(scale))
     return FA_ERR_INVALID_ARG;
-  PagedLaunch a{};
   a.win_left = a.win_right = -1;
   if (options) {
     if (options->block_mask) return FA_ERR_UNSUPPORTED;
@@ -360,16 +152,6 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
     return FA_ERR_INVALID_ARG;
   const long long extent[2] = {batch->total, heads}, o_st[2] = {o_token, o_head};
   if (o == q || !apart(o_st, extent, 2, D)) return FA_ERR_INVALID_ARG;
-  const PagedPlan plan =
-      paged_plan(batch->batch, batch->total, heads, cache->heads, D,
-                 static_cast<long long>(batch->max_pages) * cache->page_size,
-                 cache->type == FA_ELEM_E4M3);
-  if (plan.total_bytes &&
-      (!aligned(workspace, 256) || workspace_bytes < plan.total_bytes))
-    return FA_ERR_INVALID_ARG;
-  if (!page_map(&a.map_k, cache->k, cache, cache->k_page, cache->k_token, cache->k_head) ||
-      !page_map(&a.map_v, cache->v, cache, cache->v_page, cache->v_token, cache->v_head))
-    return FA_ERR_CUDA;
   a.q = q;
   a.q_token = q_token;
   a.q_head = q_head;
@@ -390,26 +172,34 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
   a.cache_elem = cache->type;
   a.elem = dtype;
   a.scale_log2 = scale * kLog2e;
+  return FA_OK;
+}
+
+// What comes from the device and its driver; many: queries go by tensor map.
+bool paged_device(PagedLaunch& a, const fa_kv_pages* cache, bool many) {
+  if (sm_count(&a.sms) != cudaSuccess || !(a.err = device_error_word())) return false;
+  if (!page_map(&a.map_k, cache->k, cache, cache->k_page, cache->k_token, cache->k_head) ||
+      !page_map(&a.map_v, cache->v, cache, cache->v_page, cache->v_token, cache->v_head))
+    return false;
+  // {D, heads, total}: a box is the heads of one key head for a tile's tokens
+  return !many ||
+         make_tmap_4d(&a.map_q, a.q,
+                      a.elem == kElemBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      static_cast<uint64_t>(a.D), static_cast<uint64_t>(a.heads),
+                      static_cast<uint64_t>(a.r.total), 1, static_cast<uint64_t>(a.q_head),
+                      static_cast<uint64_t>(a.q_token), static_cast<uint64_t>(a.q_token), 64,
+                      static_cast<uint32_t>(a.group), CU_TENSOR_MAP_SWIZZLE_128B, 2,
+                      static_cast<uint32_t>(kTile / a.group));
+}
+
+fa_status paged_launch(PagedLaunch a, const PagedPlan& plan, void* workspace, cudaStream_t s) {
   if (plan.total_bytes) {
     auto* base = static_cast<uint8_t*>(workspace);
     a.part_o = reinterpret_cast<float*>(base);
     a.part_ml = reinterpret_cast<float2*>(base + plan.o_bytes);
     a.tasks = reinterpret_cast<JoinTask*>(base + plan.o_bytes + plan.ml_bytes);
   }
-  if (sm_count(&a.sms) != cudaSuccess) return FA_ERR_CUDA;
-  a.err = device_error_word();
-  if (!a.err) return FA_ERR_CUDA;
-  // {D, heads, total}: a box is the heads of one key head for a tile's tokens
-  if (plan.part[plan.parts - 1].many &&
-      !make_tmap_4d(&a.map_q, q,
-                    dtype == FA_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                    static_cast<uint64_t>(D), static_cast<uint64_t>(heads),
-                    static_cast<uint64_t>(batch->total), 1, static_cast<uint64_t>(q_head),
-                    static_cast<uint64_t>(q_token), static_cast<uint64_t>(q_token), 64,
-                    static_cast<uint32_t>(a.group), CU_TENSOR_MAP_SWIZZLE_128B, 2,
-                    static_cast<uint32_t>(kTile / a.group)))
-    return FA_ERR_CUDA;
   for (int i = 0; i < plan.parts; ++i) {  // one after the other: they share the workspace
     const PagedPart& part = plan.part[i];
     a.block_rows = part.block_rows;
@@ -422,9 +212,187 @@ fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void*
             : static_cast<long long>(a.win_left) + a.win_right + a.block_rows / a.group + kTile;
     a.whole = part.whole || unit_keys <= (part.many ? kWholeKeysMany : kWholeKeysFew);
     const auto launch = part.many ? launch_paged_many : launch_paged_few;
-    if (launch(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
+    if (launch(a, s) != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
+}
+
+// Whether walking the shared keys once per group is worth two parts and their joining,
+// by the rows (tokens x group) of a sequence.
+constexpr int kSharedRows = 128;
+
+bool sharing_pays(int batch, int total, int group, int groups) {
+  return groups > 0 && static_cast<double>(total) * group / batch <= kSharedRows;
+}
+
+// The workspace of attention over shared prefixes, in front of the kernels' own.
+struct SharedLayout {
+  size_t o1, o2, lse1, lse2, cu, lens, rows, skip, bytes;
+};
+
+SharedLayout shared_layout(int batch, int total, int heads, int D, int groups) {
+  const size_t stats = round256(sizeof(float) * total * heads), o = stats * D;
+  SharedLayout at{};
+  size_t end = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t begin = end;
+    end += round256(bytes);
+    return begin;
+  };
+  at.o1 = take(o);
+  at.o2 = take(o);
+  at.lse1 = take(stats);
+  at.lse2 = take(stats);
+  at.cu = take(sizeof(int) * (groups + 1));
+  at.lens = take(sizeof(int) * groups);
+  at.rows = take(sizeof(int) * groups);
+  at.skip = take(sizeof(int) * batch);
+  at.bytes = end;
+  return at;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_rotary(const fa_rotary_operand* q, const fa_rotary_operand* k, int B, int N, int D,
+                    int rotary_dim, const double* inv_freq, const void* positions,
+                    int position_bits, long long position_batch_stride, float magnitude,
+                    int interleaved, int inverse, fa_elem dtype, void* stream) {
+  RotaryLaunch a{};
+  bool done;
+  const fa_positions pos{positions, position_bits, 1, 0, position_batch_stride, nullptr};
+  const fa_status st =
+      rotary_arguments(a, q, k, B, N, D, rotary_dim, inv_freq, pos, magnitude, dtype, done);
+  if (st != FA_OK || done) return st;
+  a.interleaved = interleaved != 0;
+  a.inverse = inverse != 0;
+  return launch_rotary(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_append(const fa_kv_pages* cache, const fa_ragged* batch, const void* k,
+                          long long k_token, long long k_head, const void* v, long long v_token,
+                          long long v_head, fa_elem dtype, void* stream) {
+  const fa_status st = check_batch(batch, true);
+  if (st != FA_OK) return st;
+  return cache_rows(cache, batch, batch->seqlens, nullptr, k, k_token, k_head, v, v_token, v_head, dtype,
+                    stream, true);
+}
+
+fa_status fa_cache_read(const fa_kv_pages* cache, const fa_ragged* batch, const int* starts,
+                        void* k, long long k_token, long long k_head, void* v, long long v_token,
+                        long long v_head, fa_elem dtype, void* stream) {
+  const fa_status st = check_batch(batch, false);
+  if (st != FA_OK) return st;
+  if (starts && !aligned(starts, 4)) return FA_ERR_INVALID_ARG;
+  return cache_rows(cache, batch, starts, nullptr, k, k_token, k_head, v, v_token, v_head, dtype, stream,
+                    false);
+}
+
+fa_status fa_fwd_paged_workspace_size(int batch, int total, int heads, int heads_k, int D,
+                                      long long max_keys, size_t* bytes) {
+  if (!bytes) return FA_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (!paged_sizes_ok(batch, total, heads, heads_k, D) || max_keys < 0) return FA_ERR_INVALID_ARG;
+  for (const bool fp8 : {false, true})  // whatever the cache holds
+    *bytes = std::max(
+        *bytes, paged_plan(batch, total, heads, heads_k, D, max_keys, fp8).total_bytes);
+  return FA_OK;
+}
+
+fa_status fa_fwd_paged(const void* q, long long q_token, long long q_head, void* o,
+                       long long o_token, long long o_head, float* lse, const fa_kv_pages* cache,
+                       const fa_ragged* batch, int heads, const fa_options* options, float scale,
+                       int causal, fa_elem dtype, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  PagedLaunch a{};
+  const fa_status st = paged_arguments(a, q, q_token, q_head, o, o_token, o_head, lse, cache, batch,
+                                       heads, options, scale, causal, dtype);
+  if (st != FA_OK || batch->total == 0) return st;
+  const PagedPlan plan = plan_of(a, a.r);
+  if (plan.total_bytes && (!aligned(workspace, 256) || workspace_bytes < plan.total_bytes))
+    return FA_ERR_INVALID_ARG;
+  if (!paged_device(a, cache, plan_many(plan))) return FA_ERR_CUDA;
+  return paged_launch(a, plan, workspace, static_cast<cudaStream_t>(stream));
+}
+
+fa_status fa_fwd_paged_shared_workspace_size(int batch, int total, int heads, int heads_k, int D,
+                                             long long max_keys, int groups, size_t* bytes) {
+  const fa_status st =
+      fa_fwd_paged_workspace_size(batch, total, heads, heads_k, D, max_keys, bytes);
+  if (st != FA_OK) return st;
+  if (groups < 0 || groups > batch) return FA_ERR_INVALID_ARG;
+  if (sharing_pays(batch, total, heads / heads_k, groups)) {
+    size_t parts = *bytes;
+    for (const bool fp8 : {false, true})
+      parts = std::max(
+          parts, paged_plan(groups, total, heads, heads_k, D, max_keys, fp8).total_bytes);
+    *bytes = shared_layout(batch, total, heads, D, groups).bytes + parts;
+  }
+  return FA_OK;
+}
+
+fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head, void* o,
+                              long long o_token, long long o_head, float* lse,
+                              const fa_kv_pages* cache, const fa_ragged* batch,
+                              const int* cu_groups, const int* shared_pages, int groups,
+                              int heads, float scale, fa_elem dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  PagedLaunch a{};
+  fa_status st = paged_arguments(a, q, q_token, q_head, o, o_token, o_head, lse, cache, batch,
+                                 heads, nullptr, scale, 1, dtype);
+  if (st != FA_OK) return st;
+  if (groups < 0 || groups > batch->batch ||
+      (groups > 0 && (!aligned(cu_groups, 4) || !aligned(shared_pages, 4))))
+    return FA_ERR_INVALID_ARG;
+  if (batch->total == 0) return FA_OK;
+  if (!sharing_pays(batch->batch, batch->total, a.group, groups))
+    return fa_fwd_paged(q, q_token, q_head, o, o_token, o_head, lse, cache, batch, heads, nullptr,
+                        scale, 1, dtype, workspace, workspace_bytes, stream);
+  const SharedLayout at = shared_layout(batch->batch, batch->total, heads, a.D, groups);
+  auto* base = static_cast<uint8_t*>(workspace);
+  const auto ints = [&](size_t offset) { return reinterpret_cast<int*>(base + offset); };
+  const auto floats = [&](size_t offset) { return reinterpret_cast<float*>(base + offset); };
+  // the groups as sequences: all of their rows see all of the shared keys
+  PagedLaunch first = a;
+  first.r = Ragged{a.r.table, a.r.table_stride, a.r.max_pages, ints(at.cu), ints(at.lens),
+                   groups,    a.r.total,        nullptr,       ints(at.rows)};
+  first.win_right = -1;
+  a.r.skip = ints(at.skip);
+  const PagedPlan plan1 = plan_of(first, first.r), plan2 = plan_of(a, a.r);
+  if (!aligned(workspace, 256) ||
+      workspace_bytes < at.bytes + std::max(plan1.total_bytes, plan2.total_bytes))
+    return FA_ERR_INVALID_ARG;
+  if (!paged_device(a, cache, plan_many(plan1) || plan_many(plan2))) return FA_ERR_CUDA;
+  first.sms = a.sms;
+  first.err = a.err;
+  first.map_k = a.map_k;
+  first.map_v = a.map_v;
+  first.map_q = a.map_q;
+  const auto s = static_cast<cudaStream_t>(stream);
+  Ragged whole = a.r;
+  whole.skip = nullptr;
+  if (launch_shared_setup(SharedSetup{whole, cu_groups, shared_pages, groups, a.page_log2,
+                                      ints(at.cu), ints(at.lens), ints(at.rows), ints(at.skip),
+                                      a.err},
+                          s) != cudaSuccess)
+    return FA_ERR_CUDA;
+  first.o32 = floats(at.o1);
+  first.lse = floats(at.lse1);
+  a.o32 = floats(at.o2);
+  a.lse = floats(at.lse2);
+  // one after the other: they share the workspace
+  if ((st = paged_launch(first, plan1, base + at.bytes, s)) != FA_OK) return st;
+  if ((st = paged_launch(a, plan2, base + at.bytes, s)) != FA_OK) return st;
+  const SharedJoin join{first.o32, a.o32,   first.lse,    a.lse,     ints(at.cu),
+                        groups,    a.r.cu,  a.r.batch,    a.r.total, a.heads,
+                        a.D,       a.elem,  o,            o_token,   o_head,
+                        lse};
+  return launch_shared_join(join, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

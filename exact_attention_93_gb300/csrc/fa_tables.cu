@@ -1,0 +1,293 @@
+// fa_tables.cu -- the tables of a decoder's step, from the sequences' lengths: new
+// pages taken from a stack of free ones, running sums, positions and slots; and the
+// pages' way back.
+//
+//   need_b = ceil((len_b + new_b) / page) - ceil(len_b / page)
+//   cu_b = sum of new before b,  first_b = sum of need before b
+//   page j of sequence b = free[count - 1 - first_b - (j - ceil(len_b / page))]
+//
+// What bounds it.  A few bytes a token: latency, two dependent loads and the sums
+// between them.  So one launch does it all: the CTAs of one cluster each take the
+// sums over all sequences (they fit shared memory, kChunk sequences at a time), meet
+// at the cluster's barrier, after which nobody reads the lengths any more, so that
+// they may be written in place, and write a share of the results each.  Which
+// sequence a row or a page belongs to is a binary search among sums in shared memory.
+// A page is taken from the free list where its rows need it; nobody waits for the
+// table to be written.
+//
+// All or nothing: the totals are known before the first write.
+#include <cooperative_groups.h>
+
+#include <climits>
+
+#include "fa_tables.h"
+#include "sm103_primitives.cuh"
+
+namespace fa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kTabThreads = 512, kTabWarps = kTabThreads / 32;
+constexpr int kPer = 4, kChunk = kTabThreads * kPer;  // sequences at a time
+
+struct ChunkSums {
+  int a[kChunk + 1], b[kChunk + 1];  // running sums, from the chunk's beginning
+};
+
+// Exclusive sums of two counts of each of the block's kChunk sequences (sequence
+// kPer * thread + i of the chunk): 32 bits, as the totals are known to fit.
+__device__ __forceinline__ void block_sums(const int (&x)[kPer], const int (&y)[kPer],
+                                           ChunkSums& out, int2 (&warps)[kTabWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int sx = 0, sy = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    sx += x[i];
+    sy += y[i];
+  }
+  int ux = sx, uy = sy;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int ox = __shfl_up_sync(0xffffffffu, ux, d), oy = __shfl_up_sync(0xffffffffu, uy, d);
+    if (lane >= d) {
+      ux += ox;
+      uy += oy;
+    }
+  }
+  if (lane == 31) warps[warp] = make_int2(ux, uy);
+  __syncthreads();
+  int px = ux - sx, py = uy - sy;
+#pragma unroll
+  for (int w = 0; w < kTabWarps; ++w)
+    if (w < warp) {
+      px += warps[w].x;
+      py += warps[w].y;
+    }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    out.a[threadIdx.x * kPer + i] = px;
+    out.b[threadIdx.x * kPer + i] = py;
+    px += x[i];
+    py += y[i];
+  }
+  if (threadIdx.x == kTabThreads - 1) {
+    out.a[kChunk] = px;
+    out.b[kChunk] = py;
+  }
+  __syncthreads();
+}
+
+// The last of sums[0 .. kChunk - 1] that is at most v (sums[0] = 0 <= v): the
+// sequence that element v belongs to, as those without elements share their sum with
+// the next.
+__device__ __forceinline__ int find(const int* sums, int v) {
+  int at = 0;
+#pragma unroll
+  for (int step = kChunk / 2; step > 0; step >>= 1)
+    if (sums[at + step] <= v) at += step;
+  return at;
+}
+
+struct Totals {
+  long long x, y;
+  int bad;
+};
+
+__device__ __forceinline__ Totals block_totals(Totals t, Totals (&warps)[kTabWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    t.x += __shfl_xor_sync(0xffffffffu, t.x, m);
+    t.y += __shfl_xor_sync(0xffffffffu, t.y, m);
+    t.bad |= __shfl_xor_sync(0xffffffffu, t.bad, m);
+  }
+  if (lane == 0) warps[warp] = t;
+  __syncthreads();
+  t = Totals{0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kTabWarps; ++w) {
+    t.x += warps[w].x;
+    t.y += warps[w].y;
+    t.bad |= warps[w].bad;
+  }
+  return t;
+}
+
+__device__ __forceinline__ int pages_of(int keys, int page_log2) {
+  return (keys + (1 << page_log2) - 1) >> page_log2;
+}
+
+__global__ void __launch_bounds__(kTabThreads)
+    reserve_kernel(const __grid_constant__ ReserveLaunch p) {
+  __shared__ ChunkSums sums;  // a: new tokens, b: new pages
+  __shared__ int len[kChunk];
+  __shared__ int2 warps[kTabWarps];
+  __shared__ Totals totals[kTabWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int ctas = static_cast<int>(cluster.num_blocks());
+  const int me = rank * kTabThreads + threadIdx.x, all = ctas * kTabThreads;
+  const int most = p.max_pages << p.page_log2;
+  const int count = *p.free_count;
+  // -- what is asked for, and whether it can be had
+  Totals t{0, 0, count < 0 || count > p.capacity};
+  for (int b = threadIdx.x; b < p.batch; b += kTabThreads) {
+    const int n = p.fresh[b], l = p.lens[b];
+    if (n < 0 || l < 0 || l > most || n > most - l) {
+      t.bad = 1;
+      continue;
+    }
+    t.x += n;
+    t.y += pages_of(l + n, p.page_log2) - pages_of(l, p.page_log2);
+  }
+  t = block_totals(t, totals);
+  if (t.x > p.total) t.bad = 1;
+  const int missing = t.bad ? -1 : static_cast<int>(max(0LL, t.y - count));
+  if (missing != 0) {
+    cluster.sync();
+    for (int b = me; b < p.batch; b += all) {
+      p.cu[b + 1] = 0;
+      if (p.lens_out != p.lens) p.lens_out[b] = p.lens[b];
+    }
+    for (int i = me; i < p.total; i += all) {
+      p.positions[i] = 0;
+      p.slots[i] = -1;
+    }
+    if (me == 0) {
+      p.cu[0] = 0;
+      *p.free_count_out = count;
+      *p.missing = missing;
+      if (t.bad) atomicExch(p.err, kDevErrBadIndex);
+    }
+    return;
+  }
+  // -- kChunk sequences at a time
+  int row0 = 0, taken = 0;  // rows and pages of the chunks before
+  for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
+    if (b0) __syncthreads();  // (the sums before have been read)
+    int n[kPer], need[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = threadIdx.x * kPer + i, b = b0 + j;
+      n[i] = b < p.batch ? p.fresh[b] : 0;
+      const int l = b < p.batch ? p.lens[b] : 0;
+      need[i] = pages_of(l + n[i], p.page_log2) - pages_of(l, p.page_log2);
+      len[j] = l;
+    }
+    block_sums(n, need, sums, warps);
+    cluster.sync();  // everyone has read this chunk's lengths
+    const int rows = sums.a[kChunk], pages = sums.b[kChunk];
+    const int top = count - 1 - taken;  // this chunk's first page in the free list
+    for (int j = me; j < min(kChunk, p.batch - b0); j += all) {
+      p.cu[b0 + j + 1] = row0 + sums.a[j + 1];
+      p.lens_out[b0 + j] = len[j] + sums.a[j + 1] - sums.a[j];
+    }
+    for (int m = me; m < pages; m += all) {
+      const int j = find(sums.b, m);
+      const int col = pages_of(len[j], p.page_log2) + m - sums.b[j];
+      p.table[(b0 + j) * p.table_stride + col] = p.free_pages[top - m];
+    }
+    for (int i = me; i < rows; i += all) {
+      const int j = find(sums.a, i);
+      const int pos = len[j] + i - sums.a[j], col = pos >> p.page_log2;
+      const int held = pages_of(len[j], p.page_log2);
+      const int page = col < held ? p.table[(b0 + j) * p.table_stride + col]
+                                  : p.free_pages[top - sums.b[j] - (col - held)];
+      p.positions[row0 + i] = pos;
+      p.slots[row0 + i] = (static_cast<long long>(page) << p.page_log2) +
+                          (pos & ((1 << p.page_log2) - 1));
+    }
+    row0 += rows;
+    taken += pages;
+  }
+  for (int i = row0 + me; i < p.total; i += all) {
+    p.positions[i] = 0;
+    p.slots[i] = -1;
+  }
+  if (me == 0) {
+    p.cu[0] = 0;
+    *p.free_count_out = count - taken;
+    *p.missing = 0;
+  }
+}
+
+__global__ void __launch_bounds__(kTabThreads)
+    release_kernel(const __grid_constant__ ReleaseLaunch p) {
+  __shared__ ChunkSums sums;  // b: pages given back
+  __shared__ int keep[kChunk];
+  __shared__ int2 warps[kTabWarps];
+  __shared__ Totals totals[kTabWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int ctas = static_cast<int>(cluster.num_blocks());
+  const int me = rank * kTabThreads + threadIdx.x, all = ctas * kTabThreads;
+  const int most = p.max_pages << p.page_log2;
+  const int count = *p.free_count;
+  Totals t{0, 0, count < 0 || count > p.capacity};
+  for (int b = threadIdx.x; b < p.batch; b += kTabThreads) {
+    if (!p.done[b]) continue;
+    const int l = p.lens[b], k = p.keep ? p.keep[b] : 0;
+    if (l < 0 || l > most || k < 0) t.bad = 1;
+    else t.y += max(0, pages_of(l, p.page_log2) - k);
+  }
+  t = block_totals(t, totals);
+  if (t.bad || t.y > p.capacity - count) {
+    if (me == 0) atomicExch(p.err, kDevErrBadIndex);
+    return;  // (the same in every CTA)
+  }
+  int given = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
+    if (b0) __syncthreads();
+    const int none[kPer] = {};
+    int give[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = threadIdx.x * kPer + i, b = b0 + j;
+      const bool mine = b < p.batch && p.done[b];
+      keep[j] = mine && p.keep ? p.keep[b] : 0;
+      give[i] = mine ? max(0, pages_of(p.lens[b], p.page_log2) - keep[j]) : 0;
+    }
+    block_sums(none, give, sums, warps);
+    cluster.sync();  // everyone has read this chunk's lengths, and the count
+    const int pages = sums.b[kChunk];
+    for (int m = me; m < pages; m += all) {
+      const int j = find(sums.b, m);
+      p.free_pages[count + given + m] =
+          p.table[(b0 + j) * p.table_stride + keep[j] + m - sums.b[j]];
+    }
+    for (int j = me; j < min(kChunk, p.batch - b0); j += all)
+      if (p.done[b0 + j]) p.lens[b0 + j] = 0;
+    given += pages;
+  }
+  if (me == 0) *p.free_count = count + given;
+}
+
+template <typename L>
+cudaError_t launch_cluster(void (*kern)(L), const L& a, long long items, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  const unsigned ctas = items <= 2 * kTabThreads ? 1 : 8;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kTabThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {ctas, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
+cudaError_t launch_reserve(const ReserveLaunch& a, cudaStream_t s) {
+  return launch_cluster(reserve_kernel, a, a.total, s);
+}
+
+cudaError_t launch_release(const ReleaseLaunch& a, cudaStream_t s) {
+  // (the pages are the kernel's to count: at most the table's)
+  const long long entries = static_cast<long long>(a.batch) * a.max_pages;
+  return launch_cluster(release_kernel, a, std::min<long long>(entries, a.capacity), s);
+}
+
+}  // namespace fa

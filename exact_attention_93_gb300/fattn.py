@@ -1,4 +1,5 @@
-"""ctypes binding to libfattn.so (include/fattn.h, include/fattn_cache.h).
+"""ctypes binding to libfattn.so (include/fattn.h, include/fattn_cache.h,
+include/fattn_decoder.h).
 
 Argument marshalling only: every step of the computation runs in the
 library's CUDA kernels.  The functions take torch CUDA tensors (PyTorch
@@ -17,6 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfattn.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "fattn.h")
 CACHE_HEADER = os.path.join(os.path.dirname(HERE), "include", "fattn_cache.h")
+DECODER_HEADER = os.path.join(os.path.dirname(HERE), "include", "fattn_decoder.h")
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
 FA_BF16, FA_FP16 = 0, 1
@@ -111,6 +113,18 @@ def load(path: str | None = None):
             "fa_cache_read": (i, [vp, vp, vp, vp, ll, ll, vp, ll, ll, i, vp]),
             "fa_fwd_paged_workspace_size": (i, [i, i, i, i, i, ll, ctypes.POINTER(sz)]),
             "fa_fwd_paged": (i, [vp, ll, ll, vp, ll, ll, vp, vp, vp, i, vp, f, i, i, vp, sz, vp]),
+            "fa_rotary_axes": (i, [vp, vp, i, i, i, i, vp, vp, f, i, i, i, vp]),
+            "fa_qk_norm_rotary": (i, [vp, vp, vp, vp, i, f, i, i, i, i, vp, vp, f, i, i, vp]),
+            "fa_qk_norm_rotary_bwd_workspace_size": (i, [i, ctypes.POINTER(sz)]),
+            "fa_qk_norm_rotary_bwd": (i, [vp, vp, vp, FaStrides, vp, FaStrides, vp, vp, vp, vp, i,
+                                          f, i, i, i, i, vp, vp, f, i, i, vp, sz, vp]),
+            "fa_cache_reserve": (i, [vp, vp]),
+            "fa_cache_release": (i, [vp, vp, vp, vp, ll, i, vp, i, vp, i, i, vp]),
+            "fa_cache_write": (i, [vp, vp, i, vp, ll, ll, vp, ll, ll, i, vp]),
+            "fa_fwd_paged_shared_workspace_size": (i, [i, i, i, i, i, ll, i,
+                                                       ctypes.POINTER(sz)]),
+            "fa_fwd_paged_shared": (i, [vp, ll, ll, vp, ll, ll, vp, vp, vp, vp, vp, i, i, f, i, vp,
+                                        sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -448,8 +462,8 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, deterministic=False,
 
 
 # --------------------------------------------------------------------------
-# include/fattn_cache.h: rotary positions, the paged cache, attention over it.
-# Its torch-facing calls (rotary.py, kvcache.py, attention.py) go through a small
+# include/fattn_cache.h and include/fattn_decoder.h: rotary positions, norms, the
+# paged cache, attention over it.  Their torch-facing calls (rotary.py, kvcache.py, attention.py) go through a small
 # native module, csrc/bind_torch.cpp; load() has the C entry points themselves.
 # --------------------------------------------------------------------------
 

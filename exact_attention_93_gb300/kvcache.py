@@ -9,14 +9,21 @@ uint8: values are code * 2 ** (e - 127).
 Sequences are packed along their tokens: rows cu_seqlens[b] .. cu_seqlens[b +
 1] - 1 of a (total, nheads, headdim) tensor belong to sequence b.
 attention.flash_attn_paged_func attends over what is cached here.
+
+kv_cache_reserve builds a step's tables on the GPU from how many tokens each
+sequence brings, taking pages from a stack of free ones; kv_cache_release gives
+pages back.
 """
 from __future__ import annotations
+
+from typing import NamedTuple
 
 import torch
 
 from . import fattn
 
-__all__ = ["alloc_kv_cache", "kv_cache_append", "kv_cache_read"]
+__all__ = ["CacheStep", "alloc_kv_cache", "kv_cache_append", "kv_cache_read", "kv_cache_release",
+           "kv_cache_reserve", "kv_cache_write"]
 
 _ELEMS = {torch.bfloat16: fattn.FA_ELEM_BF16, torch.float16: fattn.FA_ELEM_FP16}
 
@@ -73,3 +80,65 @@ def kv_cache_read(k_pages, v_pages, block_table, cu_seqlens, total, starts=None,
     if type(got) is int:
         fattn._check(got, "fa_cache_read")
     return got
+
+
+class CacheStep(NamedTuple):
+    """What kv_cache_reserve gives; all on the GPU."""
+    cu_seqlens: torch.Tensor  # int32 (batch + 1,): the packed rows of each sequence
+    seqlens: torch.Tensor     # int32 (batch,): lengths with the new tokens
+    positions: torch.Tensor   # int32 (total,): of each packed row, in its sequence
+    slots: torch.Tensor       # int64 (total,): page * page_size + place in the page
+    free_count: torch.Tensor  # int32 (1,): free pages left
+    missing: torch.Tensor     # int32 (1,): 0, or why nothing was taken
+
+
+def kv_cache_reserve(new_tokens, seqlens, block_table, free_pages, free_count, page_size, total,
+                     inplace=False):
+    """The tables of a step in which sequence b, seqlens[b] keys long, brings
+    new_tokens[b] more (int32 (batch,)): a CacheStep for rotary_func, kv_cache_append or
+    kv_cache_write, and attention, without a look at the lengths on the host.
+
+    Pages that a sequence lacks for its new tokens are taken from the end of
+    free_pages[:free_count] (int32; free_count int32 (1,)), in the order of the
+    sequences and of their keys, and written into block_table (int32 (batch,
+    max_pages)); its entries for pages that the sequences hold already are read, the
+    others left alone.  total is how many rows the packed tensors of the step have; rows
+    behind the last sequence get position 0 and slot -1.
+
+    All or nothing: if the free pages do not suffice, missing says how many more it
+    takes, and for bad lengths (negative, beyond the table, more new tokens than
+    total) or a free_count outside free_pages it is -1, with an error recorded as for
+    the other calls.  The table, seqlens and free_count then stay as they were, and
+    cu_seqlens is all zeros, so that what follows in the same step does nothing.
+
+    inplace=True writes the new lengths and the count over seqlens and free_count
+    instead of into new tensors.  (Without it, the call can be made again on the same
+    inputs, with the same result.)"""
+    got = fattn.bind().reserve(new_tokens, seqlens, block_table, free_pages, free_count, page_size,
+                               total, inplace)
+    if type(got) is int:
+        fattn._check(got, "fa_cache_reserve")
+    return CacheStep(*got)
+
+
+def kv_cache_release(done, seqlens, block_table, free_pages, free_count, page_size,
+                     keep_pages=None):
+    """Gives the pages of every sequence b with done[b] (bool or uint8 (batch,)) back to
+    the end of free_pages[:free_count], all in place: free_count grows, seqlens[b]
+    becomes 0, block_table stays.  keep_pages (int32 (batch,)): how many first pages of
+    each sequence are left out, because others share them, say.  Bad lengths, or more
+    pages than free_pages has room for, change nothing and are recorded as an error."""
+    status = fattn.bind().release(done, seqlens, block_table, free_pages, free_count, page_size,
+                                  keep_pages)
+    if status:
+        fattn._check(status, "fa_cache_release")
+
+
+def kv_cache_write(k, v, k_pages, v_pages, slots, k_exp=None, v_exp=None):
+    """kv_cache_append by slots: packed row i of k and v goes to slots[i] (int64 (total,),
+    page * page_size + place in the page; kv_cache_reserve's).  Rows with a negative
+    slot are not written, nor those beyond the cache, which are recorded as an error.
+    The slots of one call must be distinct."""
+    status = fattn.bind().write(k, v, k_pages, v_pages, slots, k_exp, v_exp)
+    if status:
+        fattn._check(status, "fa_cache_write")

@@ -4,7 +4,9 @@ attention.flash_attn_func, or before they go into a paged cache
 
 Pair i of the first rotary_dim elements of a head at position p is turned by
 the angle p * inv_freq[i].  rotary_frequencies gives inv_freq for the usual
-bases and for contexts stretched beyond the trained length.
+bases and for contexts stretched beyond the trained length.  Positions may have
+several axes (images, video), and qk_norm_rotary_func norms each head's row first, in
+the same pass.
 """
 from __future__ import annotations
 
@@ -14,7 +16,7 @@ import torch
 
 from . import fattn
 
-__all__ = ["rotary_frequencies", "rotary_func"]
+__all__ = ["qk_norm_rotary_func", "rotary_frequencies", "rotary_func"]
 
 
 def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_length=None,
@@ -54,7 +56,8 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     return freq.to(device), magnitude
 
 
-def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0, inplace=False):
+def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0, inplace=False,
+                sections=None, section_order="blocks"):
     """q and k (k may be None) with the first 2 * len(inv_freq) elements of
     every head turned by position, the others unchanged: (batch, seqlen,
     nheads, headdim) or packed (total, nheads, headdim) CUDA tensors of bf16,
@@ -66,6 +69,15 @@ def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0
     1, 2, ...).  Pairs are elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1)
     when interleaved.  Rotated elements are multiplied by magnitude.
 
+    sections gives positions several axes (1 to 8; row and column of a patch, or
+    time, row and column): sections[a] of the pairs are turned by their place along
+    axis a, and positions are (axes, seqlen) or (axes, batch, seqlen).  The
+    sections add up to len(inv_freq).  section_order "blocks": the first
+    sections[0] pairs go by axis 0, the next by axis 1, and so on; "turns": pairs
+    are dealt out to the axes in turns, an axis that has all of its own being passed
+    over.  inv_freq stays by pair: one spectrum over all pairs
+    (rotary_frequencies), or one for each axis, concatenated.
+
     Returns new tensors (q, k), or q alone when k is None.  Differentiable in q
     and k (the gradient is the rotation back), any number of times; tensors with
     a forward-mode tangent are refused.
@@ -74,7 +86,31 @@ def rotary_func(q, k, inv_freq, positions=None, interleaved=False, magnitude=1.0
     overlap.  (A backward pass can be captured into a CUDA graph while no eager
     graph of the same leaves is alive: torch ties their gradients to the stream
     of the graph that came first.)"""
-    out = fattn.bind().rotary(q, k, inv_freq, positions, magnitude, interleaved, inplace)
+    out = fattn.bind().rotary(q, k, inv_freq, positions, magnitude, interleaved, inplace, sections,
+                              section_order)
     if type(out) is int:
         fattn._check(out, "fa_rotary")
+    return out
+
+
+def qk_norm_rotary_func(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6,
+                        interleaved=False, magnitude=1.0, inplace=False, sections=None,
+                        section_order="blocks"):
+    """Queries and keys normed head by head and turned by position, in one pass:
+    rotary_func of q_weight * x / sqrt(mean(x ** 2) + eps), the mean over the
+    headdim elements of a head's row; elements that are not turned are normed all
+    the same.
+
+    q_weight and k_weight are (headdim,) tensors of q's type or float32, both of one
+    type, or None (ones).  Everything else as for rotary_func.  Sums and products
+    are fp32, values are rounded once; squares beyond fp32's range (magnitudes above
+    2 ** 60) are not provided for.
+
+    Differentiable once in q, k and the weights (fp32 sums in a fixed order: the same
+    call gives the same bits); only the inputs are kept for it.  Differentiating its
+    gradients raises, tensors with a forward-mode tangent are refused."""
+    out = fattn.bind().norm_rotary(q, k, q_weight, k_weight, inv_freq, positions, eps, magnitude,
+                                   interleaved, inplace, sections, section_order)
+    if type(out) is int:
+        fattn._check(out, "fa_qk_norm_rotary")
     return out
