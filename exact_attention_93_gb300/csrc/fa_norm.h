@@ -7,9 +7,10 @@
 
 namespace fa {
 
-// Blocks of the backward kernel per SM, at most; each leaves one row of D sums of the
-// weights' gradient in the workspace.
-constexpr int kNormBlocks = 8;
+// Blocks of the backward kernel per SM: as many as its registers allow at once, so that
+// all run from beginning to end.  Each leaves one row of D sums of the weights' gradient
+// in the workspace.
+constexpr int kNormBlocks = 3;
 
 struct NormLaunch {
   RotaryLaunch rot;       // forward: x -> y; backward: x, dx, and inverse
@@ -21,7 +22,8 @@ struct NormLaunch {
   RowStrides dys[2];
   void* dweight[2];  // of weight_elem; null: not wanted
   float* partial;    // [kNormBlocks * SMs][D]
-  int blocks[2];     // of queries, of keys (set at launch)
+  // of queries and of keys, set at launch: blocks, items of a token, heads of a lane group
+  int blocks[2], groups[2], per[2];
 };
 
 cudaError_t launch_norm_rotary(const NormLaunch& a, bool backward, cudaStream_t s);

@@ -32,11 +32,12 @@ constexpr int kRotThreads = 128;
 // Heads in flight per lane group: 128 bytes a lane.  (fp32: 28.0 us with four,
 // 26.2 with two, 1860 tokens of 72 heads of 128.)
 template <int kElem>
-constexpr int kUnroll = kElem == kElemFp32 ? 2 : 4;
+constexpr int kUnroll = kElem == kElemFp32 ? 3 : 5;
 
 template <int D, int kElem, bool kInterleaved, bool kAxes>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryLaunch p,
-                                                             int head_groups, long long n_items) {
+                                                             int head_groups, int per,
+                                                             long long n_items) {
   using T = typename std::conditional<kElem == kElemFp32, float, uint16_t>::type;
   using Angles = PairAngles<D, kAxes>;
   constexpr int kLanes = Angles::kLanes, kSlots = Angles::kSlots;
@@ -52,30 +53,32 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   const int all = p.heads[0] + p.heads[1];
   Angles angles;
   angles.load(table, sub, slot, rotates);
-  for (long long item = blockIdx.x * (kRotThreads / 32) + (threadIdx.x >> 5); item < n_items;
-       item += static_cast<long long>(gridDim.x) * (kRotThreads / 32)) {
-    const long long token = item / head_groups;
-    const int hg = static_cast<int>(item - token * head_groups);
-    const long long b = token / p.N, n = token - b * p.N;
-    const int h_first = hg * (kSlots * kUnroll<kElem>) + slot;
+  const T* const x0 = static_cast<const T*>(p.x[0]);
+  const T* const x1 = static_cast<const T*>(p.x[1]);
+  T* const y0 = static_cast<T*>(p.y[0]);
+  T* const y1 = static_cast<T*>(p.y[1]);
+  for (ItemWalk at(blockIdx.x * (kRotThreads / 32LL) + (threadIdx.x >> 5), n_items,
+                   gridDim.x * (kRotThreads / 32LL), head_groups, p.N);
+       at.valid(); at.next()) {
+    const int h_first = at.group * kSlots * per + slot;
+    const TokenRows<const T> xs(x0, p.xs[0], x1, p.xs[1], p.heads[0], at.b, at.n);
     Vec8<kElem> v0[kUnroll<kElem>], v1[kUnroll<kElem>];
 #pragma unroll
     for (int u = 0; u < kUnroll<kElem>; ++u) {
       const int h = h_first + u * kSlots;
-      if (h < all) {
-        const int w = h >= p.heads[0];
-        const T* x = static_cast<const T*>(p.x[w]) + b * p.xs[w].batch + n * p.xs[w].seq +
-                     (h - (w ? p.heads[0] : 0)) * p.xs[w].head;
+      if (u < per && h < all) {
+        const T* x = xs.row(h, h >= p.heads[0]);
         v0[u].load(x + e0);
         v1[u].load(x + e1);
       }
     }
     float sn[8], cs[8];
-    angles.at(p, b, n, sub, sn, cs);
+    angles.at(angles.place(p, at.b, at.n), p.magnitude, sub, sn, cs);
+    const TokenRows<T> ys(y0, p.ys[0], y1, p.ys[1], p.heads[0], at.b, at.n);
 #pragma unroll
     for (int u = 0; u < kUnroll<kElem>; ++u) {
       const int h = h_first + u * kSlots;
-      if (h >= all) continue;
+      if (u >= per || h >= all) continue;
       if (rotates) {
         float a[8], c[8];
         v0[u].get(a);
@@ -84,9 +87,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         v0[u].set(a);
         v1[u].set(c);
       }
-      const int w = h >= p.heads[0];
-      T* y = static_cast<T*>(p.y[w]) + b * p.ys[w].batch + n * p.ys[w].seq +
-             (h - (w ? p.heads[0] : 0)) * p.ys[w].head;
+      T* y = ys.row(h, h >= p.heads[0]);
       v0[u].store(y + e0);
       v1[u].store(y + e1);
     }
@@ -95,12 +96,11 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
 
 template <int D, int kElem, bool kInterleaved, bool kAxes>
 cudaError_t launch_rotary_t(const RotaryLaunch& a, cudaStream_t s) {
-  constexpr int kHeads = 32 / (D / 16) * kUnroll<kElem>;  // heads of one work item
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int groups = (a.heads[0] + a.heads[1] + kHeads - 1) / kHeads;
-  const long long items = static_cast<long long>(a.B) * a.N * groups;
+  const HeadSplit split(a.heads[0] + a.heads[1], 32 / (D / 16), kUnroll<kElem>);
+  const long long items = static_cast<long long>(a.B) * a.N * split.groups;
   const long long per_block = kRotThreads / 32;
   const long long blocks = (items + per_block - 1) / per_block;
   // Blocks stay for several items, as each first turns inv_freq into fractions of
@@ -108,7 +108,8 @@ cudaError_t launch_rotary_t(const RotaryLaunch& a, cudaStream_t s) {
   // 16 heads: 86.5 us with 16 blocks per SM, 80.5 with 64, 83.6 with one item each).
   const long long most = 64LL * sms;
   rotary_kernel<D, kElem, kInterleaved, kAxes>
-      <<<static_cast<unsigned>(blocks < most ? blocks : most), kRotThreads, 0, s>>>(a, groups, items);
+      <<<static_cast<unsigned>(blocks < most ? blocks : most), kRotThreads, 0, s>>>(a, split.groups, split.per,
+                                                                                 items);
   return cudaGetLastError();
 }
 

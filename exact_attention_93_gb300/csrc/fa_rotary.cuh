@@ -46,6 +46,10 @@ struct Vec8<kElemFp32> {
     a = *reinterpret_cast<const float4*>(p);
     b = *reinterpret_cast<const float4*>(p + 4);
   }
+  __device__ __forceinline__ void load(const uint4* p, const uint4* q) {  // the words apart
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(q);
+  }
   __device__ __forceinline__ void store(float* p) const {
     *reinterpret_cast<float4*>(p) = a;
     *reinterpret_cast<float4*>(p + 4) = b;
@@ -66,6 +70,7 @@ struct Vec8 {
   __device__ __forceinline__ void load(const uint16_t* p) {
     a = *reinterpret_cast<const uint4*>(p);
   }
+  __device__ __forceinline__ void load(const uint4* p, const uint4*) { a = *p; }
   __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = a; }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -79,6 +84,111 @@ struct Vec8 {
   __device__ __forceinline__ void set(const float (&f)[8]) {
     a = make_uint4(pack2<kElem == kElemBf16>(f[0], f[1]), pack2<kElem == kElemBf16>(f[2], f[3]),
                    pack2<kElem == kElemBf16>(f[4], f[5]), pack2<kElem == kElemBf16>(f[6], f[7]));
+  }
+};
+
+// A warp's items, `stride` apart: item i is heads of group i % groups of token i /
+// groups, which is token n of batch b.  Stepping on takes additions alone; two
+// divisions an item were a tenth of the kernels' instructions.
+struct ItemWalk {
+  long long left;  // items after this one
+  int b, n, group;
+  __device__ __forceinline__ ItemWalk(long long first, long long items, long long stride, int groups,
+                                      int N)
+      : groups_(groups), N_(N) {
+    left = first < items ? (items - 1 - first) / stride : -1;
+    const long long token = first / groups, step = stride / groups;
+    group = static_cast<int>(first - token * groups);
+    step_group_ = static_cast<int>(stride - step * groups);
+    b = static_cast<int>(token / N);
+    n = static_cast<int>(token - static_cast<long long>(b) * N);
+    step_b_ = static_cast<int>(step / N);
+    step_n_ = static_cast<int>(step - static_cast<long long>(step_b_) * N);
+  }
+  __device__ __forceinline__ bool valid() const { return left >= 0; }
+  __device__ __forceinline__ void next() {
+    --left;
+    group += step_group_;
+    n += step_n_;
+    b += step_b_;
+    if (group >= groups_) {
+      group -= groups_;
+      ++n;
+    }
+    if (n >= N_) {  // (n was below N, step_n_ is, and 1 was added at most: below 2 N)
+      n -= N_;
+      ++b;
+    }
+  }
+
+ private:
+  int groups_, N_, step_group_, step_n_, step_b_;
+};
+
+// The same where a warp keeps to one group of heads: tokens `stride` apart.
+struct TokenWalk {
+  long long left;  // tokens after this one
+  int b, n;
+  __device__ __forceinline__ TokenWalk(int first, long long tokens, int stride, int N) : N_(N) {
+    left = first < tokens ? (tokens - 1 - first) / stride : -1;
+    b = first / N;
+    n = first - b * N;
+    step_b_ = stride / N;
+    step_n_ = stride - step_b_ * N;
+  }
+  __device__ __forceinline__ bool valid() const { return left >= 0; }
+  // Whether it went into another batch beyond the stride's own.
+  __device__ __forceinline__ bool next() {
+    --left;
+    n += step_n_;
+    b += step_b_;
+    const bool wraps = n >= N_;
+    if (wraps) {
+      n -= N_;
+      ++b;
+    }
+    return wraps;
+  }
+  // What an operand's address grows by: with every token, and more when one wraps.
+  __device__ __forceinline__ long long step(const RowStrides& s) const {
+    return step_b_ * s.batch + step_n_ * s.seq;
+  }
+  __device__ __forceinline__ long long wrap(const RowStrides& s) const {
+    return s.batch - N_ * s.seq;
+  }
+
+ private:
+  int N_, step_n_, step_b_;
+};
+
+// The rows of one token in up to two operands, heads counted through both: what their
+// addresses have in common, once per token.  (The operands' own fields are read where
+// every lane reads the same: indexed by a lane's operand they cost a constant load each.)
+template <typename T>
+struct TokenRows {
+  T *q, *k;
+  long long q_head, k_head;
+  __device__ __forceinline__ TokenRows(T* x0, const RowStrides& s0, T* x1, const RowStrides& s1,
+                                       int heads0, int b, int n)
+      : q_head(s0.head), k_head(s1.head) {
+    q = x0 + b * s0.batch + n * s0.seq;
+    k = x1 + b * s1.batch + n * s1.seq - heads0 * s1.head;
+  }
+  __device__ __forceinline__ T* row(int h, bool second) const {
+    return (second ? k : q) + static_cast<unsigned long long>(second ? k_head : q_head) *
+                                  static_cast<unsigned>(h);
+  }
+};
+
+// How the heads of a token are dealt out: to `groups` items of a warp, in each of
+// which every lane group takes up to `per` heads, `slots` apart.  As few items as
+// kUnroll allows, since the angles are every item's own, and equally large ones.
+struct HeadSplit {
+  int groups, per;
+  HeadSplit(int heads, int slots, int unroll) {
+    const int each = (heads + slots - 1) / slots;
+    groups = (each + unroll - 1) / unroll;
+    per = groups ? (each + groups - 1) / groups : 0;
   }
 };
 
@@ -121,28 +231,34 @@ struct PairAngles {
       if constexpr (kAxes) axis[i] = rotates ? t.axis[pair] : 0;
     }
   }
-  // (the whole warp)
-  __device__ __forceinline__ void at(const RotaryLaunch& p, long long b, long long n, int sub,
-                                     float (&sn)[8], float (&cs)[8]) const {
+  // A token's positions, one for all pairs or one for each of the lane's share.
+  struct Place {
+    long long pos[kAxes ? kShare : 1];
+  };
+  __device__ __forceinline__ Place place(const RotaryLaunch& p, long long b, long long n) const {
     const long long first = b * p.position_bstride + n;
-    long long pos = n;
-    if constexpr (!kAxes) {
-      if (p.position_bits == 32)
-        pos = static_cast<const int*>(p.positions)[first];
-      else if (p.position_bits == 64)
-        pos = static_cast<const long long*>(p.positions)[first];
+    Place at;
+#pragma unroll
+    for (int i = 0; i < (kAxes ? kShare : 1); ++i) {
+      const long long o = kAxes ? first + axis[i] : first;
+      at.pos[i] = p.position_bits == 32   ? static_cast<const int*>(p.positions)[o]
+                  : p.position_bits == 64 ? static_cast<const long long*>(p.positions)[o]
+                                          : n;
     }
+    return at;
+  }
+  // (the whole warp)
+  __device__ __forceinline__ void at(const Place& place, float magnitude, int sub, float (&sn)[8],
+                                     float (&cs)[8]) const {
     float ms[kShare], mc[kShare];
 #pragma unroll
     for (int i = 0; i < kShare; ++i) {
-      if constexpr (kAxes)
-        pos = p.position_bits == 32 ? static_cast<const int*>(p.positions)[first + axis[i]]
-                                    : static_cast<const long long*>(p.positions)[first + axis[i]];
       // round the fraction to 32 bits; whole turns wrap away
-      const unsigned long long a = mine[i] * static_cast<unsigned long long>(pos) + 0x80000000ull;
+      const unsigned long long a =
+          mine[i] * static_cast<unsigned long long>(place.pos[kAxes ? i : 0]) + 0x80000000ull;
       sincos_turns(static_cast<uint32_t>(a >> 32), ms[i], mc[i]);
-      ms[i] *= p.magnitude;
-      mc[i] *= p.magnitude;
+      ms[i] *= magnitude;
+      mc[i] *= magnitude;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
