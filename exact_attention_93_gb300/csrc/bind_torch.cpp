@@ -724,6 +724,32 @@ void check_table(const at::Tensor& table, const at::Tensor& free_pages) {
        "free_pages must be a contiguous int32 tensor");
 }
 
+// Several one-dimensional results in one buffer, 16-byte aligned each.
+class Parts {
+ public:
+  size_t take(int64_t bytes) {
+    const size_t at = bytes_;
+    bytes_ += (static_cast<size_t>(bytes) + 15) / 16 * 16;
+    return at;
+  }
+  void allocate(const at::Tensor& like) {
+    buffer_ = at::empty({static_cast<int64_t>(bytes_)},
+                        like.options().requires_grad(false).dtype(at::kByte));
+  }
+  at::Tensor tensor(size_t at, int64_t n, at::ScalarType type) const {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(buffer_.storage()),
+                                                     buffer_.key_set(),
+                                                     c10::scalarTypeToTypeMeta(type));
+    impl->set_storage_offset(static_cast<int64_t>(at / c10::elementSize(type)));
+    impl->set_sizes_contiguous({n});
+    return at::Tensor(std::move(impl));
+  }
+
+ private:
+  at::Tensor buffer_;
+  size_t bytes_ = 0;
+};
+
 constexpr const char* kBatchInts =
     "new_tokens, seqlens and keep_pages must be contiguous int32 (batch,) tensors";
 constexpr const char* kOneInt = "free_count must be an int32 (1,) tensor";
@@ -752,11 +778,18 @@ PyObject* reserve(PyObject* const* a) {
   need(total >= 0 && total <= INT_MAX, "total must not be negative");
   const bool inplace = truth(a[7]);
   const Device device({&fresh, &lens, &table, &pages, &count});
-  const auto opt = fresh.options().requires_grad(false);
-  const at::Tensor cu = at::empty({batch + 1}, opt), positions = at::empty({total}, opt),
-                   slots = at::empty({total}, opt.dtype(at::kLong)), missing = at::empty({1}, opt),
-                   lens_out = inplace ? lens : at::empty({batch}, opt),
-                   count_out = inplace ? count : at::empty({1}, opt);
+  // One allocation for all results: each costs about as much as the kernel takes.
+  Parts parts;
+  const size_t at_slots = parts.take(8 * total), at_positions = parts.take(4 * total),
+               at_cu = parts.take(4 * (batch + 1)), at_lens = parts.take(4 * batch),
+               at_count = parts.take(4), at_missing = parts.take(4);
+  parts.allocate(fresh);
+  const at::Tensor cu = parts.tensor(at_cu, batch + 1, at::kInt),
+                   positions = parts.tensor(at_positions, total, at::kInt),
+                   slots = parts.tensor(at_slots, total, at::kLong),
+                   missing = parts.tensor(at_missing, 1, at::kInt),
+                   lens_out = inplace ? lens : parts.tensor(at_lens, batch, at::kInt),
+                   count_out = inplace ? count : parts.tensor(at_count, 1, at::kInt);
   r.block_table = table.data_ptr<int>();
   r.table_stride = batch > 1 ? table.stride(0) : std::max(table.size(1), table.stride(0));
   r.max_pages = static_cast<int>(table.size(1));

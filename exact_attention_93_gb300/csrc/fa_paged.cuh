@@ -353,6 +353,33 @@ __device__ __forceinline__ void store32(float* dst, const float (&o)[kN], float 
     *reinterpret_cast<float2*>(dst) = make_float2(o[0] * scale, o[1] * scale);
 }
 
+// A row's result from another part of the keys (PagedLaunch::add_o), loaded ahead of
+// its use: a lane's columns and the log-sum-exp in log2 units, -inf without one.
+template <int D, int kN>
+struct OtherPart {
+  float lse2, x[kN];
+  __device__ __forceinline__ OtherPart(const PagedLaunch& p, long long row, int head, int column) {
+    lse2 = p.add_lse[static_cast<long long>(head) * p.r.total + row] * 1.4426950408889634f;
+    const float* src = p.add_o + (row * p.heads + head) * D + column;
+    if constexpr (kN == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      x[0] = v.x; x[1] = v.y;
+    }
+  }
+  // Joined into the columns o, unnormalised under the maximum m (log2) and beside the sum l.
+  __device__ __forceinline__ void join(float (&o)[kN], float& m, float& l) const {
+    if (lse2 == -INFINITY) return;
+    const float top = fmaxf(m, lse2), a = ex2_approx(m - top), b = ex2_approx(lse2 - top);
+#pragma unroll
+    for (int e = 0; e < kN; ++e) o[e] = (l == 0.f ? 0.f : o[e] * a) + x[e] * b;
+    l = l * a + b;
+    m = top;
+  }
+};
+
 // A lane's columns of a finished row, in the type that the call asks for.
 template <int D, bool kBf16, int kN>
 __device__ __forceinline__ void store_row(const PagedLaunch& p, long long row, int head, int column,
@@ -364,104 +391,161 @@ __device__ __forceinline__ void store_row(const PagedLaunch& p, long long row, i
                    scale);
 }
 
-// Adds up the units that several CTAs worked on.  Block (c, y) takes a share of
-// the rows of the unit that CTA c began and did not finish; its pieces are CTA
-// c's second partial result and the first ones of the CTAs after it.  A warp's
-// lanes are the D columns of kRowsAtOnce rows, kPieces pieces of which it loads
-// side by side: the loads' latency is all this costs.  A long context over few
-// rows has up to a hundred pieces of a handful of rows, a prompt two or three
-// pieces of 256.
+// Adds up rows r0 .. r0 + kRows - 1 of the unit that CTA c began and did not finish
+// (fewer where the unit ends): its pieces are CTA c's second partial result and the
+// first ones of the CTAs after it.  A warp's lanes are the D columns of kRows rows,
+// kPieces pieces of which it loads side by side: the loads' latency is all this costs.
+template <int D, bool kBf16, int kRows, int kPieces>
+__device__ __forceinline__ void join_rows(const PagedLaunch& p, const JoinTask& task, int c, int r0) {
+  constexpr int kN = D / 32;
+  const int lane = threadIdx.x & 31;
+  float m[kRows], l[kRows] = {}, o[kRows][kN] = {};
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) m[q] = -INFINITY;
+  // up to 32 CTAs at a time: lane i knows whether CTA first + i had work
+  for (int first = c; first <= task.last; first += 32) {
+    uint32_t live = __ballot_sync(
+        0xffffffffu, first + lane <= task.last && p.tasks[min(first + lane, task.last)].rows >= 0);
+    while (live) {
+      float2 ml[kPieces][kRows];
+      float x[kPieces][kRows][kN];
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const bool some = live != 0;
+        const int i = first + (some ? __ffs(live) - 1 : 0);
+        live &= live - 1;
+        const long long at = (2LL * i + (i == c ? 1 : 0)) * p.block_rows + r0;
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+          const bool valid = some && r0 + q < task.rows;
+          ml[k][q] = valid ? p.part_ml[at + q] : make_float2(-INFINITY, 0.f);
+          // (of pieces without keys there is a maximum alone, -inf; what this
+          // finds there is not used)
+          const float* src = p.part_o + (at + q) * D + lane * kN;
+          if constexpr (kN == 4) {
+            const float4 v = valid ? *reinterpret_cast<const float4*>(src)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[k][q][0] = v.x; x[k][q][1] = v.y; x[k][q][2] = v.z; x[k][q][3] = v.w;
+          } else {
+            const float2 v = valid ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
+            x[k][q][0] = v.x; x[k][q][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+          const float m_new = fmaxf(m[q], ml[k][q].x);
+          const float ref = m_new == -INFINITY ? 0.f : m_new;
+          const float a = ex2_approx(m[q] - ref), b = ex2_approx(ml[k][q].x - ref);
+          m[q] = m_new;
+          l[q] = l[q] * a + ml[k][q].y * b;
+#pragma unroll
+          for (int e = 0; e < kN; ++e)
+            o[q][e] = o[q][e] * a + (ml[k][q].x == -INFINITY ? 0.f : x[k][q][e] * b);
+        }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) {
+    if (r0 + q >= task.rows) continue;
+    int token, head;
+    row_of(p, task.first_row, r0 + q, task.hk, token, head);
+    const long long row = task.start + token;
+    if constexpr (kRows == 1)  // (few rows)
+      if (p.add_o) OtherPart<D, kN>(p, row, head, lane * kN).join(o[q], m[q], l[q]);
+    store_row<D, kBf16>(p, row, head, lane * kN, o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
+    if (lane == 0)
+      p.lse[static_cast<long long>(head) * p.r.total + row] =
+          l[q] == 0.f ? -INFINITY : (m[q] + lg2_approx(l[q])) * kPagedLn2;
+  }
+}
+
+// Block (c, y) takes a share of the rows of CTA c's task.  A long context over few rows has
+// up to a hundred pieces of a handful of rows, a prompt two or three pieces of 256.
 constexpr int kJoinThreads = 64;
 
-template <int D, bool kBf16, int kRowsAtOnce, int kPieces>
+template <int D, bool kBf16, int kRows, int kPieces>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_join_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5;
   const JoinTask task = p.tasks[c];
-  constexpr int kN = D / 32, kWarps = kJoinThreads / 32;
-  const int step = gridDim.y * kWarps * kRowsAtOnce;
-  for (int r0 = (blockIdx.y * kWarps + warp) * kRowsAtOnce; r0 < task.rows; r0 += step) {
-    float m[kRowsAtOnce], l[kRowsAtOnce] = {}, o[kRowsAtOnce][kN] = {};
+  constexpr int kWarps = kJoinThreads / 32;
+  for (int r0 = (blockIdx.y * kWarps + warp) * kRows; r0 < task.rows;
+       r0 += gridDim.y * kWarps * kRows)
+    join_rows<D, kBf16, kRows, kPieces>(p, task, c, r0);
+}
+
+// Blocks of many rows where most CTAs have no task, as a few long units are cut into many
+// pieces: the rows of all tasks laid end to end and dealt out to the warps.  (us, like
+// this and by CTA, where nearly all of 9728 blocks find no work: 8 units of 256 rows
+// 13.5 and 23; four prompts, where they all find some, 10 more than by CTA.)
+constexpr int kJoinAllThreads = 128, kJoinTasks = 1024, kJoinAllRows = 1;
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kJoinAllThreads)
+    paged_join_all_kernel(const __grid_constant__ PagedLaunch p) {
+  pdl_wait_and_release();
+  __shared__ int begin[kJoinTasks + 1];  // first lot of kJoinAllRows rows of each CTA's task
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int all = 0;
+    for (int c0 = 0; c0 < p.sms; c0 += 8 * 32) {
+      int lots[8];  // loaded side by side
 #pragma unroll
-    for (int q = 0; q < kRowsAtOnce; ++q) m[q] = -INFINITY;
-    // up to 32 CTAs at a time: lane i knows whether CTA first + i had work
-    for (int first = c; first <= task.last; first += 32) {
-      uint32_t live = __ballot_sync(
-          0xffffffffu, first + lane <= task.last && p.tasks[min(first + lane, task.last)].rows >= 0);
-      while (live) {
-        float2 ml[kPieces][kRowsAtOnce];
-        float x[kPieces][kRowsAtOnce][kN];
+      for (int k = 0; k < 8; ++k) {
+        const int c = c0 + 32 * k + lane;
+        lots[k] = c < p.sms ? (max(0, p.tasks[c].rows) + kJoinAllRows - 1) / kJoinAllRows : 0;
+      }
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-          const bool some = live != 0;
-          const int i = first + (some ? __ffs(live) - 1 : 0);
-          live &= live - 1;
-          const long long at = (2LL * i + (i == c ? 1 : 0)) * p.block_rows + r0;
+      for (int k = 0; k < 8; ++k) {
+        const int c = c0 + 32 * k + lane;
+        int upto = lots[k];
 #pragma unroll
-          for (int q = 0; q < kRowsAtOnce; ++q) {
-            const bool valid = some && r0 + q < task.rows;
-            ml[k][q] = valid ? p.part_ml[at + q] : make_float2(-INFINITY, 0.f);
-            // (of pieces without keys there is a maximum alone, -inf; what this
-            // finds there is not used)
-            const float* src = p.part_o + (at + q) * D + lane * kN;
-            if constexpr (kN == 4) {
-              const float4 v = valid ? *reinterpret_cast<const float4*>(src)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-              x[k][q][0] = v.x; x[k][q][1] = v.y; x[k][q][2] = v.z; x[k][q][3] = v.w;
-            } else {
-              const float2 v =
-                  valid ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
-              x[k][q][0] = v.x; x[k][q][1] = v.y;
-            }
-          }
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += v;
         }
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k)
-#pragma unroll
-          for (int q = 0; q < kRowsAtOnce; ++q) {
-            const float m_new = fmaxf(m[q], ml[k][q].x);
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
-            const float a = ex2_approx(m[q] - ref), b = ex2_approx(ml[k][q].x - ref);
-            m[q] = m_new;
-            l[q] = l[q] * a + ml[k][q].y * b;
-#pragma unroll
-            for (int e = 0; e < kN; ++e)
-              o[q][e] = o[q][e] * a + (ml[k][q].x == -INFINITY ? 0.f : x[k][q][e] * b);
-          }
+        if (c < p.sms) begin[c] = all + upto - lots[k];
+        all += __shfl_sync(0xffffffffu, upto, 31);
       }
     }
-#pragma unroll
-    for (int q = 0; q < kRowsAtOnce; ++q) {
-      if (r0 + q >= task.rows) continue;
-      int token, head;
-      row_of(p, task.first_row, r0 + q, task.hk, token, head);
-      const long long row = task.start + token;
-      store_row<D, kBf16>(p, row, head, lane * kN, o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
-      if (lane == 0)
-        p.lse[static_cast<long long>(head) * p.r.total + row] =
-            l[q] == 0.f ? -INFINITY : (m[q] + lg2_approx(l[q])) * kPagedLn2;
+    if (lane == 0) begin[p.sms] = all;
+  }
+  __syncthreads();
+  const int all = begin[p.sms], step = gridDim.x * (kJoinAllThreads / 32);
+  for (int i = blockIdx.x * (kJoinAllThreads / 32) + warp; i < all; i += step) {
+    int lo = 0, hi = p.sms;  // the last task that begins at i or before
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (begin[mid] <= i) lo = mid;
+      else hi = mid;
     }
+    const JoinTask task = p.tasks[lo];
+    join_rows<D, kBf16, kJoinAllRows, 8>(p, task, lo, (i - begin[lo]) * kJoinAllRows);
   }
 }
 
 template <int D, bool kBf16>
 cudaError_t launch_join(const PagedLaunch& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  // few rows in a block: many pieces at a time; many rows: some of each
-  const bool few = a.block_rows <= 16;
+  const bool few = a.block_rows <= 16, all = !few && a.few_joins && a.sms <= kJoinTasks;
   const int rows = kJoinThreads / 32 * (few ? 1 : 2);
-  cfg.gridDim = dim3(static_cast<unsigned>(a.sms),
-                     static_cast<unsigned>((a.block_rows + rows - 1) / rows));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = all ? dim3(static_cast<unsigned>(8 * a.sms))
+                    : dim3(static_cast<unsigned>(a.sms),
+                           static_cast<unsigned>((a.block_rows + rows - 1) / rows));
+  cfg.blockDim = dim3(all ? kJoinAllThreads : kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, 1, 8>, a)
-             : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, 2, 2>, a);
+  return all   ? cudaLaunchKernelEx(&cfg, paged_join_all_kernel<D, kBf16>, a)
+         : few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, 1, 8>, a)
+               : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, 2, 2>, a);
 }
 
 }  // namespace fa

@@ -49,12 +49,18 @@
 // already with eight.  One context of 1000 keys 9 to 12 us, by the machine, of 4000 12
 // to 15, of 32000 30 to 37: launch, the look at the batch, and the joining of the
 // pieces.
+#include <type_traits>
+
 #include "fa_paged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"
 
 namespace fa {
 namespace {
+
+struct NoPart {
+  __device__ __forceinline__ NoPart(const PagedLaunch&, long long, int, int) {}
+};
 
 constexpr int kConsumers = 8;                       // warps
 constexpr int kProducers = 4;                       // K and V of either group
@@ -142,10 +148,13 @@ __device__ __forceinline__ float exp2_field(int n) {
   return __uint_as_float(static_cast<uint32_t>(min(max(n, 0), 254)) << 23);
 }
 
-template <int D, bool kFp8, bool kBf16, int NB>
+template <int D, bool kFp8, bool kBf16, int NB, bool kAdd>
 __global__ void __maxnreg__(kFewRegs)
     paged_few_kernel(const __grid_constant__ PagedLaunch p) {
-  pdl_wait_and_release();
+  // Joining another part's results, the kernels before this one are that part's: they wrote
+  // none of the lengths, and started when all earlier work had ended.  So a place is found
+  // while they end.
+  if constexpr (!kAdd) pdl_wait_and_release();
   using Smem = FewSmem<D, kFp8, NB>;
   constexpr int kRows = 8 * NB, kRowBytes = Smem::kRowBytes;
   constexpr int kSlots = Smem::kSlots, kRing = Smem::kRing;
@@ -159,6 +168,7 @@ __global__ void __maxnreg__(kFewRegs)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     const Place at = warp_place<false>(p, gridDim.x, blockIdx.x);
+    if constexpr (kAdd) pdl_wait_and_release();
     if (lane == 0) {
       s.place = at;
       if (at.left == 0 && !p.whole) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
@@ -173,6 +183,9 @@ __global__ void __maxnreg__(kFewRegs)
     fence_barrier_init();
   }
   __syncthreads();
+  if constexpr (kAdd) {
+    if (warp != 0) pdl_wait_and_release();
+  }
   volatile int* abort_flag = &s.abort_flag;
   WorkWalk<false> walk(s.place);
   Piece x;
@@ -672,6 +685,12 @@ __global__ void __maxnreg__(kFewRegs)
         const int r = nb * 8 + warp;
         constexpr int kN = D / 32;
         float top = -INFINITY, sum = 0.f, out[kN] = {};
+        int token, head;
+        row_of(p, row0, min(r, x.rows - 1), x.hk, token, head);
+        const long long row = seq.start + token;
+        // (loaded here, ahead of the barriers; of rows behind the block's, its last one's)
+        [[maybe_unused]] typename std::conditional<kAdd, OtherPart<D, kN>, NoPart>::type other(
+            p, row, head, lane * kN);
         [[maybe_unused]] int vtop = 0;
 #pragma unroll
         for (int gr = 0; gr < kGroups; ++gr) {
@@ -723,13 +742,11 @@ __global__ void __maxnreg__(kFewRegs)
         }
         if (r < x.rows) {
           if (x.whole) {
-            int token, head;
-            row_of(p, row0, r, x.hk, token, head);
-            const long long row = seq.start + token;
             if (sum == 0.f) {  // no key: zeros, also where other rows saw a NaN value
 #pragma unroll
               for (int e = 0; e < kN; ++e) out[e] = 0.f;
             }
+            if constexpr (kAdd) other.join(out, top, sum);
             store_row<D, kBf16>(p, row, head, lane * kN, out, sum == 0.f ? 0.f : 1.f / sum);
             if (lane == 0)
               p.lse[static_cast<long long>(head) * p.r.total + row] =
@@ -747,9 +764,9 @@ __global__ void __maxnreg__(kFewRegs)
   }
 }
 
-template <int D, bool kFp8, bool kBf16, int NB>
+template <int D, bool kFp8, bool kBf16, int NB, bool kAdd>
 cudaError_t launch_few_t(const PagedLaunch& a, cudaStream_t s) {
-  auto kern = paged_few_kernel<D, kFp8, kBf16, NB>;
+  auto kern = paged_few_kernel<D, kFp8, kBf16, NB, kAdd>;
   const int smem = static_cast<int>(sizeof(FewSmem<D, kFp8, NB>)) + 1024;
   static_assert(sizeof(FewSmem<D, kFp8, NB>) + 1024 <= 232448, "shared memory of one CTA");
   static AttrCache configured;
@@ -761,8 +778,11 @@ cudaError_t launch_few_t(const PagedLaunch& a, cudaStream_t s) {
 
 template <int D, bool kFp8, bool kBf16>
 cudaError_t launch_few_n(const PagedLaunch& a, cudaStream_t s) {
-  return a.block_rows == 8 ? launch_few_t<D, kFp8, kBf16, 1>(a, s)
-                           : launch_few_t<D, kFp8, kBf16, 2>(a, s);
+  if (a.add_o)
+    return a.block_rows == 8 ? launch_few_t<D, kFp8, kBf16, 1, true>(a, s)
+                             : launch_few_t<D, kFp8, kBf16, 2, true>(a, s);
+  return a.block_rows == 8 ? launch_few_t<D, kFp8, kBf16, 1, false>(a, s)
+                           : launch_few_t<D, kFp8, kBf16, 2, false>(a, s);
 }
 
 template <int D>

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   T* const y0 = static_cast<T*>(p.y[0]);
   T* const y1 = static_cast<T*>(p.y[1]);
   for (ItemWalk at(blockIdx.x * (kRotThreads / 32LL) + (threadIdx.x >> 5), n_items,
-                   gridDim.x * (kRotThreads / 32LL), head_groups, p.N);
+                   static_cast<int>(gridDim.x) * (kRotThreads / 32), head_groups, p.N);
        at.valid(); at.next()) {
     const int h_first = at.group * kSlots * per + slot;
     const TokenRows<const T> xs(x0, p.xs[0], x1, p.xs[1], p.heads[0], at.b, at.n);

@@ -87,27 +87,34 @@ struct Vec8 {
   }
 };
 
+// a / b for a >= 0, b > 0; a 64-bit division is a long instruction sequence.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // A warp's items, `stride` apart: item i is heads of group i % groups of token i /
 // groups, which is token n of batch b.  Stepping on takes additions alone; two
 // divisions an item were a tenth of the kernels' instructions.
 struct ItemWalk {
-  long long left;  // items after this one
   int b, n, group;
-  __device__ __forceinline__ ItemWalk(long long first, long long items, long long stride, int groups,
-                                      int N)
-      : groups_(groups), N_(N) {
-    left = first < items ? (items - 1 - first) / stride : -1;
-    const long long token = first / groups, step = stride / groups;
+  __device__ __forceinline__ ItemWalk(long long first, long long items, int stride, int groups, int N)
+      : at_(first), items_(items), stride_(stride), groups_(groups), N_(N) {
+    const long long token = groups > 1 ? quotient(first, groups) : first;
     group = static_cast<int>(first - token * groups);
-    step_group_ = static_cast<int>(stride - step * groups);
-    b = static_cast<int>(token / N);
+    b = static_cast<int>(quotient(token, N));
     n = static_cast<int>(token - static_cast<long long>(b) * N);
-    step_b_ = static_cast<int>(step / N);
-    step_n_ = static_cast<int>(step - static_cast<long long>(step_b_) * N);
+    step_group_ = step_b_ = step_n_ = 0;
+    if (first + stride < items) {  // (calls of few tokens have one item a warp)
+      const int step = stride / groups;
+      step_group_ = stride - step * groups;
+      step_b_ = step / N;
+      step_n_ = step - step_b_ * N;
+    }
   }
-  __device__ __forceinline__ bool valid() const { return left >= 0; }
+  __device__ __forceinline__ bool valid() const { return at_ < items_; }
   __device__ __forceinline__ void next() {
-    --left;
+    at_ += stride_;
     group += step_group_;
     n += step_n_;
     b += step_b_;
@@ -122,24 +129,24 @@ struct ItemWalk {
   }
 
  private:
-  int groups_, N_, step_group_, step_n_, step_b_;
+  long long at_, items_;
+  int stride_, groups_, N_, step_group_, step_n_, step_b_;
 };
 
 // The same where a warp keeps to one group of heads: tokens `stride` apart.
 struct TokenWalk {
-  long long left;  // tokens after this one
   int b, n;
-  __device__ __forceinline__ TokenWalk(int first, long long tokens, int stride, int N) : N_(N) {
-    left = first < tokens ? (tokens - 1 - first) / stride : -1;
+  __device__ __forceinline__ TokenWalk(int first, long long tokens, int stride, int N)
+      : at_(first), tokens_(tokens), stride_(stride), N_(N) {
     b = first / N;
     n = first - b * N;
     step_b_ = stride / N;
     step_n_ = stride - step_b_ * N;
   }
-  __device__ __forceinline__ bool valid() const { return left >= 0; }
+  __device__ __forceinline__ bool valid() const { return at_ < tokens_; }
   // Whether it went into another batch beyond the stride's own.
   __device__ __forceinline__ bool next() {
-    --left;
+    at_ += stride_;
     n += step_n_;
     b += step_b_;
     const bool wraps = n >= N_;
@@ -158,7 +165,8 @@ struct TokenWalk {
   }
 
  private:
-  int N_, step_n_, step_b_;
+  long long at_, tokens_;
+  int stride_, N_, step_n_, step_b_;
 };
 
 // The rows of one token in up to two operands, heads counted through both: what their

@@ -84,6 +84,9 @@ struct PagedLaunch {
   long long o_token, o_head;
   float* lse;  // [heads][total]
   float* o32;  // or null: O goes here in fp32, [total][heads][D], instead of o
+  // or null, few rows: results of another part of the keys to join with, as o32 and lse
+  // (-inf where a row has none)
+  const float *add_o, *add_lse;
   const uint8_t *k_exp, *v_exp;
   Ragged r;
   int heads, heads_k, group, D;
@@ -96,6 +99,7 @@ struct PagedLaunch {
   int block_rows;   // query rows of a unit
   int min_rows, max_rows;  // sequences of other numbers of rows (tokens x group) are left out
   int whole;        // units are not cut
+  int few_joins;    // few rows are left to be joined
   // unless whole:
   float* part_o;    // [2 sms][block_rows][D]
   float2* part_ml;  // [2 sms][block_rows]: maximum, sum
@@ -116,7 +120,8 @@ cudaError_t launch_paged_few(const PagedLaunch& a, cudaStream_t s);
 struct SharedSetup {
   Ragged r;
   const int *cu_groups, *shared_pages;
-  int groups, page_log2;
+  int groups, page_log2, heads;
+  float* lse;  // [heads][total] of the shared part: -inf for rows of no group
   int *cu, *lens, *rows;  // of the groups as sequences: [groups + 1], [groups], [groups]
   int* skip;              // [batch]
   uint32_t* err;
@@ -124,8 +129,6 @@ struct SharedSetup {
 
 struct SharedJoin {
   const float *o1, *o2, *lse1, *lse2;  // the shared part, the own part
-  const int* cu_groups;                // packed rows of the groups, [groups + 1]
-  int groups;
   const int* cu;
   int batch, total, heads, D, elem;
   void* o;

@@ -193,6 +193,9 @@ bool paged_device(PagedLaunch& a, const fa_kv_pages* cache, bool many) {
                       static_cast<uint32_t>(kTile / a.group));
 }
 
+// All rows of all units are at most this share of what the CTAs' tasks could hold.
+constexpr int kFewJoins = 4;
+
 fa_status paged_launch(PagedLaunch a, const PagedPlan& plan, void* workspace, cudaStream_t s) {
   if (plan.total_bytes) {
     auto* base = static_cast<uint8_t*>(workspace);
@@ -210,6 +213,9 @@ fa_status paged_launch(PagedLaunch a, const PagedPlan& plan, void* workspace, cu
         a.win_left < 0 || a.win_right < 0
             ? kMaxRows
             : static_cast<long long>(a.win_left) + a.win_right + a.block_rows / a.group + kTile;
+    // rows of the units that can be cut, one per CTA at most, for sequences of the mean length
+    const double rows = static_cast<double>(a.r.total) * a.group;
+    a.few_joins = rows * a.heads_k * kFewJoins <= static_cast<double>(a.sms) * a.block_rows;
     a.whole = part.whole || unit_keys <= (part.many ? kWholeKeysMany : kWholeKeysFew);
     const auto launch = part.many ? launch_paged_many : launch_paged_few;
     if (launch(a, s) != cudaSuccess) return FA_ERR_CUDA;
@@ -217,12 +223,59 @@ fa_status paged_launch(PagedLaunch a, const PagedPlan& plan, void* workspace, cu
   return FA_OK;
 }
 
-// Whether walking the shared keys once per group is worth two parts and their joining,
-// by the rows (tokens x group) of a sequence.
-constexpr int kSharedRows = 128;
+// Whether walking the shared keys once per group is worth two parts and their joining.
+// Sequences that share pages find one another's in L2, so that the whole cost of not
+// sharing is the key tiles that each walks again; but where the groups' keys together do
+// not stay in L2, HBM's reads are.  The lengths are on the device: the table's width
+// stands for the prefix, and a table far wider than that leads to sharing, as asked for.
+//
+// The model, in us: without sharing kOwnTile for each of a CTA's tiles; with it kSetOut for
+// the kernels before the own part (which costs the same either way) and kSharedTile for
+// each tile of up to 256 rows.  Measured, not shared and shared, 32 / 8 heads of 128, 200
+// keys of their own: 64 single tokens, prefix of 1024 keys 36 and 47, 4096 69 and 61, 16384
+// 218 and 72 (e4m3 38 and 53, 86 and 61, 272 and 76); 16 single tokens, 4096 24 and 41, 16384
+// 66 and 55; 8 groups of 8, 1024 37 and 48, 4096 121 and 70; 32 groups of 2, 4096 172 and
+// 114; 64 x 8 tokens, 4096 187 and 102, x 16 186 and 131, x 32 189 and 184; 16 x 16 tokens,
+// 4096 66 and 73.  12 / 4 heads of 64, 24 x 4 tokens, 6000 keys 31 and 41.
+struct SharedCost {
+  double own_tile, shared_tile, set_out;
+};
 
-bool sharing_pays(int batch, int total, int group, int groups) {
-  return groups > 0 && static_cast<double>(total) * group / batch <= kSharedRows;
+SharedCost shared_cost(double rows, double group_rows, int D, bool fp8) {
+  SharedCost c{};
+  const double small = D == 64 ? 0.7 : 1.0;
+  c.own_tile = small * (rows <= 8         ? (fp8 ? 0.58 : 0.46)
+                        : rows <= kFewRows ? (fp8 ? 0.92 : 0.7)
+                                           : (fp8 ? 1.7 : 1.43));
+  if (group_rows <= kFewRows) {
+    c.shared_tile = small * (fp8 ? 0.92 : 0.7);
+    c.set_out = 12;
+  } else {
+    c.shared_tile = small * (fp8 ? 3.4 : 2.8);
+    c.set_out = 30;
+  }
+  if (rows > kFewRows) c.set_out += 12;  // the own part does not join them itself
+  return c;
+}
+
+constexpr double kSharedRows = 64;  // rows (tokens x group) of a sequence
+constexpr double kCopyBytesPerUs = 6.7e6, kStaysInL2 = 64e6;
+
+bool sharing_pays(int batch, int total, int heads, int heads_k, int D, long long max_keys,
+                  int groups, bool fp8) {
+  const int group = heads / heads_k;
+  const double rows = static_cast<double>(total) * group / batch;
+  if (groups < 1 || groups >= batch || rows > kSharedRows) return false;
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) sms = 160;  // no device: sizes for the checks alone
+  const double group_rows = rows * batch / groups;
+  const SharedCost c = shared_cost(rows, group_rows, D, fp8);
+  const double tiles = std::ceil(static_cast<double>(max_keys) / kTile) * heads_k / sms;
+  const double key_bytes = static_cast<double>(max_keys) * heads_k * D * (fp8 ? 2 : 4);
+  const double hbm = groups * key_bytes > kStaysInL2 ? key_bytes / kCopyBytesPerUs : 0;
+  const double blocks = group_rows <= kFewRows ? 1 : std::ceil(group_rows / (2 * kTile));
+  return std::max(c.own_tile * tiles, hbm) * batch >
+         c.set_out + std::max(c.shared_tile * tiles * blocks, hbm) * groups;
 }
 
 // The workspace of attention over shared prefixes, in front of the kernels' own.
@@ -326,12 +379,12 @@ fa_status fa_fwd_paged_shared_workspace_size(int batch, int total, int heads, in
       fa_fwd_paged_workspace_size(batch, total, heads, heads_k, D, max_keys, bytes);
   if (st != FA_OK) return st;
   if (groups < 0 || groups > batch) return FA_ERR_INVALID_ARG;
-  if (sharing_pays(batch, total, heads / heads_k, groups)) {
-    size_t parts = *bytes;
-    for (const bool fp8 : {false, true})
-      parts = std::max(
-          parts, paged_plan(groups, total, heads, heads_k, D, max_keys, fp8).total_bytes);
-    *bytes = shared_layout(batch, total, heads, D, groups).bytes + parts;
+  const size_t plain = *bytes;
+  for (const bool fp8 : {false, true}) {  // whatever the cache holds
+    if (!sharing_pays(batch, total, heads, heads_k, D, max_keys, groups, fp8)) continue;
+    const size_t parts = std::max(
+        plain, paged_plan(groups, total, heads, heads_k, D, max_keys, fp8).total_bytes);
+    *bytes = std::max(*bytes, shared_layout(batch, total, heads, D, groups).bytes + parts);
   }
   return FA_OK;
 }
@@ -350,7 +403,9 @@ fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head
       (groups > 0 && (!aligned(cu_groups, 4) || !aligned(shared_pages, 4))))
     return FA_ERR_INVALID_ARG;
   if (batch->total == 0) return FA_OK;
-  if (!sharing_pays(batch->batch, batch->total, a.group, groups))
+  if (!sharing_pays(batch->batch, batch->total, heads, a.heads_k, a.D,
+                    static_cast<long long>(a.r.max_pages) * a.page_size, groups,
+                    a.cache_elem == kElemE4m3))
     return fa_fwd_paged(q, q_token, q_head, o, o_token, o_head, lse, cache, batch, heads, nullptr,
                         scale, 1, dtype, workspace, workspace_bytes, stream);
   const SharedLayout at = shared_layout(batch->batch, batch->total, heads, a.D, groups);
@@ -376,22 +431,25 @@ fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head
   const auto s = static_cast<cudaStream_t>(stream);
   Ragged whole = a.r;
   whole.skip = nullptr;
-  if (launch_shared_setup(SharedSetup{whole, cu_groups, shared_pages, groups, a.page_log2,
-                                      ints(at.cu), ints(at.lens), ints(at.rows), ints(at.skip),
-                                      a.err},
+  if (launch_shared_setup(SharedSetup{whole, cu_groups, shared_pages, groups, a.page_log2, heads,
+                                      floats(at.lse1), ints(at.cu), ints(at.lens), ints(at.rows),
+                                      ints(at.skip), a.err},
                           s) != cudaSuccess)
     return FA_ERR_CUDA;
   first.o32 = floats(at.o1);
   first.lse = floats(at.lse1);
-  a.o32 = floats(at.o2);
-  a.lse = floats(at.lse2);
   // one after the other: they share the workspace
   if ((st = paged_launch(first, plan1, base + at.bytes, s)) != FA_OK) return st;
+  if (!plan_many(plan2)) {  // few rows: the own part's kernels join the two
+    a.add_o = first.o32;
+    a.add_lse = first.lse;
+    return paged_launch(a, plan2, base + at.bytes, s);
+  }
+  a.o32 = floats(at.o2);
+  a.lse = floats(at.lse2);
   if ((st = paged_launch(a, plan2, base + at.bytes, s)) != FA_OK) return st;
-  const SharedJoin join{first.o32, a.o32,   first.lse,    a.lse,     ints(at.cu),
-                        groups,    a.r.cu,  a.r.batch,    a.r.total, a.heads,
-                        a.D,       a.elem,  o,            o_token,   o_head,
-                        lse};
+  const SharedJoin join{first.o32, a.o32, first.lse, a.lse, a.r.cu,  a.r.batch, a.r.total,
+                        a.heads,   a.D,   a.elem,    o,     o_token, o_head,    lse};
   return launch_shared_join(join, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -28,17 +28,21 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kTabThreads = 512, kTabWarps = kTabThreads / 32;
-constexpr int kPer = 4, kChunk = kTabThreads * kPer;  // sequences at a time
+// One CTA for a step of few tokens, a cluster of eight larger ones for prompts.
+constexpr int kFewThreads = 512, kManyThreads = 1024, kManyCtas = 8;
+constexpr int kChunk = 2048;  // sequences at a time
 
 struct ChunkSums {
   int a[kChunk + 1], b[kChunk + 1];  // running sums, from the chunk's beginning
 };
 
-// Exclusive sums of two counts of each of the block's kChunk sequences (sequence
-// kPer * thread + i of the chunk): 32 bits, as the totals are known to fit.
-__device__ __forceinline__ void block_sums(const int (&x)[kPer], const int (&y)[kPer],
-                                           ChunkSums& out, int2 (&warps)[kTabWarps]) {
+// Exclusive sums of two counts of each of the block's kChunk sequences, kPer of them a
+// thread's: 32 bits, as the totals are known to fit.
+template <int kThreads>
+__device__ __forceinline__ void block_sums(const int (&x)[kChunk / kThreads],
+                                           const int (&y)[kChunk / kThreads], ChunkSums& out,
+                                           int2 (&warps)[kThreads / 32]) {
+  constexpr int kPer = kChunk / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int sx = 0, sy = 0;
 #pragma unroll
@@ -59,7 +63,7 @@ __device__ __forceinline__ void block_sums(const int (&x)[kPer], const int (&y)[
   __syncthreads();
   int px = ux - sx, py = uy - sy;
 #pragma unroll
-  for (int w = 0; w < kTabWarps; ++w)
+  for (int w = 0; w < kThreads / 32; ++w)
     if (w < warp) {
       px += warps[w].x;
       py += warps[w].y;
@@ -71,7 +75,7 @@ __device__ __forceinline__ void block_sums(const int (&x)[kPer], const int (&y)[
     px += x[i];
     py += y[i];
   }
-  if (threadIdx.x == kTabThreads - 1) {
+  if (threadIdx.x == kThreads - 1) {
     out.a[kChunk] = px;
     out.b[kChunk] = py;
   }
@@ -94,7 +98,8 @@ struct Totals {
   int bad;
 };
 
-__device__ __forceinline__ Totals block_totals(Totals t, Totals (&warps)[kTabWarps]) {
+template <int kThreads>
+__device__ __forceinline__ Totals block_totals(Totals t, Totals (&warps)[kThreads / 32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) {
@@ -106,7 +111,7 @@ __device__ __forceinline__ Totals block_totals(Totals t, Totals (&warps)[kTabWar
   __syncthreads();
   t = Totals{0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < kTabWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     t.x += warps[w].x;
     t.y += warps[w].y;
     t.bad |= warps[w].bad;
@@ -118,21 +123,23 @@ __device__ __forceinline__ int pages_of(int keys, int page_log2) {
   return (keys + (1 << page_log2) - 1) >> page_log2;
 }
 
-__global__ void __launch_bounds__(kTabThreads)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
     reserve_kernel(const __grid_constant__ ReserveLaunch p) {
   __shared__ ChunkSums sums;  // a: new tokens, b: new pages
   __shared__ int len[kChunk];
-  __shared__ int2 warps[kTabWarps];
-  __shared__ Totals totals[kTabWarps];
+  constexpr int kPer = kChunk / kThreads;
+  __shared__ int2 warps[kThreads / 32];
+  __shared__ Totals totals[kThreads / 32];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int ctas = static_cast<int>(cluster.num_blocks());
-  const int me = rank * kTabThreads + threadIdx.x, all = ctas * kTabThreads;
+  const int me = rank * kThreads + threadIdx.x, all = ctas * kThreads;
   const int most = p.max_pages << p.page_log2;
   const int count = *p.free_count;
   // -- what is asked for, and whether it can be had
   Totals t{0, 0, count < 0 || count > p.capacity};
-  for (int b = threadIdx.x; b < p.batch; b += kTabThreads) {
+  for (int b = threadIdx.x; b < p.batch; b += kThreads) {
     const int n = p.fresh[b], l = p.lens[b];
     if (n < 0 || l < 0 || l > most || n > most - l) {
       t.bad = 1;
@@ -141,7 +148,7 @@ __global__ void __launch_bounds__(kTabThreads)
     t.x += n;
     t.y += pages_of(l + n, p.page_log2) - pages_of(l, p.page_log2);
   }
-  t = block_totals(t, totals);
+  t = block_totals<kThreads>(t, totals);
   if (t.x > p.total) t.bad = 1;
   const int missing = t.bad ? -1 : static_cast<int>(max(0LL, t.y - count));
   if (missing != 0) {
@@ -162,6 +169,8 @@ __global__ void __launch_bounds__(kTabThreads)
     }
     return;
   }
+  const bool aligned = ((reinterpret_cast<uintptr_t>(p.positions) |
+                         reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
   // -- kChunk sequences at a time
   int row0 = 0, taken = 0;  // rows and pages of the chunks before
   for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
@@ -175,7 +184,7 @@ __global__ void __launch_bounds__(kTabThreads)
       need[i] = pages_of(l + n[i], p.page_log2) - pages_of(l, p.page_log2);
       len[j] = l;
     }
-    block_sums(n, need, sums, warps);
+    block_sums<kThreads>(n, need, sums, warps);
     cluster.sync();  // everyone has read this chunk's lengths
     const int rows = sums.a[kChunk], pages = sums.b[kChunk];
     const int top = count - 1 - taken;  // this chunk's first page in the free list
@@ -188,15 +197,49 @@ __global__ void __launch_bounds__(kTabThreads)
       const int col = pages_of(len[j], p.page_log2) + m - sums.b[j];
       p.table[(b0 + j) * p.table_stride + col] = p.free_pages[top - m];
     }
-    for (int i = me; i < rows; i += all) {
-      const int j = find(sums.a, i);
-      const int pos = len[j] + i - sums.a[j], col = pos >> p.page_log2;
-      const int held = pages_of(len[j], p.page_log2);
-      const int page = col < held ? p.table[(b0 + j) * p.table_stride + col]
-                                  : p.free_pages[top - sums.b[j] - (col - held)];
-      p.positions[row0 + i] = pos;
-      p.slots[row0 + i] = (static_cast<long long>(page) << p.page_log2) +
-                          (pos & ((1 << p.page_log2) - 1));
+    // Four rows a thread where there are more rows than threads: what one has looked up
+    // mostly serves the next, and a search and a page's load, one after the other, are the
+    // time that this takes.
+    const int each = rows > all ? 4 : 1;
+    const bool wide = each == 4 && row0 % 4 == 0 && aligned;
+    for (int i0 = each * me; i0 < rows; i0 += each * all) {
+      int pos[4] = {};
+      long long slot[4] = {};
+      int j = 0, ends = -1, held = 0, col = -1, page = 0;
+#pragma unroll
+      for (int t4 = 0; t4 < 4; ++t4) {
+        const int i = i0 + t4;
+        if (t4 >= each || i >= rows) break;
+        if (i >= ends) {
+          j = find(sums.a, i);
+          ends = sums.a[j + 1];
+          held = pages_of(len[j], p.page_log2);
+          col = -1;
+        }
+        pos[t4] = len[j] + i - sums.a[j];
+        const int c = pos[t4] >> p.page_log2;
+        if (c != col) {
+          col = c;
+          page = c < held ? p.table[(b0 + j) * p.table_stride + c]
+                          : p.free_pages[top - sums.b[j] - (c - held)];
+        }
+        slot[t4] = (static_cast<long long>(page) << p.page_log2) +
+                   (pos[t4] & ((1 << p.page_log2) - 1));
+      }
+      int* const to = p.positions + row0 + i0;
+      long long* const at = p.slots + row0 + i0;
+      if (wide && i0 + 4 <= rows) {
+        *reinterpret_cast<int4*>(to) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<longlong2*>(at) = make_longlong2(slot[0], slot[1]);
+        *reinterpret_cast<longlong2*>(at + 2) = make_longlong2(slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (int t4 = 0; t4 < 4; ++t4)
+          if (t4 < each && i0 + t4 < rows) {
+            to[t4] = pos[t4];
+            at[t4] = slot[t4];
+          }
+      }
     }
     row0 += rows;
     taken += pages;
@@ -212,26 +255,28 @@ __global__ void __launch_bounds__(kTabThreads)
   }
 }
 
-__global__ void __launch_bounds__(kTabThreads)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
     release_kernel(const __grid_constant__ ReleaseLaunch p) {
   __shared__ ChunkSums sums;  // b: pages given back
   __shared__ int keep[kChunk];
-  __shared__ int2 warps[kTabWarps];
-  __shared__ Totals totals[kTabWarps];
+  constexpr int kPer = kChunk / kThreads;
+  __shared__ int2 warps[kThreads / 32];
+  __shared__ Totals totals[kThreads / 32];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int ctas = static_cast<int>(cluster.num_blocks());
-  const int me = rank * kTabThreads + threadIdx.x, all = ctas * kTabThreads;
+  const int me = rank * kThreads + threadIdx.x, all = ctas * kThreads;
   const int most = p.max_pages << p.page_log2;
   const int count = *p.free_count;
   Totals t{0, 0, count < 0 || count > p.capacity};
-  for (int b = threadIdx.x; b < p.batch; b += kTabThreads) {
+  for (int b = threadIdx.x; b < p.batch; b += kThreads) {
     if (!p.done[b]) continue;
     const int l = p.lens[b], k = p.keep ? p.keep[b] : 0;
     if (l < 0 || l > most || k < 0) t.bad = 1;
     else t.y += max(0, pages_of(l, p.page_log2) - k);
   }
-  t = block_totals(t, totals);
+  t = block_totals<kThreads>(t, totals);
   if (t.bad || t.y > p.capacity - count) {
     if (me == 0) atomicExch(p.err, kDevErrBadIndex);
     return;  // (the same in every CTA)
@@ -248,7 +293,7 @@ __global__ void __launch_bounds__(kTabThreads)
       keep[j] = mine && p.keep ? p.keep[b] : 0;
       give[i] = mine ? max(0, pages_of(p.lens[b], p.page_log2) - keep[j]) : 0;
     }
-    block_sums(none, give, sums, warps);
+    block_sums<kThreads>(none, give, sums, warps);
     cluster.sync();  // everyone has read this chunk's lengths, and the count
     const int pages = sums.b[kChunk];
     for (int m = me; m < pages; m += all) {
@@ -264,30 +309,35 @@ __global__ void __launch_bounds__(kTabThreads)
 }
 
 template <typename L>
-cudaError_t launch_cluster(void (*kern)(L), const L& a, long long items, cudaStream_t s) {
+cudaError_t launch_cluster(void (*few)(L), void (*many)(L), const L& a, bool large, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const unsigned ctas = items <= 2 * kTabThreads ? 1 : 8;
+  const unsigned ctas = large ? kManyCtas : 1;
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kTabThreads);
+  cfg.blockDim = dim3(large ? kManyThreads : kFewThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {ctas, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, large ? many : few, a);
 }
+
+// Items (tokens, table entries) from which a cluster pays.
+constexpr long long kLarge = 1024;
 
 }  // namespace
 
 cudaError_t launch_reserve(const ReserveLaunch& a, cudaStream_t s) {
-  return launch_cluster(reserve_kernel, a, a.total, s);
+  return launch_cluster(reserve_kernel<kFewThreads>, reserve_kernel<kManyThreads>, a,
+                        a.total > kLarge, s);
 }
 
 cudaError_t launch_release(const ReleaseLaunch& a, cudaStream_t s) {
   // (the pages are the kernel's to count: at most the table's)
   const long long entries = static_cast<long long>(a.batch) * a.max_pages;
-  return launch_cluster(release_kernel, a, std::min<long long>(entries, a.capacity), s);
+  return launch_cluster(release_kernel<kFewThreads>, release_kernel<kManyThreads>, a,
+                        std::min<long long>(entries, a.capacity) > kLarge, s);
 }
 
 }  // namespace fa

@@ -189,12 +189,13 @@ def test_shared_arguments(lib):
     c = pages()
     r = Ragged(FAKE, 200, 200, FAKE, FAKE, 4, 4)
     n = ctypes.c_size_t(7)
+    r.max_pages = r.table_stride = 1 << 20  # so wide that sharing pays
     size = lambda groups, total=4: lib.fa_fwd_paged_shared_workspace_size(  # noqa: E731
-        4, total, 4, 2, 64, 3200, groups, ctypes.byref(n))
+        4, total, 4, 2, 64, 1 << 24, groups, ctypes.byref(n))
     assert size(-1) == INV and size(5) == INV
     assert size(0) == OK
     plain = ctypes.c_size_t()
-    assert lib.fa_fwd_paged_workspace_size(4, 4, 4, 2, 64, 3200, ctypes.byref(plain)) == OK
+    assert lib.fa_fwd_paged_workspace_size(4, 4, 4, 2, 64, 1 << 24, ctypes.byref(plain)) == OK
     assert n.value == plain.value
     assert size(2) == OK and n.value > plain.value + 2 * 4 * 4 * 64 * 4
 

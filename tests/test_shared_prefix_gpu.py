@@ -24,6 +24,28 @@ def shared_batch(rows, ctx, groups, Hk, D, page, dtype, fp8, **kw):
     return b
 
 
+def columns(b):
+    """Spare columns for a table so wide that keys are walked once for a group: by the width the
+    call judges what sharing saves."""
+    return (1 << 24) // (len(b.rows) * b.heads_k * b.page)
+
+
+def widen(b):
+    table = torch.full((len(b.rows), b.table.shape[1] + columns(b)), 1 << 30, dtype=torch.int32)
+    table[:, :b.table.shape[1]] = b.table
+    b.table = table
+    return b
+
+
+def divided(b, H, groups=(0,)):
+    """Whether the call walks shared keys once for a group: then it needs room for two parts."""
+    n, m, lib = ctypes.c_size_t(), ctypes.c_size_t(), fattn.load()
+    args = (len(b.rows), b.total, H, b.heads_k, b.D, b.table.shape[1] * b.page)
+    assert lib.fa_fwd_paged_workspace_size(*args, ctypes.byref(n)) == 0
+    assert lib.fa_fwd_paged_shared_workspace_size(*args, len(groups), ctypes.byref(m)) == 0
+    return m.value > n.value
+
+
 def tensors(groups):
     cu = [groups[0][0]] + [hi for _, hi, _ in groups] if groups else [0]
     return (torch.tensor(cu, dtype=torch.int32, device="cuda"),
@@ -79,17 +101,23 @@ CASES = [
     ([1] * 40, [2100 + 3 * i for i in range(40)], [(0, 40, 16)], 10, 2, 128, 128, BF, False),
     ([2] * 20, [1030] * 20, [(0, 3, 60), (3, 4, 50), (4, 20, 64)], 8, 8, 64, 16, BF, True),
     ([1, 1, 1, 1], [256, 512, 256, 300], [(0, 1, 1), (1, 4, 1)], 64, 1, 64, 256, HF, False),
+    ([1] * 6, [256, 512, 256, 300, 700, 1000], [(0, 6, 1)], 64, 1, 64, 256, HF, False),
+    ([1] * 6, [256, 512, 256, 300, 700, 1000], [(0, 6, 1)], 64, 1, 128, 128, BF, True),
     ([17, 30, 8], [400, 401, 402], [(0, 3, 25)], 4, 1, 128, 16, BF, False),
     ([17, 30, 8], [400, 401, 402], [(0, 3, 25)], 4, 1, 128, 16, HF, True),
-    ([90, 200, 60], [200, 201, 202], [(0, 3, 12)], 4, 2, 64, 16, BF, False),  # not divided
+    ([90, 200, 60], [200, 201, 202], [(0, 3, 12)], 4, 2, 64, 16, BF, False),  # too many rows
 ]
 
 
-@pytest.mark.parametrize("wide", [False, True])  # wide tables: work may be cut and joined
+@pytest.mark.parametrize("wide", [False, True])  # wide tables: shared keys are walked once
 @pytest.mark.parametrize("rows,ctx,groups,H,Hk,D,page,dtype,fp8", CASES)
 def test_groups(rows, ctx, groups, H, Hk, D, page, dtype, fp8, wide):
-    b = shared_batch(rows, ctx, groups, Hk, D, page, dtype, fp8, seed=len(rows) + H,
-                     spare_cols=2000 // page + 200 if wide else 2)
+    b = shared_batch(rows, ctx, groups, Hk, D, page, dtype, fp8, seed=len(rows) + H)
+    if wide:
+        widen(b)
+    few = sum(rows) * (H // Hk) / len(rows) <= 64
+    if not wide or not few or 2 * len(groups) < len(rows):  # (else it pays hardly or not)
+        assert divided(b, H, groups) == (wide and few)
     q, o, lse = run(b, H, groups)
     assert fattn.fa_device_error() == fattn.FA_OK
     check(b, H, q, o, lse)
@@ -100,8 +128,9 @@ def test_groups(rows, ctx, groups, H, Hk, D, page, dtype, fp8, wide):
 
 @pytest.mark.parametrize("fp8", [False, True])
 def test_long_prefix(fp8):
-    b = shared_batch([1] * 12, [20000 + 50 * i for i in range(12)], [(0, 12, 312)], 2, 128, 64, BF, fp8,
-                     seed=2)
+    b = widen(shared_batch([1] * 12, [20000 + 50 * i for i in range(12)], [(0, 12, 312)], 2, 128, 64,
+                           BF, fp8, seed=2))
+    assert divided(b, 8)
     q, o, lse = run(b, 8, [(0, 12, 312)])
     check(b, 8, q, o, lse)
     q, o, lse = run(b, 8, [(0, 12, 312)], scale=-0.3)
@@ -110,10 +139,23 @@ def test_long_prefix(fp8):
     check(b, 8, q, o, lse, scale=0.0)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_sequences_and_short_tables(fp8):
+    # units are not cut below 1536 keys, and sharing pays all the same for 1100 of them
+    n = 140
+    groups = [(0, 100, 60), (100, n, 50)]
+    b = shared_batch([1] * n, [960 + i for i in range(n)], groups, 8, 128, 16, BF, fp8, seed=5)
+    b.table = b.table[:, :95].contiguous()
+    assert divided(b, 16, groups) and b.table.shape[1] * 16 <= 1536
+    q, o, lse = run(b, 16, groups)
+    check(b, 16, q, o, lse)
+
+
 def test_no_more_is_shared_than_lies_before_every_new_token():
     # the second sequence's new tokens begin in page 3, whatever is claimed; the third is
     # shorter than its rows; the fourth has no rows and does not count
-    b = shared_batch([1, 4, 3, 0], [200, 60, -1, 0], [(0, 2, 3)], 2, 64, 16, BF, False, seed=3)
+    b = widen(shared_batch([1, 4, 3, 0], [200, 60, -1, 0], [(0, 2, 3)], 2, 64, 16, BF, False, seed=3))
+    assert divided(b, 4)
     for claim in (4, 12, 1 << 20):
         for end in (2, 3, 4):
             q, o, lse = run(b, 4, [(0, end, min(claim, b.table.shape[1]))])
@@ -124,7 +166,7 @@ def test_no_more_is_shared_than_lies_before_every_new_token():
 
 
 def test_groups_of_nothing():
-    b = shared_batch([1, 1, 2], [64, 80, 5], [(0, 2, 4)], 2, 64, 16, HF, False, seed=3)
+    b = widen(shared_batch([1, 1, 2], [64, 80, 5], [(0, 2, 4)], 2, 64, 16, HF, False, seed=3))
     want = run(b, 4, [])
     check(b, 4, *want)
     for groups in ([(0, 0, 0)], [(3, 3, 4)], [(0, 3, 0)], [(1, 1, 2), (1, 2, 3)], [(0, 1, 4), (1, 3, 0)]):
@@ -151,18 +193,21 @@ def call_c(q, o, lse, b, groups):
                             ctypes.addressof(c), ctypes.addressof(r), ptr(cu_groups), ptr(shared),
                             len(groups), H, D ** -0.5, code[q.dtype], w, size,
                             torch.cuda.current_stream().cuda_stream)
-    assert lib.fa_fwd_paged_shared(*args(ptr(ws), n.value - 1)) == fattn.FA_ERR_INVALID_ARG
-    assert lib.fa_fwd_paged_shared(*args(ptr(ws) + 16, n.value)) == fattn.FA_ERR_INVALID_ARG
-    assert lib.fa_fwd_paged_shared(*args(ptr(ws), n.value)) == fattn.FA_OK
+    if n.value:
+        assert lib.fa_fwd_paged_shared(*args(ptr(ws), n.value // 2)) == fattn.FA_ERR_INVALID_ARG
+        assert lib.fa_fwd_paged_shared(*args(ptr(ws) + 16, n.value)) == fattn.FA_ERR_INVALID_ARG
+    assert lib.fa_fwd_paged_shared(*args(ptr(ws) if n.value else None, n.value)) == fattn.FA_OK
     torch.cuda.synchronize()
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("spare", [1, 200])
-def test_rows_behind_the_last_sequence_and_rows_without_keys(fp8, spare):
+@pytest.mark.parametrize("wide", [False, True])
+def test_rows_behind_the_last_sequence_and_rows_without_keys(fp8, wide):
     groups = [(0, 3, 2), (3, 5, 0)]
-    b = shared_batch([1, 1, 2, 4, 1], [40, 33, 32, -2, 0], groups, 2, 128, 16, BF, fp8, seed=2, tail=5,
-                     spare_cols=spare)
+    b = shared_batch([1, 1, 2, 4, 1], [40, 33, 32, -2, 0], groups, 2, 128, 16, BF, fp8, seed=2, tail=5)
+    if wide:
+        widen(b)
+    assert divided(b, 4, groups) == wide
     q = queries(b, 4)
     o = torch.full((b.total, 2, 4, 128), 7.0, dtype=BF, device="cuda")[:, 1]  # strided results
     lse = torch.full((4, b.total), 7.0, device="cuda")
@@ -177,7 +222,8 @@ def test_rows_behind_the_last_sequence_and_rows_without_keys(fp8, spare):
 def test_values_that_are_not_finite():
     # a NaN value in the shared part reaches the group and nobody else
     groups = [(0, 2, 2), (2, 4, 2)]
-    b = shared_batch([1] * 4, [40] * 4, groups, 1, 64, 16, BF, False, seed=2)
+    b = widen(shared_batch([1] * 4, [40] * 4, groups, 1, 64, 16, BF, False, seed=2))
+    assert divided(b, 2, groups)
     first = int(b.table[0, 1])
     b.pool[1, first, 3, 0, 5] = math.nan
     q, o, lse = run(b, 2, groups)
@@ -188,7 +234,8 @@ def test_values_that_are_not_finite():
 @pytest.mark.parametrize("bad", ["order", "beyond", "negative", "pages", "table", "length"])
 def test_bad_groups_and_tables_are_contained(bad):
     groups = [(0, 2, 3), (2, 4, 3)]
-    b = shared_batch([1] * 4, [100] * 4, groups, 2, 64, 16, BF, False, seed=6)
+    b = widen(shared_batch([1] * 4, [100] * 4, groups, 2, 64, 16, BF, False, seed=6))
+    assert divided(b, 4, groups)
     k, v, table, cu, lens, _ = b.gpu()
     q = queries(b, 4).cuda()
     c, p = tensors(groups)
@@ -217,8 +264,8 @@ def test_bad_groups_and_tables_are_contained(bad):
 
 def test_streams_and_graphs():
     groups = [(0, 6, 20)]
-    b = shared_batch([1] * 6, [900, 320, 330, 500, 321, 2500], groups, 4, 128, 16, BF, False, seed=8,
-                     spare_cols=60)
+    b = widen(shared_batch([1] * 6, [900, 320, 330, 500, 321, 2500], groups, 4, 128, 16, BF, False, seed=8))
+    assert divided(b, 16, groups)
     k, v, table, cu, lens, _ = b.gpu()
     c, p = tensors(groups)
     qs = [queries(b, 16, seed=i).cuda() for i in range(3)]
