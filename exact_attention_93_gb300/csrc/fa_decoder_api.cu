@@ -166,6 +166,7 @@ fa_status fa_cache_reserve(const fa_reserve* r, void* stream) {
   a.free_count_out = r->free_count_out;
   a.missing = r->missing;
   a.slots = r->slots;
+  a.in_place = a.lens_out == a.lens || a.free_count_out == a.free_count;
   a.err = device_error_word();
   if (!a.err) return FA_ERR_CUDA;
   return launch_reserve(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;

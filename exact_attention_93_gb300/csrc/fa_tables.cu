@@ -7,13 +7,12 @@
 //   page j of sequence b = free[count - 1 - first_b - (j - ceil(len_b / page))]
 //
 // What bounds it.  A few bytes a token: latency, two dependent loads and the sums
-// between them.  So one launch does it all: the CTAs of one cluster each take the
-// sums over all sequences (they fit shared memory, kChunk sequences at a time), meet
-// at the cluster's barrier, after which nobody reads the lengths any more, so that
-// they may be written in place, and write a share of the results each.  Which
-// sequence a row or a page belongs to is a binary search among sums in shared memory.
-// A page is taken from the free list where its rows need it; nobody waits for the
-// table to be written.
+// between them.  So one launch does it all: every CTA takes the sums over all sequences
+// (they fit shared memory, kChunk sequences at a time) and writes a share of the results.
+// Which sequence a row or a page belongs to is a binary search among sums in shared
+// memory.  A page is taken from the free list where its rows need it; nobody waits for
+// the table to be written.  Written in place, lengths and count must have been read by all
+// CTAs before: these are one cluster then, and meet at its barrier.
 //
 // All or nothing: the totals are known before the first write.
 #include <cooperative_groups.h>
@@ -28,8 +27,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-// One CTA for a step of few tokens, a cluster of eight larger ones for prompts.
-constexpr int kFewThreads = 512, kManyThreads = 1024, kManyCtas = 8;
+// One CTA for a step of few tokens, several larger ones for prompts: a cluster of eight, or,
+// where nothing is written in place, as many as there are rows for.  (48 prompts, 111000
+// tokens: 8 CTAs of 512 threads, a row a thread, 16.3 us; four rows a thread 11.5.)
+constexpr int kFewThreads = 512, kManyThreads = 1024, kClusterCtas = 8, kMostCtas = 32;
 constexpr int kChunk = 2048;  // sequences at a time
 
 struct ChunkSums {
@@ -131,28 +132,34 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kPer = kChunk / kThreads;
   __shared__ int2 warps[kThreads / 32];
   __shared__ Totals totals[kThreads / 32];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank());
-  const int ctas = static_cast<int>(cluster.num_blocks());
-  const int me = rank * kThreads + threadIdx.x, all = ctas * kThreads;
+  const int me = blockIdx.x * kThreads + threadIdx.x, all = gridDim.x * kThreads;
   const int most = p.max_pages << p.page_log2;
   const int count = *p.free_count;
-  // -- what is asked for, and whether it can be had
+  // -- what is asked for, and whether it can be had; the first chunk stays at hand
   Totals t{0, 0, count < 0 || count > p.capacity};
-  for (int b = threadIdx.x; b < p.batch; b += kThreads) {
-    const int n = p.fresh[b], l = p.lens[b];
+  const auto add = [&](int n, int l) {
     if (n < 0 || l < 0 || l > most || n > most - l) {
       t.bad = 1;
-      continue;
+      return;
     }
     t.x += n;
     t.y += pages_of(l + n, p.page_log2) - pages_of(l, p.page_log2);
+  };
+  int n[kPer], l[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = threadIdx.x * kPer + i;
+    n[i] = b < p.batch ? p.fresh[b] : 0;
+    l[i] = b < p.batch ? p.lens[b] : 0;
   }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) add(n[i], l[i]);
+  for (int b = kChunk + threadIdx.x; b < p.batch; b += kThreads) add(p.fresh[b], p.lens[b]);
   t = block_totals<kThreads>(t, totals);
   if (t.x > p.total) t.bad = 1;
   const int missing = t.bad ? -1 : static_cast<int>(max(0LL, t.y - count));
   if (missing != 0) {
-    cluster.sync();
+    if (p.in_place) cg::this_cluster().sync();
     for (int b = me; b < p.batch; b += all) {
       p.cu[b + 1] = 0;
       if (p.lens_out != p.lens) p.lens_out[b] = p.lens[b];
@@ -175,17 +182,19 @@ __global__ void __launch_bounds__(kThreads)
   int row0 = 0, taken = 0;  // rows and pages of the chunks before
   for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
     if (b0) __syncthreads();  // (the sums before have been read)
-    int n[kPer], need[kPer];
+    int need[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int j = threadIdx.x * kPer + i, b = b0 + j;
-      n[i] = b < p.batch ? p.fresh[b] : 0;
-      const int l = b < p.batch ? p.lens[b] : 0;
-      need[i] = pages_of(l + n[i], p.page_log2) - pages_of(l, p.page_log2);
-      len[j] = l;
+      if (b0) {
+        n[i] = b < p.batch ? p.fresh[b] : 0;
+        l[i] = b < p.batch ? p.lens[b] : 0;
+      }
+      need[i] = pages_of(l[i] + n[i], p.page_log2) - pages_of(l[i], p.page_log2);
+      len[j] = l[i];
     }
     block_sums<kThreads>(n, need, sums, warps);
-    cluster.sync();  // everyone has read this chunk's lengths
+    if (p.in_place) cg::this_cluster().sync();  // everyone has read this chunk's lengths
     const int rows = sums.a[kChunk], pages = sums.b[kChunk];
     const int top = count - 1 - taken;  // this chunk's first page in the free list
     for (int j = me; j < min(kChunk, p.batch - b0); j += all) {
@@ -263,10 +272,7 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kPer = kChunk / kThreads;
   __shared__ int2 warps[kThreads / 32];
   __shared__ Totals totals[kThreads / 32];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank());
-  const int ctas = static_cast<int>(cluster.num_blocks());
-  const int me = rank * kThreads + threadIdx.x, all = ctas * kThreads;
+  const int me = blockIdx.x * kThreads + threadIdx.x, all = gridDim.x * kThreads;
   const int most = p.max_pages << p.page_log2;
   const int count = *p.free_count;
   Totals t{0, 0, count < 0 || count > p.capacity};
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kThreads)
       give[i] = mine ? max(0, pages_of(p.lens[b], p.page_log2) - keep[j]) : 0;
     }
     block_sums<kThreads>(none, give, sums, warps);
-    cluster.sync();  // everyone has read this chunk's lengths, and the count
+    cg::this_cluster().sync();  // everyone has read this chunk's lengths, and the count
     const int pages = sums.b[kChunk];
     for (int m = me; m < pages; m += all) {
       const int j = find(sums.b, m);
@@ -308,36 +314,41 @@ __global__ void __launch_bounds__(kThreads)
   if (me == 0) *p.free_count = count + given;
 }
 
+// `cluster`: the CTAs wait for one another.
 template <typename L>
-cudaError_t launch_cluster(void (*few)(L), void (*many)(L), const L& a, bool large, cudaStream_t s) {
+cudaError_t launch_tables(void (*kern)(L), const L& a, int ctas, int threads, bool cluster,
+                          cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const unsigned ctas = large ? kManyCtas : 1;
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(large ? kManyThreads : kFewThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {ctas, 1, 1};
+  attr[0].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, large ? many : few, a);
+  cfg.numAttrs = cluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// Items (tokens, table entries) from which a cluster pays.
+// Items (tokens, table entries) from which several CTAs pay.
 constexpr long long kLarge = 1024;
 
 }  // namespace
 
 cudaError_t launch_reserve(const ReserveLaunch& a, cudaStream_t s) {
-  return launch_cluster(reserve_kernel<kFewThreads>, reserve_kernel<kManyThreads>, a,
-                        a.total > kLarge, s);
+  if (a.total <= kLarge)
+    return launch_tables(reserve_kernel<kFewThreads>, a, 1, kFewThreads, true, s);
+  const int ctas = a.in_place ? kClusterCtas
+                              : std::min(kMostCtas, (a.total - 1) / (4 * kManyThreads) + 1);
+  return launch_tables(reserve_kernel<kManyThreads>, a, ctas, kManyThreads, a.in_place, s);
 }
 
 cudaError_t launch_release(const ReleaseLaunch& a, cudaStream_t s) {
   // (the pages are the kernel's to count: at most the table's)
   const long long entries = static_cast<long long>(a.batch) * a.max_pages;
-  return launch_cluster(release_kernel<kFewThreads>, release_kernel<kManyThreads>, a,
-                        std::min<long long>(entries, a.capacity) > kLarge, s);
+  if (std::min<long long>(entries, a.capacity) <= kLarge)
+    return launch_tables(release_kernel<kFewThreads>, a, 1, kFewThreads, true, s);
+  return launch_tables(release_kernel<kManyThreads>, a, kClusterCtas, kManyThreads, true, s);
 }
 
 }  // namespace fa

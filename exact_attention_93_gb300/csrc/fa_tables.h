@@ -15,6 +15,7 @@ struct ReserveLaunch {
   const int *free_pages, *free_count;
   int *cu, *lens_out, *positions, *free_count_out, *missing;
   long long* slots;
+  int in_place;  // lens_out is lens, or free_count_out free_count
   uint32_t* err;
 };
 
