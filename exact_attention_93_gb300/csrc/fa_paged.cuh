@@ -20,7 +20,7 @@
 //
 // Weights.  The few-row kernel gives all units of a sequence the number of key
 // tiles that any of its queries sees, at least 1 (a sequence usually is one
-// block).  The many-row kernel counts each block's own tiles, plus kUnitCost
+// block), and PagedLaunch::unit_cost more.  The many-row kernel counts each block's own tiles, plus kUnitCost
 // for what a unit costs beside its tiles: under a causal mask the blocks of a
 // prompt see from one tile to all of them.  The sums over blocks that this
 // needs are sums of floor((a + i b) / 128), taken in closed form.
@@ -94,7 +94,7 @@ struct SeqWork {
       int lo, hi;
       visible_span(p, s, 0, s.rows, lo, hi);
       first = lo / kTile;
-      flat = max(1, (hi + kTile - 1) / kTile - first);
+      flat = max(1, (hi + kTile - 1) / kTile - first) + p.unit_cost;
     }
   }
   // Weight of the blocks before block i of a head.
@@ -268,7 +268,7 @@ struct WorkWalk {
         p.whole ? weight : static_cast<int>(min(at.left, static_cast<long long>(weight - off)));
     x.whole = take == weight;
     x.slot = off > 0 ? 0 : 1;
-    const int base = kMany ? lo_tile - kUnitCost : w.first;
+    const int base = kMany ? lo_tile - kUnitCost : w.first - p.unit_cost;
     x.tile0 = max(base + off, lo_tile);
     x.tile1 = min(base + off + take, hi_tile);
     x.last = -1;

@@ -100,6 +100,7 @@ struct PagedLaunch {
   int min_rows, max_rows;  // sequences of other numbers of rows (tokens x group) are left out
   int whole;        // units are not cut
   int few_joins;    // few rows are left to be joined
+  int unit_cost;    // few-row kernel: what a unit costs beside its key tiles, in tiles
   // unless whole:
   float* part_o;    // [2 sms][block_rows][D]
   float2* part_ml;  // [2 sms][block_rows]: maximum, sum

@@ -278,6 +278,12 @@ bool sharing_pays(int batch, int total, int heads, int heads_k, int D, long long
          c.set_out + std::max(c.shared_tile * tiles * blocks, hbm) * groups;
 }
 
+// Behind a shared prefix most sequences have few keys of their own, so what a unit costs
+// beside its tiles counts in sharing out the work.  (us, a whole call, in tiles 0, 1, 2, 3 and
+// 5: 64 sequences of 16 to 2000 own keys 87, 86, 83, 84 and 83; 128 of 1 to 1500, e4m3, 100,
+// 97, 94, 93 and 93.)
+constexpr int kOwnUnitCost = 3;
+
 // The workspace of attention over shared prefixes, in front of the kernels' own.
 struct SharedLayout {
   size_t o1, o2, lse1, lse2, cu, lens, rows, skip, bytes;
@@ -443,6 +449,7 @@ fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head
   if (!plan_many(plan2)) {  // few rows: the own part's kernels join the two
     a.add_o = first.o32;
     a.add_lse = first.lse;
+    a.unit_cost = kOwnUnitCost;
     return paged_launch(a, plan2, base + at.bytes, s);
   }
   a.o32 = floats(at.o2);
