@@ -23,6 +23,7 @@
 
 #include <climits>
 #include <cstring>
+#include <exception>
 #include <optional>
 #include <string>
 #include <vector>
@@ -31,10 +32,13 @@
 
 namespace {
 
-// Raised as the Python exception of the given type.
-struct Refuse {
+// Raised as the Python exception of the given type.  (A std::exception, so that autograd's
+// own threads hand it on as well.)
+struct Refuse : std::exception {
+  Refuse(PyObject* t, const char* w) : type(t), text(w) {}
+  const char* what() const noexcept override { return text; }
   PyObject* type;
-  const char* what;
+  const char* text;
 };
 
 [[noreturn]] void refuse(const char* what) { throw Refuse{PyExc_ValueError, what}; }
@@ -962,7 +966,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
     return kFn(args);
   } catch (const Refuse& r) {
-    PyErr_SetString(r.type, r.what);
+    PyErr_SetString(r.type, r.text);
     return nullptr;
   }
   END_HANDLE_TH_ERRORS

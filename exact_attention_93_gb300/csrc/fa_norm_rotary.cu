@@ -44,10 +44,13 @@ namespace {
 constexpr int kNormThreads = 128, kNormWarps = kNormThreads / 32;
 // Heads in flight per lane group, and blocks per SM, as many as the registers allow at
 // once: all blocks run from beginning to end.
+// Forward, 16-bit: four, or five where that makes fewer items of a token's heads (us, four and
+// five: 20000 tokens of 16 + 4 heads of 128 41.4 and 38.5, 65536 of 8 + 8 87 and 95).
 template <int kElem>
 constexpr int kFwdUnroll = kElem == kElemFp32 ? 3 : 4;
 template <int kElem>
-constexpr int kFwdBlocks = kElem == kElemFp32 ? 3 : 4;
+constexpr int kFwdMost = kElem == kElemFp32 ? 3 : 5;
+constexpr int fwd_blocks(int unroll) { return unroll == 4 ? 4 : 3; }
 template <int kElem>
 constexpr int kBwdUnroll = kElem == kElemFp32 ? 1 : 2;
 constexpr int kStages = 3;  // of the backward's ring
@@ -192,12 +195,12 @@ __device__ __forceinline__ float row_sum(float v) {
 template <int kElem>
 using ElemOf = typename std::conditional<kElem == kElemFp32, float, uint16_t>::type;
 
-template <int D, int kElem, bool kInterleaved, bool kAxes>
-__global__ void __launch_bounds__(kNormThreads, kFwdBlocks<kElem>)
+template <int D, int kElem, bool kInterleaved, bool kAxes, int kUnroll>
+__global__ void __launch_bounds__(kNormThreads, fwd_blocks(kUnroll))
     norm_rotary_kernel(const __grid_constant__ NormLaunch p, int head_groups, int per) {
   using T = ElemOf<kElem>;
   using Angles = PairAngles<D, kAxes>;
-  constexpr int kLanes = Angles::kLanes, kSlots = Angles::kSlots, kUnroll = kFwdUnroll<kElem>;
+  constexpr int kLanes = Angles::kLanes, kSlots = Angles::kSlots;
   __shared__ PairTable<D, kAxes> table;
   __shared__ float4 weight[2][4][D / 16];
   const RotaryLaunch& r = p.rot;
@@ -466,21 +469,29 @@ __global__ void __launch_bounds__(kSumThreads)
   }
 }
 
-template <int D, int kElem, bool kInterleaved, bool kAxes>
-cudaError_t launch_fwd_t(const NormLaunch& a, cudaStream_t s) {
+template <int D, int kElem, bool kInterleaved, bool kAxes, int kUnroll>
+cudaError_t launch_fwd_u(const NormLaunch& a, const HeadSplit& split, cudaStream_t s) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const HeadSplit split(a.rot.heads[0] + a.rot.heads[1], 32 / (D / 16), kFwdUnroll<kElem>);
   const long long items = static_cast<long long>(a.rot.B) * a.rot.N * split.groups;
   // (warps for every group of heads, however few tokens there are)
-  const long long most = std::max(static_cast<long long>(kFwdBlocks<kElem>) * sms,
+  const long long most = std::max(static_cast<long long>(fwd_blocks(kUnroll)) * sms,
                                   (split.groups + kNormWarps - 1LL) / kNormWarps);
   const long long blocks = (items + kNormWarps - 1) / kNormWarps;
-  norm_rotary_kernel<D, kElem, kInterleaved, kAxes>
+  norm_rotary_kernel<D, kElem, kInterleaved, kAxes, kUnroll>
       <<<static_cast<unsigned>(blocks < most ? blocks : most), kNormThreads, 0, s>>>(
           a, split.groups, split.per);
   return cudaGetLastError();
+}
+
+template <int D, int kElem, bool kInterleaved, bool kAxes>
+cudaError_t launch_fwd_t(const NormLaunch& a, cudaStream_t s) {
+  const int heads = a.rot.heads[0] + a.rot.heads[1], slots = 32 / (D / 16);
+  const HeadSplit split(heads, slots, kFwdUnroll<kElem>), wide(heads, slots, kFwdMost<kElem>);
+  if (wide.groups < split.groups)
+    return launch_fwd_u<D, kElem, kInterleaved, kAxes, kFwdMost<kElem>>(a, wide, s);
+  return launch_fwd_u<D, kElem, kInterleaved, kAxes, kFwdUnroll<kElem>>(a, split, s);
 }
 
 template <int D, int kElem, bool kInterleaved, bool kAxes>

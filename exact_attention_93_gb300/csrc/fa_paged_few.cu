@@ -151,10 +151,7 @@ __device__ __forceinline__ float exp2_field(int n) {
 template <int D, bool kFp8, bool kBf16, int NB, bool kAdd>
 __global__ void __maxnreg__(kFewRegs)
     paged_few_kernel(const __grid_constant__ PagedLaunch p) {
-  // Joining another part's results, the kernels before this one are that part's: they wrote
-  // none of the lengths, and started when all earlier work had ended.  So a place is found
-  // while they end.
-  if constexpr (!kAdd) pdl_wait_and_release();
+  pdl_wait_and_release();
   using Smem = FewSmem<D, kFp8, NB>;
   constexpr int kRows = 8 * NB, kRowBytes = Smem::kRowBytes;
   constexpr int kSlots = Smem::kSlots, kRing = Smem::kRing;
@@ -168,7 +165,6 @@ __global__ void __maxnreg__(kFewRegs)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     const Place at = warp_place<false>(p, gridDim.x, blockIdx.x);
-    if constexpr (kAdd) pdl_wait_and_release();
     if (lane == 0) {
       s.place = at;
       if (at.left == 0 && !p.whole) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
@@ -183,9 +179,6 @@ __global__ void __maxnreg__(kFewRegs)
     fence_barrier_init();
   }
   __syncthreads();
-  if constexpr (kAdd) {
-    if (warp != 0) pdl_wait_and_release();
-  }
   volatile int* abort_flag = &s.abort_flag;
   WorkWalk<false> walk(s.place);
   Piece x;

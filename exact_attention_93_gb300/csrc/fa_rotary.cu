@@ -42,8 +42,6 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   using Angles = PairAngles<D, kAxes>;
   constexpr int kLanes = Angles::kLanes, kSlots = Angles::kSlots;
   __shared__ PairTable<D, kAxes> table;
-  table.fill(p);
-  __syncthreads();
   const int half = p.rotary >> 1;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, slot = lane / kLanes;
   const bool rotates = sub * 16 < p.rotary;
@@ -51,27 +49,32 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   const int e0 = rotates && !kInterleaved ? sub * 8 : sub * 16;
   const int e1 = rotates && !kInterleaved ? half + sub * 8 : sub * 16 + 8;
   const int all = p.heads[0] + p.heads[1];
-  Angles angles;
-  angles.load(table, sub, slot, rotates);
   const T* const x0 = static_cast<const T*>(p.x[0]);
   const T* const x1 = static_cast<const T*>(p.x[1]);
   T* const y0 = static_cast<T*>(p.y[0]);
   T* const y1 = static_cast<T*>(p.y[1]);
-  for (ItemWalk at(blockIdx.x * (kRotThreads / 32LL) + (threadIdx.x >> 5), n_items,
-                   static_cast<int>(gridDim.x) * (kRotThreads / 32), head_groups, p.N);
-       at.valid(); at.next()) {
-    const int h_first = at.group * kSlots * per + slot;
+  ItemWalk at(blockIdx.x * (kRotThreads / 32LL) + (threadIdx.x >> 5), n_items,
+              static_cast<int>(gridDim.x) * (kRotThreads / 32), head_groups, p.N);
+  Vec8<kElem> v0[kUnroll<kElem>], v1[kUnroll<kElem>];
+  const auto load = [&]() {
     const TokenRows<const T> xs(x0, p.xs[0], x1, p.xs[1], p.heads[0], at.b, at.n);
-    Vec8<kElem> v0[kUnroll<kElem>], v1[kUnroll<kElem>];
 #pragma unroll
     for (int u = 0; u < kUnroll<kElem>; ++u) {
-      const int h = h_first + u * kSlots;
+      const int h = (at.group * per + u) * kSlots + slot;
       if (u < per && h < all) {
         const T* x = xs.row(h, h >= p.heads[0]);
         v0[u].load(x + e0);
         v1[u].load(x + e1);
       }
     }
+  };
+  if (at.valid()) load();  // on its way while the table is filled
+  table.fill(p);
+  __syncthreads();
+  Angles angles;
+  angles.load(table, sub, slot, rotates);
+  while (at.valid()) {
+    const int h_first = at.group * kSlots * per + slot;
     float sn[8], cs[8];
     angles.at(angles.place(p, at.b, at.n), p.magnitude, sub, sn, cs);
     const TokenRows<T> ys(y0, p.ys[0], y1, p.ys[1], p.heads[0], at.b, at.n);
@@ -91,6 +94,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
       v0[u].store(y + e0);
       v1[u].store(y + e1);
     }
+    at.next();
+    if (at.valid()) load();
   }
 }
 

@@ -51,7 +51,7 @@ def norm(x, w, eps):
 def close(got, ref, tol):
     """Within tol; where the definition gives NaN (of infinities) the result has it too, and
     where a row has one the rest, zeros by the definition, are equal."""
-    got, ref = got.cpu().double(), ref.double()
+    got, ref = got.detach().cpu().double(), ref.double()
     assert torch.equal(torch.isnan(got), torch.isnan(ref))
     off = (got - ref).abs() - tol.nan_to_num(nan=0.0)
     off = off[~torch.isnan(ref)]
@@ -300,6 +300,27 @@ def test_norm_parts_absent():
     assert (s - hw - kw).abs().max() <= 2.0 ** -24 * 400 * 64 * 8
 
 
+@pytest.mark.parametrize("dtype,D,H,Hk", [(F32, 64, 33000, 7), (BF, 128, 5, 30001), (HF, 64, 24, 40)])
+def test_norm_many_heads(dtype, D, H, Hk):
+    # more groups of heads than the gradient's kernel has warps, and uneven ones
+    g = torch.Generator().manual_seed(H)
+    freq, _ = rotary.rotary_frequencies(D, device="cpu")
+    x = [torch.randn(1, 2, h, D, generator=g).to(dtype) for h in (H, Hk)]
+    dy = [torch.randn(t.shape, generator=g).to(dtype) for t in x]
+    w = [(1 + 0.3 * torch.randn(D, generator=g)) for _ in range(2)]
+    pos = torch.tensor([[7, 1000]])
+    leaves = [t.cuda().requires_grad_() for t in x + w]
+    y = rotary.qk_norm_rotary_func(*leaves, freq.cuda(), positions=pos.cuda())
+    got = torch.autograd.grad(y, leaves, [d.cuda() for d in dy])
+    for i in range(2):
+        xn, _ = norm(x[i], w[i], 1e-6)
+        ref = turn(xn, pos, freq)
+        close(y[i], ref, bound_norm(ref, xn, 1.0, dtype, D))
+        dx, dw, tol_x, tol_w = norm_grads(x[i], dy[i], w[i], 1e-6, lambda d: turn(d, pos, freq, inverse=True))
+        close(got[i], dx, tol_x + R.EPS[dtype] * 1.01 * dx.abs() + fp16_floor(dtype))
+        close(got[2 + i], dw, tol_w + R.EPS[F32] * 1.01 * dw.abs())
+
+
 def test_norm_broadcast_and_strided_gradients():
     g = torch.Generator().manual_seed(9)
     freq, _ = rotary.rotary_frequencies(64)
@@ -434,5 +455,11 @@ def test_norm_refusals():
     y = call(z, None, w, None, freq)
     with torch.no_grad():
         z += 1
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+    v = w.clone().requires_grad_()
+    y = call(x * 1, None, v, None, freq)
+    with torch.no_grad():
+        v += 1
     with pytest.raises(RuntimeError):
         y.sum().backward()
