@@ -432,6 +432,10 @@ __device__ __forceinline__ void join_rows(const PagedLaunch& p, const JoinTask& 
           }
         }
       }
+      // (All loads before the first use.  The blocks per SM that the kernels ask for leave
+      // room for that: without them the compiler kept to 32 registers, and used each piece
+      // before it loaded the next: 13.5 us instead of 8 for 8 units of 256 rows.)
+      asm volatile("" ::: "memory");
 #pragma unroll
       for (int k = 0; k < kPieces; ++k)
 #pragma unroll
@@ -467,7 +471,7 @@ __device__ __forceinline__ void join_rows(const PagedLaunch& p, const JoinTask& 
 constexpr int kJoinThreads = 64;
 
 template <int D, bool kBf16, int kRows, int kPieces>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 4)
     paged_join_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
   const int c = blockIdx.x, warp = threadIdx.x >> 5;
@@ -481,11 +485,11 @@ __global__ void __launch_bounds__(kJoinThreads)
 // Blocks of many rows where most CTAs have no task, as a few long units are cut into many
 // pieces: the rows of all tasks laid end to end and dealt out to the warps.  (us, like
 // this and by CTA, where nearly all of 9728 blocks find no work: 8 units of 256 rows
-// 13.5 and 23; four prompts, where they all find some, 10 more than by CTA.)
+// 8 and 23; four prompts, where they all find some, 10 more than by CTA.)
 constexpr int kJoinAllThreads = 128, kJoinTasks = 1024, kJoinAllRows = 1;
 
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kJoinAllThreads)
+__global__ void __launch_bounds__(kJoinAllThreads, 4)
     paged_join_all_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
   __shared__ int begin[kJoinTasks + 1];  // first lot of kJoinAllRows rows of each CTA's task
