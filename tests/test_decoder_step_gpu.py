@@ -152,3 +152,40 @@ def test_a_step_without_pages_does_nothing():
     for t in dec.pages[:2]:
         assert (t == 0).all()
     assert fattn.fa_device_error() == fattn.FA_OK
+
+
+def test_a_step_in_inference_mode_and_from_two_threads():
+    import threading
+    heads, heads_k, D, batch = 8, 2, 128, 3
+    dtype = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    data = [[torch.randn(batch, h, D, device="cuda", generator=gen).to(dtype)
+             for h in (heads, heads_k, heads_k)] for _ in range(20)]
+    new = torch.ones(batch, dtype=I32, device="cuda")
+
+    def generate(mode):
+        with mode():
+            dec = Decoder(batch, 12, heads, heads_k, D, dtype, dtype, True)
+            return [dec.step(*x, new)[0].clone() for x in data], dec.lens.tolist()
+
+    want, lens = generate(torch.no_grad)
+    got, lens2 = generate(torch.inference_mode)
+    assert lens == lens2 == [20] * batch
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # each thread on a stream and a cache of its own
+    results = [None] * 2
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            results[i] = generate(torch.no_grad)
+            torch.cuda.current_stream().synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for got, lens2 in results:
+        assert lens2 == lens and all(torch.equal(a, b) for a, b in zip(want, got))
+    assert fattn.fa_device_error() == fattn.FA_OK
