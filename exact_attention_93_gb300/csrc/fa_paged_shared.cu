@@ -8,7 +8,14 @@
 // The shared part of a group is attention of all its rows over one sequence of keys,
 // none of them masked: every shared key lies before every new token.  So the kernels
 // of fa_paged_few.cu and fa_paged_many.cu do either part, once for the groups and once
-// for the sequences behind their shared pages, with O in fp32.
+// for the sequences behind their shared pages, with the first part's O in fp32.  Where the
+// second takes the few-row kernel, that one and its joining kernel add the first part to
+// their rows before they store them; else a kernel here reads both.
+//
+// Measured (32 query and 8 key heads of 128, in a graph): 64 single tokens under 16000 shared
+// keys, 16 to 2000 of their own, 77 us (each walking all of its keys 209): groups 3, shared
+// part 30 and 8 to join, own part 32 and 5; what bounds each is said in their files, and five
+// starts.
 #include <climits>
 
 #include "fa_ragged.cuh"

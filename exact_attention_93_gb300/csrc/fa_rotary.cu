@@ -16,21 +16,25 @@
 // Work split.  A warp takes one token and up to kUnroll heads per lane group:
 // D / 16 lanes cover a head, two 16-byte loads each (elements i and
 // i + rotary/2, or 16 neighbours when interleaved), so a warp covers
-// 512 / D heads at a time.  The angles of a lane's 8 pairs depend on the
+// 512 / D heads at a time; the first loads are on their way while the pairs' table
+// is filled.  The angles of a lane's 8 pairs depend on the
 // token alone and serve all of its heads; the lane groups of a warp compute
 // a share of them each and exchange them by shuffles.
 //
-// Measured: 65536 tokens of 16 heads of 128, bf16, 80.7 us, 6.65 TB/s, 98 % of
-// the measured copy rate; 5003 tokens of 40 heads 18 us; 32 tokens of 40 heads
-// 3.2 us.
+// Measured: 65536 tokens of 16 heads of 128, bf16, 80.4 us, 6.7 TB/s, the measured
+// copy rate; 20000 tokens of 20 heads 34 us; 5003 tokens of 40 heads 19 us; 32 tokens of
+// 40 heads 2.8 us.  Along three axes, 32768 tokens of 20 heads 53 us, 6.3 TB/s.  (With four
+// heads in flight instead of five, and the last item of a token's heads left with the
+// rest, 20 heads took 66 us: one head in four of the second item's was there.)
 #include "fa_rotary.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int kRotThreads = 128;
-// Heads in flight per lane group: 128 bytes a lane.  (fp32: 28.0 us with four,
-// 26.2 with two, 1860 tokens of 72 heads of 128.)
+// Heads in flight per lane group, at most: as many in each of a token's items, and few
+// items, as each works its angles out anew.  (fp32, four and two: 28.0 and 26.2 us, 1860
+// tokens of 72 heads of 128.)
 template <int kElem>
 constexpr int kUnroll = kElem == kElemFp32 ? 3 : 5;
 

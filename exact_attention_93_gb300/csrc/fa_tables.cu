@@ -15,6 +15,9 @@
 // CTAs before: these are one cluster then, and meet at its barrier.
 //
 // All or nothing: the totals are known before the first write.
+//
+// Measured (in a graph): 64 single tokens 3.9 us, 48 prompts of 111000 tokens in pages of
+// 16 7.9 us.
 #include <cooperative_groups.h>
 
 #include <climits>
