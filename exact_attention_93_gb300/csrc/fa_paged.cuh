@@ -79,22 +79,24 @@ __device__ __forceinline__ long long tile_sum(int n, int a, int b) {
                    static_cast<uint32_t>(a + skip * b));
 }
 
-// A sequence as the work split sees it.
-template <bool kMany>
+// A sequence as the work split sees it.  kParts, here and below: the call is one of two
+// over parts of the keys (fa_paged_shared.cu); ordinary calls' kernels know nothing of it,
+// as the looks at what it needs cost short calls 1 to 3 %.
+template <bool kMany, bool kParts>
 struct SeqWork {
   Seq s;
   int blocks;  // query blocks per key head
   int flat;    // few rows: the weight of every unit
   int first;   // few rows: the first key tile
   __device__ __forceinline__ void load(const PagedLaunch& p, int b, uint32_t* err = nullptr) {
-    s = load_seq(p.r, p.page_log2, b, err);
+    s = load_seq<kParts>(p.r, p.page_log2, b, err);
     const int rows = s.rows * p.group;
     blocks = rows < p.min_rows || rows > p.max_rows ? 0 : (rows + p.block_rows - 1) / p.block_rows;
     if constexpr (!kMany) {
       int lo, hi;
       visible_span(p, s, 0, s.rows, lo, hi);
       first = lo / kTile;
-      flat = max(1, (hi + kTile - 1) / kTile - first) + p.unit_cost;
+      flat = max(1, (hi + kTile - 1) / kTile - first) + (kParts ? p.unit_cost : 0);
     }
   }
   // Weight of the blocks before block i of a head.
@@ -144,12 +146,12 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 }
 
 // Where CTA c of n begins, by one warp.
-template <bool kMany>
+template <bool kMany, bool kParts>
 __device__ __forceinline__ Place warp_place(const PagedLaunch& p, int n, int c) {
   const int lane = threadIdx.x & 31;
   Place at{};
   // lane i sums over sequences i, i + 32, ...; the first 32 stay at hand
-  SeqWork<kMany> w;
+  SeqWork<kMany, kParts> w;
   long long seq0 = 0;
   for (int b = lane; b < p.r.batch; b += 32) {
     w.load(p, b, c == 0 ? p.err : nullptr);
@@ -233,10 +235,10 @@ struct JoinTask {
 };
 
 // Walks a CTA's stretch.  Every role of the CTA runs its own copy.
-template <bool kMany>
+template <bool kMany, bool kParts>
 struct WorkWalk {
   Place at;
-  SeqWork<kMany> w;
+  SeqWork<kMany, kParts> w;
   bool loaded;
   __device__ __forceinline__ explicit WorkWalk(const Place& start) : at(start), loaded(false) {}
   __device__ __forceinline__ bool next(const PagedLaunch& p, Piece& x) {
@@ -268,7 +270,7 @@ struct WorkWalk {
         p.whole ? weight : static_cast<int>(min(at.left, static_cast<long long>(weight - off)));
     x.whole = take == weight;
     x.slot = off > 0 ? 0 : 1;
-    const int base = kMany ? lo_tile - kUnitCost : w.first - p.unit_cost;
+    const int base = kMany ? lo_tile - kUnitCost : w.first - (kParts ? p.unit_cost : 0);
     x.tile0 = max(base + off, lo_tile);
     x.tile1 = min(base + off + take, hi_tile);
     x.last = -1;
@@ -299,10 +301,13 @@ struct PageFeed {
   int lo, hi;      // pages that hold a visible key
   int cur, next;
   __device__ __forceinline__ int load(int i) const { return i >= lo && i <= hi ? table[i] : -1; }
+  template <bool kParts>
   __device__ __forceinline__ void start(const PagedLaunch& p, int b, int tile, int key_lo,
                                         int key_hi) {
-    table = p.r.table + (p.r.rows ? p.r.rows[b] : b) * p.r.table_stride +
-            (p.r.skip ? p.r.skip[b] : 0);
+    table = p.r.table + b * p.r.table_stride;
+    if constexpr (kParts)
+      table = p.r.table + (p.r.rows ? p.r.rows[b] : b) * p.r.table_stride +
+              (p.r.skip ? p.r.skip[b] : 0);
     first = (tile * kTile) >> p.page_log2;
     lo = key_lo >> p.page_log2;
     hi = (key_hi - 1) >> p.page_log2;
@@ -357,8 +362,8 @@ __device__ __forceinline__ void store32(float* dst, const float (&o)[kN], float 
 // its use: a lane's columns and the log-sum-exp in log2 units, -inf without one.
 template <int D, int kN>
 struct OtherPart {
-  float lse2, x[kN];
-  __device__ __forceinline__ OtherPart(const PagedLaunch& p, long long row, int head, int column) {
+  float lse2 = -INFINITY, x[kN] = {};
+  __device__ __forceinline__ void load(const PagedLaunch& p, long long row, int head, int column) {
     lse2 = p.add_lse[static_cast<long long>(head) * p.r.total + row] * 1.4426950408889634f;
     const float* src = p.add_o + (row * p.heads + head) * D + column;
     if constexpr (kN == 4) {
@@ -381,10 +386,10 @@ struct OtherPart {
 };
 
 // A lane's columns of a finished row, in the type that the call asks for.
-template <int D, bool kBf16, int kN>
+template <int D, bool kBf16, bool kParts, int kN>
 __device__ __forceinline__ void store_row(const PagedLaunch& p, long long row, int head, int column,
                                           const float (&o)[kN], float scale) {
-  if (p.o32)
+  if (kParts && p.o32)
     store32(p.o32 + (row * p.heads + head) * D + column, o, scale);
   else
     store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head + column, o,
@@ -458,8 +463,12 @@ __device__ __forceinline__ void join_rows(const PagedLaunch& p, const JoinTask& 
     row_of(p, task.first_row, r0 + q, task.hk, token, head);
     const long long row = task.start + token;
     if constexpr (kRows == 1)  // (few rows)
-      if (p.add_o) OtherPart<D, kN>(p, row, head, lane * kN).join(o[q], m[q], l[q]);
-    store_row<D, kBf16>(p, row, head, lane * kN, o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
+      if (p.add_o) {
+        OtherPart<D, kN> other;
+        other.load(p, row, head, lane * kN);
+        other.join(o[q], m[q], l[q]);
+      }
+    store_row<D, kBf16, true>(p, row, head, lane * kN, o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
     if (lane == 0)
       p.lse[static_cast<long long>(head) * p.r.total + row] =
           l[q] == 0.f ? -INFINITY : (m[q] + lg2_approx(l[q])) * kPagedLn2;

@@ -49,18 +49,12 @@
 // already with eight.  One context of 1000 keys 9 to 12 us, by the machine, of 4000 12
 // to 15, of 32000 30 to 37: launch, the look at the batch, and the joining of the
 // pieces.
-#include <type_traits>
-
 #include "fa_paged.cuh"
 #include "fa_serve.h"
 #include "sm103_primitives.cuh"
 
 namespace fa {
 namespace {
-
-struct NoPart {
-  __device__ __forceinline__ NoPart(const PagedLaunch&, long long, int, int) {}
-};
 
 constexpr int kConsumers = 8;                       // warps
 constexpr int kProducers = 4;                       // K and V of either group
@@ -148,7 +142,7 @@ __device__ __forceinline__ float exp2_field(int n) {
   return __uint_as_float(static_cast<uint32_t>(min(max(n, 0), 254)) << 23);
 }
 
-template <int D, bool kFp8, bool kBf16, int NB, bool kAdd>
+template <int D, bool kFp8, bool kBf16, int NB, bool kParts>
 __global__ void __maxnreg__(kFewRegs)
     paged_few_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
@@ -164,7 +158,7 @@ __global__ void __maxnreg__(kFewRegs)
   Smem& s = *reinterpret_cast<Smem*>(smem_raw + (-smem_u32(smem_raw) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
-    const Place at = warp_place<false>(p, gridDim.x, blockIdx.x);
+    const Place at = warp_place<false, kParts>(p, gridDim.x, blockIdx.x);
     if (lane == 0) {
       s.place = at;
       if (at.left == 0 && !p.whole) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
@@ -180,7 +174,7 @@ __global__ void __maxnreg__(kFewRegs)
   }
   __syncthreads();
   volatile int* abort_flag = &s.abort_flag;
-  WorkWalk<false> walk(s.place);
+  WorkWalk<false, kParts> walk(s.place);
   Piece x;
 
   if (warp >= kConsumers) {
@@ -196,7 +190,7 @@ __global__ void __maxnreg__(kFewRegs)
     uint32_t loads = 0;  // this warp's
     while (walk.next(p, x)) {
       PageFeed feed;
-      feed.start(p, x.b, x.tile0, x.lo, x.hi);
+      feed.start<kParts>(p, x.b, x.tile0, x.lo, x.hi);
       for (int tile = x.tile0 + ((group - static_cast<int>(tiles)) & (kGroups - 1));
            tile < x.tile1; tile += kGroups) {
         const int k0 = tile * kTile + lane * box_rows;
@@ -678,13 +672,17 @@ __global__ void __maxnreg__(kFewRegs)
         const int r = nb * 8 + warp;
         constexpr int kN = D / 32;
         float top = -INFINITY, sum = 0.f, out[kN] = {};
-        int token, head;
-        row_of(p, row0, min(r, x.rows - 1), x.hk, token, head);
-        const long long row = seq.start + token;
-        // (loaded here, ahead of the barriers; of rows behind the block's, its last one's)
-        [[maybe_unused]] typename std::conditional<kAdd, OtherPart<D, kN>, NoPart>::type other(
-            p, row, head, lane * kN);
         [[maybe_unused]] int vtop = 0;
+        // another part's result for this row, loaded ahead of the barriers (of rows behind the
+        // block's, its last one's)
+        [[maybe_unused]] OtherPart<D, kN> other;
+        if constexpr (kParts) {
+          if (p.add_o) {
+            int token, head;
+            row_of(p, row0, min(r, x.rows - 1), x.hk, token, head);
+            other.load(p, seq.start + token, head, lane * kN);
+          }
+        }
 #pragma unroll
         for (int gr = 0; gr < kGroups; ++gr) {
           if (group == gr)
@@ -735,12 +733,15 @@ __global__ void __maxnreg__(kFewRegs)
         }
         if (r < x.rows) {
           if (x.whole) {
+            int token, head;
+            row_of(p, row0, r, x.hk, token, head);
+            const long long row = seq.start + token;
             if (sum == 0.f) {  // no key: zeros, also where other rows saw a NaN value
 #pragma unroll
               for (int e = 0; e < kN; ++e) out[e] = 0.f;
             }
-            if constexpr (kAdd) other.join(out, top, sum);
-            store_row<D, kBf16>(p, row, head, lane * kN, out, sum == 0.f ? 0.f : 1.f / sum);
+            if constexpr (kParts) other.join(out, top, sum);
+            store_row<D, kBf16, kParts>(p, row, head, lane * kN, out, sum == 0.f ? 0.f : 1.f / sum);
             if (lane == 0)
               p.lse[static_cast<long long>(head) * p.r.total + row] =
                   sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kPagedLn2;
@@ -757,9 +758,9 @@ __global__ void __maxnreg__(kFewRegs)
   }
 }
 
-template <int D, bool kFp8, bool kBf16, int NB, bool kAdd>
+template <int D, bool kFp8, bool kBf16, int NB, bool kParts>
 cudaError_t launch_few_t(const PagedLaunch& a, cudaStream_t s) {
-  auto kern = paged_few_kernel<D, kFp8, kBf16, NB, kAdd>;
+  auto kern = paged_few_kernel<D, kFp8, kBf16, NB, kParts>;
   const int smem = static_cast<int>(sizeof(FewSmem<D, kFp8, NB>)) + 1024;
   static_assert(sizeof(FewSmem<D, kFp8, NB>) + 1024 <= 232448, "shared memory of one CTA");
   static AttrCache configured;
@@ -771,7 +772,7 @@ cudaError_t launch_few_t(const PagedLaunch& a, cudaStream_t s) {
 
 template <int D, bool kFp8, bool kBf16>
 cudaError_t launch_few_n(const PagedLaunch& a, cudaStream_t s) {
-  if (a.add_o)
+  if (a.parts)
     return a.block_rows == 8 ? launch_few_t<D, kFp8, kBf16, 1, true>(a, s)
                              : launch_few_t<D, kFp8, kBf16, 2, true>(a, s);
   return a.block_rows == 8 ? launch_few_t<D, kFp8, kBf16, 1, false>(a, s)

@@ -186,7 +186,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-template <int D, bool kFp8, bool kBf16, bool kAlibi>
+template <int D, bool kFp8, bool kBf16, bool kAlibi, bool kParts>
 __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
     paged_many_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
       while (!stop && take_unit(s, taken++, u, p.err, abort_flag)) {
         if (u.first > u.last) continue;
         PageFeed feed;
-        feed.start(p, u.b, u.first, u.key_lo, u.key_hi);
+        feed.start<kParts>(p, u.b, u.first, u.key_lo, u.key_hi);
         // Q once the last S product of the unit before has read it
         if (units > 0 && !many_warp_wait(&s.q_empty, (units - 1) & 1, p.err, abort_flag)) break;
         if (lane == 0) {
@@ -423,9 +423,9 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
       mbar_wait(&s.drain, 0, p.err, &zero, 100000000ull);
     } else if (warp == 10) {
       // -------------------------------------------------------------- units
-      const Place at = warp_place<true>(p, gridDim.x, blockIdx.x);
+      const Place at = warp_place<true, kParts>(p, gridDim.x, blockIdx.x);
       if (lane == 0 && at.left == 0 && !p.whole) p.tasks[blockIdx.x] = JoinTask{-1, 0, 0, 0, 0};
-      WorkWalk<true> walk(at);
+      WorkWalk<true, kParts> walk(at);
       Piece x;
       for (uint32_t n = 0;; ++n) {
         const bool more = walk.next(p, x);
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
         // This row's 128-byte pieces in the output: D / 64 of 16-bit elements,
         // D / 32 of fp32.  (The loops stay rolled: unrolled, the epilogue spent
         // most of its 2.5 us waiting for its own instructions.)
-        const bool narrow = whole && !p.o32;
+        const bool narrow = whole && !(kParts && p.o32);
         uint8_t* out = narrow ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) +
                                                            row * p.o_token + head * p.o_head)
                        : whole ? reinterpret_cast<uint8_t*>(p.o32 + (row * p.heads + head) * D)
@@ -977,9 +977,9 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
   }
 }
 
-template <int D, bool kFp8, bool kBf16, bool kAlibi>
+template <int D, bool kFp8, bool kBf16, bool kAlibi, bool kParts = false>
 cudaError_t launch_many_t(const PagedLaunch& a, cudaStream_t s) {
-  auto kern = paged_many_kernel<D, kFp8, kBf16, kAlibi>;
+  auto kern = paged_many_kernel<D, kFp8, kBf16, kAlibi, kParts>;
   const int smem = static_cast<int>(sizeof(ManySmem<D, kFp8>)) + 1024;
   static_assert(sizeof(ManySmem<D, kFp8>) + 1024 <= 232448, "shared memory of one CTA");
   static AttrCache configured;
@@ -992,6 +992,9 @@ cudaError_t launch_many_t(const PagedLaunch& a, cudaStream_t s) {
 template <int D, bool kFp8>
 cudaError_t launch_many_d(const PagedLaunch& a, cudaStream_t s) {
   const bool bf16 = a.elem == kElemBf16, alibi = a.alibi != nullptr;
+  if (a.parts)  // (without biases)
+    return bf16 ? launch_many_t<D, kFp8, true, false, true>(a, s)
+                : launch_many_t<D, kFp8, false, false, true>(a, s);
   return bf16 ? (alibi ? launch_many_t<D, kFp8, true, true>(a, s)
                        : launch_many_t<D, kFp8, true, false>(a, s))
               : (alibi ? launch_many_t<D, kFp8, false, true>(a, s)

@@ -36,6 +36,8 @@ struct Seq {
   int pos0;         // position of row `start`: len - rows (negative: rows without keys)
 };
 
+// kParts: without the pages that r.skip leaves out.
+template <bool kParts = false>
 __device__ __forceinline__ Seq load_seq(const Ragged& r, int page_log2, int b, uint32_t* err) {
   Seq s;
   const int c0 = r.cu[b], c1 = r.cu[b + 1], n = r.lens[b];
@@ -43,7 +45,8 @@ __device__ __forceinline__ Seq load_seq(const Ragged& r, int page_log2, int b, u
   s.rows = min(max(c1, s.start), r.total) - s.start;
   const long long most = static_cast<long long>(r.max_pages) << page_log2;
   s.len = static_cast<int>(min(static_cast<long long>(max(n, 0)), most));
-  if (r.skip) s.len -= r.skip[b] << page_log2;
+  if constexpr (kParts)
+    if (r.skip) s.len -= r.skip[b] << page_log2;
   s.pos0 = s.len - s.rows;
   if (err && (n < 0 || n > most || c0 < 0 || c1 < c0 || c1 > r.total))
     atomicExch(err, kDevErrBadIndex);

@@ -32,13 +32,15 @@ namespace fa {
 namespace {
 
 constexpr int kRotThreads = 128;
-// Heads in flight per lane group, at most: as many in each of a token's items, and few
-// items, as each works its angles out anew.  (fp32, four and two: 28.0 and 26.2 us, 1860
-// tokens of 72 heads of 128.)
+// Heads in flight per lane group: as many in each of a token's items, and few items, as
+// each works its angles out anew; two where there are no more, for more warps then.  (us, five
+// and two: 30000 tokens of 8 heads of 64 20.9 and 16.3, 100000 of 2 of 128 57.9 and 43.4.
+// fp32, three and two: 1860 tokens of 72 heads of 128 22.9 and 23.1, 20000 of 16 57.1 and 54.1.)
 template <int kElem>
-constexpr int kUnroll = kElem == kElemFp32 ? 3 : 5;
+constexpr int kMostHeads = kElem == kElemFp32 ? 2 : 5;
+constexpr int kFewHeads = 2;
 
-template <int D, int kElem, bool kInterleaved, bool kAxes>
+template <int D, int kElem, bool kInterleaved, bool kAxes, int kUnroll>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryLaunch p,
                                                              int head_groups, int per,
                                                              long long n_items) {
@@ -59,11 +61,11 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   T* const y1 = static_cast<T*>(p.y[1]);
   ItemWalk at(blockIdx.x * (kRotThreads / 32LL) + (threadIdx.x >> 5), n_items,
               static_cast<int>(gridDim.x) * (kRotThreads / 32), head_groups, p.N);
-  Vec8<kElem> v0[kUnroll<kElem>], v1[kUnroll<kElem>];
+  Vec8<kElem> v0[kUnroll], v1[kUnroll];
   const auto load = [&]() {
     const TokenRows<const T> xs(x0, p.xs[0], x1, p.xs[1], p.heads[0], at.b, at.n);
 #pragma unroll
-    for (int u = 0; u < kUnroll<kElem>; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int h = (at.group * per + u) * kSlots + slot;
       if (u < per && h < all) {
         const T* x = xs.row(h, h >= p.heads[0]);
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     angles.at(angles.place(p, at.b, at.n), p.magnitude, sub, sn, cs);
     const TokenRows<T> ys(y0, p.ys[0], y1, p.ys[1], p.heads[0], at.b, at.n);
 #pragma unroll
-    for (int u = 0; u < kUnroll<kElem>; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int h = h_first + u * kSlots;
       if (u >= per || h >= all) continue;
       if (rotates) {
@@ -103,12 +105,12 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   }
 }
 
-template <int D, int kElem, bool kInterleaved, bool kAxes>
-cudaError_t launch_rotary_t(const RotaryLaunch& a, cudaStream_t s) {
+template <int D, int kElem, bool kInterleaved, bool kAxes, int kUnroll>
+cudaError_t launch_rotary_u(const RotaryLaunch& a, cudaStream_t s) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const HeadSplit split(a.heads[0] + a.heads[1], 32 / (D / 16), kUnroll<kElem>);
+  const HeadSplit split(a.heads[0] + a.heads[1], 32 / (D / 16), kUnroll);
   const long long items = static_cast<long long>(a.B) * a.N * split.groups;
   const long long per_block = kRotThreads / 32;
   const long long blocks = (items + per_block - 1) / per_block;
@@ -116,10 +118,17 @@ cudaError_t launch_rotary_t(const RotaryLaunch& a, cudaStream_t s) {
   // a turn in fp64; but few enough items that they end together (65536 tokens of
   // 16 heads: 86.5 us with 16 blocks per SM, 80.5 with 64, 83.6 with one item each).
   const long long most = 64LL * sms;
-  rotary_kernel<D, kElem, kInterleaved, kAxes>
-      <<<static_cast<unsigned>(blocks < most ? blocks : most), kRotThreads, 0, s>>>(a, split.groups, split.per,
-                                                                                 items);
+  rotary_kernel<D, kElem, kInterleaved, kAxes, kUnroll>
+      <<<static_cast<unsigned>(blocks < most ? blocks : most), kRotThreads, 0, s>>>(
+          a, split.groups, split.per, items);
   return cudaGetLastError();
+}
+
+template <int D, int kElem, bool kInterleaved, bool kAxes>
+cudaError_t launch_rotary_t(const RotaryLaunch& a, cudaStream_t s) {
+  if (a.heads[0] + a.heads[1] <= kFewHeads * 32 / (D / 16))
+    return launch_rotary_u<D, kElem, kInterleaved, kAxes, kFewHeads>(a, s);
+  return launch_rotary_u<D, kElem, kInterleaved, kAxes, kMostHeads<kElem>>(a, s);
 }
 
 template <int D, int kElem>

@@ -83,6 +83,9 @@ struct PagedLaunch {
   void* o;
   long long o_token, o_head;
   float* lse;  // [heads][total]
+  // The call is one of two over parts of the keys; if not, what follows here, unit_cost,
+  // r.skip and r.rows are not looked at.
+  int parts;
   float* o32;  // or null: O goes here in fp32, [total][heads][D], instead of o
   // or null, few rows: results of another part of the keys to join with, as o32 and lse
   // (-inf where a row has none)

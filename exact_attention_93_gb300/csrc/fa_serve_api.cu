@@ -423,6 +423,7 @@ fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head
   first.r = Ragged{a.r.table, a.r.table_stride, a.r.max_pages, ints(at.cu), ints(at.lens),
                    groups,    a.r.total,        nullptr,       ints(at.rows)};
   first.win_right = -1;
+  first.parts = a.parts = 1;
   a.r.skip = ints(at.skip);
   const PagedPlan plan1 = plan_of(first, first.r), plan2 = plan_of(a, a.r);
   if (!aligned(workspace, 256) ||
