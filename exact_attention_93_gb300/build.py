@@ -127,7 +127,8 @@ def link_bind(obj, torch_lib):
     # process that imports it
     tmp = BIND + f".tmp{os.getpid()}"
     run(["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:libfattn.so", "-L" + torch_lib,
-         "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"],
+         "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda",
+         "-Wl,-rpath,$ORIGIN"],
         "link failed")
     os.replace(tmp, BIND)
     with open(BIND_STAMP, "w") as f:
