@@ -104,7 +104,7 @@ def qk_norm_rotary_func(q, k, q_weight, k_weight, inv_freq, positions=None, eps=
     q_weight and k_weight are (headdim,) tensors of q's type or float32, both of one
     type, or None (ones).  Everything else as for rotary_func.  Sums and products
     are fp32, values are rounded once; squares beyond fp32's range (magnitudes above
-    2 ** 60) are not provided for.
+    2 ** 60, or below 2 ** -60 where eps is as small) are not provided for.
 
     Differentiable once in q, k and the weights (fp32 sums in a fixed order: the same
     call gives the same bits); only the inputs are kept for it.  Differentiating its

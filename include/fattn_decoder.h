@@ -54,7 +54,8 @@ fa_status fa_rotary_axes(const fa_rotary_operand* q, const fa_rotary_operand* k,
  *                       ones; k_weight belongs to k.  8-byte aligned at least.
  *   eps                 not negative, finite.
  *
- * Squares are summed in fp32: a row of magnitudes beyond 2^60 comes out as zeros.
+ * Squares are summed in fp32: a row of magnitudes beyond 2^60 may come out as zeros, and
+ * one below 2^-60 loses bits where eps is as small.  With eps = 0 a row of zeros gives NaN.
  * The other arguments as for fa_rotary_axes.
  */
 fa_status fa_qk_norm_rotary(const fa_rotary_operand* q, const fa_rotary_operand* k,

@@ -244,6 +244,25 @@ def test_norm_gradients(dtype, wdtype, D, rdim, sections, interleaved):
             close(got[2 + i], dw, tol_w)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_without_eps(dtype):
+    g = torch.Generator().manual_seed(4)
+    freq, _ = rotary.rotary_frequencies(64, device="cpu")
+    x = (torch.randn(1, 6, 3, 64, generator=g) * torch.tensor([1e-15, 1e-6, 1.0, 1e9, 1e15, 1.0])[:, None, None]).to(dtype)
+    x[0, 5, 1] = 0.0  # 0 / 0 by the definition
+    w = 1 + 0.3 * torch.randn(64, generator=g)
+    dy = torch.randn(x.shape, generator=g).to(dtype)
+    pos = torch.arange(6)[None]
+    lx, lw = x.cuda().requires_grad_(), w.cuda().requires_grad_()
+    y = rotary.qk_norm_rotary_func(lx, None, lw, None, freq.cuda(), eps=0.0)
+    gx, = torch.autograd.grad(y, (lx,), (dy.cuda(),))
+    xn, _ = norm(x, w, 0.0)
+    ref = turn(xn, pos, freq)
+    close(y, ref, bound_norm(ref, xn, 1.0, dtype, 64))
+    dx, _, tol, _ = norm_grads(x, dy, w, 0.0, lambda d: turn(d, pos, freq, inverse=True))
+    close(gx, dx, tol + R.EPS[dtype] * 1.01 * dx.abs())
+
+
 def test_norm_gradient_against_differences():
     # differences of the 64-bit definition: f(t) = sum of c * y(x + t dx, w + t dw)
     g = torch.Generator().manual_seed(5)
