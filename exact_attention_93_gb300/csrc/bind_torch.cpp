@@ -11,9 +11,12 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/Context.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/record_function.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -113,9 +116,19 @@ PyObject* pair(at::Tensor a, at::Tensor b) {
 
 PyObject* status(fa_status s) { return PyLong_FromLong(static_cast<long>(s)); }
 
+// Whether anyone behind torch's dispatcher wants a part in an allocation: deterministic
+// algorithms, which fill what is not initialised, dispatch modes and transforms, or the profiler.
+bool dispatched() {
+  const at::Context& context = at::globalContext();
+  return (context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory()) ||
+         !(c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set).empty() ||
+         at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION).has_value();
+}
+
 // An uninitialised tensor on x's device.  (What at::empty comes to behind its dispatcher,
 // which costs a third of the 1.8 us that an allocation takes through it.)
 at::Tensor make(const at::Tensor& x, at::IntArrayRef sizes, at::ScalarType type) {
+  if (dispatched()) return at::empty(sizes, at::TensorOptions().dtype(type).device(x.device()));
   return at::Tensor(at::detail::empty_cuda(sizes, type, x.device(), std::nullopt));
 }
 
