@@ -103,7 +103,9 @@ def kv_cache_reserve(new_tokens, seqlens, block_table, free_pages, free_count, p
     sequences and of their keys, and written into block_table (int32 (batch,
     max_pages)); its entries for pages that the sequences hold already are read, the
     others left alone.  total is how many rows the packed tensors of the step have; rows
-    behind the last sequence get position 0 and slot -1.
+    behind the last sequence get position 0 and slot -1.  A page below zero where a new
+    key goes, in the table or among the free ones, is recorded as an error, and its rows
+    get slot -1 too.
 
     All or nothing: if the free pages do not suffice, missing says how many more it
     takes, and for bad lengths (negative, beyond the table, more new tokens than

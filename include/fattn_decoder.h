@@ -108,7 +108,9 @@ fa_status fa_qk_norm_rotary_bwd(const fa_rotary_operand* q, const fa_rotary_oper
  *   seqlens_out   int32 [batch]: seqlens + new_tokens.  May be seqlens.
  *   positions     int32 [total]: of packed row i, its position in its sequence.
  *   slots         int64 [total]: page * page_size + position % page_size, where its key
- *                 goes.  Rows behind the last sequence get position 0 and slot -1.
+ *                 goes.  Rows behind the last sequence get position 0 and slot -1.  A page
+ *                 below zero where a new key goes, in the table or among the free ones, is
+ *                 recorded as a device error, and its rows get slot -1 too.
  *   free_count_out  int32 [1]: *free_count less the pages taken.  May be free_count.
  *   missing       int32 [1]: 0; or, when free pages do not suffice, how many more it
  *                 takes; or -1 when an argument on the device is bad: a negative length,
