@@ -417,9 +417,17 @@ fa_elem weight_elem(const at::Tensor& x, const at::Tensor& wq, const at::Tensor&
 
 const void* address(const at::Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
 
+// A weight as the library takes it, on 8 bytes: a view into a buffer of many parameters,
+// which may lie anywhere, is copied.
+at::Tensor weight_operand(const at::Tensor& w) {
+  const bool ok = reinterpret_cast<uintptr_t>(address(w)) % 8 == 0;
+  return ok ? w : w.clone();
+}
+
 fa_status normed(const at::Tensor& q, const at::Tensor& yq, const at::Tensor& k,
-                 const at::Tensor& yk, const at::Tensor& wq, const at::Tensor& wk, const Norm& n,
-                 const Device& device) {
+                 const at::Tensor& yk, const at::Tensor& weight_q, const at::Tensor& weight_k,
+                 const Norm& n, const Device& device) {
+  const at::Tensor wq = weight_operand(weight_q), wk = weight_operand(weight_k);
   const int64_t dim = q.dim(), B = dim == 4 ? q.size(0) : 1, N = q.size(dim - 3);
   need(B <= INT_MAX && N <= INT_MAX, "tensors too large");
   const fa_rotary_operand a = rotary_operand(q, yq);
@@ -451,6 +459,7 @@ void norm_gradients(std::vector<NormOperand>& ops, const Norm& n) {
   fa_strides gs[2] = {};
   for (size_t i = 0; i < ops.size(); ++i) {
     ops[i].g = grad_operand(ops[i].g);
+    ops[i].w = weight_operand(ops[i].w);
     ops[i].dx = like(ops[i].x);
     o[i] = rotary_operand(ops[i].x, ops[i].dx);
     gs[i] = rotary_operand(ops[i].g, ops[i].dx).xs;
