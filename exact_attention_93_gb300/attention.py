@@ -222,7 +222,9 @@ def flash_attn_paged_func(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
     cu_groups[g] .. cu_groups[g + 1] - 1 a group, whose rows of block_table agree in their
     first shared_pages[g] entries (int32 (groups,)).  Those keys are then walked once for
     the group instead of once for each sequence, where that is faster by the sizes (the
-    table's width stands for the prefix); the results are the same up to rounding.
+    table's width stands for the prefix, and every sequence is taken to be in a group: with
+    a table far wider than the prefixes, or most sequences in none, a call without groups
+    may be faster); the results are the same up to rounding.
     No more pages are shared than lie before every new token of the group.  For causal
     attention without window and biases."""
     if alibi_slopes is not None or window_size != (-1, -1):

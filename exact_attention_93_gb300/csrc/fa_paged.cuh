@@ -359,12 +359,16 @@ __device__ __forceinline__ void store32(float* dst, const float (&o)[kN], float 
 }
 
 // A row's result from another part of the keys (PagedLaunch::add_o), loaded ahead of
-// its use: a lane's columns and the log-sum-exp in log2 units, -inf without one.
+// its use: a lane's columns and the log-sum-exp in log2 units, -inf without one.  (Of rows
+// that have none it loads what lies there, and drops it: nobody has to fill their places,
+// and no load waits for another.)
 template <int D, int kN>
 struct OtherPart {
   float lse2 = -INFINITY, x[kN] = {};
   __device__ __forceinline__ void load(const PagedLaunch& p, long long row, int head, int column) {
-    lse2 = p.add_lse[static_cast<long long>(head) * p.r.total + row] * 1.4426950408889634f;
+    const int first = *p.add_first, end = *p.add_end;
+    const float lse = p.add_lse[static_cast<long long>(head) * p.r.total + row];
+    lse2 = row >= first && row < end ? lse * 1.4426950408889634f : -INFINITY;
     const float* src = p.add_o + (row * p.heads + head) * D + column;
     if constexpr (kN == 4) {
       const float4 v = *reinterpret_cast<const float4*>(src);

@@ -68,14 +68,6 @@ __global__ void __launch_bounds__(kSetupThreads)
     p.cu[g] = packed(lo);
     if (g == p.groups - 1) p.cu[p.groups] = packed(hi);
   }
-  // rows of no group have no shared part
-  const auto none = [&](int from, int to) {
-    for (long long i = threadIdx.x; i < static_cast<long long>(to - from) * p.heads;
-         i += kSetupThreads)
-      p.lse[i / (to - from) * p.r.total + from + i % (to - from)] = -INFINITY;
-  };
-  if (g == 0) none(packed(0), packed(lo));
-  if (g == p.groups - 1) none(packed(hi), packed(p.r.batch));
   for (int b = lo + threadIdx.x; b < hi; b += kSetupThreads)
     p.skip[b] = load_seq(p.r, p.page_log2, b, nullptr).rows > 0 ? pages : 0;
   if (g == 0)
@@ -94,6 +86,7 @@ __global__ void __launch_bounds__(kSharedThreads)
   constexpr int kN = D / 32;
   const int lane = threadIdx.x & 31;
   const int first = max(p.cu[0], 0), last = min(p.cu[p.batch], p.total);
+  const int first1 = *p.first, last1 = *p.end;
   const long long n = static_cast<long long>(last - first) * p.heads;
   for (long long i = blockIdx.x * (kSharedThreads / 32LL) + (threadIdx.x >> 5); i < n;
        i += gridDim.x * (kSharedThreads / 32LL)) {
@@ -101,8 +94,9 @@ __global__ void __launch_bounds__(kSharedThreads)
     const int head = static_cast<int>(i % p.heads);
     const long long stat = static_cast<long long>(head) * p.total + row;
     const long long at = (static_cast<long long>(row) * p.heads + head) * D + lane * kN;
-    const float a = p.lse1[stat] * 1.4426950408889634f;
-    const bool both = a != -INFINITY;
+    const float lse1 = p.lse1[stat];
+    const bool both = row >= first1 && row < last1 && lse1 != -INFINITY;
+    const float a = both ? lse1 * 1.4426950408889634f : -INFINITY;
     const float b = p.lse2[stat] * 1.4426950408889634f;
     float x[kN], y[kN];
 #pragma unroll

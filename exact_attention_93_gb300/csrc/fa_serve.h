@@ -87,9 +87,10 @@ struct PagedLaunch {
   // r.skip and r.rows are not looked at.
   int parts;
   float* o32;  // or null: O goes here in fp32, [total][heads][D], instead of o
-  // or null, few rows: results of another part of the keys to join with, as o32 and lse
-  // (-inf where a row has none)
+  // or null, few rows: results of another part of the keys to join with, as o32 and lse, of
+  // rows *add_first to *add_end - 1
   const float *add_o, *add_lse;
+  const int *add_first, *add_end;
   const uint8_t *k_exp, *v_exp;
   Ragged r;
   int heads, heads_k, group, D;
@@ -124,8 +125,7 @@ cudaError_t launch_paged_few(const PagedLaunch& a, cudaStream_t s);
 struct SharedSetup {
   Ragged r;
   const int *cu_groups, *shared_pages;
-  int groups, page_log2, heads;
-  float* lse;  // [heads][total] of the shared part: -inf for rows of no group
+  int groups, page_log2;
   int *cu, *lens, *rows;  // of the groups as sequences: [groups + 1], [groups], [groups]
   int* skip;              // [batch]
   uint32_t* err;
@@ -133,6 +133,7 @@ struct SharedSetup {
 
 struct SharedJoin {
   const float *o1, *o2, *lse1, *lse2;  // the shared part, the own part
+  const int *first, *end;  // rows *first to *end - 1 have a shared part
   const int* cu;
   int batch, total, heads, D, elem;
   void* o;

@@ -227,7 +227,10 @@ fa_status paged_launch(PagedLaunch a, const PagedPlan& plan, void* workspace, cu
 // Sequences that share pages find one another's in L2, so that the whole cost of not
 // sharing is the key tiles that each walks again; but where the groups' keys together do
 // not stay in L2, HBM's reads are.  The lengths are on the device: the table's width
-// stands for the prefix, and a table far wider than that leads to sharing, as asked for.
+// stands for the prefix, and a table far wider than that leads to sharing, as asked for.  So
+// are the groups' ends: every sequence is taken to be in one.  (Two of 512 sequences of 8
+// tokens over 2048 keys, 1024 of them shared, not shared 715 us, shared 778; 8 of 64 single
+// tokens over 4096 keys, all shared, 147 and 164.)
 //
 // The model, in us: without sharing kOwnTile for each of a CTA's tiles; with it kSetOut for
 // the kernels before the own part (which costs the same either way) and kSharedTile for
@@ -438,10 +441,10 @@ fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head
   const auto s = static_cast<cudaStream_t>(stream);
   Ragged whole = a.r;
   whole.skip = nullptr;
-  if (launch_shared_setup(SharedSetup{whole, cu_groups, shared_pages, groups, a.page_log2, heads,
-                                      floats(at.lse1), ints(at.cu), ints(at.lens), ints(at.rows),
-                                      ints(at.skip), a.err},
-                          s) != cudaSuccess)
+  if (launch_shared_setup(
+          SharedSetup{whole, cu_groups, shared_pages, groups, a.page_log2, ints(at.cu),
+                      ints(at.lens), ints(at.rows), ints(at.skip), a.err},
+          s) != cudaSuccess)
     return FA_ERR_CUDA;
   first.o32 = floats(at.o1);
   first.lse = floats(at.lse1);
@@ -450,14 +453,17 @@ fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head
   if (!plan_many(plan2)) {  // few rows: the own part's kernels join the two
     a.add_o = first.o32;
     a.add_lse = first.lse;
+    a.add_first = ints(at.cu);
+    a.add_end = ints(at.cu) + groups;
     a.unit_cost = kOwnUnitCost;
     return paged_launch(a, plan2, base + at.bytes, s);
   }
   a.o32 = floats(at.o2);
   a.lse = floats(at.lse2);
   if ((st = paged_launch(a, plan2, base + at.bytes, s)) != FA_OK) return st;
-  const SharedJoin join{first.o32, a.o32, first.lse, a.lse, a.r.cu,  a.r.batch, a.r.total,
-                        a.heads,   a.D,   a.elem,    o,     o_token, o_head,    lse};
+  const SharedJoin join{first.o32,   a.o32,     first.lse, a.lse,   ints(at.cu), ints(at.cu) + groups,
+                        a.r.cu,      a.r.batch, a.r.total, a.heads, a.D,         a.elem,
+                        o,           o_token,   o_head,    lse};
   return launch_shared_join(join, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -180,7 +180,9 @@ fa_status fa_cache_write(const fa_kv_pages* cache, const long long* slots, int t
  *   workspace     fa_fwd_paged_shared_workspace_size bytes, 256-byte aligned.
  *
  * Which way is taken goes by the sizes that the host knows (for the prefix the width of the
- * table): where sharing would cost more than it saves, each sequence walks all of its keys.
+ * table, and every sequence is taken to be in a group): where sharing would cost more than it
+ * saves, each sequence walks all of its keys.  A call most of whose sequences are in no group,
+ * or whose table is far wider than its prefixes, may be better off without groups.
  * The other arguments as for fa_fwd_paged.  The parts are joined in fp32 before the one
  * rounding of the result.  Deterministic.  Under an e4m3 cache what the products keep
  * goes by the kernel that the shared and the own part take, as stated there.
