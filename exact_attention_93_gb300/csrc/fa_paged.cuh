@@ -404,7 +404,7 @@ __device__ __forceinline__ void store_row(const PagedLaunch& p, long long row, i
 // (fewer where the unit ends): its pieces are CTA c's second partial result and the
 // first ones of the CTAs after it.  A warp's lanes are the D columns of kRows rows,
 // kPieces pieces of which it loads side by side: the loads' latency is all this costs.
-template <int D, bool kBf16, int kRows, int kPieces>
+template <int D, bool kBf16, bool kParts, int kRows, int kPieces>
 __device__ __forceinline__ void join_rows(const PagedLaunch& p, const JoinTask& task, int c, int r0) {
   constexpr int kN = D / 32;
   const int lane = threadIdx.x & 31;
@@ -466,13 +466,13 @@ __device__ __forceinline__ void join_rows(const PagedLaunch& p, const JoinTask& 
     int token, head;
     row_of(p, task.first_row, r0 + q, task.hk, token, head);
     const long long row = task.start + token;
-    if constexpr (kRows == 1)  // (few rows)
+    if constexpr (kParts && kRows == 1)  // (as for all blocks of few rows)
       if (p.add_o) {
         OtherPart<D, kN> other;
         other.load(p, row, head, lane * kN);
         other.join(o[q], m[q], l[q]);
       }
-    store_row<D, kBf16, true>(p, row, head, lane * kN, o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
+    store_row<D, kBf16, kParts>(p, row, head, lane * kN, o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
     if (lane == 0)
       p.lse[static_cast<long long>(head) * p.r.total + row] =
           l[q] == 0.f ? -INFINITY : (m[q] + lg2_approx(l[q])) * kPagedLn2;
@@ -483,7 +483,7 @@ __device__ __forceinline__ void join_rows(const PagedLaunch& p, const JoinTask& 
 // up to a hundred pieces of a handful of rows, a prompt two or three pieces of 256.
 constexpr int kJoinThreads = 64;
 
-template <int D, bool kBf16, int kRows, int kPieces>
+template <int D, bool kBf16, bool kParts, int kRows, int kPieces>
 __global__ void __launch_bounds__(kJoinThreads, 4)
     paged_join_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   constexpr int kWarps = kJoinThreads / 32;
   for (int r0 = (blockIdx.y * kWarps + warp) * kRows; r0 < task.rows;
        r0 += gridDim.y * kWarps * kRows)
-    join_rows<D, kBf16, kRows, kPieces>(p, task, c, r0);
+    join_rows<D, kBf16, kParts, kRows, kPieces>(p, task, c, r0);
 }
 
 // Blocks of many rows where most CTAs have no task, as a few long units are cut into many
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
 // 8 and 23; four prompts, where they all find some, 10 more than by CTA.)
 constexpr int kJoinAllThreads = 128, kJoinTasks = 1024, kJoinAllRows = 1;
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kParts>
 __global__ void __launch_bounds__(kJoinAllThreads, 4)
     paged_join_all_kernel(const __grid_constant__ PagedLaunch p) {
   pdl_wait_and_release();
@@ -541,11 +541,11 @@ __global__ void __launch_bounds__(kJoinAllThreads, 4)
       else hi = mid;
     }
     const JoinTask task = p.tasks[lo];
-    join_rows<D, kBf16, kJoinAllRows, 8>(p, task, lo, (i - begin[lo]) * kJoinAllRows);
+    join_rows<D, kBf16, kParts, kJoinAllRows, 8>(p, task, lo, (i - begin[lo]) * kJoinAllRows);
   }
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kParts>
 cudaError_t launch_join(const PagedLaunch& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   const bool few = a.block_rows <= 16, all = !few && a.few_joins && a.sms <= kJoinTasks;
@@ -560,9 +560,9 @@ cudaError_t launch_join(const PagedLaunch& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return all   ? cudaLaunchKernelEx(&cfg, paged_join_all_kernel<D, kBf16>, a)
-         : few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, 1, 8>, a)
-               : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, 2, 2>, a);
+  return all   ? cudaLaunchKernelEx(&cfg, paged_join_all_kernel<D, kBf16, kParts>, a)
+         : few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, kParts, 1, 8>, a)
+               : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kBf16, kParts, 2, 2>, a);
 }
 
 }  // namespace fa

@@ -767,7 +767,7 @@ cudaError_t launch_few_t(const PagedLaunch& a, cudaStream_t s) {
   cudaError_t e = ensure_dynamic_smem(kern, smem, configured);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, static_cast<unsigned>(a.sms), kFewThreads, smem, s, a);
-  return e != cudaSuccess || a.whole ? e : launch_join<D, kBf16>(a, s);
+  return e != cudaSuccess || a.whole ? e : launch_join<D, kBf16, kParts>(a, s);
 }
 
 template <int D, bool kFp8, bool kBf16>
