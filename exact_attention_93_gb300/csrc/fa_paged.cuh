@@ -359,16 +359,18 @@ __device__ __forceinline__ void store32(float* dst, const float (&o)[kN], float 
 }
 
 // A row's result from another part of the keys (PagedLaunch::add_o), loaded ahead of
-// its use: a lane's columns and the log-sum-exp in log2 units, -inf without one.  (Of rows
+// its use: a lane's columns, the maximum in log2 units and the sum, 0 without one.  (Of rows
 // that have none it loads what lies there, and drops it: nobody has to fill their places,
-// and no load waits for another.)
+// and no load waits for another.  Maximum and sum stay apart as in cut pieces: the logarithm
+// of the sum would be rounded to the maximum's size, and weigh the parts wrong by 2^-23 of it.)
 template <int D, int kN>
 struct OtherPart {
-  float lse2 = -INFINITY, x[kN] = {};
+  float2 ml = {-INFINITY, 0.f};
+  float x[kN] = {};
   __device__ __forceinline__ void load(const PagedLaunch& p, long long row, int head, int column) {
     const int first = *p.add_first, end = *p.add_end;
-    const float lse = p.add_lse[static_cast<long long>(head) * p.r.total + row];
-    lse2 = row >= first && row < end ? lse * 1.4426950408889634f : -INFINITY;
+    ml = p.add_ml[static_cast<long long>(head) * p.r.total + row];
+    if (row < first || row >= end) ml = make_float2(-INFINITY, 0.f);
     const float* src = p.add_o + (row * p.heads + head) * D + column;
     if constexpr (kN == 4) {
       const float4 v = *reinterpret_cast<const float4*>(src);
@@ -380,8 +382,8 @@ struct OtherPart {
   }
   // Joined into the columns o, unnormalised under the maximum m (log2) and beside the sum l.
   __device__ __forceinline__ void join(float (&o)[kN], float& m, float& l) const {
-    if (lse2 == -INFINITY) return;
-    const float top = fmaxf(m, lse2), a = ex2_approx(m - top), b = ex2_approx(lse2 - top);
+    if (ml.y == 0.f) return;
+    const float top = fmaxf(m, ml.x), a = ex2_approx(m - top), b = ml.y * ex2_approx(ml.x - top);
 #pragma unroll
     for (int e = 0; e < kN; ++e) o[e] = (l == 0.f ? 0.f : o[e] * a) + x[e] * b;
     l = l * a + b;
@@ -398,6 +400,15 @@ __device__ __forceinline__ void store_row(const PagedLaunch& p, long long row, i
   else
     store16<kBf16>(static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head + column, o,
                    scale);
+}
+
+// And what belongs to it for all its columns, by one lane.
+template <bool kParts>
+__device__ __forceinline__ void store_stats(const PagedLaunch& p, long long row, int head, float m,
+                                            float l) {
+  const long long at = static_cast<long long>(head) * p.r.total + row;
+  if (kParts && p.o32) p.ml32[at] = make_float2(m, l);
+  else p.lse[at] = l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kPagedLn2;
 }
 
 // Adds up rows r0 .. r0 + kRows - 1 of the unit that CTA c began and did not finish
@@ -473,9 +484,7 @@ __device__ __forceinline__ void join_rows(const PagedLaunch& p, const JoinTask& 
         other.join(o[q], m[q], l[q]);
       }
     store_row<D, kBf16, kParts>(p, row, head, lane * kN, o[q], l[q] == 0.f ? 0.f : 1.f / l[q]);
-    if (lane == 0)
-      p.lse[static_cast<long long>(head) * p.r.total + row] =
-          l[q] == 0.f ? -INFINITY : (m[q] + lg2_approx(l[q])) * kPagedLn2;
+    if (lane == 0) store_stats<kParts>(p, row, head, m[q], l[q]);
   }
 }
 

@@ -742,9 +742,7 @@ __global__ void __maxnreg__(kFewRegs)
             }
             if constexpr (kParts) other.join(out, top, sum);
             store_row<D, kBf16, kParts>(p, row, head, lane * kN, out, sum == 0.f ? 0.f : 1.f / sum);
-            if (lane == 0)
-              p.lse[static_cast<long long>(head) * p.r.total + row] =
-                  sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kPagedLn2;
+            if (lane == 0) store_stats<kParts>(p, row, head, top, sum);
           } else {
             const long long at = (2LL * blockIdx.x + x.slot) * kRows + r;
             float* dst = p.part_o + at * D + lane * kN;

@@ -872,11 +872,8 @@ __global__ void __launch_bounds__(ManyWarps<kFp8>::kThreads, 1)
             (2LL * blockIdx.x + max(u.slot, 0)) * p.block_rows + t * tile_rows + r;
         const long long row = u.start + token;
         if (mine) {
-          if (whole)
-            p.lse[static_cast<long long>(head) * p.r.total + row] =
-                l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kPagedLn2;
-          else
-            p.part_ml[at] = make_float2(m, l);
+          if (whole) store_stats<kParts>(p, row, head, m, l);
+          else p.part_ml[at] = make_float2(m, l);
         }
         // This row's 128-byte pieces in the output: D / 64 of 16-bit elements,
         // D / 32 of fp32.  (The loops stay rolled: unrolled, the epilogue spent

@@ -1,9 +1,10 @@
 // fa_paged_shared.cu -- attention over prefixes that sequences share: groups of
 // sequences made to look like sequences, and the joining of the two parts.
 //
-// The softmax of a row over shared and own keys is joined from its parts' results:
+// The softmax of a row over shared and own keys is joined from its parts' results, each of
+// them o_i divided by its sum l_i of 2^(score - m_i):
 //
-//   lse = log(e^lse1 + e^lse2),   o = e^(lse1 - lse) o1 + e^(lse2 - lse) o2
+//   m = max(m1, m2),   w_i = l_i 2^(m_i - m),   o = (w1 o1 + w2 o2) / (w1 + w2)
 //
 // The shared part of a group is attention of all its rows over one sequence of keys,
 // none of them masked: every shared key lies before every new token.  So the kernels
@@ -94,23 +95,25 @@ __global__ void __launch_bounds__(kSharedThreads)
     const int head = static_cast<int>(i % p.heads);
     const long long stat = static_cast<long long>(head) * p.total + row;
     const long long at = (static_cast<long long>(row) * p.heads + head) * D + lane * kN;
-    const float lse1 = p.lse1[stat];
-    const bool both = row >= first1 && row < last1 && lse1 != -INFINITY;
-    const float a = both ? lse1 * 1.4426950408889634f : -INFINITY;
-    const float b = p.lse2[stat] * 1.4426950408889634f;
+    const float2 own = p.ml2[stat];
+    float2 other = p.ml1[stat];
+    if (row < first1 || row >= last1) other = make_float2(-INFINITY, 0.f);
+    const bool both = other.y != 0.f;
     float x[kN], y[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
       x[e] = both ? p.o1[at + e] : 0.f;
       y[e] = p.o2[at + e];
     }
-    const float top = fmaxf(a, b), ref = top == -INFINITY ? 0.f : top;
-    const float wa = ex2_approx(a - ref), wb = ex2_approx(b - ref), sum = wa + wb;
+    const float top = fmaxf(other.x, own.x), ref = top == -INFINITY ? 0.f : top;
+    const float wa = other.y * ex2_approx(other.x - ref), wb = own.y * ex2_approx(own.x - ref);
+    const float sum = wa + wb;
     const float per = sum == 0.f ? 0.f : 1.f / sum;
+    const float ua = wa * per, ub = wb * per;
     uint32_t out[kN / 2];
 #pragma unroll
     for (int e = 0; e < kN; e += 2)
-      out[e / 2] = pack2<kBf16>((x[e] * wa + y[e] * wb) * per, (x[e + 1] * wa + y[e + 1] * wb) * per);
+      out[e / 2] = pack2<kBf16>(x[e] * ua + y[e] * ub, x[e + 1] * ua + y[e + 1] * ub);
     uint16_t* dst = static_cast<uint16_t*>(p.o) + row * p.o_token + head * p.o_head + lane * kN;
     if constexpr (kN == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[kN / 2 - 1]);
     else *reinterpret_cast<uint32_t*>(dst) = out[0];

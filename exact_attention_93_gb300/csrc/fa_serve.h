@@ -86,10 +86,14 @@ struct PagedLaunch {
   // The call is one of two over parts of the keys; if not, what follows here, unit_cost,
   // r.skip and r.rows are not looked at.
   int parts;
-  float* o32;  // or null: O goes here in fp32, [total][heads][D], instead of o
-  // or null, few rows: results of another part of the keys to join with, as o32 and lse, of
+  // or null: O goes to o32 in fp32, [total][heads][D], instead of o, and to ml32, [heads][total],
+  // the rows' maxima (log2) and sums, instead of their lse
+  float* o32;
+  float2* ml32;
+  // or null, few rows: results of another part of the keys to join with, as o32 and ml32, of
   // rows *add_first to *add_end - 1
-  const float *add_o, *add_lse;
+  const float* add_o;
+  const float2* add_ml;
   const int *add_first, *add_end;
   const uint8_t *k_exp, *v_exp;
   Ragged r;
@@ -132,7 +136,8 @@ struct SharedSetup {
 };
 
 struct SharedJoin {
-  const float *o1, *o2, *lse1, *lse2;  // the shared part, the own part
+  const float *o1, *o2;  // the shared part, the own part
+  const float2 *ml1, *ml2;
   const int *first, *end;  // rows *first to *end - 1 have a shared part
   const int* cu;
   int batch, total, heads, D, elem;

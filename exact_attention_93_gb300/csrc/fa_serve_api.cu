@@ -289,11 +289,11 @@ constexpr int kOwnUnitCost = 3;
 
 // The workspace of attention over shared prefixes, in front of the kernels' own.
 struct SharedLayout {
-  size_t o1, o2, lse1, lse2, cu, lens, rows, skip, bytes;
+  size_t o1, o2, ml1, ml2, cu, lens, rows, skip, bytes;
 };
 
 SharedLayout shared_layout(int batch, int total, int heads, int D, int groups) {
-  const size_t stats = round256(sizeof(float) * total * heads), o = stats * D;
+  const size_t rows = static_cast<size_t>(total) * heads;
   SharedLayout at{};
   size_t end = 0;
   const auto take = [&](size_t bytes) {
@@ -301,10 +301,10 @@ SharedLayout shared_layout(int batch, int total, int heads, int D, int groups) {
     end += round256(bytes);
     return begin;
   };
-  at.o1 = take(o);
-  at.o2 = take(o);
-  at.lse1 = take(stats);
-  at.lse2 = take(stats);
+  at.o1 = take(sizeof(float) * rows * D);
+  at.o2 = take(sizeof(float) * rows * D);
+  at.ml1 = take(sizeof(float2) * rows);
+  at.ml2 = take(sizeof(float2) * rows);
   at.cu = take(sizeof(int) * (groups + 1));
   at.lens = take(sizeof(int) * groups);
   at.rows = take(sizeof(int) * groups);
@@ -421,6 +421,7 @@ fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head
   auto* base = static_cast<uint8_t*>(workspace);
   const auto ints = [&](size_t offset) { return reinterpret_cast<int*>(base + offset); };
   const auto floats = [&](size_t offset) { return reinterpret_cast<float*>(base + offset); };
+  const auto stats = [&](size_t offset) { return reinterpret_cast<float2*>(base + offset); };
   // the groups as sequences: all of their rows see all of the shared keys
   PagedLaunch first = a;
   first.r = Ragged{a.r.table, a.r.table_stride, a.r.max_pages, ints(at.cu), ints(at.lens),
@@ -447,21 +448,21 @@ fa_status fa_fwd_paged_shared(const void* q, long long q_token, long long q_head
           s) != cudaSuccess)
     return FA_ERR_CUDA;
   first.o32 = floats(at.o1);
-  first.lse = floats(at.lse1);
+  first.ml32 = stats(at.ml1);
   // one after the other: they share the workspace
   if ((st = paged_launch(first, plan1, base + at.bytes, s)) != FA_OK) return st;
   if (!plan_many(plan2)) {  // few rows: the own part's kernels join the two
     a.add_o = first.o32;
-    a.add_lse = first.lse;
+    a.add_ml = first.ml32;
     a.add_first = ints(at.cu);
     a.add_end = ints(at.cu) + groups;
     a.unit_cost = kOwnUnitCost;
     return paged_launch(a, plan2, base + at.bytes, s);
   }
   a.o32 = floats(at.o2);
-  a.lse = floats(at.lse2);
+  a.ml32 = stats(at.ml2);
   if ((st = paged_launch(a, plan2, base + at.bytes, s)) != FA_OK) return st;
-  const SharedJoin join{first.o32,   a.o32,     first.lse, a.lse,   ints(at.cu), ints(at.cu) + groups,
+  const SharedJoin join{first.o32,   a.o32,     first.ml32, a.ml32,  ints(at.cu), ints(at.cu) + groups,
                         a.r.cu,      a.r.batch, a.r.total, a.heads, a.D,         a.elem,
                         o,           o_token,   o_head,    lse};
   return launch_shared_join(join, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -1,5 +1,7 @@
-"""Attention over shared prefixes at the ends of its ranges: sequences in no group."""
+"""Attention over shared prefixes at the ends of its ranges: scores far from zero, sequences in no
+group."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -35,6 +37,60 @@ def shares(b, H, groups):
     torch.cuda.synchronize()
     assert st in (fattn.FA_OK, fattn.FA_ERR_INVALID_ARG)
     return st == fattn.FA_ERR_INVALID_ARG
+
+
+def hold(b, i, w, x):
+    """Makes x the keys (w = 0) or the values of sequence i."""
+    vals, exps = R.quantise(x) if b.fp8 else (x.double(), None)
+    (b.k, b.v)[w][i] = vals
+    for j in range(len(x)):
+        page, off = int(b.table[i, j // b.page]), j % b.page
+        if b.fp8:
+            codes = torch.ldexp(vals[j], 127 - exps[j].int()[:, None]).float().to(R.E4M3)
+            b.pool[w].view(torch.uint8)[page, off] = codes.view(torch.uint8)
+            b.exp[w][page, :, off] = exps[j]
+        else:
+            b.pool[w][page, off] = vals[j].to(b.dtype)
+
+
+@pytest.mark.parametrize("dtype,fp8", [(BF, False), (HF, False), (BF, True), (HF, True)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tokens", [1, 4, 8])  # the own part: eight rows, 16, many
+def test_scores_far_from_zero(tokens, D, dtype, fp8):
+    # Scores are 65536 less 0, 1 or 2 in log2 units, all of them and the weights exact (sums of
+    # two products of whole numbers, a scale of one, powers of two), so what the parts' joining
+    # does to the result is all that is off but for its own rounding: two exponentials, a sum
+    # and a quotient, 2^-21 of the weights' sum, one, in which 2^-20 leaves room.
+    n, page, batch = 256, 16, 8
+    scale = math.log(2.0)
+    assert float(torch.tensor(scale, dtype=torch.float32) *
+                 torch.tensor(1.4426950408889634, dtype=torch.float32)) == 1.0
+    groups = [(0, batch, n // page)]
+    b = P.shared_batch([tokens] * batch, [n + 250 + i for i in range(batch)], groups, 2, D, page, dtype,
+                       fp8, seed=D)
+    g = torch.Generator().manual_seed(1)
+    low = lambda k: -torch.randint(0, 3, (k, 2), generator=g).double()  # noqa: E731
+    first = low(n)
+    for i in range(batch):
+        own = b.lens[i] - n
+        k = torch.zeros(b.lens[i], 2, D, dtype=torch.float64)
+        k[..., 0] = 256
+        k[..., 1] = torch.cat((first, low(own)))
+        v = torch.ones(b.lens[i], 2, D, dtype=torch.float64)
+        v[n:] = -1
+        hold(b, i, 0, k)
+        hold(b, i, 1, v)
+    P.widen(b)
+    assert shares(b, 8, groups)
+    q = torch.zeros(b.total, 8, D)
+    q[..., 0], q[..., 1] = 256, 1
+    q = q.to(dtype)
+    ro, rl, _, _ = R.attention(b, q, scale)
+    _, o, lse = P.run(b, 8, groups, q=q, scale=scale)
+    tol = R.EPS[dtype] * 1.01 * ro.abs() + 2.0 ** -20 + 2.0 ** -25
+    off = (o.double() - ro).abs()
+    assert (off <= tol).all(), (off.max(), float((off / tol).max()))
+    assert ((lse.double() - rl).abs() <= 2.0 ** -22 * rl.abs()).all()
 
 
 @pytest.mark.parametrize("fp8", [False, True])
