@@ -16,14 +16,14 @@
 // Work split.  A warp takes one token and up to kUnroll heads per lane group:
 // D / 16 lanes cover a head, two 16-byte loads each (elements i and
 // i + rotary/2, or 16 neighbours when interleaved), so a warp covers
-// 512 / D heads at a time; the first loads are on their way while the pairs' table
+// 512 / D heads at a time; the first loads of 16-bit rows are on their way while the pairs' table
 // is filled.  The angles of a lane's 8 pairs depend on the
 // token alone and serve all of its heads; the lane groups of a warp compute
 // a share of them each and exchange them by shuffles.
 //
 // Measured: 65536 tokens of 16 heads of 128, bf16, 80.4 us, 6.7 TB/s, the measured
-// copy rate; 20000 tokens of 20 heads 34 us; 5003 tokens of 40 heads 19 us; 32 tokens of
-// 40 heads 2.8 us.  Along three axes, 32768 tokens of 20 heads 53 us, 6.3 TB/s.  (With four
+// copy rate; 20000 tokens of 20 heads 34 us; 5003 tokens of 40 heads 18.5 us; 32 tokens of
+// 40 heads 2.6 us.  Along three axes, 32768 tokens of 20 heads 53 us, 6.3 TB/s.  (With four
 // heads in flight instead of five, and the last item of a token's heads left with the
 // rest, 20 heads took 66 us: one head in four of the second item's was there.)
 #include "fa_rotary.cuh"
@@ -36,9 +36,18 @@ constexpr int kRotThreads = 128;
 // each works its angles out anew; two where there are no more, for more warps then.  (us, five
 // and two: 30000 tokens of 8 heads of 64 20.9 and 16.3, 100000 of 2 of 128 57.9 and 43.4.
 // fp32, three and two: 1860 tokens of 72 heads of 128 22.9 and 23.1, 20000 of 16 57.1 and 54.1.)
+// Two also where these make no more than kFewItems items per SM: a call then costs what one
+// warp takes.  (Five and two, of 40 heads of 128: 32 tokens 3.0 and 2.6, 250 tokens, 8 items per
+// SM, 3.13 and 3.06, 500 3.6 and 3.8.)
 template <int kElem>
 constexpr int kMostHeads = kElem == kElemFp32 ? 2 : 5;
 constexpr int kFewHeads = 2;
+constexpr long long kFewItems = 8;
+// fp32 rows take twice the registers, and loaded across the filling of the pairs' table they
+// leave room for fewer blocks: there they are loaded behind it.  (us, ahead and behind: 500 tokens
+// of 40 heads of 128 6.7 and 6.3, 1860 of 72 23.3 and 23.1.)
+template <int kElem>
+constexpr bool kLoadsAhead = kElem != kElemFp32;
 
 template <int D, int kElem, bool kInterleaved, bool kAxes, int kUnroll>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryLaunch p,
@@ -74,9 +83,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
       }
     }
   };
-  if (at.valid()) load();  // on its way while the table is filled
+  if (kLoadsAhead<kElem> && at.valid()) load();  // on its way while the table is filled
   table.fill(p);
   __syncthreads();
+  if (!kLoadsAhead<kElem> && at.valid()) load();
   Angles angles;
   angles.load(table, sub, slot, rotates);
   while (at.valid()) {
@@ -126,7 +136,11 @@ cudaError_t launch_rotary_u(const RotaryLaunch& a, cudaStream_t s) {
 
 template <int D, int kElem, bool kInterleaved, bool kAxes>
 cudaError_t launch_rotary_t(const RotaryLaunch& a, cudaStream_t s) {
-  if (a.heads[0] + a.heads[1] <= kFewHeads * 32 / (D / 16))
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const HeadSplit split(a.heads[0] + a.heads[1], 32 / (D / 16), kFewHeads);
+  if (split.groups <= 1 || static_cast<long long>(a.B) * a.N * split.groups <= kFewItems * sms)
     return launch_rotary_u<D, kElem, kInterleaved, kAxes, kFewHeads>(a, s);
   return launch_rotary_u<D, kElem, kInterleaved, kAxes, kMostHeads<kElem>>(a, s);
 }
