@@ -215,7 +215,8 @@ def flash_attn_paged_func(q, k_pages, v_pages, block_table, cu_seqlens, seqlens,
     flash_attn_func, in positions of the sequence.  Returns (total, nheads,
     headdim) (and the fp32 (nheads, total) log-sum-exp when return_lse).  A row
     that sees no key gets zeros and -inf; rows behind the last sequence are not
-    written.  Forward only.
+    written.  Scores, sums and the joining of parts are fp32; a weight is rounded to 16 bits
+    (q's type, fp16 over an e4m3 cache) for its product with the values.  Forward only.
 
     Sequences that share their first pages (answers to one prompt, requests under one
     system prompt) can say so: cu_groups (int32 (groups + 1,)) makes sequences
